@@ -18,6 +18,14 @@
  *   pa_swap_blocks       swap-out / swap-in between the GPU pool and a CPU
  *                        swap space, all pairs and layers
  *
+ * A cache that stays within a budget (no counterpart in the pages):
+ *   pa_rotary_cache_write        pa_cache_write with rotary positions (several
+ *                        axes) on query and key: once tokens are dropped a
+ *                        token's slot no longer tells its position
+ *   pa_decode_attention_scored, pa_prefill_scores  the attention weight every
+ *                        cached token received, added up per KV head
+ *   pa_evict_tokens      keeps the tokens that matter, compacts the rest away
+ *
  * Conventions for every entry point:
  *   - Every pointer named "device" is device memory owned by the caller; the
  *     library allocates nothing, keeps no state between calls and never
@@ -129,6 +137,76 @@ pa_status_t pa_cache_write_ex(const void *key, const void *value, void *k_cache,
                               int num_blocks, int block_size, int num_kv_heads, int head_dim,
                               pa_dtype_t dtype, unsigned int *dev_error_word,
                               pa_stream_t stream);
+
+/* Most frequencies (pairs) and position axes of a pa_rotary_t. */
+#define PA_MAX_ROTARY_PAIRS 128
+#define PA_MAX_ROTARY_AXES 8
+
+/* Rotary frequencies, filled by pa_rotary_init (host memory, copied by every
+ * call that takes it; plain data, no handle to free). */
+typedef struct {
+    int32_t rotary_dim;   /* elements of a head that turn: twice the pairs */
+    int32_t num_axes;     /* rows of `positions` that are read */
+    int32_t interleaved;  /* 0: pairs (i, i + rotary_dim / 2); 1: (2i, 2i + 1) */
+    float scale;          /* factor on the turned elements */
+    uint64_t turns[PA_MAX_ROTARY_PAIRS];  /* frequency: 2^64 times the turns per position, mod 2^64 */
+    uint8_t axis[PA_MAX_ROTARY_PAIRS];    /* position axis of each pair */
+} pa_rotary_t;
+
+/*
+ * pa_rotary_init -- frequencies for pa_rotary_cache_write.  Host only.
+ *
+ * inv_freq      HOST, [num_pairs] angular frequencies (radians per position),
+ *               finite; scaled variants pass their scaled values
+ * axes          HOST, [num_pairs] position axis of each pair, in
+ *               [0, PA_MAX_ROTARY_AXES); NULL: axis 0 for all
+ * num_pairs     a multiple of 8, at most PA_MAX_ROTARY_PAIRS
+ *               (PA_ERR_UNSUPPORTED otherwise); 2 num_pairs elements of a head
+ *               turn
+ * scale         factor on the turned elements (1 for the plain form)
+ */
+pa_status_t pa_rotary_init(pa_rotary_t *rotary, const double *inv_freq, const int32_t *axes,
+                           int num_pairs, int interleaved, float scale);
+
+/*
+ * pa_rotary_cache_write -- turn each new token's query and key by its
+ * position, and write its key and value rows into the pool slot named by
+ * slot_mapping.
+ *
+ * Defines: with pair i of a head at elements (i, i + rotary_dim / 2), or
+ * (2i, 2i + 1) when interleaved, and angle = positions[axis[i]][t] * inv_freq[i],
+ *     (x, y) -> scale * (x cos - y sin, y cos + x sin)
+ * for every query head (to query_out) and KV head of the key; elements from
+ * rotary_dim on and the value are unchanged.  The key and the value go to the
+ * slot as pa_cache_write puts them there.  The angle is exact modulo a turn
+ * for any 64-bit position before it is rounded to fp32; rotations are fp32,
+ * rounded once (to nearest even).
+ *
+ * query_out     device, token t's heads at t * query_out_stride; may be
+ *               `query` itself with the same stride (in place), and must not
+ *               overlap the inputs otherwise
+ * query, key, value  device; token t's [heads][head_dim] at t * stride, so the
+ *               three may be slices of one projection's rows.  Strides count
+ *               elements, are multiples of 8 and at least a token's row;
+ *               bases are 16-byte aligned
+ * positions     device int64 [rotary->num_axes][num_tokens]; any values
+ * rotary        HOST, from pa_rotary_init; rotary_dim <= head_dim
+ * slot_mapping  device int64 [num_tokens]; < 0: a padding token, whose key
+ *               and value are not written (its query is still turned)
+ * block_size    a power of two in [PA_MIN_BLOCK_SIZE, PA_MAX_BLOCK_SIZE]
+ * head_dim      64, 128 or 256; dtype PA_F16 or PA_BF16
+ * dev_error_word  device, may be NULL: PA_ERRBIT_SLOT_OOB for a slot past the
+ *               pool (that token's key and value are skipped)
+ * Distinct tokens must name distinct slots (two writes to one slot race).
+ */
+pa_status_t pa_rotary_cache_write(void *query_out, int64_t query_out_stride, const void *query,
+                                  int64_t query_stride, const void *key, int64_t key_stride,
+                                  const void *value, int64_t value_stride,
+                                  const int64_t *positions, const pa_rotary_t *rotary,
+                                  void *k_cache, void *v_cache, const int64_t *slot_mapping,
+                                  int num_tokens, int num_blocks, int block_size, int num_heads,
+                                  int num_kv_heads, int head_dim, pa_dtype_t dtype,
+                                  unsigned int *dev_error_word, pa_stream_t stream);
 
 /*
  * pa_decode_workspace_size -- bytes of device workspace pa_decode_attention

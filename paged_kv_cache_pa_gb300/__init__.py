@@ -15,6 +15,11 @@ device, raises.
     prefill_attention(query, k_cache, v_cache, block_tables, query_start_loc,
                       context_lens, max_query_len, max_context_len, scale, ...)
 
+A cache that stays within a budget:
+
+    rotary_cache_write(query, key, value, positions, rotary, k_cache, v_cache,
+                       slot_mapping, ...)
+
 Pools are [num_blocks][num_kv_heads][block_size][head_dim]; the block size
 is read from their third dimension: 16 goes to the plain entry points, other
 supported sizes (powers of two from 8 to 256) to the ``*_ex`` ones.
@@ -34,11 +39,13 @@ __all__ = ["cache_write", "decode_attention", "decode_attention_contiguous",
            "status_string", "PaError", "library_path", "load_library", "BLOCK_SIZE",
            "ERRBIT_BLOCK_OOB", "ERRBIT_SLOT_OOB", "ERRBIT_CONTEXT_LEN", "ERRBIT_TIMEOUT",
            "ERRBIT_INTERNAL",
-           "MAX_LAYERS", "BLOCK_SIZES", "swap_blocks", "prefill_attention"]
+           "MAX_LAYERS", "BLOCK_SIZES", "swap_blocks", "prefill_attention",
+           "Rotary", "rotary_cache_write", "MAX_ROTARY_PAIRS"]
 
 BLOCK_SIZE = 16
 BLOCK_SIZES = (8, 16, 32, 64, 128, 256)
 MAX_LAYERS = 128
+MAX_ROTARY_PAIRS = 128
 PA_F16, PA_BF16, PA_F32 = 0, 1, 2
 ERRBIT_BLOCK_OOB, ERRBIT_SLOT_OOB, ERRBIT_CONTEXT_LEN, ERRBIT_TIMEOUT = 1, 2, 4, 8
 ERRBIT_INTERNAL = 16  # PA_DEBUG builds only
@@ -50,9 +57,13 @@ _lock = threading.Lock()
 
 # entry point -> (restype, argtypes)
 _P, _I, _U64 = ctypes.c_void_p, ctypes.c_int, ctypes.c_uint64
+_I64 = ctypes.c_int64
 _SIGNATURES = {
     "pa_cache_write": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _P, _P]),
     "pa_cache_write_ex": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "pa_rotary_init": (_I, [_P, _P, _P, _I, _I, ctypes.c_float]),
+    "pa_rotary_cache_write": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                   _I, _I, _I, _I, _I, _I, _I, _P, _P]),
     "pa_decode_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "pa_decode_partition_tokens": (_I, [_I, _I, _I]),
     "pa_decode_kernel_launches": (_I, [_I, _I, _I, _I, _I]),
@@ -160,6 +171,96 @@ def cache_write(key, value, k_cache, v_cache, slot_mapping, error_word=None,
         _check(lib.pa_cache_write(*args, *tail), "pa_cache_write")
     else:
         _check(lib.pa_cache_write_ex(*args, bs, *tail), "pa_cache_write_ex")
+
+
+class _RotaryStruct(ctypes.Structure):
+    """pa_rotary_t."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("num_axes", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("turns", ctypes.c_uint64 * MAX_ROTARY_PAIRS),
+                ("axis", ctypes.c_uint8 * MAX_ROTARY_PAIRS)]
+
+
+class Rotary:
+    """Rotary frequencies for rotary_cache_write, made once and kept.
+
+    inv_freq: radians per position of each pair (a multiple of 8 pairs, at
+    most 128), scaled variants their scaled values; axes: the position axis of
+    each pair (all 0 when not given), e.g. ``[0] * 16 + [1] * 24 + [2] * 24``
+    for time, height and width; interleaved: pairs are neighbouring elements
+    instead of the two halves of the turned part; scale: factor on the turned
+    elements."""
+
+    def __init__(self, inv_freq: Sequence[float], axes: Optional[Sequence[int]] = None,
+                 interleaved: bool = False, scale: float = 1.0):
+        freqs = [float(f) for f in inv_freq]
+        n = len(freqs)
+        if axes is not None and len(axes) != n:
+            raise ValueError("axes must name one axis per frequency")
+        ax = None if axes is None else (ctypes.c_int32 * n)(*[int(a) for a in axes])
+        self._struct = _RotaryStruct()
+        self._ptr = ctypes.addressof(self._struct)
+        _check(load_library().pa_rotary_init(
+            self._ptr, ctypes.cast((ctypes.c_double * n)(*freqs), _P),
+            None if ax is None else ctypes.cast(ax, _P), n, int(bool(interleaved)),
+            float(scale)), "pa_rotary_init")
+
+    @property
+    def rotary_dim(self) -> int:
+        return self._struct.rotary_dim
+
+    @property
+    def num_axes(self) -> int:
+        return self._struct.num_axes
+
+
+def _rows(t, name):
+    """Pointer and token stride (elements) of [T][heads][D] whose heads are
+    dense and whose tokens may be apart (a slice of a projection's rows)."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    _, h, d = t.shape
+    st = t.stride()
+    if st[2] != 1 or (h > 1 and st[1] != d):
+        raise ValueError(f"{name} must have dense heads")
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else h * d)
+
+
+def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_cache,
+                       slot_mapping, query_out=None, error_word=None, stream=None):
+    """Turn query [T][H][D] and key [T][Hkv][D] by positions (int64
+    [axes][T], or [T] for one axis) and write key and value [T][Hkv][D] into
+    pool slot slot_mapping[t] (int64; < 0 skips key and value).  Token strides
+    are free (slices of one projection's rows).  Returns the turned query:
+    ``query_out``, ``query`` itself for an update in place, or a new dense
+    tensor."""
+    import torch
+    nb, hkv, bs, d = k_cache.shape
+    T, H, D = query.shape
+    if tuple(key.shape) != (T, hkv, d) or key.shape != value.shape or D != d:
+        raise ValueError("shape mismatch between query/key/value and the pools")
+    if v_cache.shape != k_cache.shape or not (
+            query.dtype == key.dtype == value.dtype == k_cache.dtype == v_cache.dtype):
+        raise ValueError("pools, query, key and value must have one dtype, the pools one shape")
+    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
+        raise TypeError("slot_mapping and positions must be int64")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    if positions.shape[-1:] != (T,) or positions.dim() > 2 or \
+            (positions.shape[0] if positions.dim() == 2 else 1) < rotary.num_axes:
+        raise ValueError("positions must be [axes][T] with an axis for each the frequencies name")
+    if query_out is None:
+        query_out = torch.empty(T, H, D, dtype=query.dtype, device=query.device)
+    elif query_out.shape != query.shape or query_out.dtype != query.dtype:
+        raise ValueError("query_out must match the query")
+    st = load_library().pa_rotary_cache_write(
+        *_rows(query_out, "query_out"), *_rows(query, "query"), *_rows(key, "key"),
+        *_rows(value, "value"), _dev(positions, "positions"), rotary._ptr,
+        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"),
+        T, nb, bs, H, hkv, d, _dtype_code(query.dtype), _opt_ptr(error_word, "error_word"),
+        _stream_ptr(stream, query.device))
+    _check(st, "pa_rotary_cache_write")
+    return query_out
 
 
 def decode_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,

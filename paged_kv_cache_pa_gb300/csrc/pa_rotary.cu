@@ -1,0 +1,328 @@
+// pa_rotary.cu -- pa_rotary_init and pa_rotary_cache_write: rotary positions
+// on the query and the key, fused with the write of key and value into the
+// paged cache.
+//
+// What it computes: pair i (of rotary_dim / 2) of a head has the angular
+// frequency w_i and takes its position from axis a_i; token t turns it by
+//     angle = position[a_i][t] * w_i,
+//     (x, y) -> scale * (x cos - y sin, y cos + x sin),
+// with (x, y) the elements (i, i + rotary_dim / 2) or, interleaved,
+// (2i, 2i + 1) of the head; elements from rotary_dim on pass through.
+//
+// Angles.  Only the angle's fraction of a turn matters, and positions are
+// whole numbers, so the frequency is kept as a 64-bit binary fraction of a
+// turn, F = frac(w / 2 pi) 2^64: the product position * F modulo 2^64 (one
+// wrapping integer multiply) is the fraction of a turn exactly, however far
+// the position, where a 32-bit product w * position is off by 0.03 rad at
+// position 10^6.  The fraction, read as a signed number, goes to sincospi,
+// one rounding to 32 bits before it.
+//
+// Bound: HBM.  Every row is read once and written once.  A row of head_dim
+// elements belongs to head_dim / 16 threads of two 16-byte chunks each, the
+// two halves of its eight pairs (or two neighbouring chunks when interleaved
+// or past rotary_dim), so a rotation never leaves its thread.  A token's
+// sines and cosines are computed once a CTA, for all its heads, while its
+// first rows are in flight.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "pa.h"
+#include "pa_host.cuh"
+#include "pa_launch.cuh"
+#include "pa_nvtx.cuh"
+#include "pa_ptx.cuh"
+
+namespace pa {
+namespace {
+
+constexpr int kRotThreads = 256;
+constexpr int kRotBatch = 4;  // rows a thread has in flight
+
+struct RotaryParams {
+    const uint4 *q, *k, *v;
+    uint4 *q_out, *k_cache, *v_cache;
+    long long q_stride, k_stride, v_stride, q_out_stride;  // 16-byte chunks between tokens
+    const int64_t *positions;                              // [num_axes][num_tokens]
+    const int64_t *slot_mapping;
+    long long num_slots;
+    int num_tokens, num_heads, num_kv_heads, block_shift;
+    int lg_lpr;        // log2 of a row's threads (head_dim / 16)
+    int lg_rows;       // log2 of the rows a token's threads take at once
+    unsigned int *err;
+    pa_rotary_t rot;
+};
+
+template <typename T>
+struct Pack;
+template <>
+struct Pack<__half> {
+    static __device__ __forceinline__ float2 up(uint32_t u) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    }
+    static __device__ __forceinline__ uint32_t down(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+template <>
+struct Pack<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 up(uint32_t u) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+    }
+    static __device__ __forceinline__ uint32_t down(float a, float b) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+// Eight pairs: x in chunk a and y in chunk b, element by element.
+template <typename T>
+__device__ __forceinline__ void turn_halves(uint4 &a, uint4 &b, const float2 (&cs)[8]) {
+    uint32_t *pa_ = reinterpret_cast<uint32_t *>(&a), *pb = reinterpret_cast<uint32_t *>(&b);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = Pack<T>::up(pa_[i]), y = Pack<T>::up(pb[i]);
+        const float2 c0 = cs[2 * i], c1 = cs[2 * i + 1];
+        pa_[i] = Pack<T>::down(x.x * c0.x - y.x * c0.y, x.y * c1.x - y.y * c1.y);
+        pb[i] = Pack<T>::down(y.x * c0.x + x.x * c0.y, y.y * c1.x + x.y * c1.y);
+    }
+}
+
+// Four pairs of neighbouring elements.
+template <typename T>
+__device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 *cs) {
+    uint32_t *p = reinterpret_cast<uint32_t *>(&a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 x = Pack<T>::up(p[i]);
+        p[i] = Pack<T>::down(x.x * cs[i].x - x.y * cs[i].y, x.y * cs[i].x + x.x * cs[i].y);
+    }
+}
+
+// A CTA takes 256 / (threads a row * rows at once) tokens; thread = (token,
+// row, unit j of the row).  A token's rows are its query heads, its key heads
+// and its value heads.
+template <typename T, bool IL>
+__global__ void __launch_bounds__(kRotThreads)
+    rotary_cache_write_kernel(const __grid_constant__ RotaryParams P) {
+    __shared__ float2 s_cs[kRotThreads / 4][8];  // [token][unit][pair], a unit per row thread
+    pdl_trigger();
+    const int lpr = 1 << P.lg_lpr, rows_at_once = 1 << P.lg_rows;
+    const int j = threadIdx.x & (lpr - 1);
+    const int r0 = ((int)threadIdx.x >> P.lg_lpr) & (rows_at_once - 1);
+    const int tl = (int)threadIdx.x >> (P.lg_lpr + P.lg_rows);
+    const int tokens = kRotThreads >> (P.lg_lpr + P.lg_rows);
+    const long long t = (long long)blockIdx.x * tokens + tl;
+    const bool live = t < P.num_tokens;
+    const int H = P.num_heads, Hkv = P.num_kv_heads, rows = H + 2 * Hkv;
+    const int pairs = P.rot.rotary_dim / 2, rot_units = pairs / 8;
+    pdl_wait();  // earlier kernels on the stream may still read or write what this touches
+
+    const int64_t slot = live ? P.slot_mapping[t] : -1;
+    const bool to_cache = slot >= 0 && slot < P.num_slots;  // < 0: padding
+    if (live && slot >= P.num_slots && r0 == 0 && j == 0 && P.err)
+        atomicOr(P.err, PA_ERRBIT_SLOT_OOB);
+
+    // this thread's two chunks of a row
+    int ca, cb;
+    if (IL || j >= rot_units) {
+        ca = 2 * j;
+        cb = 2 * j + 1;
+    } else {
+        ca = j;
+        cb = j + rot_units;
+    }
+    const uint4 *src[3] = {P.q + (live ? t : 0) * P.q_stride, P.k + (live ? t : 0) * P.k_stride,
+                           P.v + (live ? t : 0) * P.v_stride};
+    const int lg_cpr = P.lg_lpr + 1;  // log2 of a row's chunks
+    auto row_ptr = [&](int r) {
+        return r < H ? src[0] + ((size_t)r << lg_cpr)
+                     : r < H + Hkv ? src[1] + ((size_t)(r - H) << lg_cpr)
+                                   : src[2] + ((size_t)(r - H - Hkv) << lg_cpr);
+    };
+    uint4 a[kRotBatch], b[kRotBatch];
+    auto load = [&](int rb) {
+#pragma unroll
+        for (int u = 0; u < kRotBatch; ++u) {
+            const int r = rb + u * rows_at_once;
+            if (live && r < rows && (r < H || to_cache)) {
+                const uint4 *p = row_ptr(r);
+                a[u] = __ldcs(p + ca);
+                b[u] = __ldcs(p + cb);
+            }
+        }
+    };
+    load(r0);
+
+    // sines and cosines of the CTA's tokens, once each
+    for (int i = threadIdx.x; i < tokens * pairs; i += kRotThreads) {
+        const int tok = i / pairs, pr = i - tok * pairs;
+        const long long tt = (long long)blockIdx.x * tokens + tok;
+        if (tt < P.num_tokens) {
+            const int64_t pos = P.positions[(size_t)P.rot.axis[pr] * P.num_tokens + tt];
+            const uint64_t turn = (uint64_t)pos * P.rot.turns[pr];  // modulo one turn
+            float s, c;
+            sincospif(__ll2float_rn((long long)turn) * 0x1p-63f, &s, &c);
+            s_cs[(tok << P.lg_lpr) + (pr >> 3)][pr & 7] = make_float2(c * P.rot.scale,
+                                                                      s * P.rot.scale);
+        }
+    }
+    __syncthreads();
+    if (!live) return;
+    const bool turns = j < rot_units;
+    float2 cs[8];
+    if (turns) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) cs[e] = s_cs[(tl << P.lg_lpr) + j][e];
+    }
+    const size_t cache_row =
+        to_cache ? (((size_t)(slot >> P.block_shift) * Hkv) << P.block_shift) +
+                       (size_t)(slot & ((1 << P.block_shift) - 1))
+                 : 0;
+    uint4 *const q_out = P.q_out + t * P.q_out_stride;
+    for (int rb = r0; rb < rows; rb += kRotBatch * rows_at_once) {
+        if (rb != r0) load(rb);
+#pragma unroll
+        for (int u = 0; u < kRotBatch; ++u) {
+            const int r = rb + u * rows_at_once;
+            if (r >= rows || (r >= H && !to_cache)) continue;
+            if (turns && r < H + Hkv) {
+                if (IL) {
+                    turn_neighbours<T>(a[u], cs);
+                    turn_neighbours<T>(b[u], cs + 4);
+                } else {
+                    turn_halves<T>(a[u], b[u], cs);
+                }
+            }
+            uint4 *dst;
+            if (r < H) {
+                dst = q_out + ((size_t)r << lg_cpr);
+            } else {
+                const int h = r < H + Hkv ? r - H : r - H - Hkv;
+                dst = (r < H + Hkv ? P.k_cache : P.v_cache) +
+                      ((cache_row + ((size_t)h << P.block_shift)) << lg_cpr);
+            }
+            dst[ca] = a[u];
+            dst[cb] = b[u];
+        }
+    }
+}
+
+int log2_of(int x) {
+    int l = 0;
+    while ((1 << l) < x) ++l;
+    return l;
+}
+
+}  // namespace
+}  // namespace pa
+
+extern "C" pa_status_t pa_rotary_init(pa_rotary_t *rotary, const double *inv_freq,
+                                      const int32_t *axes, int num_pairs, int interleaved,
+                                      float scale) {
+    if (!rotary || !inv_freq) return PA_ERR_INVALID_ARG;
+    if (num_pairs <= 0 || num_pairs % 8 != 0 || num_pairs > PA_MAX_ROTARY_PAIRS)
+        return PA_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return PA_ERR_INVALID_ARG;
+    pa_rotary_t r;
+    std::memset(&r, 0, sizeof(r));
+    r.rotary_dim = 2 * num_pairs;
+    r.num_axes = 1;
+    r.interleaved = interleaved ? 1 : 0;
+    r.scale = scale;
+    constexpr double kTwoPi = 6.283185307179586476925286766559;
+    for (int i = 0; i < num_pairs; ++i) {
+        if (!std::isfinite(inv_freq[i])) return PA_ERR_INVALID_ARG;
+        const int a = axes ? axes[i] : 0;
+        if (a < 0 || a >= PA_MAX_ROTARY_AXES) return PA_ERR_INVALID_ARG;
+        if (a + 1 > r.num_axes) r.num_axes = a + 1;
+        r.axis[i] = (uint8_t)a;
+        double f = std::fmod(inv_freq[i] / kTwoPi, 1.0);
+        const bool neg = f < 0.0;
+        if (neg) f = -f;
+        const uint64_t u = (uint64_t)std::ldexp(f, 64);  // f < 1: below 2^64
+        r.turns[i] = neg ? 0u - u : u;
+    }
+    *rotary = r;
+    return PA_OK;
+}
+
+extern "C" pa_status_t pa_rotary_cache_write(
+    void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+    const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+    const int64_t *positions, const pa_rotary_t *rotary, void *k_cache, void *v_cache,
+    const int64_t *slot_mapping, int num_tokens, int num_blocks, int block_size, int num_heads,
+    int num_kv_heads, int head_dim, pa_dtype_t dtype, unsigned int *dev_error_word,
+    pa_stream_t stream) {
+    PA_NVTX_RANGE("pa_rotary_cache_write");
+    using namespace pa;
+    if (num_tokens < 0 || num_blocks <= 0 || num_heads <= 0 || num_kv_heads <= 0 || !rotary)
+        return PA_ERR_INVALID_ARG;
+    const int shift = pool_block_shift(block_size);
+    if (shift < 0) return PA_ERR_UNSUPPORTED;
+    if (!is_16bit(dtype)) return PA_ERR_INVALID_ARG;
+    if (!head_dim_supported(head_dim)) return PA_ERR_UNSUPPORTED;
+    if (rotary->rotary_dim <= 0 || rotary->rotary_dim % 16 != 0 || rotary->rotary_dim > head_dim ||
+        rotary->num_axes < 1 || rotary->num_axes > PA_MAX_ROTARY_AXES)
+        return PA_ERR_INVALID_ARG;
+    for (int i = 0; i < rotary->rotary_dim / 2; ++i)
+        if (rotary->axis[i] >= rotary->num_axes) return PA_ERR_INVALID_ARG;
+    if ((long long)num_heads + 2ll * num_kv_heads > (1 << 20)) return PA_ERR_UNSUPPORTED;
+    const long long q_row = (long long)num_heads * head_dim;
+    const long long kv_row = (long long)num_kv_heads * head_dim;
+    if (query_stride < q_row || query_out_stride < q_row || key_stride < kv_row ||
+        value_stride < kv_row || query_stride % 8 || query_out_stride % 8 || key_stride % 8 ||
+        value_stride % 8)
+        return PA_ERR_INVALID_ARG;
+    if (num_tokens == 0) return PA_OK;
+    if (!query_out || !query || !key || !value || !positions || !k_cache || !v_cache ||
+        !slot_mapping)
+        return PA_ERR_INVALID_ARG;
+    for (const void *p : {(const void *)query_out, query, key, value, (const void *)k_cache,
+                          (const void *)v_cache})
+        if (!is_aligned(p, 16)) return PA_ERR_INVALID_ARG;
+
+    RotaryParams P;
+    P.q = (const uint4 *)query;
+    P.k = (const uint4 *)key;
+    P.v = (const uint4 *)value;
+    P.q_out = (uint4 *)query_out;
+    P.k_cache = (uint4 *)k_cache;
+    P.v_cache = (uint4 *)v_cache;
+    P.q_stride = query_stride / 8;
+    P.k_stride = key_stride / 8;
+    P.v_stride = value_stride / 8;
+    P.q_out_stride = query_out_stride / 8;
+    P.positions = positions;
+    P.slot_mapping = slot_mapping;
+    P.num_slots = (long long)num_blocks << shift;
+    P.num_tokens = num_tokens;
+    P.num_heads = num_heads;
+    P.num_kv_heads = num_kv_heads;
+    P.block_shift = shift;
+    P.lg_lpr = log2_of(head_dim / 16);
+    // rows a token's threads take at once: all of them, up to the CTA
+    const int max_rows = kRotThreads >> P.lg_lpr;
+    const int rows = num_heads + 2 * num_kv_heads;
+    P.lg_rows = log2_of(rows < max_rows ? rows : max_rows);
+    P.err = dev_error_word;
+    P.rot = *rotary;
+    const int tokens = kRotThreads >> (P.lg_lpr + P.lg_rows);
+    const dim3 grid((unsigned)((num_tokens + tokens - 1) / tokens));
+    const cudaStream_t st = (cudaStream_t)stream;
+    cudaError_t e;
+    if (dtype == PA_F16)
+        e = rotary->interleaved
+                ? launch_pdl(rotary_cache_write_kernel<__half, true>, grid, dim3(kRotThreads), 0, st, P)
+                : launch_pdl(rotary_cache_write_kernel<__half, false>, grid, dim3(kRotThreads), 0, st, P);
+    else
+        e = rotary->interleaved
+                ? launch_pdl(rotary_cache_write_kernel<__nv_bfloat16, true>, grid, dim3(kRotThreads), 0, st, P)
+                : launch_pdl(rotary_cache_write_kernel<__nv_bfloat16, false>, grid, dim3(kRotThreads), 0, st, P);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+}
