@@ -509,6 +509,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const __grid_const
     const int hl = tid / TPH, th = tid % TPH;        // head within the CTA, thread within the head
     const int h = blockIdx.y * HPC + hl;
     const int grp = th / (C / CPT), c0 = (th % (C / CPT)) * CPT;  // partition group, first column
+    // The next kernel on the stream waits for this grid alone, so this grid
+    // must not end before the attention kernels have: one CTA waits for them
+    // whatever its sequence needs.
+    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();
     const int L = P.context_lens[s];  // an input: complete before this grid launched
     if (L <= 0 || L > P.max_context_len) return;  // empty or invalid: a zero row
     // One partition for sure: no split, and no shared prefix.  A sequence can
