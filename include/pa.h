@@ -329,6 +329,49 @@ pa_status_t pa_decode_attention_ex(void *out, pa_dtype_t out_dtype, const void *
                                    unsigned int *dev_error_word, pa_stream_t stream);
 
 /*
+ * pa_decode_scored_workspace_size -- bytes of device workspace
+ * pa_decode_attention_scored needs for these sizes: that of
+ * pa_decode_attention without shared prefixes, and a logit
+ * (4 bytes) for every sequence, query head and position below max_context_len
+ * rounded up to 16.  0 for invalid sizes.  Host only.
+ */
+size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim, int max_context_len);
+
+/*
+ * pa_decode_attention_scored -- pa_decode_attention_ex that also adds the
+ * attention weight every cached token received to its score.
+ *
+ * Defines: out as pa_decode_attention does, and for sequence s, KV head hk and
+ * token t < context_lens[s], with p_gt the softmax weight of token t for query
+ * head hk * G + g,
+ *     scores[s][hk][t] += sum_{g < G} p_gt .
+ * Weights and sums are fp32.  Scores of positions from context_lens[s] on, of
+ * an empty or invalid sequence, and of tokens in a skipped block are left as
+ * they were.  A new position's score has to be zero before its first call
+ * (pa_evict_tokens leaves it so).
+ *
+ * scores        device fp32 [num_seqs][num_kv_heads][score_stride]; row s
+ *               belongs to the batch's sequence s, like the block table's row
+ * score_stride  >= max_context_len
+ * workspace     >= pa_decode_scored_workspace_size(...) bytes, 256-byte aligned
+ * Every other argument, the checks and the error bits are those of
+ * pa_decode_attention_ex.  Sequences that share a prefix are read one by one
+ * here: their weights differ.  Enqueues the kernels of pa_decode_attention and
+ * one that turns logits into weights; results do not depend on the order in
+ * which work finishes.
+ */
+pa_status_t pa_decode_attention_scored(void *out, pa_dtype_t out_dtype, const void *query,
+                                       const void *k_cache, const void *v_cache,
+                                       const int32_t *block_tables, int max_blocks_per_seq,
+                                       const int32_t *context_lens, int max_context_len,
+                                       int num_seqs, int num_heads, int num_kv_heads,
+                                       int head_dim, int num_blocks, int block_size, float scale,
+                                       pa_dtype_t dtype, float *scores, int64_t score_stride,
+                                       void *workspace, size_t workspace_bytes,
+                                       unsigned int *dev_error_word, pa_stream_t stream);
+
+/*
  * pa_prefill_workspace_size -- bytes of device workspace pa_prefill_attention
  * needs for these sizes: the work list (8-16 bytes per work item) and room
  * for the partial results of up to 160 split items (4 x 128 x (head_dim + 2)

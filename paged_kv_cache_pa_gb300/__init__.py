@@ -19,6 +19,8 @@ A cache that stays within a budget:
 
     rotary_cache_write(query, key, value, positions, rotary, k_cache, v_cache,
                        slot_mapping, ...)
+    decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
+                            max_context_len, scale, scores, ...)
 
 Pools are [num_blocks][num_kv_heads][block_size][head_dim]; the block size
 is read from their third dimension: 16 goes to the plain entry points, other
@@ -40,7 +42,8 @@ __all__ = ["cache_write", "decode_attention", "decode_attention_contiguous",
            "ERRBIT_BLOCK_OOB", "ERRBIT_SLOT_OOB", "ERRBIT_CONTEXT_LEN", "ERRBIT_TIMEOUT",
            "ERRBIT_INTERNAL",
            "MAX_LAYERS", "BLOCK_SIZES", "swap_blocks", "prefill_attention",
-           "Rotary", "rotary_cache_write", "MAX_ROTARY_PAIRS"]
+           "Rotary", "rotary_cache_write", "decode_attention_scored",
+           "decode_scored_workspace_size", "MAX_ROTARY_PAIRS"]
 
 BLOCK_SIZE = 16
 BLOCK_SIZES = (8, 16, 32, 64, 128, 256)
@@ -73,6 +76,10 @@ _SIGNATURES = {
                                     _I, ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P]),
     "pa_decode_attention_contiguous": (_I, [_P, _I, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I,
                                             ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P]),
+    "pa_decode_scored_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "pa_decode_attention_scored": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I,
+                                        _I, ctypes.c_float, _I, _P, _I64, _P, ctypes.c_size_t,
+                                        _P, _P]),
     "pa_copy_blocks": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _P, _P]),
     "pa_copy_blocks_ex": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     "pa_prefill_attention": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I,
@@ -344,6 +351,60 @@ def decode_attention_contiguous(query, k_cache, v_cache, context_lens, max_conte
         workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
         _stream_ptr(stream, query.device))
     _check(st, "pa_decode_attention_contiguous")
+    return out
+
+
+def decode_scored_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int,
+                                 head_dim: int, max_context_len: int) -> int:
+    return int(load_library().pa_decode_scored_workspace_size(num_seqs, num_heads, num_kv_heads,
+                                                              head_dim, max_context_len))
+
+
+def _score_rows(scores, rows, name="scores"):
+    """Pointer and row stride of fp32 scores [..rows..][stride]."""
+    import torch
+    if scores.dtype != torch.float32:
+        raise TypeError(f"{name} must be float32")
+    if scores.dim() != 3 or tuple(scores.shape[:2]) != rows:
+        raise ValueError(f"{name} must be [S][Hkv][positions]")
+    return _dev(scores, name), scores.shape[2]
+
+
+def decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
+                            max_context_len: int, scale: float, scores, out=None,
+                            out_dtype=None, workspace=None, error_word=None, stream=None):
+    """decode_attention that also adds the attention weight each cached token
+    received, summed over the query heads of its KV head, to ``scores`` (fp32
+    [S][Hkv][>= max_context_len], row s for the batch's sequence s).
+    ``workspace`` (uint8, >= decode_scored_workspace_size bytes) is allocated
+    here when not given.  Returns ``out``."""
+    import torch
+    S, H, D = query.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    if d2 != D or v_cache.shape != k_cache.shape:
+        raise ValueError("pool shape mismatch")
+    if k_cache.dtype != query.dtype or v_cache.dtype != query.dtype:
+        raise ValueError("pools must match the query dtype")
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise TypeError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S][max_blocks], context_lens [S]")
+    sc, stride = _score_rows(scores, (S, hkv))
+    if out is None:
+        out = torch.empty(S, H, D, dtype=out_dtype or torch.float32, device=query.device)
+    elif out.shape != query.shape:
+        raise ValueError("out must match the query")
+    if workspace is None:
+        nbytes = decode_scored_workspace_size(S, H, hkv, D, int(max_context_len))
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=query.device)
+    st = load_library().pa_decode_attention_scored(
+        _dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"), _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"), block_tables.shape[1],
+        _dev(context_lens, "context_lens"), int(max_context_len), S, H, hkv, D, nb, bs,
+        float(scale), _dtype_code(query.dtype), sc, stride, _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
+        _stream_ptr(stream, query.device))
+    _check(st, "pa_decode_attention_scored")
     return out
 
 

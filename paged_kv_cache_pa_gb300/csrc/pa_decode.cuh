@@ -49,6 +49,13 @@
 //     the workspace and the merge kernel combines the sequence's partitions.
 // Scores are kept in base-2 units (q is pre-scaled by scale * log2 e) so the
 // exponentials are single ex2 instructions.
+//
+// The SCORED form of the kernels also leaves each token's score (the logit in
+// base-2 units, -inf in a skipped block) in the workspace, and every piece's
+// (max, sum) even where the piece is its sequence's only one: a weight needs
+// the whole row's maximum and sum, which only exist when all pieces are done
+// (pa_decode_scored.cu turns the logits into weights).  It runs without
+// shared-prefix items, so piece p of a sequence starts at token p * part_tokens.
 #pragma once
 
 #include <cuda.h>
@@ -155,6 +162,10 @@ struct DecodeParams {
     int4 *items;       // the list this launch takes (entries as above)
     int *nparts;       // per sequence: its partitions (0: empty or invalid)
     float *part_m, *part_l, *part_acc;
+    // SCORED form: logits [num_seqs][num_heads][logit_stride] in base-2 units;
+    // logit_stride is a multiple of kBlock, so a whole chunk can be written
+    float *logits;
+    size_t logit_stride;
     unsigned int *err;
 };
 
@@ -497,7 +508,7 @@ __device__ __forceinline__ void run_producer(const DecodeParams &P, T *sk, T *sv
 // ---------------------------------------------------------------------------
 // consumer warps
 // ---------------------------------------------------------------------------
-template <int D, int GM, typename T, int R>
+template <int D, int GM, typename T, int R, bool SCORED>
 __device__ __forceinline__ void run_consumer(const DecodeParams &P, const T *sk, const T *sv,
                                              const T *sq, const StageMeta *meta, uint64_t *full,
                                              uint64_t *empty, uint64_t *cbar, float *s_acc,
@@ -602,6 +613,19 @@ __device__ __forceinline__ void run_consumer(const DecodeParams &P, const T *sk,
                 for (int off = LPR / 2; off > 0; off >>= 1)
                     sc[i][g] += __shfl_xor_sync(0xffffffffu, sc[i][g], off);
 
+        if constexpr (SCORED) {  // lane g of a row leaves head g's logit
+            static_assert(GM <= LPR, "a lane per head");
+            const size_t t0 = (size_t)mt.p * P.part_tokens + (size_t)mt.j * kBlock;
+            float *dst = P.logits + ((size_t)mt.s * P.num_heads + (size_t)mt.hk * G) * P.logit_stride + t0;
+#pragma unroll
+            for (int i = 0; i < NI; ++i)
+#pragma unroll
+                for (int g = 0; g < GM; ++g)
+                    if (c == g && g < G)
+                        dst[(size_t)g * P.logit_stride + cw * kRowsPerWarp + i * RPI + rg] =
+                            valid[i] ? sc[i][g] : -INFINITY;
+        }
+
         // running softmax over the rows this lane has seen
         float pr[NI][GM];
 #pragma unroll
@@ -686,23 +710,22 @@ __device__ __forceinline__ void run_consumer(const DecodeParams &P, const T *sk,
                 o += s_acc[((size_t)w * GM + g) * D + d] * cf;
             }
             const int h = mt.hk * G + g;
-            if (mt.nparts == 1) {
+            const size_t pi = ((size_t)mt.s * H + h) * P.max_parts + mt.p;
+            if (mt.nparts == 1)
                 store_out(P.out, P.out_dtype, ((size_t)mt.s * H + h) * D + d,
                           Lsum > 0.f ? o / Lsum : 0.f);
-            } else {
-                const size_t pi = ((size_t)mt.s * H + h) * P.max_parts + mt.p;
+            else
                 P.part_acc[pi * D + d] = o;
-                if (d == 0) {
-                    P.part_m[pi] = M;
-                    P.part_l[pi] = Lsum;
-                }
+            if ((SCORED || mt.nparts > 1) && d == 0) {
+                P.part_m[pi] = M;
+                P.part_l[pi] = Lsum;
             }
         }
         if (!consumer_sync(1)) return;  // merge buffers free for the next item
     }
 }
 
-template <int D, int GM, typename T, int R, int MINB, bool DIRECT>
+template <int D, int GM, typename T, int R, int MINB, bool DIRECT, bool SCORED>
 __global__ void __launch_bounds__(kThreads, MINB) paged_decode_kernel(const __grid_constant__ DecodeParams P) {
     extern __shared__ __align__(128) unsigned char smem[];
     using L = Layout<D, GM, R>;
@@ -733,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, MINB) paged_decode_kernel(const __gr
     if (warp == 0)
         run_producer<D, GM, T, R, DIRECT>(P, sk, sv, sq, meta, full, empty, abort_flag, lane);
     else
-        run_consumer<D, GM, T, R>(P, sk, sv, sq, meta, full, empty, cbar, s_acc, s_m, s_l,
+        run_consumer<D, GM, T, R, SCORED>(P, sk, sv, sq, meta, full, empty, cbar, s_acc, s_m, s_l,
                                   abort_flag, warp - 1, lane);
 }
 
@@ -754,6 +777,20 @@ pa_status_t launch_decode_d128(const DecodeParams &P, pa_dtype_t dtype, int grid
                                cudaStream_t stream, int kernel);
 pa_status_t launch_decode_d256(const DecodeParams &P, pa_dtype_t dtype, int grid_cap,
                                cudaStream_t stream, int kernel);
+
+// The SCORED forms (P.logits set; one attention kernel, no shared-prefix
+// items; defined in pa_decode_scored_d{64,128,256}.cu).
+pa_status_t launch_decode_scored_d64(const DecodeParams &P, pa_dtype_t dtype, int grid_cap,
+                                     cudaStream_t stream);
+pa_status_t launch_decode_scored_d128(const DecodeParams &P, pa_dtype_t dtype, int grid_cap,
+                                      cudaStream_t stream);
+pa_status_t launch_decode_scored_d256(const DecodeParams &P, pa_dtype_t dtype, int grid_cap,
+                                      cudaStream_t stream);
+
+// The weight pass of the SCORED form (pa_decode_scored.cu): adds every
+// token's attention weight to scores[s][hk][t].
+pa_status_t launch_decode_weights(const DecodeParams &P, float *scores, long long score_stride,
+                                  cudaStream_t stream);
 
 // Number of streaming multiprocessors of the current device (cached).
 int current_sm_count();

@@ -78,14 +78,19 @@ size_t align256(size_t x) { return (x + 255) / 256 * 256; }
 struct WsLayout {
     int part_tokens, max_parts, group_seqs;
     long long list_cap;  // entries per list
-    size_t items0_off, items1_off, nparts_off, m_off, l_off, acc_off, bytes;
+    size_t items0_off, items1_off, nparts_off, m_off, l_off, acc_off;
+    size_t logits_off, logit_stride;  // the scored form's logits
+    size_t bytes;
 };
 
+// scored: the scored form has no shared-prefix items, keeps every piece's
+// (max, sum), and has room for the logits.
 WsLayout ws_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
-                   int max_context_len) {
+                   int max_context_len, bool scored = false) {
     WsLayout w;
     w.part_tokens = choose_part_tokens(num_seqs, num_kv_heads, max_context_len);
-    w.group_seqs = group_seqs(num_seqs, num_heads / num_kv_heads, head_dim, max_context_len);
+    w.group_seqs =
+        scored ? 0 : group_seqs(num_seqs, num_heads / num_kv_heads, head_dim, max_context_len);
     const int np = max_context_len > 0 ? (max_context_len + w.part_tokens - 1) / w.part_tokens : 1;
     // a sequence in a run has the shared prefix's pieces and its own: at most
     // one partition more than its length alone needs
@@ -99,17 +104,21 @@ WsLayout ws_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
     off = align256(off + (size_t)(w.group_seqs ? w.list_cap : 1) * sizeof(int4));
     w.nparts_off = off;
     off = align256(off + (size_t)num_seqs * sizeof(int));
-    if (w.max_parts > 1) {
-        const size_t n = (size_t)num_seqs * num_heads * w.max_parts;
+    w.m_off = w.l_off = w.acc_off = off;
+    const size_t n = (size_t)num_seqs * num_heads * w.max_parts;
+    if (w.max_parts > 1 || scored) {
         w.m_off = off;
         off = align256(off + n * 4);
         w.l_off = off;
         off = align256(off + n * 4);
+    }
+    if (w.max_parts > 1) {
         w.acc_off = off;
         off = align256(off + n * head_dim * 4);
-    } else {
-        w.m_off = w.l_off = w.acc_off = off;
     }
+    w.logits_off = off;
+    w.logit_stride = ((size_t)max_context_len + kBlock - 1) / kBlock * kBlock;
+    if (scored) off = align256(off + (size_t)num_seqs * num_heads * w.logit_stride * 4);
     w.bytes = off;
     return w;
 }
@@ -674,14 +683,15 @@ extern "C" int pa_decode_kernel_launches(int num_seqs, int num_heads, int num_kv
 namespace {
 
 // Shared implementation of the paged (contig_rows == 0) and contiguous
-// (contig_rows > 0) entry points.
+// (contig_rows > 0) entry points; scores != nullptr: the scored form.
 pa_status_t decode_impl(void *out, pa_dtype_t out_dtype, const void *query, const void *k_cache,
                         const void *v_cache, const int32_t *block_tables, int max_blocks_per_seq,
                         int contig_rows, const int32_t *context_lens, int max_context_len,
                         int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                         int num_blocks, int block_size, float scale, pa_dtype_t dtype,
                         void *workspace, size_t workspace_bytes, unsigned int *dev_error_word,
-                        pa_stream_t stream) {
+                        pa_stream_t stream, float *scores = nullptr,
+                        long long score_stride = 0) {
     const int block_shift = block_shift_of(block_size);
     if (block_shift < 0) return PA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || max_context_len < 0)
@@ -711,7 +721,9 @@ pa_status_t decode_impl(void *out, pa_dtype_t out_dtype, const void *query, cons
     if (!aligned(out, 16) || !aligned(query, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
         return PA_ERR_INVALID_ARG;
     if (!aligned(workspace, 256)) return PA_ERR_WORKSPACE;
-    const WsLayout w = ws_layout(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len);
+    const bool scored = scores != nullptr;
+    const WsLayout w =
+        ws_layout(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len, scored);
     if (workspace_bytes < w.bytes) return PA_ERR_WORKSPACE;
 
     if (w.max_parts > kMaxParts) return PA_ERR_UNSUPPORTED;
@@ -768,6 +780,10 @@ pa_status_t decode_impl(void *out, pa_dtype_t out_dtype, const void *query, cons
     P.part_m = reinterpret_cast<float *>(ws + w.m_off);
     P.part_l = reinterpret_cast<float *>(ws + w.l_off);
     P.part_acc = reinterpret_cast<float *>(ws + w.acc_off);
+    if (scored) {
+        P.logits = reinterpret_cast<float *>(ws + w.logits_off);
+        P.logit_stride = w.logit_stride;
+    }
     P.err = dev_error_word;
     cudaStream_t st = (cudaStream_t)stream;
 
@@ -805,6 +821,11 @@ pa_status_t decode_impl(void *out, pa_dtype_t out_dtype, const void *query, cons
     long long cap = direct ? (long long)num_seqs * num_kv_heads : w.list_cap * num_kv_heads;
     if (cap > INT_MAX) cap = INT_MAX;
     auto launch = [&](int kernel) -> pa_status_t {
+        if (scored) {
+            if (head_dim == 64) return launch_decode_scored_d64(P, dtype, (int)cap, st);
+            if (head_dim == 128) return launch_decode_scored_d128(P, dtype, (int)cap, st);
+            return launch_decode_scored_d256(P, dtype, (int)cap, st);
+        }
         if (head_dim == 64) return launch_decode_d64(P, dtype, (int)cap, st, kernel);
         if (head_dim == 128) return launch_decode_d128(P, dtype, (int)cap, st, kernel);
         return launch_decode_d256(P, dtype, (int)cap, st, kernel);
@@ -832,6 +853,10 @@ pa_status_t decode_impl(void *out, pa_dtype_t out_dtype, const void *query, cons
         st_launch = launch(kKernelByGroup);
     }
     if (st_launch != PA_OK) return st_launch;
+    if (scored) {
+        st_launch = launch_decode_weights(P, scores, score_stride, st);
+        if (st_launch != PA_OK) return st_launch;
+    }
 
     if (merge) {
         if (num_heads > 65535) return PA_ERR_UNSUPPORTED;
@@ -900,4 +925,28 @@ extern "C" pa_status_t pa_decode_attention_contiguous(
                        context_lens, max_context_len, num_seqs, num_heads, num_kv_heads,
                        head_dim, 0, PA_BLOCK_SIZE, scale, dtype, workspace, workspace_bytes,
                        dev_error_word, stream);
+}
+
+extern "C" size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                                  int head_dim, int max_context_len) {
+    if (num_seqs < 0 || num_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || max_context_len < 0)
+        return 0;
+    return ws_layout(num_seqs, num_heads, num_kv_heads, head_dim, max_context_len, true).bytes;
+}
+
+extern "C" pa_status_t pa_decode_attention_scored(
+    void *out, pa_dtype_t out_dtype, const void *query, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *context_lens,
+    int max_context_len, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+    int num_blocks, int block_size, float scale, pa_dtype_t dtype, float *scores,
+    int64_t score_stride, void *workspace, size_t workspace_bytes, unsigned int *dev_error_word,
+    pa_stream_t stream) {
+    PA_NVTX_RANGE("pa_decode_attention_scored");
+    if (score_stride < max_context_len) return PA_ERR_INVALID_ARG;
+    if (num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
+    if (num_seqs > 0 && (!scores || !aligned(scores, 4))) return PA_ERR_INVALID_ARG;
+    return decode_impl(out, out_dtype, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                       0, context_lens, max_context_len, num_seqs, num_heads, num_kv_heads,
+                       head_dim, num_blocks, block_size, scale, dtype, workspace, workspace_bytes,
+                       dev_error_word, stream, scores, score_stride);
 }

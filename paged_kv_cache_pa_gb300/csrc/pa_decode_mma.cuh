@@ -344,7 +344,7 @@ __device__ __forceinline__ void run_producer_mma(const DecodeParams &P, unsigned
 // ---------------------------------------------------------------------------
 // consumer warps: warp w takes block w of every stage
 // ---------------------------------------------------------------------------
-template <int D, typename T, int R, int W>
+template <int D, typename T, int R, int W, bool SCORED>
 __device__ __forceinline__ void run_consumer_mma(const DecodeParams &P, unsigned char *sk,
                                                  unsigned char *sv, const unsigned char *sq,
                                                  const StageMeta *meta, uint64_t *full,
@@ -414,6 +414,19 @@ __device__ __forceinline__ void run_consumer_mma(const DecodeParams &P, unsigned
 
         const int vb = min(kBlock, max(0, mt.nvalid - cw * kBlock));  // my block's tokens
         const bool mine = vb > 0 && !(((unsigned)mt.flags >> (8 + cw)) & 1u);
+        // SCORED: where this lane's logits of row g go (tokens 2t, 2t + 1 and
+        // 8 + 2t, 9 + 2t of the warp's chunk)
+        float2 *lg = nullptr;
+        if constexpr (SCORED) {
+            if (vb > 0 && g < G) {
+                const size_t t0 = (size_t)mt.p * P.part_tokens + (size_t)(mt.j * W + cw) * kBlock;
+                lg = reinterpret_cast<float2 *>(
+                    P.logits +
+                    ((size_t)mt.s * P.num_heads + (size_t)mt.hk * G + g) * P.logit_stride + t0 +
+                    2 * t);
+                if (!mine) lg[0] = lg[4] = make_float2(-INFINITY, -INFINITY);  // a skipped block
+            }
+        }
         if (mine) {
             unsigned char *kt = sk + (size_t)(slot * W + cw) * KB * kBoxBytes;
             unsigned char *vt = sv + (size_t)(slot * W + cw) * KB * kBoxBytes;
@@ -443,6 +456,12 @@ __device__ __forceinline__ void run_consumer_mma(const DecodeParams &P, unsigned
             if (2 * t + 1 >= vb) x[1] = -INFINITY;
             if (8 + 2 * t >= vb) x[2] = -INFINITY;
             if (9 + 2 * t >= vb) x[3] = -INFINITY;
+            if constexpr (SCORED) {
+                if (lg) {
+                    lg[0] = make_float2(x[0], x[1]);
+                    lg[4] = make_float2(x[2], x[3]);
+                }
+            }
             float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
@@ -515,7 +534,7 @@ __device__ __forceinline__ void run_consumer_mma(const DecodeParams &P, unsigned
 // epilogue warp: merge the four consumer warps' states of each item and write
 // the output row (one partition) or the partition's partial state
 // ---------------------------------------------------------------------------
-template <int D, int W>
+template <int D, int W, bool SCORED>
 __device__ __forceinline__ void run_epilogue_mma(const DecodeParams &P, uint64_t *acc_full,
                                                  uint64_t *acc_empty, const float *s_acc,
                                                  const float *s_m, const float *s_l,
@@ -560,7 +579,7 @@ __device__ __forceinline__ void run_epilogue_mma(const DecodeParams &P, uint64_t
                 else
                     P.part_acc[pi * D + d] = ov;
             }
-            if (nparts > 1 && lane == 0) {
+            if ((SCORED || nparts > 1) && lane == 0) {
                 P.part_m[pi] = M;
                 P.part_l[pi] = Lsum;
             }
@@ -586,7 +605,7 @@ __device__ __forceinline__ void run_epilogue_mma(const DecodeParams &P, uint64_t
     }
 }
 
-template <int D, typename T, int R, int MINB, int W, bool DIRECT>
+template <int D, typename T, int R, int MINB, int W, bool DIRECT, bool SCORED>
 __global__ void __launch_bounds__(threads_mma<W>(), MINB)
     paged_decode_mma_kernel(const __grid_constant__ DecodeParams P) {
     extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -624,10 +643,10 @@ __global__ void __launch_bounds__(threads_mma<W>(), MINB)
     if (warp == 0)
         run_producer_mma<D, T, R, W, DIRECT>(P, sk, sv, sq, meta, full, empty, abort_flag, lane);
     else if (warp <= W)
-        run_consumer_mma<D, T, R, W>(P, sk, sv, sq, meta, full, empty, acc_full, acc_empty, s_acc,
+        run_consumer_mma<D, T, R, W, SCORED>(P, sk, sv, sq, meta, full, empty, acc_full, acc_empty, s_acc,
                                   s_m, s_l, info, abort_flag, warp - 1, lane);
     else
-        run_epilogue_mma<D, W>(P, acc_full, acc_empty, s_acc, s_m, s_l, info, abort_flag, lane);
+        run_epilogue_mma<D, W, SCORED>(P, acc_full, acc_empty, s_acc, s_m, s_l, info, abort_flag, lane);
 }
 
 }  // namespace pa

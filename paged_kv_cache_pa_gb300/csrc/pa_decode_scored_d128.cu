@@ -1,0 +1,10 @@
+// pa_decode_scored_d128.cu -- instantiations of the scored form of paged decode
+// attention for head_dim 128 (fp16 / bf16).
+#include "pa_decode_launch.cuh"
+
+namespace pa {
+pa_status_t launch_decode_scored_d128(const DecodeParams &P, pa_dtype_t dtype, int grid_cap,
+                                     cudaStream_t stream) {
+    return dispatch_scored<128>(P, dtype, grid_cap, stream);
+}
+}  // namespace pa

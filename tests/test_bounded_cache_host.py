@@ -88,3 +88,32 @@ def test_rotary_axis_past_the_rows_is_refused(lib):
     r.axis[5] = 1
     assert lib.pa_rotary_cache_write(P, 512, P, 512, P, 128, P, 128, P, ctypes.addressof(r), P, P, P,
                                      4, 4, 16, 8, 2, 64, 0, None, None) == INVALID
+
+
+def _scored(lib, **kw):
+    a = dict(out=P, odt=2, q=P, k=P, v=P, tab=P, mb=8, lens=P, L=100, S=2, H=8, Hkv=2, D=64, nb=16,
+             bs=16, dt=0, sc=P, stride=100, ws=P, wb=1 << 30)
+    a.update(kw)
+    return lib.pa_decode_attention_scored(a["out"], a["odt"], a["q"], a["k"], a["v"], a["tab"], a["mb"],
+                                          a["lens"], a["L"], a["S"], a["H"], a["Hkv"], a["D"], a["nb"],
+                                          a["bs"], 0.1, a["dt"], a["sc"], a["stride"], a["ws"], a["wb"],
+                                          None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"S": 0}, OK), ({"S": 0, "sc": None}, OK), ({"S": -1}, INVALID), ({"stride": 99}, INVALID),
+    ({"sc": None}, INVALID), ({"sc": P + 2}, INVALID), ({"H": 9}, INVALID), ({"H": 18}, UNSUPPORTED),
+    ({"D": 80}, UNSUPPORTED), ({"bs": 24}, UNSUPPORTED), ({"dt": 2}, INVALID), ({"odt": 1}, INVALID),
+    ({"L": 129, "stride": 129}, INVALID), ({"ws": None}, INVALID), ({"ws": P + 16}, WORKSPACE),
+    ({"wb": 100}, WORKSPACE), ({"q": P + 8}, INVALID), ({"out": None}, INVALID), ({"tab": None}, INVALID),
+    ({"lens": None}, INVALID), ({"nb": 0}, INVALID), ({"mb": 0}, INVALID)])
+def test_decode_scored_refusals(lib, kw, want):
+    assert _scored(lib, **kw) == want
+
+
+def test_decode_scored_workspace_size(lib):
+    a = pa.decode_scored_workspace_size(64, 12, 2, 128, 4096)
+    assert a >= 64 * 12 * 4096 * 4
+    assert pa.decode_scored_workspace_size(64, 12, 2, 128, 8192) > a
+    assert pa.decode_scored_workspace_size(-1, 12, 2, 128, 10) == 0
+    assert _scored(lib, wb=pa.decode_scored_workspace_size(2, 8, 2, 64, 100) - 1) == WORKSPACE
