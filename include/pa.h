@@ -441,6 +441,75 @@ pa_status_t pa_prefill_attention(void *out, pa_dtype_t out_dtype, const void *qu
                                  unsigned int *dev_error_word, pa_stream_t stream);
 
 /*
+ * pa_prefill_attention_lse -- pa_prefill_attention that also gives each row's
+ * log-sum-exp, lse[t][h] = ln sum_{j <= p} exp(x_j) (natural logarithm, fp32),
+ * for pa_prefill_scores or a later merge with other keys.
+ *
+ * lse           device fp32 [num_tokens][num_heads], 4-byte aligned, or NULL
+ *               (then this is pa_prefill_attention).  A row without a readable
+ *               key, or of a sequence whose lengths break the rules, gets -inf.
+ */
+pa_status_t pa_prefill_attention_lse(void *out, pa_dtype_t out_dtype, const void *query,
+                                     const void *k_cache, const void *v_cache,
+                                     const int32_t *block_tables, int max_blocks_per_seq,
+                                     const int32_t *query_start_loc, const int32_t *context_lens,
+                                     int max_query_len, int max_context_len, int num_seqs,
+                                     int num_tokens, int num_heads, int num_kv_heads,
+                                     int head_dim, int num_blocks, int block_size, float scale,
+                                     pa_dtype_t dtype, float *lse, void *workspace,
+                                     size_t workspace_bytes, unsigned int *dev_error_word,
+                                     pa_stream_t stream);
+
+/*
+ * pa_prefill_scores_workspace_size -- bytes of device workspace
+ * pa_prefill_scores needs for these sizes; 0 for invalid ones.  Host only.
+ */
+size_t pa_prefill_scores_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
+                                        int head_dim, int max_query_len, int max_context_len);
+
+/*
+ * pa_prefill_scores -- add the attention weight that new tokens give to every
+ * cached token to its score: the prompt's counterpart of
+ * pa_decode_attention_scored.
+ *
+ * Defines: sequence s has n_s = query_start_loc[s+1] - query_start_loc[s]
+ * query rows, those of its last n_s positions (a whole prompt, one chunk of
+ * it, or only a window of its last tokens).  With c = context_lens[s] - n_s,
+ * row i at position c + i, and lse the row's log-sum-exp,
+ *     scores[s][hk][j] += sum_{g < G} sum_{i >= j - c} exp(scale <q_ig, k_j> - lse_ig)
+ * for j < context_lens[s], token j of the sequence read at block
+ * block_tables[s][j / block_size].  fp32 sums in a fixed order.  A row whose
+ * lse is -inf adds nothing.
+ *
+ * query         device [num_tokens][num_heads][head_dim], dtype
+ * lse           device fp32 [num_tokens][num_heads], the rows' log-sum-exp
+ *               (pa_prefill_attention_lse; for a window, its rows of it)
+ * k_cache       device pool [num_blocks][num_kv_heads][block_size][head_dim]
+ * scores        device fp32 [num_seqs][num_kv_heads][score_stride], updated in
+ *               place; positions from context_lens[s] on, and tokens in a
+ *               skipped block, are left as they were
+ * score_stride  >= max_context_len
+ * head_dim 64 or 128 (PA_ERR_UNSUPPORTED otherwise); num_seqs and
+ * num_kv_heads at most 65535.  Lengths, tables and limits are those of
+ * pa_prefill_attention.
+ * workspace     device, >= pa_prefill_scores_workspace_size(...) bytes,
+ *               256-byte aligned; calls in flight at once must not share one
+ * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence
+ *               whose lengths break the rules (its scores are left as they
+ *               were), PA_ERRBIT_BLOCK_OOB (the block's keys are skipped),
+ *               PA_ERRBIT_TIMEOUT
+ */
+pa_status_t pa_prefill_scores(const void *query, const float *lse, const void *k_cache,
+                              const int32_t *block_tables, int max_blocks_per_seq,
+                              const int32_t *query_start_loc, const int32_t *context_lens,
+                              int max_query_len, int max_context_len, int num_seqs,
+                              int num_tokens, int num_heads, int num_kv_heads, int head_dim,
+                              int num_blocks, int block_size, float scale, pa_dtype_t dtype,
+                              float *scores, int64_t score_stride, void *workspace,
+                              size_t workspace_bytes, unsigned int *dev_error_word,
+                              pa_stream_t stream);
+
+/*
  * pa_decode_attention_contiguous -- the same decode attention over a
  * contiguous (unpaged) KV cache: sequence s's tokens for KV head hk are rows
  * 0 .. context_lens[s]-1 of k_cache[s][hk] and v_cache[s][hk]; no block
@@ -589,6 +658,77 @@ pa_status_t pa_swap_blocks(void *const *dst_k_caches, void *const *dst_v_caches,
                            int num_dst_blocks, int num_src_blocks, int block_size,
                            int num_kv_heads, int head_dim, pa_dtype_t dtype,
                            unsigned int *dev_error_word, pa_stream_t stream);
+
+/*
+ * pa_evict_workspace_size -- bytes of device workspace pa_evict_tokens needs
+ * for these sizes; 0 for invalid ones.  Host only.
+ */
+size_t pa_evict_workspace_size(int num_layers, int num_seqs, int num_kv_heads,
+                               int max_context_len, int max_keep_len);
+
+/*
+ * pa_evict_tokens -- shrink sequences to a budget: keep the first tokens, the
+ * last ones and those with the highest scores, in their order, and compact K,
+ * V and the scores onto them; all sequences and layers in one call.
+ *
+ * Defines: for sequence s with L = context_lens[s] tokens,
+ *     n = min(L, keep_lens[s]),  recent = min(num_recent, n),
+ *     sink = min(num_sink, n - recent),
+ * and for every layer and KV head on its own: tokens 0 .. sink-1, tokens
+ * L-recent .. L-1, and the n - recent - sink tokens between them with the
+ * highest scores (equal scores: the lowest index; a NaN ranks below
+ * everything) are kept.  With i_0 < i_1 < .. < i_{n-1} the kept tokens,
+ *     K'[j] = K[i_j], V'[j] = V[i_j], scores'[j] = scores[i_j]   (j < n)
+ *     scores'[j] = 0                                             (n <= j < L)
+ *     new_lens[s] = n.
+ * Values are copied unchanged.  Positions from n on of the last block, and
+ * scores from L on, are left as they were.  L <= keep_lens[s] keeps everything.
+ * Attention does not depend on the order of the cached tokens, and rotated
+ * keys keep their positions (pa_rotary_cache_write).
+ *
+ * k_caches, v_caches, scores, scores_out, kept  HOST arrays of num_layers
+ *               device pointers (distinct layers: distinct memory)
+ * scores        fp32 [num_seqs][num_kv_heads][score_stride]
+ * scores_out    the same with score_out_stride, not overlapping scores; NULL:
+ *               scores are updated in place
+ * kept          int32 [num_seqs][num_kv_heads][kept_stride], gets i_j for
+ *               j < n and is otherwise left as it was; NULL: not wanted
+ * score_stride, score_out_stride >= max_context_len, kept_stride >= max_keep_len
+ * block_tables  device int32 [num_seqs][max_blocks_per_seq]: the tokens
+ * dst_block_tables  device int32 [num_seqs][dst_max_blocks_per_seq]: where K'
+ *               and V' go, blocks that no source table of the call names; NULL:
+ *               in place, into the first ceil(n / block_size) blocks of
+ *               block_tables, which no other sequence may then share (make
+ *               them private first, pa_bm_seq_make_private); blocks behind
+ *               those are only read
+ * context_lens, keep_lens  device int32 [num_seqs]
+ * new_lens      device int32 [num_seqs]; other memory than both
+ * max_context_len  host-known bound on context_lens, <= block_size *
+ *               max_blocks_per_seq
+ * max_keep_len  host-known bound on n, <= max_context_len
+ * num_layers    1 .. PA_MAX_LAYERS; num_seqs, num_kv_heads at most 65535
+ * head_dim 64, 128 or 256; block_size a power of two in [PA_MIN_BLOCK_SIZE,
+ * PA_MAX_BLOCK_SIZE]; dtype PA_F16 or PA_BF16
+ * workspace     device, >= pa_evict_workspace_size(...) bytes, 256-byte
+ *               aligned; calls in flight at once must not share one
+ * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence
+ *               with L outside [0, max_context_len], a negative keep_lens or
+ *               n > max_keep_len (it is left as it was, new_lens[s] = L);
+ *               PA_ERRBIT_BLOCK_OOB (a row from or to a block outside the pool
+ *               is not moved); PA_ERRBIT_TIMEOUT
+ */
+pa_status_t pa_evict_tokens(void *const *k_caches, void *const *v_caches, int num_layers,
+                            const float *const *scores, int64_t score_stride,
+                            float *const *scores_out, int64_t score_out_stride,
+                            int32_t *const *kept, int64_t kept_stride,
+                            const int32_t *block_tables, int max_blocks_per_seq,
+                            const int32_t *dst_block_tables, int dst_max_blocks_per_seq,
+                            const int32_t *context_lens, const int32_t *keep_lens,
+                            int32_t *new_lens, int max_context_len, int max_keep_len,
+                            int num_sink, int num_recent, int num_seqs, int num_blocks,
+                            int block_size, int num_kv_heads, int head_dim, pa_dtype_t dtype,
+                            void *workspace, size_t workspace_bytes,
+                            unsigned int *dev_error_word, pa_stream_t stream);
 
 /* Static, human-readable name of a status. */
 const char *pa_status_string(pa_status_t status);

@@ -90,6 +90,17 @@ pa_status_t pa_bm_build_batch(const pa_block_manager_t *bm, const int64_t *seqs,
                               int32_t *block_tables, int max_blocks_per_seq,
                               int32_t *context_lens);
 
+/* Make the blocks that hold the first num_tokens tokens of a GPU-resident
+ * sequence its own, before pa_evict_tokens compacts into them: every one that
+ * is shared is replaced by a fresh block, and the (old, new) pair is queued
+ * for pa_bm_take_copies.  PA_ERR_NO_BLOCKS if the pool is short. */
+pa_status_t pa_bm_seq_make_private(pa_block_manager_t *bm, int64_t seq, int num_tokens);
+/* Set a GPU-resident sequence's length to num_tokens (at most its length) and
+ * release the blocks behind, after pa_evict_tokens.  A released block may be
+ * handed out again at once: enqueue the eviction before the work that writes
+ * to it. */
+pa_status_t pa_bm_seq_shrink(pa_block_manager_t *bm, int64_t seq, int num_tokens);
+
 /* Copy-on-write pairs queued so far, oldest first: moves up to cap pairs to
  * pairs_out ([cap][2] int64, (src, dst)) and returns how many it moved;
  * pa_bm_num_copies tells how many are queued. */

@@ -21,6 +21,10 @@ A cache that stays within a budget:
                        slot_mapping, ...)
     decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
                             max_context_len, scale, scores, ...)
+    prefill_scores(query, lse, k_cache, block_tables, query_start_loc, context_lens,
+                   max_query_len, max_context_len, scale, scores, ...)
+    evict_tokens(k_caches, v_caches, scores, block_tables, context_lens, keep_lens,
+                 max_context_len, max_keep_len, num_sink, num_recent, ...)
 
 Pools are [num_blocks][num_kv_heads][block_size][head_dim]; the block size
 is read from their third dimension: 16 goes to the plain entry points, other
@@ -43,7 +47,8 @@ __all__ = ["cache_write", "decode_attention", "decode_attention_contiguous",
            "ERRBIT_INTERNAL",
            "MAX_LAYERS", "BLOCK_SIZES", "swap_blocks", "prefill_attention",
            "Rotary", "rotary_cache_write", "decode_attention_scored",
-           "decode_scored_workspace_size", "MAX_ROTARY_PAIRS"]
+           "decode_scored_workspace_size", "prefill_scores", "prefill_scores_workspace_size",
+           "evict_tokens", "evict_workspace_size", "MAX_ROTARY_PAIRS"]
 
 BLOCK_SIZE = 16
 BLOCK_SIZES = (8, 16, 32, 64, 128, 256)
@@ -84,8 +89,18 @@ _SIGNATURES = {
     "pa_copy_blocks_ex": (_I, [_P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
     "pa_prefill_attention": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I,
                                   _I, _I, _I, ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P]),
+    "pa_prefill_attention_lse": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I,
+                                      _I, _I, _I, _I, ctypes.c_float, _I, _P, _P,
+                                      ctypes.c_size_t, _P, _P]),
+    "pa_prefill_scores": (_I, [_P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I,
+                               ctypes.c_float, _I, _P, _I64, _P, ctypes.c_size_t, _P, _P]),
+    "pa_prefill_scores_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
     "pa_prefill_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "pa_swap_blocks": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "pa_evict_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "pa_evict_tokens": (_I, [_P, _P, _I, _P, _I64, _P, _I64, _P, _I64, _P, _I, _P, _I, _P, _P,
+                             _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _I, _P, ctypes.c_size_t,
+                             _P, _P]),
     "pa_status_string": (ctypes.c_char_p, [_I]),
 }
 
@@ -487,13 +502,14 @@ def prefill_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, hea
 
 def prefill_attention(query, k_cache, v_cache, block_tables, query_start_loc, context_lens,
                       max_query_len: int, max_context_len: int, scale: float, out=None,
-                      out_dtype=None, workspace=None, error_word=None, stream=None):
+                      out_dtype=None, workspace=None, error_word=None, stream=None, lse=None):
     """Chunked-prefill attention: query [T][H][D] holds every sequence's new
     tokens (sequence s: rows query_start_loc[s] .. query_start_loc[s+1]-1),
     already written to the cache as its last positions; context_lens[s]
     counts the tokens after the chunk.  ``workspace`` (uint8, >=
-    prefill_workspace_size bytes) is allocated here when not given.  Returns
-    out [T][H][D]."""
+    prefill_workspace_size bytes) is allocated here when not given.  ``lse``
+    (fp32 [T][H], optional) gets each row's log-sum-exp.  Returns out
+    [T][H][D]."""
     import torch
     T, H, D = query.shape
     nb, hkv, bs, d2 = k_cache.shape
@@ -512,13 +528,155 @@ def prefill_attention(query, k_cache, v_cache, block_tables, query_start_loc, co
     if workspace is None:
         nbytes = prefill_workspace_size(S, H, hkv, D, int(max_query_len))
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=query.device)
-    st = load_library().pa_prefill_attention(
-        _dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"), _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"), block_tables.shape[1],
+    head = (_dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"),
+            _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+            _dev(block_tables, "block_tables"), block_tables.shape[1],
+            _dev(query_start_loc, "query_start_loc"), _dev(context_lens, "context_lens"),
+            int(max_query_len), int(max_context_len), S, T, H, hkv, D, nb, bs, float(scale),
+            _dtype_code(query.dtype))
+    tail = (_dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
+            _opt_ptr(error_word, "error_word"), _stream_ptr(stream, query.device))
+    lib = load_library()
+    if lse is None:
+        _check(lib.pa_prefill_attention(*head, *tail), "pa_prefill_attention")
+    else:
+        _check(lib.pa_prefill_attention_lse(*head, _lse_ptr(lse, T, H), *tail),
+               "pa_prefill_attention_lse")
+    return out
+
+
+def _lse_ptr(lse, T, H):
+    import torch
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (T, H):
+        raise ValueError("lse must be float32 [T][H]")
+    return _dev(lse, "lse")
+
+
+def prefill_scores_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int,
+                                  head_dim: int, max_query_len: int,
+                                  max_context_len: int) -> int:
+    return int(load_library().pa_prefill_scores_workspace_size(
+        num_seqs, num_heads, num_kv_heads, head_dim, max_query_len, max_context_len))
+
+
+def prefill_scores(query, lse, k_cache, block_tables, query_start_loc, context_lens,
+                   max_query_len: int, max_context_len: int, scale: float, scores,
+                   workspace=None, error_word=None, stream=None):
+    """Add the attention weight that each sequence's query rows (rows
+    query_start_loc[s] .. query_start_loc[s+1]-1 of query [T][H][D], its last
+    positions: a prompt, a chunk or a window) give to its cached tokens to
+    ``scores`` (fp32 [S][Hkv][>= max_context_len]).  ``lse`` [T][H] is the rows'
+    log-sum-exp (prefill_attention's).  ``workspace`` (uint8, >=
+    prefill_scores_workspace_size bytes) is allocated here when not given.
+    Returns ``scores``."""
+    import torch
+    T, H, D = query.shape
+    nb, hkv, bs, d2 = k_cache.shape
+    if d2 != D or k_cache.dtype != query.dtype:
+        raise ValueError("the pool must match the query")
+    for t, n in ((block_tables, "block_tables"), (query_start_loc, "query_start_loc"),
+                 (context_lens, "context_lens")):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{n} must be int32")
+    S = context_lens.shape[0]
+    if query_start_loc.shape != (S + 1,) or block_tables.dim() != 2 or \
+            block_tables.shape[0] != S:
+        raise ValueError("query_start_loc must be [S+1], block_tables [S][max_blocks]")
+    sc, stride = _score_rows(scores, (S, hkv))
+    if workspace is None:
+        nbytes = prefill_scores_workspace_size(S, H, hkv, D, int(max_query_len),
+                                               int(max_context_len))
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=query.device)
+    st = load_library().pa_prefill_scores(
+        _dev(query, "query"), _lse_ptr(lse, T, H), _dev(k_cache, "k_cache"),
+        _dev(block_tables, "block_tables"), block_tables.shape[1],
         _dev(query_start_loc, "query_start_loc"), _dev(context_lens, "context_lens"),
         int(max_query_len), int(max_context_len), S, T, H, hkv, D, nb, bs, float(scale),
-        _dtype_code(query.dtype), _dev(workspace, "workspace"),
+        _dtype_code(query.dtype), sc, stride, _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
         _stream_ptr(stream, query.device))
-    _check(st, "pa_prefill_attention")
-    return out
+    _check(st, "pa_prefill_scores")
+    return scores
+
+
+def evict_workspace_size(num_layers: int, num_seqs: int, num_kv_heads: int, max_context_len: int,
+                         max_keep_len: int) -> int:
+    return int(load_library().pa_evict_workspace_size(num_layers, num_seqs, num_kv_heads,
+                                                      max_context_len, max_keep_len))
+
+
+def _layer_ptrs(xs, name):
+    return ctypes.cast((ctypes.c_void_p * len(xs))(*[_dev(x, name) for x in xs]), ctypes.c_void_p)
+
+
+def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block_tables,
+                 context_lens, keep_lens, max_context_len: int, max_keep_len: int,
+                 num_sink: int = 0, num_recent: int = 0, dst_block_tables=None,
+                 scores_out: Optional[Sequence] = None, kept: Optional[Sequence] = None,
+                 new_lens=None, workspace=None, error_word=None, stream=None):
+    """Shrink every sequence s to min(context_lens[s], keep_lens[s]) tokens in
+    every layer: each KV head keeps the first num_sink, the last num_recent
+    and the highest-scored tokens between them, in their order (equal scores:
+    the lowest index), and K, V and the scores are compacted onto them.
+
+    k_caches, v_caches, scores: one per layer; scores fp32 [S][Hkv][>=
+    max_context_len], vacated positions become zero.  In place unless
+    dst_block_tables (int32 [S][blocks], blocks no source table names) says
+    where K and V go and scores_out (one per layer) where the scores go.
+    kept (int32 [S][Hkv][>= max_keep_len] per layer) gets the kept tokens'
+    positions.  max_keep_len bounds the lengths left.  ``workspace`` (uint8,
+    >= evict_workspace_size bytes) is allocated here when not given.  Returns
+    new_lens, int32 [S]."""
+    import torch
+    L = len(k_caches)
+    if not L or len(v_caches) != L or len(scores) != L:
+        raise ValueError("need the same, non-zero number of K pools, V pools and scores")
+    nb, hkv, bs, d = k_caches[0].shape
+    dt = k_caches[0].dtype
+    for c in (*k_caches, *v_caches):
+        if c.shape != k_caches[0].shape or c.dtype != dt:
+            raise ValueError("all pools must have one shape and dtype")
+    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
+                 (keep_lens, "keep_lens")):
+        if t.dtype != torch.int32:
+            raise TypeError(f"{n} must be int32")
+    S = context_lens.shape[0]
+    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
+            keep_lens.shape != (S,):
+        raise ValueError("block_tables must be [S][max_blocks], context_lens and keep_lens [S]")
+    if dst_block_tables is not None and (
+            dst_block_tables.dtype != torch.int32 or dst_block_tables.dim() != 2 or
+            dst_block_tables.shape[0] != S):
+        raise ValueError("dst_block_tables must be int32 [S][blocks]")
+
+    def rows(xs, name, dtype):  # one shape and type for all layers
+        if len(xs) != L:
+            raise ValueError(f"need one {name} per layer")
+        for x in xs:
+            if x.dtype != dtype or x.shape != xs[0].shape or x.dim() != 3 or \
+                    x.shape[0] != S or x.shape[1] != hkv:
+                raise ValueError(f"{name} must be {dtype} [S][Hkv][positions] in every layer")
+        return _layer_ptrs(xs, name), xs[0].shape[2]
+
+    sc = rows(scores, "scores", torch.float32)
+    out = (None, 0) if scores_out is None else rows(scores_out, "scores_out", torch.float32)
+    kp = (None, 0) if kept is None else rows(kept, "kept", torch.int32)
+    if new_lens is None:
+        new_lens = torch.empty(S, dtype=torch.int32, device=context_lens.device)
+    elif new_lens.dtype != torch.int32 or new_lens.shape != (S,):
+        raise ValueError("new_lens must be int32 [S]")
+    if workspace is None:
+        nbytes = evict_workspace_size(L, S, hkv, int(max_context_len), int(max_keep_len))
+        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=context_lens.device)
+    st = load_library().pa_evict_tokens(
+        _layer_ptrs(k_caches, "k_caches"), _layer_ptrs(v_caches, "v_caches"), L, *sc, *out, *kp,
+        _dev(block_tables, "block_tables"), block_tables.shape[1],
+        _opt_ptr(dst_block_tables, "dst_block_tables"),
+        0 if dst_block_tables is None else dst_block_tables.shape[1],
+        _dev(context_lens, "context_lens"), _dev(keep_lens, "keep_lens"),
+        _dev(new_lens, "new_lens"), int(max_context_len), int(max_keep_len), int(num_sink),
+        int(num_recent), S, nb, bs, hkv, d, _dtype_code(dt), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
+        _stream_ptr(stream, k_caches[0].device))
+    _check(st, "pa_evict_tokens")
+    return new_lens

@@ -257,6 +257,40 @@ pa_status_t pa_bm_seq_append(pa_block_manager_t *bm, int64_t seq, int num_tokens
     return PA_OK;
 }
 
+pa_status_t pa_bm_seq_make_private(pa_block_manager_t *bm, int64_t seq, int num_tokens) {
+    if (!bm || num_tokens < 0) return PA_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> g(bm->mu);
+    Seq *s = bm->find(seq);
+    if (!s || s->on_cpu || num_tokens > s->n) return PA_ERR_INVALID_ARG;
+    const size_t nb = ((size_t)num_tokens + bm->block_size - 1) / bm->block_size;
+    int shared = 0;
+    for (size_t i = 0; i < nb; ++i) shared += bm->gpu.refs(s->table[i]) > 1;
+    if (shared > bm->gpu.num_free()) return PA_ERR_NO_BLOCKS;
+    for (size_t i = 0; i < nb; ++i) {
+        const int old = s->table[i];
+        if (bm->gpu.refs(old) <= 1) continue;
+        const int fresh = bm->gpu.alloc();
+        bm->copies.emplace_back(old, fresh);
+        bm->gpu.release(old);
+        s->table[i] = fresh;
+    }
+    return PA_OK;
+}
+
+pa_status_t pa_bm_seq_shrink(pa_block_manager_t *bm, int64_t seq, int num_tokens) {
+    if (!bm || num_tokens < 0) return PA_ERR_INVALID_ARG;
+    std::lock_guard<std::mutex> g(bm->mu);
+    Seq *s = bm->find(seq);
+    if (!s || s->on_cpu || num_tokens > s->n) return PA_ERR_INVALID_ARG;
+    const size_t nb = ((size_t)num_tokens + bm->block_size - 1) / bm->block_size;
+    while (s->table.size() > nb) {
+        bm->gpu.release(s->table.back());
+        s->table.pop_back();
+    }
+    s->n = num_tokens;
+    return PA_OK;
+}
+
 int pa_bm_blocks_needed(const pa_block_manager_t *bm, int64_t seq, int num_tokens) {
     if (!bm || num_tokens < 0) return -1;
     std::lock_guard<std::mutex> g(bm->mu);

@@ -12,6 +12,8 @@ C++ code of ``libpa_gb300.so``.  The manager produces the kernels' inputs::
     pairs = bm.take_copies()                  # -> pa_copy_blocks
     tables, lens = bm.build_batch([s, child], max_blocks)   # -> pa_decode_attention
     out_pairs = bm.swap_out([s, child])       # -> pa_swap_blocks (GPU -> CPU)
+    bm.make_private(s, n)                     # (copies) -> pa_evict_tokens, in place
+    bm.shrink(s, n)                           # n tokens left
 """
 from __future__ import annotations
 
@@ -37,6 +39,8 @@ _SIGNATURES = {
     "pa_bm_seq_fork": (_I, [_P, _I64, ctypes.POINTER(_I64)]),
     "pa_bm_seq_free": (_I, [_P, _I64]),
     "pa_bm_seq_append": (_I, [_P, _I64, _I, _P]),
+    "pa_bm_seq_make_private": (_I, [_P, _I64, _I]),
+    "pa_bm_seq_shrink": (_I, [_P, _I64, _I]),
     "pa_bm_blocks_needed": (_I, [_P, _I64, _I]),
     "pa_bm_seq_len": (_I, [_P, _I64]),
     "pa_bm_seq_on_cpu": (_I, [_P, _I64]),
@@ -137,6 +141,17 @@ class BlockManager:
                                           slots.ctypes.data if num_tokens else None),
                "pa_bm_seq_append")
         return slots
+
+    def make_private(self, seq: int, num_tokens: int) -> None:
+        """Before an eviction in place: the blocks of the first num_tokens
+        tokens become the sequence's own (copies queued); raises NoFreeBlocks."""
+        _check(self._lib.pa_bm_seq_make_private(self._h, seq, num_tokens),
+               "pa_bm_seq_make_private")
+
+    def shrink(self, seq: int, num_tokens: int) -> None:
+        """After an eviction: the sequence holds num_tokens tokens; the blocks
+        behind them are released."""
+        _check(self._lib.pa_bm_seq_shrink(self._h, seq, num_tokens), "pa_bm_seq_shrink")
 
     def blocks_needed(self, seq: int, num_tokens: int) -> int:
         return self._lib.pa_bm_blocks_needed(self._h, seq, num_tokens)

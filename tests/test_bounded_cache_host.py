@@ -117,3 +117,118 @@ def test_decode_scored_workspace_size(lib):
     assert pa.decode_scored_workspace_size(64, 12, 2, 128, 8192) > a
     assert pa.decode_scored_workspace_size(-1, 12, 2, 128, 10) == 0
     assert _scored(lib, wb=pa.decode_scored_workspace_size(2, 8, 2, 64, 100) - 1) == WORKSPACE
+
+
+def _pscores(lib, **kw):
+    a = dict(q=P, lse=P, k=P, tab=P, mb=8, qsl=P, lens=P, mq=50, L=100, S=2, T=60, H=8, Hkv=2, D=64, nb=16,
+             bs=16, dt=0, sc=P, stride=100, ws=P, wb=1 << 30)
+    a.update(kw)
+    return lib.pa_prefill_scores(a["q"], a["lse"], a["k"], a["tab"], a["mb"], a["qsl"], a["lens"], a["mq"],
+                                 a["L"], a["S"], a["T"], a["H"], a["Hkv"], a["D"], a["nb"], a["bs"], 0.1,
+                                 a["dt"], a["sc"], a["stride"], a["ws"], a["wb"], None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"S": 0}, OK), ({"T": 0}, OK), ({"mq": 0}, OK), ({"S": -1}, INVALID), ({"T": -1}, INVALID),
+    ({"mq": -1}, INVALID), ({"L": -1}, INVALID), ({"nb": 0}, INVALID), ({"mb": 0}, INVALID),
+    ({"H": 9}, INVALID), ({"D": 256}, UNSUPPORTED), ({"D": 32}, UNSUPPORTED), ({"bs": 4}, UNSUPPORTED),
+    ({"dt": 2}, INVALID), ({"L": 129, "stride": 129}, INVALID), ({"stride": 99}, INVALID), ({"q": None}, INVALID),
+    ({"lse": None}, INVALID), ({"k": None}, INVALID), ({"tab": None}, INVALID), ({"qsl": None}, INVALID),
+    ({"lens": None}, INVALID), ({"sc": None}, INVALID), ({"ws": None}, INVALID), ({"q": P + 8}, INVALID),
+    ({"lse": P + 1}, INVALID), ({"sc": P + 2}, INVALID), ({"k": P + 4}, INVALID), ({"ws": P + 64}, WORKSPACE),
+    ({"wb": 0}, WORKSPACE), ({"S": 70000}, UNSUPPORTED)])
+def test_prefill_scores_refusals(lib, kw, want):
+    assert _pscores(lib, **kw) == want
+
+
+def test_prefill_lse_refuses_a_misaligned_pointer(lib):
+    st = lib.pa_prefill_attention_lse(P, 2, P, P, P, P, 8, P, P, 50, 100, 2, 60, 8, 2, 64, 16, 16, 0.1, 0,
+                                      P + 2, P, 1 << 30, None, None)
+    assert st == INVALID
+    assert pa.prefill_scores_workspace_size(2, 8, 2, 96, 50, 100) == 0
+    assert pa.prefill_scores_workspace_size(2, 8, 3, 64, 50, 100) == 0
+
+
+def _ptrs(*ps):
+    return ctypes.cast((ctypes.c_void_p * len(ps))(*ps), ctypes.c_void_p)
+
+
+def _evict(lib, **kw):
+    a = dict(k=_ptrs(P, P), v=_ptrs(P, P), layers=2, sc=_ptrs(P, P), ss=100, so=None, sos=0, kept=None, ks=0, tab=P,
+             mb=8, dst=None, dmb=0, lens=P, keep=P, new=2 * P, L=100, K=50, sink=4, recent=4, S=2, nb=16, bs=16,
+             Hkv=2, D=64, dt=0, ws=P, wb=1 << 30)
+    a.update(kw)
+    return lib.pa_evict_tokens(a["k"], a["v"], a["layers"], a["sc"], a["ss"], a["so"], a["sos"], a["kept"], a["ks"],
+                               a["tab"], a["mb"], a["dst"], a["dmb"], a["lens"], a["keep"], a["new"], a["L"], a["K"],
+                               a["sink"], a["recent"], a["S"], a["nb"], a["bs"], a["Hkv"], a["D"], a["dt"], a["ws"],
+                               a["wb"], None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    ({"S": 0}, OK), ({"S": -1}, INVALID), ({"layers": 0}, INVALID), ({"layers": 129}, UNSUPPORTED),
+    ({"L": -1}, INVALID), ({"K": -1}, INVALID), ({"K": 101}, INVALID), ({"sink": -1}, INVALID),
+    ({"recent": -1}, INVALID), ({"nb": 0}, INVALID), ({"mb": 0}, INVALID), ({"Hkv": 0}, INVALID),
+    ({"bs": 48}, UNSUPPORTED), ({"D": 32}, UNSUPPORTED), ({"dt": 2}, INVALID), ({"L": 129, "ss": 129}, INVALID),
+    ({"ss": 99}, INVALID), ({"so": _ptrs(P, P), "sos": 99}, INVALID), ({"kept": _ptrs(P, P), "ks": 49}, INVALID),
+    ({"dst": P, "dmb": 3}, INVALID), ({"dst": P, "dmb": 0}, INVALID), ({"k": None}, INVALID), ({"v": None}, INVALID),
+    ({"sc": None}, INVALID), ({"tab": None}, INVALID), ({"lens": None}, INVALID), ({"keep": None}, INVALID),
+    ({"new": None}, INVALID), ({"new": P}, INVALID), ({"k": _ptrs(P, None)}, INVALID), ({"v": _ptrs(P, P + 8)}, INVALID),
+    ({"sc": _ptrs(P, P + 2)}, INVALID), ({"so": _ptrs(P, None), "sos": 100}, INVALID),
+    ({"kept": _ptrs(P, P + 1), "ks": 50}, INVALID), ({"ws": P + 128}, WORKSPACE), ({"ws": None}, INVALID),
+    ({"wb": 100}, WORKSPACE), ({"S": 65536}, UNSUPPORTED), ({"Hkv": 65536}, UNSUPPORTED)])
+def test_evict_refusals(lib, kw, want):
+    assert _evict(lib, **kw) == want
+
+
+def test_evict_workspace_size(lib):
+    a = pa.evict_workspace_size(4, 8, 2, 1000, 500)
+    assert a >= 4 * 8 * 2 * 500 * 4
+    assert pa.evict_workspace_size(0, 8, 2, 1000, 500) == 0
+    assert pa.evict_workspace_size(129, 8, 2, 1000, 500) == 0
+    assert pa.evict_workspace_size(4, 8, 2, 1000, -1) == 0
+
+
+def test_manager_make_private_and_shrink():
+    from paged_kv_cache_pa_gb300.manager import BlockManager, NoFreeBlocks
+    bm = BlockManager(10, 0, 16)
+    a = bm.new_sequence()
+    bm.append(a, 70)                       # 5 blocks, the last with 6 tokens
+    b = bm.fork(a)
+    bm.make_private(b, 33)                 # its first three blocks
+    assert bm.table(a) == [0, 1, 2, 3, 4] and bm.table(b) == [5, 6, 7, 3, 4]
+    assert bm.take_copies().tolist() == [[0, 5], [1, 6], [2, 7]]
+    bm.make_private(a, 33)                 # already its own
+    assert bm.take_copies().tolist() == [] and bm.table(a) == [0, 1, 2, 3, 4]
+    bm.shrink(b, 33)
+    assert bm.table(b) == [5, 6, 7] and bm.seq_len(b) == 33 and bm.num_free_gpu == 2
+    assert bm.refcount(3) == 1 and bm.refcount(4) == 1
+    assert bm.append(b, 2).tolist() == [7 * 16 + 1, 7 * 16 + 2]   # goes on behind the kept tokens
+    bm.shrink(a, 70)
+    assert bm.seq_len(a) == 70
+    bm.shrink(a, 0)
+    assert bm.table(a) == [] and bm.num_free_gpu == 7
+    c = bm.fork(b)
+    assert bm.append(a, 7 * 16).size == 112 and bm.num_free_gpu == 0
+    with pytest.raises(NoFreeBlocks):
+        bm.make_private(c, 1)
+    assert bm.table(c) == bm.table(b) and bm.take_copies().tolist() == []
+    for bad in (-1, 36):
+        with pytest.raises(pa.PaError):
+            bm.shrink(b, bad)
+        with pytest.raises(pa.PaError):
+            bm.make_private(b, bad)
+    with pytest.raises(pa.PaError):
+        bm.shrink(99, 0)
+    bm.close()
+
+
+def test_manager_swapped_out_sequences_are_refused():
+    from paged_kv_cache_pa_gb300.manager import BlockManager
+    bm = BlockManager(4, 4, 16)
+    a = bm.new_sequence()
+    bm.append(a, 20)
+    bm.swap_out([a])
+    for f in (bm.shrink, bm.make_private):
+        with pytest.raises(pa.PaError):
+            f(a, 1)
+    bm.close()
