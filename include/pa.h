@@ -708,7 +708,9 @@ size_t pa_evict_workspace_size(int num_layers, int num_seqs, int num_kv_heads,
  * max_keep_len  host-known bound on n, <= max_context_len
  * num_layers    1 .. PA_MAX_LAYERS; num_seqs, num_kv_heads at most 65535
  * head_dim 64, 128 or 256; block_size a power of two in [PA_MIN_BLOCK_SIZE,
- * PA_MAX_BLOCK_SIZE]; dtype PA_F16 or PA_BF16
+ * PA_MAX_BLOCK_SIZE]; dtype PA_F16 or PA_BF16; max_context_len at most 393216,
+ * and layers x sequences x KV heads x (max_keep_len / 32) below 2^31
+ * (PA_ERR_UNSUPPORTED otherwise)
  * workspace     device, >= pa_evict_workspace_size(...) bytes, 256-byte
  *               aligned; calls in flight at once must not share one
  * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence

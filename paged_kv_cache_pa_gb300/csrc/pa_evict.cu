@@ -3,20 +3,22 @@
 // and compact K, V and the scores onto them.
 //
 // A unit is one (layer, sequence, KV head).  Two kernels for all units:
-//   * select: one CTA a unit.  The scores are mapped to whole numbers of the
-//     same order, the m-th largest of the middle is found digit by digit (a
-//     radix selection: a histogram of 8 bits a pass, narrowed to the digit
-//     that holds the m-th largest), and one more pass in index order numbers
-//     the kept tokens -- those above the threshold and the first of those at
-//     it -- with a scan, so equal scores go to the lowest index whatever the
-//     timing.  The scores move to their new places in the same pass: a kept
-//     token's place is never past its index, and a tile is read whole before
-//     any of it is written.
-//   * move: the K and V rows of the kept tokens, 16 bytes a thread, in
-//     ascending tiles; again a tile is read before it is written, which makes
-//     the move safe within the sequence's own blocks.
+//   * select: one CTA a unit, or a cluster of up to eight where units are few
+//     and long, each CTA with a contiguous segment of the scores in shared
+//     memory, read once.  Scores are mapped to whole numbers of the same
+//     order, and the m-th largest of the middle is found digit by digit (a
+//     radix selection: a histogram of 11, 11 and 10 bits, narrowed each time
+//     to the digit that holds the m-th largest; a cluster adds its CTAs'
+//     histograms through distributed shared memory).  Two more passes count
+//     and place the kept tokens in index order -- those above the threshold
+//     and the first of those at it -- so equal scores go to the lowest index
+//     whatever the timing.
+//   * move: the K and V rows of the kept tokens, 32 KB a CTA through
+//     registers.
+//
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <cstring>
 
@@ -30,10 +32,8 @@ namespace pa {
 namespace {
 
 constexpr int kSelThreads = 512;
-constexpr int kSelPer = 8;  // tokens a thread numbers at once
-constexpr int kSelTile = kSelThreads * kSelPer;
 constexpr int kMoveThreads = 256;
-constexpr int kMoveBatch = 8;  // 16-byte chunks a thread has in flight
+constexpr int kMoveBatch = 8;  // 16-byte pieces a thread has in flight
 
 struct EvictLayer {
     uint4 *k, *v;
@@ -49,7 +49,10 @@ struct EvictParams {
     int max_blocks_per_seq, dst_max_blocks_per_seq;
     const int32_t *context_lens, *keep_lens;
     int32_t *new_lens;
-    int32_t *index;  // [units][max_keep_len]: the kept tokens of each unit, ascending
+    int32_t *index;   // [units][max_keep_len]: the kept tokens of each unit, ascending
+    unsigned *ticket; // [units]: chunks taken (in place)
+    unsigned *flags;  // [units][max_chunks]: chunks read (in place)
+    int max_chunks;
     int max_context_len, max_keep_len, num_sink, num_recent;
     int num_seqs, num_kv_heads, num_blocks, block_shift;
     int lg_cpr;    // log2 of a row's 16-byte chunks
@@ -83,168 +86,362 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-// grid (KV head, sequence, layer)
+// Histogram digits of the radix selection: 11, 11 and 10 bits.
+constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+// A 32-bit word of another CTA of the cluster, at the place of `p` in this one's shared memory.
+__device__ __forceinline__ unsigned ld_cluster(const unsigned *p, uint32_t rank) {
+    uint32_t a, v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+
+// grid (cluster rank, unit): CS CTAs a unit, each with a contiguous segment of
+// its tokens in shared memory.
+template <int CS>
 __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictParams P) {
-    __shared__ unsigned hist[256];
-    __shared__ unsigned s_digit, s_need;
-    __shared__ unsigned s_warp[kSelThreads / 32];
+    extern __shared__ float s_x[];  // this CTA's segment of the scores
+    __shared__ unsigned hist[2][kBins];
+    __shared__ unsigned s_warp[kSelThreads / 32], s_digit, s_need;
+    constexpr int kWarps = kSelThreads / 32;
     pdl_trigger();
     pdl_wait();  // earlier kernels may still write what this reads, or read what it writes
-    const int hk = blockIdx.x, s = blockIdx.y, l = blockIdx.z;
+    const unsigned unit = blockIdx.x / CS;
+    const int rank = CS > 1 ? (int)cluster_rank() : 0;
+    const int hk = (int)(unit % (unsigned)P.num_kv_heads);
+    const unsigned ls = unit / (unsigned)P.num_kv_heads;
+    const int s = (int)(ls % (unsigned)P.num_seqs), l = (int)(ls / (unsigned)P.num_seqs);
     const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
     const SeqPlan q = seq_plan(P, s);
-    if (tid == 0 && hk == 0 && l == 0) {
+    if (tid == 0 && rank == 0 && hk == 0 && l == 0) {
         P.new_lens[s] = q.ok ? q.n : q.L;
         if (!q.ok && P.err) atomicOr(P.err, PA_ERRBIT_CONTEXT_LEN);
     }
-    if (!q.ok || q.L == 0) return;
-    const size_t unit = ((size_t)l * P.num_seqs + s) * P.num_kv_heads + hk;
+    if (!q.ok || q.L == 0) return;  // the same in the whole cluster
     const size_t head = (size_t)s * P.num_kv_heads + hk;
     const float *sc = P.layer[l].scores + head * P.score_stride;
     float *out = P.layer[l].scores_out + head * P.score_out_stride;
-    int32_t *idx = P.index + unit * P.max_keep_len;
+    int32_t *idx = P.index + (size_t)unit * P.max_keep_len;
     int32_t *kept = P.layer[l].kept ? P.layer[l].kept + head * P.kept_stride : nullptr;
+    if (P.in_place) {  // the move kernel's order of chunks
+        if (tid == 0 && rank == 0) P.ticket[unit] = 0u;
+        unsigned *flags = P.flags + (size_t)unit * P.max_chunks;
+        for (int i = rank * kSelThreads + tid; i < P.max_chunks; i += CS * kSelThreads) flags[i] = 0u;
+    }
+    if (q.n == q.L) {  // everything stays where it is (the move needs no list)
+        for (int t = rank * kSelThreads + tid; t < q.L; t += CS * kSelThreads) {
+            if (kept) kept[t] = t;
+            if (out != sc) out[t] = sc[t];
+        }
+        return;
+    }
+    const int seg = (q.L + CS - 1) / CS, t0 = rank * seg;
+    const int cnt = max(0, min(seg, q.L - t0));  // this CTA's tokens t0 .. t0 + cnt - 1
+    for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0u;
+    {
+        int i = tid;
+        for (; i + 7 * kSelThreads < cnt; i += 8 * kSelThreads) {
+            float x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = sc[t0 + i + u * kSelThreads];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) s_x[i + u * kSelThreads] = x[u];
+        }
+        for (; i < cnt; i += kSelThreads) s_x[i] = sc[t0 + i];
+    }
+    __syncthreads();
     const int m0 = q.sink, m1 = q.L - q.recent;  // the middle
 
     // the mid-th largest key of the middle: threshold, and how many at it stay
     uint32_t thr = 0u;
     unsigned need = 0u;
-    if (q.n < q.L && q.mid > 0) {
+    if (q.mid > 0) {
         unsigned left = (unsigned)q.mid;
         uint32_t mask = 0u;
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            if (tid < 256) hist[tid] = 0u;
-            __syncthreads();
-            for (int t = m0 + tid; t < m1; t += kSelThreads) {
-                const uint32_t key = order_key(sc[t]);
-                if ((key & mask) == thr) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+        const int i0 = max(0, m0 - t0), i1 = min(cnt, m1 - t0);
+#pragma unroll
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
+            const int bins = pass == 2 ? 1024 : 2048;
+            unsigned *h = hist[pass & 1];
+            for (int b = i0 + 32 * wid; b < i1; b += kSelThreads) {
+                const int i = b + lane;
+                const uint32_t key = i < i1 ? order_key(s_x[i]) : 0u;
+                const bool in = i < i1 && (key & mask) == thr;
+                const unsigned bin = (key >> shift) & (unsigned)(bins - 1);
+                if (pass == 0) {  // few distinct leading digits: one add for the lanes that share one
+                    const unsigned peers = __match_any_sync(0xffffffffu, in ? bin : ~0u);
+                    if (in && lane == __ffs(peers) - 1) atomicAdd(&h[bin], (unsigned)__popc(peers));
+                } else if (in) {
+                    atomicAdd(&h[bin], 1u);
+                }
             }
+            if (CS > 1) cluster_sync();
+            else __syncthreads();
+            // largest digits first: thread i has bins bins-1-4i .. bins-4-4i
+            unsigned c[4], sum = 0u;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int b = bins - 1 - (4 * tid + k);
+                c[k] = 0u;
+                if (b >= 0) {
+                    if constexpr (CS > 1) {
+#pragma unroll
+                        for (int r = 0; r < CS; ++r) c[k] += ld_cluster(&h[b], (uint32_t)r);
+                    } else {
+                        c[k] = h[b];
+                    }
+                }
+                sum += c[k];
+            }
+            unsigned incl = sum;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += u;
+            }
+            if (lane == 31) s_warp[wid] = incl;
+            if (pass < 2)  // the other histogram: read last before the barrier above
+                for (int i = tid; i < kBins; i += kSelThreads) hist[(pass + 1) & 1][i] = 0u;
             __syncthreads();
-            if (wid == 0) {  // the digit whose keys, largest first, reach `left`
-                unsigned c[8], sum = 0u;
+            unsigned before = incl - sum;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += c[i] = hist[255 - (lane * 8 + i)];
-                unsigned incl = sum;
+            for (int w = 0; w < kWarps; ++w) before += w < wid ? s_warp[w] : 0u;
+            if (before < left && before + sum >= left) {  // one thread
+                int k = 0;
+                unsigned b4 = before;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
-                    if (lane >= o) incl += u;
-                }
-                unsigned before = incl - sum;
-                if (before < left && incl >= left) {
-                    int i = 0;
-                    while (before + c[i] < left) before += c[i++];
-                    s_digit = 255u - (unsigned)(lane * 8 + i);
-                    s_need = left - before;
-                }
+                for (int e = 0; e < 3; ++e)
+                    if (k == e && b4 + c[e] < left) {
+                        b4 += c[e];
+                        k = e + 1;
+                    }
+                s_digit = (unsigned)(bins - 1 - (4 * tid + k));
+                s_need = left - b4;
             }
             __syncthreads();
             thr |= s_digit << shift;
-            mask |= 255u << shift;
+            mask |= (unsigned)(bins - 1) << shift;
             left = s_need;
-            __syncthreads();
         }
         need = left;
     }
 
-    // number the kept tokens in index order
-    int base_gt = 0, base_eq = 0;
-    for (int t0 = 0; t0 < q.L; t0 += kSelTile) {
-        const int t = t0 + tid * kSelPer;
-        float x[kSelPer];
-        unsigned cls = 0u;  // 2 bits a token: 1 above the threshold or fixed, 2 at it
-        unsigned cnt = 0u;  // above in the low half, at it in the high half
-#pragma unroll
-        for (int i = 0; i < kSelPer; ++i) {
-            x[i] = t + i < q.L ? sc[t + i] : 0.f;
-            if (t + i >= q.L) continue;
-            const uint32_t key = order_key(x[i]);
-            const bool fixed = q.n == q.L || t + i < m0 || t + i >= m1;
-            if (fixed || (q.mid > 0 && key > thr)) {
-                cls |= 1u << (2 * i);
-                cnt += 1u;
-            } else if (q.mid > 0 && key == thr) {
-                cls |= 2u << (2 * i);
-                cnt += 1u << 16;
+    // Number the kept tokens in index order.  A warp has a contiguous part of
+    // the segment, 32 tokens a step: count, then place.
+    const int part = ((cnt + kWarps - 1) / kWarps + 31) & ~31;
+    const int w0 = wid * part, w1 = min(cnt, w0 + part);
+    auto classify = [&](int i, unsigned &gt, unsigned &eq) {
+        bool above = false, at = false;
+        if (i < w1) {
+            const int t = t0 + i;
+            if (t < m0 || t >= m1) {
+                above = true;
+            } else if (q.mid > 0) {
+                const uint32_t key = order_key(s_x[i]);
+                above = key > thr;
+                at = key == thr;
             }
         }
-        unsigned incl = cnt;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-        }
-        if (lane == 31) s_warp[wid] = incl;
-        __syncthreads();  // and: the whole tile has been read
-        unsigned before = incl - cnt, total = 0u;
-        for (int w = 0; w < kSelThreads / 32; ++w) {
-            if (w < wid) before += s_warp[w];
-            total += s_warp[w];
-        }
-        int gt = base_gt + (int)(before & 0xffffu), eq = base_eq + (int)(before >> 16);
-#pragma unroll
-        for (int i = 0; i < kSelPer; ++i) {
-            const unsigned c = (cls >> (2 * i)) & 3u;
-            if (c == 1u || (c == 2u && eq < (int)need)) {
-                const int p = gt + min(eq, (int)need);
-                idx[p] = t + i;
-                if (kept) kept[p] = t + i;
-                out[p] = x[i];
-            }
-            gt += c == 1u;
-            eq += c == 2u;
-        }
-        base_gt += (int)(total & 0xffffu);
-        base_eq += (int)(total >> 16);
-        __syncthreads();
+        gt = __ballot_sync(0xffffffffu, above);
+        eq = __ballot_sync(0xffffffffu, at);
+    };
+    unsigned n_gt = 0u, n_eq = 0u;
+    for (int i = w0; i < w1; i += 32) {
+        unsigned gt, eq;
+        classify(i + lane, gt, eq);
+        n_gt += (unsigned)__popc(gt);
+        n_eq += (unsigned)__popc(eq);
     }
-    for (int p = q.n + tid; p < q.L; p += kSelThreads) out[p] = 0.f;  // vacated positions
+    // the parts before this one: in the CTA, then in the cluster
+    if (lane == 0) {
+        hist[1][wid] = n_gt;  // (read last in pass 1, before pass 2's barrier)
+        hist[1][kWarps + wid] = n_eq;
+    }
+    if (CS > 1) cluster_sync();
+    else __syncthreads();
+    unsigned b_gt = 0u, b_eq = 0u;
+    for (int r = 0; r <= rank; ++r)
+        for (int w = 0; w < kWarps; ++w) {
+            if (r == rank && w >= wid) break;
+            b_gt += CS > 1 ? ld_cluster(&hist[1][w], (uint32_t)r) : hist[1][w];
+            b_eq += CS > 1 ? ld_cluster(&hist[1][kWarps + w], (uint32_t)r) : hist[1][kWarps + w];
+        }
+    const unsigned below = (1u << lane) - 1u;
+    for (int i = w0; i < w1; i += 32) {
+        unsigned gt, eq;
+        classify(i + lane, gt, eq);
+        const unsigned g = b_gt + (unsigned)__popc(gt & below), e = b_eq + (unsigned)__popc(eq & below);
+        if (((gt >> lane) & 1u) || (((eq >> lane) & 1u) && e < need)) {
+            const unsigned p = g + min(e, need);
+            idx[p] = t0 + i + lane;
+            if (kept) kept[p] = t0 + i + lane;
+            out[p] = s_x[i + lane];
+        }
+        b_gt += (unsigned)__popc(gt);
+        b_eq += (unsigned)__popc(eq);
+    }
+    for (int p = q.n + rank * kSelThreads + tid; p < q.L; p += CS * kSelThreads) out[p] = 0.f;
+    if (CS > 1) cluster_sync();  // no CTA leaves while another may read its counts
 }
 
-// grid (KV head, sequence, layer x {K, V})
-__global__ void __launch_bounds__(kMoveThreads)
-    evict_move_kernel(const __grid_constant__ EvictParams P) {
-    pdl_trigger();
-    pdl_wait();
-    const int hk = blockIdx.x, s = blockIdx.y, l = blockIdx.z >> 1;
-    const SeqPlan q = seq_plan(P, s);
-    if (!q.ok || (P.in_place && q.n == q.L)) return;
-    uint4 *pool = blockIdx.z & 1 ? P.layer[l].v : P.layer[l].k;
-    const int32_t *idx =
-        P.index + (((size_t)l * P.num_seqs + s) * P.num_kv_heads + hk) * P.max_keep_len;
-    const int32_t *src = P.block_tables + (size_t)s * P.max_blocks_per_seq;
-    const int32_t *dst = P.in_place ? src : P.dst_block_tables + (size_t)s * P.dst_max_blocks_per_seq;
-    const int c = threadIdx.x & ((1 << P.lg_cpr) - 1), r = threadIdx.x >> P.lg_cpr;
-    const int rows = kMoveThreads >> P.lg_cpr, in_block = (1 << P.block_shift) - 1;
-    auto at = [&](const int32_t *table, int t) -> uint4 * {
-        const int b = table[t >> P.block_shift];
-        if (b < 0 || b >= P.num_blocks) {
-            if (c == 0 && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
-            return nullptr;
-        }
-        return pool + (((((size_t)b * P.num_kv_heads + hk) << P.block_shift) + (t & in_block))
-                       << P.lg_cpr) + c;
-    };
-    for (int i0 = 0; i0 < q.n; i0 += rows * kMoveBatch) {
-        uint4 x[kMoveBatch];
-        bool have[kMoveBatch];
-#pragma unroll
-        for (int u = 0; u < kMoveBatch; ++u) {
-            const int i = i0 + u * rows + r;
-            const uint4 *p = i < q.n ? at(src, idx[i]) : nullptr;
-            have[u] = p != nullptr;
-            if (have[u]) x[u] = *p;
-        }
-        __syncthreads();  // the tile has been read
-#pragma unroll
-        for (int u = 0; u < kMoveBatch; ++u) {
-            const int i = i0 + u * rows + r;
-            if (!have[u]) continue;
-            uint4 *p = at(dst, i);
-            if (p) *p = x[u];
+// Wait until the flags of chunks 0 .. c-1 are set; false if the wait gave up.
+__device__ __forceinline__ bool wait_chunks(const unsigned *flags, int c) {
+    const uint64_t start = globaltimer_ns();
+    for (int i = threadIdx.x; i < c; i += kMoveThreads) {
+        for (uint32_t polls = 0;; ++polls) {
+            unsigned v;
+            asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(flags + i) : "memory");
+            if (v) break;
+            if (polls >= kWaitLimitPolls || globaltimer_ns() - start > kWaitLimitNs) return false;
         }
     }
+    return true;
+}
+
+// grid (units x max_chunks): a CTA moves one chunk of a unit's K and V rows,
+// kMoveBatch 16-byte pieces a thread.  In place a chunk's new rows may lie on
+// old rows of chunks before it, never of chunks after it (a kept token moves
+// towards the front), so a CTA reads its chunk into registers, sets the
+// chunk's flag, and writes once every chunk before it has been read.  Chunks
+// are taken in order by a counter, so those it waits for have been started,
+// and a chunk's reads wait for nothing.
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads)
+    evict_move_kernel(const __grid_constant__ EvictParams P) {
+    __shared__ int s_chunk;
+    pdl_trigger();
+    pdl_wait();
+    const unsigned unit = blockIdx.x / (unsigned)P.max_chunks;
+    int chunk = (int)(blockIdx.x - unit * (unsigned)P.max_chunks);
+    const int hk = (int)(unit % (unsigned)P.num_kv_heads);
+    const unsigned ls = unit / (unsigned)P.num_kv_heads;
+    const int s = (int)(ls % (unsigned)P.num_seqs), l = (int)(ls / (unsigned)P.num_seqs);
+    const SeqPlan q = seq_plan(P, s);
+    if (!q.ok || (IN_PLACE && q.n == q.L)) return;
+    const int lg_rows = 10 - P.lg_cpr;  // rows of a chunk: kMoveThreads * kMoveBatch / 2 pieces of K
+    static_assert(kMoveThreads * kMoveBatch / 2 == 1 << 10, "pieces of a chunk");
+    const int chunks = (q.n + (1 << lg_rows) - 1) >> lg_rows;
+    if (chunk >= chunks) return;
+    if (IN_PLACE) {
+        if (threadIdx.x == 0) s_chunk = (int)atomicAdd(&P.ticket[unit], 1u);
+        __syncthreads();
+        chunk = s_chunk;
+    }
+    unsigned *flags = P.flags + (size_t)unit * P.max_chunks;
+    const int32_t *idx = P.index + (size_t)unit * P.max_keep_len;
+    const int32_t *src = P.block_tables + (size_t)s * P.max_blocks_per_seq;
+    const int32_t *dst = IN_PLACE ? src : P.dst_block_tables + (size_t)s * P.dst_max_blocks_per_seq;
+    const int c = threadIdx.x & ((1 << P.lg_cpr) - 1), r = threadIdx.x >> P.lg_cpr;
+    const int step = kMoveThreads >> P.lg_cpr, in_block = (1 << P.block_shift) - 1;
+    const int i0 = chunk << lg_rows;
+    constexpr int kRows = kMoveBatch / 2;  // a thread's rows; a K and a V piece each
+    size_t from[kRows], to[kRows];
+    bool have[kRows];
+    bool oob = false;
+    auto place = [&](const int32_t *table, int t, size_t &at) -> bool {
+        const int b = table[t >> P.block_shift];
+        at = ((((size_t)b * P.num_kv_heads + hk) << P.block_shift) + (t & in_block)) << P.lg_cpr;
+        return b >= 0 && b < P.num_blocks;
+    };
+    const bool all = q.n == q.L;
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const int i = i0 + u * step + r;
+        have[u] = i < q.n;
+        if (!have[u]) continue;
+        const int t = all ? i : idx[i];
+        const bool a = place(src, t, from[u]), b = place(dst, i, to[u]);
+        oob |= !a || !b;
+        have[u] = a && b && !(IN_PLACE && t == i);  // a row that stays needs no move
+    }
+    if (oob && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
+    uint4 k[kRows], v[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        if (have[u]) {
+            k[u] = P.layer[l].k[from[u] + c];
+            v[u] = P.layer[l].v[from[u] + c];
+        }
+    if (IN_PLACE) {
+        __syncthreads();  // the chunk has been read
+        if (threadIdx.x == 0) {
+            __threadfence();
+            asm volatile("st.release.gpu.global.u32 [%0], %1;" ::"l"(flags + chunk), "r"(1u) : "memory");
+        }
+        if (__syncthreads_or(!wait_chunks(flags, chunk))) {
+            if (threadIdx.x == 0 && P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
+            return;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u)
+        if (have[u]) {
+            P.layer[l].k[to[u] + c] = k[u];
+            P.layer[l].v[to[u] + c] = v[u];
+        }
+}
+
+// Workspace: the kept tokens of every unit, then (in place) a chunk counter
+// and the chunks' flags of every unit.  A chunk has 32, 64 or 128 rows.
+struct EvictWork {
+    size_t ticket, flags, bytes;
+    long long max_chunks;
+};
+EvictWork evict_work(size_t units, int max_keep_len, int rows) {
+    EvictWork w;
+    w.max_chunks = ((long long)max_keep_len + rows - 1) / rows;
+    w.ticket = round_up_256(units * max_keep_len * sizeof(int32_t));
+    w.flags = round_up_256(w.ticket + units * sizeof(unsigned));
+    w.bytes = round_up_256(w.flags + units * (size_t)w.max_chunks * sizeof(unsigned)) + 256;
+    return w;
+}
+
+// Tokens of one CTA's segment at most: 48 Ki scores (192 KB) beside the
+// histograms.
+constexpr long long kMaxSegment = 48 * 1024;
+
+template <int CS>
+cudaError_t launch_select(const EvictParams &P, unsigned units, size_t smem, cudaStream_t stream) {
+    auto kern = evict_select_kernel<CS>;
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> attr_set[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)(kMaxSegment * 4));
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_relaxed);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(units * CS);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CS;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CS > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, P);
 }
 
 }  // namespace
@@ -257,8 +454,7 @@ extern "C" size_t pa_evict_workspace_size(int num_layers, int num_seqs, int num_
     if (num_layers <= 0 || num_layers > PA_MAX_LAYERS || num_seqs < 0 || num_kv_heads <= 0 ||
         max_context_len < 0 || max_keep_len < 0)
         return 0;
-    const size_t units = (size_t)num_layers * num_seqs * num_kv_heads;
-    return round_up_256(units * max_keep_len * sizeof(int32_t)) + 256;
+    return evict_work((size_t)num_layers * num_seqs * num_kv_heads, max_keep_len, 32).bytes;
 }
 
 extern "C" pa_status_t pa_evict_tokens(
@@ -280,6 +476,10 @@ extern "C" pa_status_t pa_evict_tokens(
     if (!is_16bit(dtype)) return PA_ERR_INVALID_ARG;
     if (!head_dim_supported(head_dim)) return PA_ERR_UNSUPPORTED;
     if (num_kv_heads > 65535 || num_seqs > 65535) return PA_ERR_UNSUPPORTED;
+    const long long units = (long long)num_layers * num_seqs * num_kv_heads;
+    if (max_context_len > kMaxSegment * kMaxCluster || units * kMaxCluster >= (1ll << 31) ||
+        units * ((max_keep_len + 31ll) / 32) >= (1ll << 31))
+        return PA_ERR_UNSUPPORTED;
     if (max_keep_len > max_context_len ||
         (long long)max_context_len > (long long)block_size * max_blocks_per_seq ||
         score_stride < max_context_len || (scores_out && score_out_stride < max_context_len) ||
@@ -324,7 +524,13 @@ extern "C" pa_status_t pa_evict_tokens(
     P.context_lens = context_lens;
     P.keep_lens = keep_lens;
     P.new_lens = new_lens;
-    P.index = (int32_t *)workspace;
+    const int rows = 2048 / (head_dim / 4);  // of a chunk
+    const EvictWork w = evict_work((size_t)units, max_keep_len, rows);
+    unsigned char *ws = static_cast<unsigned char *>(workspace);
+    P.index = reinterpret_cast<int32_t *>(ws);
+    P.ticket = reinterpret_cast<unsigned *>(ws + w.ticket);
+    P.flags = reinterpret_cast<unsigned *>(ws + w.flags);
+    P.max_chunks = (int)w.max_chunks;
     P.max_context_len = max_context_len;
     P.max_keep_len = max_keep_len;
     P.num_sink = num_sink;
@@ -337,13 +543,23 @@ extern "C" pa_status_t pa_evict_tokens(
     P.in_place = dst_block_tables ? 0 : 1;
     P.err = dev_error_word;
     const cudaStream_t st = (cudaStream_t)stream;
-    if (launch_pdl(evict_select_kernel,
-                   dim3((unsigned)num_kv_heads, (unsigned)num_seqs, (unsigned)num_layers),
-                   dim3(kSelThreads), 0, st, P) != cudaSuccess)
-        return PA_ERR_CUDA;
-    return launch_pdl(evict_move_kernel,
-                      dim3((unsigned)num_kv_heads, (unsigned)num_seqs, (unsigned)(2 * num_layers)),
-                      dim3(kMoveThreads), 0, st, P) == cudaSuccess
-               ? PA_OK
-               : PA_ERR_CUDA;
+    // CTAs a unit: as many as its scores need to fit shared memory, and more
+    // (8 at most) while that fills the GPU and leaves each 4096 tokens
+    const int sms = device_sms();
+    if (sms <= 0) return PA_ERR_CUDA;
+    int cs = 1;
+    while (cs < kMaxCluster && (max_context_len > kMaxSegment * cs ||
+                                (units * cs * 2 <= sms && max_context_len >= 4096 * 2 * cs)))
+        cs *= 2;
+    const size_t smem = ((size_t)max_context_len + cs - 1) / cs * sizeof(float);
+    cudaError_t e = cs == 1   ? launch_select<1>(P, (unsigned)units, smem, st)
+                    : cs == 2 ? launch_select<2>(P, (unsigned)units, smem, st)
+                    : cs == 4 ? launch_select<4>(P, (unsigned)units, smem, st)
+                              : launch_select<8>(P, (unsigned)units, smem, st);
+    if (e != cudaSuccess) return PA_ERR_CUDA;
+    if (P.max_chunks == 0) return PA_OK;  // nothing is kept anywhere
+    const dim3 grid((unsigned)(units * P.max_chunks));
+    e = P.in_place ? launch_pdl(evict_move_kernel<true>, grid, dim3(kMoveThreads), 0, st, P)
+                   : launch_pdl(evict_move_kernel<false>, grid, dim3(kMoveThreads), 0, st, P);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }

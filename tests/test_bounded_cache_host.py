@@ -175,7 +175,9 @@ def _evict(lib, **kw):
     ({"new": None}, INVALID), ({"new": P}, INVALID), ({"k": _ptrs(P, None)}, INVALID), ({"v": _ptrs(P, P + 8)}, INVALID),
     ({"sc": _ptrs(P, P + 2)}, INVALID), ({"so": _ptrs(P, None), "sos": 100}, INVALID),
     ({"kept": _ptrs(P, P + 1), "ks": 50}, INVALID), ({"ws": P + 128}, WORKSPACE), ({"ws": None}, INVALID),
-    ({"wb": 100}, WORKSPACE), ({"S": 65536}, UNSUPPORTED), ({"Hkv": 65536}, UNSUPPORTED)])
+    ({"wb": 100}, WORKSPACE), ({"S": 65536}, UNSUPPORTED), ({"Hkv": 65536}, UNSUPPORTED),
+    ({"L": 393217, "ss": 393217, "mb": 1 << 20}, UNSUPPORTED),
+    ({"S": 65535, "Hkv": 65535, "L": 100, "K": 50}, UNSUPPORTED)])
 def test_evict_refusals(lib, kw, want):
     assert _evict(lib, **kw) == want
 

@@ -142,6 +142,21 @@ def test_long_sequences(out_of_place):
     _check(c, _scores(1, 3, 1, 70001, seed=9, levels=100), [69999, 5, 12288], 0, 0, out_of_place)
 
 
+@pytest.mark.parametrize("L,n,levels", [(393216, 200000, None), (196609, 1, 3), (100000, 99999, 1), (9000, 4000, 50)])
+def test_long_sequences_split_over_a_cluster(L, n, levels):
+    c = Cache([L, 7], 1, 64, torch.float16, 256, seed=17)
+    _check(c, _scores(1, 2, 1, L, seed=18, levels=levels), [n, 5], 100, 300)
+
+
+@pytest.mark.parametrize("n", [3000, 4095])
+def test_in_place_moves_by_one_and_by_many(n):
+    """One early token leaves (every later row moves by one), or a quarter does."""
+    c = Cache([4096] * 3, 2, 128, torch.bfloat16, 16, seed=19)
+    sc = _scores(1, 3, 2, 4096, seed=20)
+    sc[..., 5] = -1.0
+    _check(c, sc, [n] * 3, 0, 0)
+
+
 def test_many_layers_and_sequences():
     lens = list(np.random.default_rng(9).integers(0, 200, 30))
     c = Cache(lens, 4, 64, torch.bfloat16, 16, seed=9, layers=5)
