@@ -681,7 +681,8 @@ size_t pa_evict_workspace_size(int num_layers, int num_seqs, int num_kv_heads,
  *     K'[j] = K[i_j], V'[j] = V[i_j], scores'[j] = scores[i_j]   (j < n)
  *     scores'[j] = 0                                             (n <= j < L)
  *     new_lens[s] = n.
- * Values are copied unchanged.  Positions from n on of the last block, and
+ * Values are copied unchanged (of a score, a NaN's payload and the sign of a
+ * zero may be lost).  Positions from n on of the last block, and
  * scores from L on, are left as they were.  L <= keep_lens[s] keeps everything.
  * Attention does not depend on the order of the cached tokens, and rotated
  * keys keep their positions (pa_rotary_cache_write).

@@ -788,9 +788,10 @@ pa_status_t launch_decode_scored_d256(const DecodeParams &P, pa_dtype_t dtype, i
                                       cudaStream_t stream);
 
 // The weight pass of the SCORED form (pa_decode_scored.cu): adds every
-// token's attention weight to scores[s][hk][t].
+// token's attention weight to scores[s][hk][t] and, where `merge` says that a
+// sequence may have several partitions, merges them.
 pa_status_t launch_decode_weights(const DecodeParams &P, float *scores, long long score_stride,
-                                  cudaStream_t stream);
+                                  bool merge, cudaStream_t stream);
 
 // Number of streaming multiprocessors of the current device (cached).
 int current_sm_count();

@@ -79,11 +79,15 @@ __device__ __forceinline__ SeqPlan seq_plan(const EvictParams &P, int s) {
     return q;
 }
 
-// A score as a whole number of the same order; NaN below everything, -0 = 0.
+// A score as a whole number of the same order, and back: NaN is 0, below
+// everything, and -0 is 0 (the only two whose bits do not come back).
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x) return 0u;
     const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
     return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+}
+__device__ __forceinline__ float score_of(uint32_t key) {
+    return __uint_as_float((key >> 31) ? key ^ 0x80000000u : ~key);
 }
 
 // Histogram digits of the radix selection: 11, 11 and 10 bits.
@@ -112,9 +116,11 @@ __device__ __forceinline__ unsigned ld_cluster(const unsigned *p, uint32_t rank)
 template <int CS>
 __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictParams P) {
-    extern __shared__ float s_x[];  // this CTA's segment of the scores
+    extern __shared__ uint4 s_key4[];  // the order keys of this CTA's segment, four a word
     __shared__ unsigned hist[2][kBins];
     __shared__ unsigned s_warp[kSelThreads / 32], s_digit, s_need;
+    __shared__ unsigned s_total;  // the segment's tokens above the threshold, and at it << 16
+    uint32_t *const s_key = reinterpret_cast<uint32_t *>(s_key4);
     constexpr int kWarps = kSelThreads / 32;
     pdl_trigger();
     pdl_wait();  // earlier kernels may still write what this reads, or read what it writes
@@ -147,7 +153,7 @@ __global__ void __launch_bounds__(kSelThreads)
         }
         return;
     }
-    const int seg = (q.L + CS - 1) / CS, t0 = rank * seg;
+    const int seg = ((q.L + CS - 1) / CS + 3) & ~3, t0 = rank * seg;
     const int cnt = max(0, min(seg, q.L - t0));  // this CTA's tokens t0 .. t0 + cnt - 1
     for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0u;
     {
@@ -157,9 +163,9 @@ __global__ void __launch_bounds__(kSelThreads)
 #pragma unroll
             for (int u = 0; u < 8; ++u) x[u] = sc[t0 + i + u * kSelThreads];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s_x[i + u * kSelThreads] = x[u];
+            for (int u = 0; u < 8; ++u) s_key[i + u * kSelThreads] = order_key(x[u]);
         }
-        for (; i < cnt; i += kSelThreads) s_x[i] = sc[t0 + i];
+        for (; i < cnt; i += kSelThreads) s_key[i] = order_key(sc[t0 + i]);
     }
     __syncthreads();
     const int m0 = q.sink, m1 = q.L - q.recent;  // the middle
@@ -176,16 +182,14 @@ __global__ void __launch_bounds__(kSelThreads)
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const int bins = pass == 2 ? 1024 : 2048;
             unsigned *h = hist[pass & 1];
-            for (int b = i0 + 32 * wid; b < i1; b += kSelThreads) {
-                const int i = b + lane;
-                const uint32_t key = i < i1 ? order_key(s_x[i]) : 0u;
-                const bool in = i < i1 && (key & mask) == thr;
-                const unsigned bin = (key >> shift) & (unsigned)(bins - 1);
-                if (pass == 0) {  // few distinct leading digits: one add for the lanes that share one
-                    const unsigned peers = __match_any_sync(0xffffffffu, in ? bin : ~0u);
-                    if (in && lane == __ffs(peers) - 1) atomicAdd(&h[bin], (unsigned)__popc(peers));
-                } else if (in) {
-                    atomicAdd(&h[bin], 1u);
+            for (int j = tid; 4 * j < i1; j += kSelThreads) {
+                const uint4 k4 = s_key4[j];
+                const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int i = 4 * j + u;
+                    if (i >= i0 && i < i1 && ((key[u] ^ thr) & mask) == 0u)
+                        atomicAdd(&h[(key[u] >> shift) & (unsigned)(bins - 1)], 1u);
                 }
             }
             if (CS > 1) cluster_sync();
@@ -240,58 +244,82 @@ __global__ void __launch_bounds__(kSelThreads)
     }
 
     // Number the kept tokens in index order.  A warp has a contiguous part of
-    // the segment, 32 tokens a step: count, then place.
-    const int part = ((cnt + kWarps - 1) / kWarps + 31) & ~31;
+    // the segment, four tokens a lane and step: count, then place.
+    const int part = ((cnt + kWarps - 1) / kWarps + 127) & ~127;
     const int w0 = wid * part, w1 = min(cnt, w0 + part);
-    auto classify = [&](int i, unsigned &gt, unsigned &eq) {
-        bool above = false, at = false;
-        if (i < w1) {
-            const int t = t0 + i;
-            if (t < m0 || t >= m1) {
-                above = true;
-            } else if (q.mid > 0) {
-                const uint32_t key = order_key(s_x[i]);
-                above = key > thr;
-                at = key == thr;
-            }
+    const int f0 = m0 - t0, f1 = m1 - t0;  // the middle, as places of the segment
+    const bool some = q.mid > 0;
+    // tokens i .. i + 3: bit u of the low half: above the threshold (or always
+    // kept); of the high half: at it
+    auto classify = [&](int i) -> unsigned {
+        if (i >= w1) return 0u;
+        const uint4 k4 = s_key4[i >> 2];
+        const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
+        unsigned c = 0u;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool in = i + u < w1, fixed = i + u < f0 || i + u >= f1;
+            if (in && (fixed || (some && key[u] > thr))) c |= 1u << u;
+            if (in && !fixed && some && key[u] == thr) c |= 0x10000u << u;
         }
-        gt = __ballot_sync(0xffffffffu, above);
-        eq = __ballot_sync(0xffffffffu, at);
+        return c;
     };
-    unsigned n_gt = 0u, n_eq = 0u;
-    for (int i = w0; i < w1; i += 32) {
-        unsigned gt, eq;
-        classify(i + lane, gt, eq);
-        n_gt += (unsigned)__popc(gt);
-        n_eq += (unsigned)__popc(eq);
-    }
+    auto counts = [](unsigned c) -> unsigned {  // above, at << 16
+        return (unsigned)__popc(c & 0xffffu) | ((unsigned)__popc(c >> 16) << 16);
+    };
+    unsigned mine = 0u;
+    for (int i = w0 + 4 * lane; i < w1; i += 128) mine += counts(classify(i));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    if (lane == 0) s_warp[wid] = mine;
+    __syncthreads();
     // the parts before this one: in the CTA, then in the cluster
-    if (lane == 0) {
-        hist[1][wid] = n_gt;  // (read last in pass 1, before pass 2's barrier)
-        hist[1][kWarps + wid] = n_eq;
+    unsigned prior = lane < kWarps ? s_warp[lane] : 0u;
+    unsigned total = prior;
+    if (lane >= wid) prior = 0u;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        prior += __shfl_xor_sync(0xffffffffu, prior, o);
+        total += __shfl_xor_sync(0xffffffffu, total, o);
     }
-    if (CS > 1) cluster_sync();
-    else __syncthreads();
-    unsigned b_gt = 0u, b_eq = 0u;
-    for (int r = 0; r <= rank; ++r)
-        for (int w = 0; w < kWarps; ++w) {
-            if (r == rank && w >= wid) break;
-            b_gt += CS > 1 ? ld_cluster(&hist[1][w], (uint32_t)r) : hist[1][w];
-            b_eq += CS > 1 ? ld_cluster(&hist[1][kWarps + w], (uint32_t)r) : hist[1][kWarps + w];
+    unsigned b_gt = prior & 0xffffu, b_eq = prior >> 16;
+    if constexpr (CS > 1) {
+        if (tid == 0) s_total = total;
+        cluster_sync();
+        unsigned other = lane < rank ? ld_cluster(&s_total, (uint32_t)lane) : 0u;
+        unsigned o_gt = other & 0xffffu, o_eq = other >> 16;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            o_gt += __shfl_xor_sync(0xffffffffu, o_gt, o);
+            o_eq += __shfl_xor_sync(0xffffffffu, o_eq, o);
         }
-    const unsigned below = (1u << lane) - 1u;
-    for (int i = w0; i < w1; i += 32) {
-        unsigned gt, eq;
-        classify(i + lane, gt, eq);
-        const unsigned g = b_gt + (unsigned)__popc(gt & below), e = b_eq + (unsigned)__popc(eq & below);
-        if (((gt >> lane) & 1u) || (((eq >> lane) & 1u) && e < need)) {
-            const unsigned p = g + min(e, need);
-            idx[p] = t0 + i + lane;
-            if (kept) kept[p] = t0 + i + lane;
-            out[p] = s_x[i + lane];
+        b_gt += o_gt;
+        b_eq += o_eq;
+    }
+    for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
+        const unsigned c = classify(i), own = counts(c);
+        unsigned incl = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
         }
-        b_gt += (unsigned)__popc(gt);
-        b_eq += (unsigned)__popc(eq);
+        unsigned g = b_gt + ((incl - own) & 0xffffu), e = b_eq + ((incl - own) >> 16);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const bool above = (c >> u) & 1u, at = (c >> (16 + u)) & 1u;
+            if (above || (at && e < need)) {
+                const unsigned p = g + min(e, need);
+                idx[p] = t0 + i + u;
+                if (kept) kept[p] = t0 + i + u;
+                out[p] = score_of(s_key[i + u]);
+            }
+            g += above;
+            e += at;
+        }
+        const unsigned all = __shfl_sync(0xffffffffu, incl, 31);
+        b_gt += all & 0xffffu;
+        b_eq += all >> 16;
     }
     for (int p = q.n + rank * kSelThreads + tid; p < q.L; p += CS * kSelThreads) out[p] = 0.f;
     if (CS > 1) cluster_sync();  // no CTA leaves while another may read its counts
@@ -551,7 +579,7 @@ extern "C" pa_status_t pa_evict_tokens(
     while (cs < kMaxCluster && (max_context_len > kMaxSegment * cs ||
                                 (units * cs * 2 <= sms && max_context_len >= 4096 * 2 * cs)))
         cs *= 2;
-    const size_t smem = ((size_t)max_context_len + cs - 1) / cs * sizeof(float);
+    const size_t smem = ((((size_t)max_context_len + cs - 1) / cs + 3) & ~(size_t)3) * sizeof(float);
     cudaError_t e = cs == 1   ? launch_select<1>(P, (unsigned)units, smem, st)
                     : cs == 2 ? launch_select<2>(P, (unsigned)units, smem, st)
                     : cs == 4 ? launch_select<4>(P, (unsigned)units, smem, st)

@@ -166,3 +166,16 @@ def test_captured_into_a_graph_and_replayed():
         g.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, ref) and torch.equal(sc, want + want)
+
+
+@pytest.mark.parametrize("H,Hkv", [(2, 2), (12, 2)])
+def test_nan_stays_with_its_sequence_and_head(H, Hkv):
+    c = Cache([600, 90], Hkv, 64, torch.bfloat16, seed=11)
+    q = _q(2, H, 64, torch.bfloat16)
+    clean = torch.zeros(2, Hkv, 600, device=DEV)
+    pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, 600, 0.125, clean)
+    c.k[0][int(c.tables_host[0, 3]), 1, 5] = float("nan")  # token 53 of sequence 0, head 1
+    got = torch.zeros_like(clean)
+    pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, 600, 0.125, got)
+    assert bool(torch.isnan(got[0, 1, :600]).all())
+    assert torch.equal(got[0, 0], clean[0, 0]) and torch.equal(got[1], clean[1])
