@@ -9,7 +9,7 @@
 // A row without weight (no readable block, every logit -inf: L = 0) adds
 // nothing.  One thread owns a token's score, so the sum's order is fixed.
 //
-// A warp takes 512 tokens of one (sequence, KV head): it works out M and 1 / L
+// A warp takes 256 tokens of one (sequence, KV head): it works out M and 1 / L
 // of each head itself (a lane a piece), so the CTA has no barrier, and its
 // loads of the logits, 16 bytes a lane, are all in flight together.  The
 // first CTAs of the grid merge the sequences' partitions meanwhile (the same
@@ -20,6 +20,8 @@
 // reads.
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "pa_decode.cuh"
 #include "pa_decode_merge.cuh"
 #include "pa_launch.cuh"
@@ -27,86 +29,111 @@
 namespace pa {
 namespace {
 
-constexpr int kWarpTokens = 512;
+constexpr int kSteps = 2;  // 128 tokens each, four a lane
+constexpr int kWarpTokens = 128 * kSteps;
 constexpr int kWeightWarps = kMergeThreads / 32;
-constexpr int kMaxGroup = 8;
 
-// Tokens t0 .. t0 + 511 of (sequence s, KV head hk), by one warp.
-template <bool VEC>
+// Tokens t0 .. t0 + 255 of (sequence s, KV head hk), by one warp.  GM: the
+// group's heads, rounded up to 1, 2, 4 or 8.
+template <int GM>
 __device__ __forceinline__ void add_weights(const DecodeParams &P, float *__restrict__ scores,
                                             long long score_stride, int s, int hk, int t0,
-                                            int lane) {
+                                            bool vec, int lane) {
     const int L = P.context_lens[s], G = P.G;
     if (L <= 0 || L > P.max_context_len || t0 >= L) return;  // empty or invalid: nothing to add
     const size_t row0 = (size_t)s * P.num_heads + (size_t)hk * G;
     const int np = (L + P.part_tokens - 1) / P.part_tokens;
-    float M[kMaxGroup], inv[kMaxGroup];
+    const int n = min(kWarpTokens, L - t0);
+    // every load of the first 32 pieces and of the old scores in flight at once
+    float M[GM], inv[GM];
 #pragma unroll
-    for (int g = 0; g < kMaxGroup; ++g) {
-        M[g] = inv[g] = 0.f;
-        if (g >= G) continue;
-        const float *pm = P.part_m + (row0 + g) * P.max_parts;
-        const float *pl = P.part_l + (row0 + g) * P.max_parts;
-        float m = -INFINITY, l = 0.f;
-        for (int p = lane; p < np; p += 32) {
-            const float mp = pm[p], lp = pl[p];
-            const float mn = fmaxf(m, mp);
-            if (mn != -INFINITY) l = l * ex2(m - mn) + lp * ex2(mp - mn);
-            m = mn;
-        }
+    for (int g = 0; g < GM; ++g) {
+        const bool in = g < G && lane < np;
+        M[g] = in ? P.part_m[(row0 + g) * P.max_parts + lane] : -INFINITY;
+        inv[g] = in ? P.part_l[(row0 + g) * P.max_parts + lane] : 0.f;
+    }
+    float *sc = scores + ((long long)s * P.num_kv_heads + hk) * score_stride + t0;
+    float4 old[kSteps], w[kSteps];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            const float mo = __shfl_xor_sync(0xffffffffu, m, o);
-            const float lo = __shfl_xor_sync(0xffffffffu, l, o);
-            const float mn = fmaxf(m, mo);
-            if (mn != -INFINITY) l = l * ex2(m - mn) + lo * ex2(mo - mn);
-            m = mn;
+    for (int i = 0; i < kSteps; ++i) {
+        const int t = i * 128 + 4 * lane;
+        w[i] = old[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (vec && t + 4 <= n) {
+            old[i] = *reinterpret_cast<const float4 *>(sc + t);
+        } else {
+            if (t < n) old[i].x = sc[t];
+            if (t + 1 < n) old[i].y = sc[t + 1];
+            if (t + 2 < n) old[i].z = sc[t + 2];
+            if (t + 3 < n) old[i].w = sc[t + 3];
         }
-        M[g] = m == -INFINITY ? 0.f : m;
+    }
+    for (int p = lane + 32; p < np; p += 32) {  // contexts of many pieces
+#pragma unroll
+        for (int g = 0; g < GM; ++g) {
+            if (g >= G) continue;
+            const float mp = P.part_m[(row0 + g) * P.max_parts + p];
+            const float lp = P.part_l[(row0 + g) * P.max_parts + p];
+            const float mn = fmaxf(M[g], mp);
+            const float ms = mn == -INFINITY ? 0.f : mn;
+            inv[g] = inv[g] * ex2(M[g] - ms) + lp * ex2(mp - ms);
+            M[g] = mn;
+        }
+    }
+#pragma unroll
+    for (int g = 0; g < GM; ++g) {
+        float m = M[g];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = m == -INFINITY ? 0.f : m;
+        float l = inv[g] * ex2(M[g] - m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        M[g] = m;
         // an empty row weighs nothing; a NaN sum goes on to the weights
         inv[g] = l == 0.f ? 0.f : 1.f / l;
     }
+    // (the logits' rows reach a multiple of 16 tokens)
     const float *lg = P.logits + row0 * P.logit_stride + t0;
-    float *sc = scores + ((long long)s * P.num_kv_heads + hk) * score_stride + t0;
-    const int n = min(kWarpTokens, L - t0);
 #pragma unroll
-    for (int i = 0; i < kWarpTokens / 128; ++i) {
-        const int t = i * 128 + 4 * lane;
-        if (t >= n) break;
-        // (the logits' rows reach a multiple of 16 tokens)
-        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int g = 0; g < GM; ++g) {
+        if (g >= G) continue;
+        float4 x[kSteps];
 #pragma unroll
-        for (int g = 0; g < kMaxGroup; ++g) {
-            if (g >= G) break;
-            const float4 x = *reinterpret_cast<const float4 *>(lg + (size_t)g * P.logit_stride + t);
-            w.x = fmaf(ex2(x.x - M[g]), inv[g], w.x);
-            w.y = fmaf(ex2(x.y - M[g]), inv[g], w.y);
-            w.z = fmaf(ex2(x.z - M[g]), inv[g], w.z);
-            w.w = fmaf(ex2(x.w - M[g]), inv[g], w.w);
+        for (int i = 0; i < kSteps; ++i) {
+            const int t = i * 128 + 4 * lane;
+            if (t < n) x[i] = *reinterpret_cast<const float4 *>(lg + (size_t)g * P.logit_stride + t);
         }
-        if (VEC && t + 4 <= n) {
-            float4 o = *reinterpret_cast<float4 *>(sc + t);
-            o.x += w.x;
-            o.y += w.y;
-            o.z += w.z;
-            o.w += w.w;
+#pragma unroll
+        for (int i = 0; i < kSteps; ++i) {
+            w[i].x = fmaf(ex2(x[i].x - M[g]), inv[g], w[i].x);
+            w[i].y = fmaf(ex2(x[i].y - M[g]), inv[g], w[i].y);
+            w[i].z = fmaf(ex2(x[i].z - M[g]), inv[g], w[i].z);
+            w[i].w = fmaf(ex2(x[i].w - M[g]), inv[g], w[i].w);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+        const int t = i * 128 + 4 * lane;
+        const float4 o = make_float4(old[i].x + w[i].x, old[i].y + w[i].y, old[i].z + w[i].z,
+                                     old[i].w + w[i].w);
+        if (vec && t + 4 <= n) {
             *reinterpret_cast<float4 *>(sc + t) = o;
         } else {
-            sc[t] += w.x;
-            if (t + 1 < n) sc[t + 1] += w.y;
-            if (t + 2 < n) sc[t + 2] += w.z;
-            if (t + 3 < n) sc[t + 3] += w.w;
+            if (t < n) sc[t] = o.x;
+            if (t + 1 < n) sc[t + 1] = o.y;
+            if (t + 2 < n) sc[t + 2] = o.z;
+            if (t + 3 < n) sc[t + 3] = o.w;
         }
     }
 }
 
 // CTAs 0 .. merges - 1: the merge of (sequence, HPC heads); the others: warp
-// tasks (sequence, KV head, 512-token range), ranges fastest.
-template <int D, int HPC, bool VEC>
+// tasks (sequence, KV head, 256-token range), ranges fastest.
+template <int D, int HPC, int GM>
 __global__ void __launch_bounds__(kMergeThreads)
     decode_weights_kernel(const __grid_constant__ DecodeParams P, float *__restrict__ scores,
                           long long score_stride, int merges, int head_groups, int ranges,
-                          unsigned tasks) {
+                          unsigned tasks, bool vec) {
     pdl_trigger();
     pdl_wait();  // the logits and the pieces' states
     if ((int)blockIdx.x < merges) {
@@ -116,9 +143,9 @@ __global__ void __launch_bounds__(kMergeThreads)
     const unsigned task = (blockIdx.x - (unsigned)merges) * kWeightWarps + threadIdx.x / 32;
     if (task >= tasks) return;
     const unsigned unit = task / (unsigned)ranges;
-    add_weights<VEC>(P, scores, score_stride, (int)(unit / (unsigned)P.num_kv_heads),
+    add_weights<GM>(P, scores, score_stride, (int)(unit / (unsigned)P.num_kv_heads),
                      (int)(unit % (unsigned)P.num_kv_heads),
-                     (int)(task - unit * (unsigned)ranges) * kWarpTokens, threadIdx.x & 31);
+                     (int)(task - unit * (unsigned)ranges) * kWarpTokens, vec, threadIdx.x & 31);
 }
 
 }  // namespace
@@ -127,10 +154,8 @@ pa_status_t launch_decode_weights(const DecodeParams &P, float *scores, long lon
                                   bool merge, cudaStream_t stream) {
     const long long ranges = (P.max_context_len + kWarpTokens - 1) / kWarpTokens;
     const long long tasks = (long long)P.num_seqs * P.num_kv_heads * ranges;
-    // heads a merging CTA, as in the merge kernel's launch
-    int hpc = 1;
-    while (hpc < 8 && (long long)P.num_seqs * ((P.num_heads + hpc - 1) / hpc) > kMergeMaxCtas)
-        hpc *= 2;
+    // heads a merging CTA: several when there are many (see merge_heads)
+    const int hpc = (long long)P.num_seqs * P.num_heads > kMergeMaxCtas ? 4 : 1;
     const int groups = (P.num_heads + hpc - 1) / hpc;
     const long long merges = merge ? (long long)P.num_seqs * groups : 0;
     const long long ctas = merges + (tasks + kWeightWarps - 1) / kWeightWarps;
@@ -140,17 +165,23 @@ pa_status_t launch_decode_weights(const DecodeParams &P, float *scores, long lon
     cudaError_t e = cudaErrorInvalidValue;
     auto go = [&](auto kern) {
         e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kMergeThreads), 0, stream, P, scores,
-                       score_stride, (int)merges, groups, (int)ranges, (unsigned)tasks);
+                       score_stride, (int)merges, groups, (int)ranges, (unsigned)tasks, vec);
     };
-#define PA_WEIGHTS(D, H)                             \
-    if (P.head_dim == D && hpc == H) {               \
-        if (vec) go(decode_weights_kernel<D, H, true>); \
-        else go(decode_weights_kernel<D, H, false>); \
-    }
-    PA_WEIGHTS(64, 1) PA_WEIGHTS(64, 2) PA_WEIGHTS(64, 4) PA_WEIGHTS(64, 8)
-    PA_WEIGHTS(128, 1) PA_WEIGHTS(128, 2) PA_WEIGHTS(128, 4) PA_WEIGHTS(128, 8)
-    PA_WEIGHTS(256, 1) PA_WEIGHTS(256, 2) PA_WEIGHTS(256, 4) PA_WEIGHTS(256, 8)
-#undef PA_WEIGHTS
+    const int gm = P.G == 1 ? 1 : P.G == 2 ? 2 : P.G <= 4 ? 4 : 8;
+    auto group = [&](auto d, auto h) {
+        constexpr int D = decltype(d)::value, H = decltype(h)::value;
+        if (gm == 1) go(decode_weights_kernel<D, H, 1>);
+        else if (gm == 2) go(decode_weights_kernel<D, H, 2>);
+        else if (gm == 4) go(decode_weights_kernel<D, H, 4>);
+        else go(decode_weights_kernel<D, H, 8>);
+    };
+    auto dim = [&](auto d) {
+        if (hpc == 1) group(d, std::integral_constant<int, 1>());
+        else group(d, std::integral_constant<int, 4>());
+    };
+    if (P.head_dim == 64) dim(std::integral_constant<int, 64>());
+    else if (P.head_dim == 128) dim(std::integral_constant<int, 128>());
+    else dim(std::integral_constant<int, 256>());
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
