@@ -19,7 +19,7 @@
 // kernel is persistent, one CTA per SM; items are numbered from the first keys
 // on (with whole prompts those see the most queries) and dealt out forth and
 // back, so every CTA's share is about as heavy and no list is needed.
-// Twelve warps:
+// Twenty warps:
 //   * warp 0 (producer): the item's K tiles into one of two K buffers, block
 //     by block (tiled bulk copies, TMA), then its query tiles into a ring.  It
 //     runs ahead into the next item;
@@ -28,11 +28,18 @@
 //     each; causal: tiles whose rows all lie before the keys are left out;
 //   * warp 2 allocates tensor memory, warp 3 is idle (the lanes a warp may
 //     read go by its number modulo 4);
-//   * warps 4..7 and 8..11 (key tile 0 and 1): one key a thread.  Each stages
-//     the rows' lse (base 2) in shared memory, loads S from tensor memory
-//     32 columns at a time, and sums 2^(x scale log2 e - lse) over the columns
-//     it may see -- a range [lo, hi) of the tile, from its key's position.
-// Sums are fp32 in two levels: the 32-column steps of a tile, then tiles.
+//   * warps 4..19: four groups of four, group (t, b) for the products of key
+//     tile t in buffer b, one key a thread.  Each stages the rows' lse (base
+//     2, negated) in shared memory, loads S from tensor memory 16 columns at a
+//     time, and sums 2^(x scale log2 e - lse) over the columns it may see -- a
+//     range [lo, hi) of the tile, from its key's position.  At the item's end
+//     group (t, 1) hands its sums to group (t, 0), which adds them and writes.
+// Sums are fp32 in levels: the columns of a tile in pairs of chains, tiles,
+// groups.
+//
+// A wait that gives up sets the abort flag; the groups then go through the
+// rest of their products without waiting or writing, so that their named
+// barriers always meet.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -55,7 +62,8 @@ constexpr int kKeys = 128;    // keys of a tile (tensor-memory lanes)
 constexpr int kTiles = 2;     // key tiles of an item
 constexpr int kItemKeys = kKeys * kTiles;
 constexpr int kMaxCols = 128; // rows of a query tile
-constexpr int kThreadsS = 384;
+constexpr int kGroups = 4;    // of four warps: key tile and buffer
+constexpr int kThreadsS = 128 + 128 * kGroups;
 constexpr uint32_t kTmemColsS = 512;  // S of tile t, buffer b at 128 (2 t + b)
 constexpr uint32_t kKSlice = kKeys * 128;  // bytes of a 64-element slice of a K tile
 
@@ -85,12 +93,11 @@ struct SLayout {
     static constexpr size_t k_off = 0;
     static constexpr size_t q_off = 2 * kbuf;
     static constexpr size_t tiles = q_off + RQ * qstage;
-    // before the tiles: lse [tile][2][128], its dead-row flags [tile][2][4], barriers
-    static constexpr size_t dead_off = kTiles * 2 * kMaxCols * 4;
-    static constexpr size_t bar_off = dead_off + kTiles * 2 * 4 * 4;
-    // k_full[2], k_free[2], q_full[RQ], q_free[RQ], s_full[2][2], s_free[2][2],
-    // staged[2], done
-    static constexpr int kBars = 4 + 2 * RQ + 8 + 2 + 1;
+    // before the tiles: lse [group][128], its dead-row flags [group][4], barriers
+    static constexpr size_t dead_off = kGroups * kMaxCols * 4;
+    static constexpr size_t bar_off = dead_off + kGroups * 4 * 4;
+    // k_full[2], k_free[2], q_full[RQ], q_free[RQ], s_full[2][2], s_free[2][2], done
+    static constexpr int kBars = 4 + 2 * RQ + 8 + 1;
     static constexpr size_t tmem_off = bar_off + 8 * kBars;
     static constexpr size_t flag_off = tmem_off + 4;
     static constexpr size_t small = (flag_off + 4 + 1023) / 1024 * 1024;
@@ -99,7 +106,7 @@ struct SLayout {
 };
 
 struct SBars {
-    uint64_t *k_full, *k_free, *q_full, *q_free, *s_full, *s_free, *staged, *done;
+    uint64_t *k_full, *k_free, *q_full, *q_free, *s_full, *s_free, *done;
 };
 
 // One work item, worked out by every role for itself.
@@ -136,11 +143,11 @@ __device__ __forceinline__ unsigned item_id(unsigned r) {
     return r * gridDim.x + ((r & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
 }
 
-// Whether key tile t has a product with token tile tt: it has keys, and the
-// tile's last token sees the first of them.
-__device__ __forceinline__ bool tile_on(const ScoreParams &P, const SItem &it, int t, int tt) {
+// First token tile that key tile t has a product with (the tile that holds the
+// first token to see the tile's first key); tt1 if it has no keys.
+__device__ __forceinline__ int first_tile(const ScoreParams &P, const SItem &it, int t) {
     const int key = it.k0 + t * kKeys;
-    return key < it.L && it.c + min(it.n, (tt + 1) << P.lg_nq) - 1 >= key;
+    return key < it.L ? max(0, key - it.c) >> P.lg_nq : it.tt1;
 }
 
 // ---------------------------------------------------------------------------
@@ -258,6 +265,7 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, uint32_t fmt
         const SItem it = score_item(P, item_id(r));
         if (!it.run) continue;
         const int kb = kc & 1;
+        const int first[kTiles] = {first_tile(P, it, 0), first_tile(P, it, 1)};
         ok = mbar_wait(&B.k_full[kb], (uint32_t)(kc >> 1) & 1u, abort_flag);
         for (int tt = it.tt0; ok && tt < it.tt1; ++tt)
             for (int hg = 0; ok && hg < P.head_groups; ++hg, ++qc) {
@@ -267,7 +275,7 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, uint32_t fmt
                 const uint32_t qt = aq + (uint32_t)(st * L::qstage);
 #pragma unroll
                 for (int t = 0; t < kTiles; ++t) {
-                    if (!ok || !tile_on(P, it, t, tt)) continue;
+                    if (!ok || tt < first[t]) continue;
                     const int b = sc[t] & 1;
                     ok = mbar_wait(&B.s_free[2 * t + b], (uint32_t)((sc[t] >> 1) & 1) ^ 1u, abort_flag);
                     if (!ok) break;
@@ -297,156 +305,202 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, uint32_t fmt
 }
 
 // ---------------------------------------------------------------------------
-// warps 4..11: weights and sums, key tile t, one key a thread
+// warps 4..19: weights and sums of group (t, b), one key a thread
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
-    tmem_ld16(taddr, *reinterpret_cast<uint32_t(*)[16]>(&r[0]));
-    tmem_ld16(taddr + 16u, *reinterpret_cast<uint32_t(*)[16]>(&r[16]));
+// Two fp32 values in a 64-bit register: one instruction for both.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
-// 32 columns from column c on: the sum of the weights.  ALL: every column is
-// visible; else those in [lo, hi) whose row has a weight at all (a row
-// without has lse = +inf here).
+// One product of this thread's key: the weights of `cols` columns of tensor
+// memory (a multiple of 32), 16 at a time, in four chains of pairs.  ALL: every
+// column is visible; else those in [lo, hi) whose row has a weight at all (a
+// row without has nl = -inf).  nl: the rows' negated lse.  The buffer is given
+// back through `bar` once all of it has been loaded.
 template <bool ALL>
-__device__ __forceinline__ float sum32(const uint32_t (&u)[32], const float *lse, int c, int lo,
-                                       int hi, float sc) {
-    float a[8];
+__device__ __forceinline__ float sum_product(uint32_t taddr, int cols, const float *nl, int lo,
+                                             int hi, uint64_t sc2, uint64_t *bar) {
+    uint64_t a[4] = {0ull, 0ull, 0ull, 0ull};
+    auto add = [&](const uint32_t (&u)[16], int c) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) a[i] = 0.f;
+        for (int i = 0; i < 16; i += 4) {
+            const float4 l4 = *reinterpret_cast<const float4 *>(nl + c + i);
+            const float l[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        const float4 l4 = *reinterpret_cast<const float4 *>(lse + c + i);
-        const float l[4] = {l4.x, l4.y, l4.z, l4.w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const float p = ex2(fmaf(__uint_as_float(u[i + k]), sc, -l[k]));
-            const int col = c + i + k;
-            a[(i + k) % 8] += ALL || (col >= lo && col < hi && l[k] != INFINITY) ? p : 0.f;
+            for (int k = 0; k < 4; k += 2) {
+                const float2 x =
+                    unpair(fma2(pair(__uint_as_float(u[i + k]), __uint_as_float(u[i + k + 1])),
+                                sc2, pair(l[k], l[k + 1])));
+                float p0 = ex2(x.x), p1 = ex2(x.y);
+                if (!ALL) {
+                    const int col = c + i + k;
+                    if (col < lo || col >= hi || l[k] == -INFINITY) p0 = 0.f;
+                    if (col + 1 < lo || col + 1 >= hi || l[k + 1] == -INFINITY) p1 = 0.f;
+                }
+                a[(i + k) / 2 % 4] = add2(a[(i + k) / 2 % 4], pair(p0, p1));
+            }
         }
+    };
+    uint32_t ua[16], ub[16];
+    tmem_ld16(taddr, ua);
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 32) {
+        tmem_wait_ld();
+        tmem_ld16(taddr + (uint32_t)(c + 16), ub);
+        add(ua, c);
+        tmem_wait_ld();
+        if (c + 32 < cols) {
+            tmem_ld16(taddr + (uint32_t)(c + 32), ua);
+        } else {  // the buffer may take the next product
+            tc_fence_before();
+            mbar_arrive(bar);
+        }
+        add(ub, c + 16);
     }
-    return ((a[0] + a[1]) + (a[2] + a[3])) + ((a[4] + a[5]) + (a[6] + a[7]));
+    const float2 v = unpair(add2(add2(a[0], a[1]), add2(a[2], a[3])));
+    return v.x + v.y;
 }
 
-__device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, float *s_lse,
+__device__ __forceinline__ void bar_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(int id, int threads) {
+    asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+
+__device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int b, float *s_lse,
                                                volatile int *s_dead, uint32_t tmem,
                                                const SBars &B, volatile int *abort_flag, int wq,
                                                int lane) {
     const int rk = 32 * wq + lane;  // this thread's key of the tile, and the row it stages
     const int cols = 1 << (P.lg_nh + P.lg_nq);
-    const uint32_t tm = tmem + (uint32_t)(256 * t) + ((uint32_t)(32 * wq) << 16);
-    // the stream of this tile's products: item round r, token tile tt, head group hg
-    struct Pos {
-        unsigned r;
-        SItem it;
-        int tt, hg;
-        bool live;
+    const uint32_t tb = tmem + (uint32_t)(128 * (2 * t + b)) + ((uint32_t)(32 * wq) << 16);
+    float *nl = s_lse + (2 * t + b) * kMaxCols;
+    float *other = s_lse + (2 * t + 1) * kMaxCols;  // where group (t, 1) leaves its sums
+    volatile int *dead = s_dead + (2 * t + b) * 4;
+    const int bar_own = 1 + 2 * t + b, bar_full = 5 + t, bar_free = 7 + t;
+    const uint64_t sc2 = pair(P.scale_log2, P.scale_log2);
+    // staged row rk of a product (token tile tt, head group hg): its negated lse in base 2, -inf
+    // for no such row or no weight
+    auto row_lse = [&](const SItem &it, int tt, int hg) {
+        const int i = (tt << P.lg_nq) + (rk >> P.lg_nh);
+        if (rk >= cols || tt >= it.tt1 || i >= it.n) return -INFINITY;
+        const int h = it.hk * P.G + (hg << P.lg_nh) + (rk & ((1 << P.lg_nh) - 1));
+        const float l = __ldg(&P.lse[(size_t)(it.tok0 + i) * P.num_heads + h]);
+        return l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
     };
-    auto settle = [&](Pos &p) {  // to the first product at or after (r, tt, hg)
-        for (;;) {
-            if (p.it.run) {
-                while (p.tt < p.it.tt1 && !tile_on(P, p.it, t, p.tt)) ++p.tt;
-                if (p.tt < p.it.tt1) return;
-            }
-            const unsigned id = item_id(++p.r);
-            if (id >= P.num_items) {
-                p.live = false;
-                return;
-            }
-            p.it = score_item(P, id);
-            p.tt = p.it.tt0;
-            p.hg = 0;
+    // the next item with keys for this tile, from round r on
+    auto next_item = [&](unsigned &r, SItem &it) {
+        for (; item_id(r) < P.num_items; ++r) {
+            it = score_item(P, item_id(r));
+            if (it.run && it.k0 + t * kKeys < it.L) return true;
         }
+        return false;
     };
-    auto row_lse = [&](const Pos &p) {  // staged row's lse, base 2; +inf: no such row, or no weight
-        const int i = (p.tt << P.lg_nq) + (rk >> P.lg_nh);
-        if (!p.live || rk >= cols || i >= p.it.n) return INFINITY;
-        const int h = p.it.hk * P.G + (p.hg << P.lg_nh) + (rk & ((1 << P.lg_nh) - 1));
-        const float l = __ldg(&P.lse[(size_t)(p.it.tok0 + i) * P.num_heads + h]);
-        return l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
-    };
-    Pos cur;
-    cur.r = 0;
-    cur.live = item_id(0) < P.num_items;
-    if (!cur.live) return;
-    cur.it = score_item(P, item_id(0));
-    cur.tt = cur.it.tt0;
-    cur.hg = 0;
-    settle(cur);
-    float next_lse = row_lse(cur);
-    int count = 0;  // products taken
+    unsigned r = 0;
+    SItem nx;
+    bool live = next_item(r, nx);
+    int cnt = 0;          // products of the tile before this item
+    int taken = 0;        // products of this group
+    bool gave = false;    // group (t, 1): sums handed over and not yet taken
     bool ok = true;
-    while (cur.live) {
-        // a new item: its score, if this key takes part
-        const SItem it = cur.it;
+    float next = 0.f;     // the row's lse of this group's next product
+    float old = 0.f;      // the key's score before (group (t, 0))
+    int blk = -1;         // and its block
+    int tt = 0, hg = 0;   // this group's next product
+    auto step = [&](int by) {
+        for (hg += by; hg >= P.head_groups; hg -= P.head_groups) ++tt;
+    };
+    auto prefetch = [&]() {  // of item nx, whose products start at number cnt
+        tt = first_tile(P, nx, t);
+        hg = 0;
+        step((cnt ^ b) & 1);
+        next = row_lse(nx, tt, hg);
+        const int key = nx.k0 + t * kKeys + rk;
+        if (b == 0 && key < nx.L) {
+            blk = __ldg(&P.block_tables[(size_t)nx.s * P.max_blocks_per_seq + (key >> P.block_shift)]);
+            old = P.scores[((long long)nx.s * P.num_kv_heads + nx.hk) * P.score_stride + key];
+        }
+    };
+    if (live) prefetch();
+    while (live) {
+        const SItem it = nx;
+        const int first = first_tile(P, it, t), np = (it.tt1 - first) * P.head_groups;
         const int key = it.k0 + t * kKeys + rk;
-        float *dst = nullptr;
-        float old = 0.f, acc = 0.f;
-        if (key < it.L) {
-            const int blk = __ldg(&P.block_tables[(size_t)it.s * P.max_blocks_per_seq + (key >> P.block_shift)]);
-            if (blk >= 0 && blk < P.num_blocks) {
-                dst = P.scores + ((long long)it.s * P.num_kv_heads + it.hk) * P.score_stride + key;
-                old = *dst;
+        const float old_now = old;
+        const int blk_now = blk;
+        float acc = 0.f;
+        int p = (cnt ^ b) & 1;
+        cnt += np;
+        ++r;
+        live = next_item(r, nx);
+        for (;; p += 2) {
+            const bool last = p + 2 >= np;  // this group's last product of the item, or none at all
+            const float mine = next;
+            const int tok = tt << P.lg_nq;  // the product's first token
+            if (last) {
+                if (live) prefetch();
+                if (p >= np) break;
+            } else {
+                step(2);
+                next = row_lse(it, tt, hg);  // arrives during this product
             }
-        }
-        for (;;) {
-            const int b = count & 1;
-            float *lse = s_lse + (t * 2 + b) * kMaxCols;
-            volatile int *dead = s_dead + (t * 2 + b) * 4;
-            // stage this product's lse; buffer b was last read two products ago
-            if (rk < cols) lse[rk] = next_lse;
-            const bool any_dead = __any_sync(0xffffffffu, rk < cols && next_lse == INFINITY);
+            if (gave) {  // the sums lie where the lse goes
+                bar_sync(bar_free, 256);
+                gave = false;
+            }
+            bar_sync(bar_own, 128);  // every thread has read the previous product's lse
+            if (rk < cols) nl[rk] = mine;
+            const bool any_dead = __any_sync(0xffffffffu, rk < cols && mine == -INFINITY);
             if (lane == 0) dead[wq] = any_dead;
-            mbar_arrive(&B.staged[t]);
-            const int tt = cur.tt;
-            if (++cur.hg == P.head_groups) {
-                cur.hg = 0;
-                ++cur.tt;
-            }
-            const unsigned r = cur.r;
-            settle(cur);
-            next_lse = row_lse(cur);  // arrives during this product
-            ok = mbar_wait(&B.staged[t], (uint32_t)count & 1u, abort_flag) &&
-                 mbar_wait(&B.s_full[2 * t + b], (uint32_t)(count >> 1) & 1u, abort_flag);
+            bar_sync(bar_own, 128);
+            const int done = taken++;
+            if (ok) ok = mbar_wait(&B.s_full[2 * t + b], (uint32_t)done & 1u, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) break;
-            tc_fence_after();
-            const int first = key - it.c - (tt << P.lg_nq);  // first token of the tile that sees the key
-            const int lo = max(0, first) << P.lg_nh;
-            const int hi = (it.n - (tt << P.lg_nq)) << P.lg_nh;
-            const bool all = __all_sync(0xffffffffu, lo == 0) && hi >= cols &&
-                             !(dead[0] | dead[1] | dead[2] | dead[3]);
-            const uint32_t tb = tm + (uint32_t)(128 * b);
-            uint32_t ua[32], ub[32];
-            float sum = 0.f;
-            tmem_ld32(tb, ua);
-            for (int c = 0; c < cols; c += 64) {
-                tmem_wait_ld();
-                const bool more = c + 32 < cols;
-                if (more) tmem_ld32(tb + (uint32_t)(c + 32), ub);
-                if (!more) {
-                    tc_fence_before();
-                    mbar_arrive(&B.s_free[2 * t + b]);
-                }
-                sum += all ? sum32<true>(ua, lse, c, lo, hi, P.scale_log2)
-                           : sum32<false>(ua, lse, c, lo, hi, P.scale_log2);
-                if (!more) break;
-                tmem_wait_ld();
-                const bool again = c + 64 < cols;
-                if (again) {
-                    tmem_ld32(tb + (uint32_t)(c + 64), ua);
-                } else {
-                    tc_fence_before();
-                    mbar_arrive(&B.s_free[2 * t + b]);
-                }
-                sum += all ? sum32<true>(ub, lse, c + 32, lo, hi, P.scale_log2)
-                           : sum32<false>(ub, lse, c + 32, lo, hi, P.scale_log2);
+            if (!ok) *abort_flag = 1;  // at once: no sum that lacks this product is written
+            if (ok) {
+                tc_fence_after();
+                const int lo = max(0, key - it.c - tok) << P.lg_nh;
+                const int hi = (it.n - tok) << P.lg_nh;
+                const bool all = __all_sync(0xffffffffu, lo == 0) && hi >= cols &&
+                                 !(dead[0] | dead[1] | dead[2] | dead[3]);
+                acc += all ? sum_product<true>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b])
+                           : sum_product<false>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b]);
             }
-            acc += sum;
-            ++count;
-            if (!cur.live || cur.r != r) break;
+            if (last) break;
         }
-        if (!ok) break;
-        if (dst) *dst = old + acc;
+        // the item's sums
+        if (b == 1) {
+            if (gave) bar_sync(bar_free, 256);
+            bar_sync(bar_own, 128);  // every thread has read the last product's lse
+            other[rk] = acc;
+            bar_arrive(bar_full, 256);
+            gave = true;
+        } else {
+            bar_sync(bar_full, 256);
+            acc += other[rk];
+            bar_arrive(bar_free, 256);
+            if (ok && !*abort_flag && key < it.L && blk_now >= 0 && blk_now < P.num_blocks)
+                P.scores[((long long)it.s * P.num_kv_heads + it.hk) * P.score_stride + key] =
+                    old_now + acc;
+        }
     }
     if (!ok) {
         *abort_flag = 1;
@@ -481,15 +535,13 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     B.q_free = B.q_full + RQ;
     B.s_full = B.q_free + RQ;
     B.s_free = B.s_full + 4;
-    B.staged = B.s_free + 4;
-    B.done = B.staged + 2;
+    B.done = B.s_free + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         prefetch_tmap(&P.tmap_q);
         prefetch_tmap(&P.tmap_k);
         for (int b = 0; b < L::kBars; ++b) mbar_init(&bars[b], 1);
         for (int b = 0; b < 4; ++b) mbar_init(&B.s_free[b], kKeys);
-        for (int b = 0; b < 2; ++b) mbar_init(&B.staged[b], kKeys);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -510,7 +562,8 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         }
         __syncwarp();
     } else if (warp >= 4) {
-        run_score_sums(P, (warp - 4) >> 2, s_lse, s_dead, tmem, B, abort_flag, warp & 3, lane);
+        run_score_sums(P, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, tmem, B, abort_flag,
+                       warp & 3, lane);
     }
     tc_fence_before();
     __syncthreads();
