@@ -20,26 +20,30 @@
 // on (with whole prompts those see the most queries) and dealt out forth and
 // back, so every CTA's share is about as heavy and no list is needed.
 // Twenty warps:
-//   * warp 0 (producer): the item's K tiles into one of two K buffers, block
-//     by block (tiled bulk copies, TMA), then its query tiles into a ring.  It
-//     runs ahead into the next item;
-//   * warp 1 (one thread): S_t = K_t Q^T (M = 128 keys, N = the tile's rows,
-//     K = head_dim) for both key tiles into one of two tensor-memory buffers
-//     each; causal: tiles whose rows all lie before the keys are left out;
-//   * warp 2 allocates tensor memory, warp 3 is idle (the lanes a warp may
-//     read go by its number modulo 4);
+//   * warp 0 (producer): K tiles into a ring of 128-key slots, block by block
+//     (tiled bulk copies, TMA), and query tiles into another; it runs ahead
+//     into the next item;
+//   * warps 1 and 2 (one thread each): S_t = K_t Q^T (M = 128 keys, N = the
+//     tile's rows, K = head_dim) for key tile 0 and 1 into one of two
+//     tensor-memory buffers each (two issuers: the waits of one fall into the
+//     other's products); causal: a key tile starts with the query tile that
+//     holds the first token to see its first key, so the second tile's copy
+//     has time while the first one works alone.  Warp 1 allocates tensor
+//     memory;
+//   * warp 3 brings the rows' lse (base 2, negated) into a ring beside the
+//     query tiles', with a flag for tiles that hold rows without a weight;
 //   * warps 4..19: four groups of four, group (t, b) for the products of key
-//     tile t in buffer b, one key a thread.  Each stages the rows' lse (base
-//     2, negated) in shared memory, loads S from tensor memory 16 columns at a
-//     time, and sums 2^(x scale log2 e - lse) over the columns it may see -- a
+//     tile t in buffer b, one key a thread (the lanes a warp may read go by
+//     its number modulo 4).  Each loads S from tensor memory 16 columns at a
+//     time and sums 2^(x scale log2 e - lse) over the columns it may see -- a
 //     range [lo, hi) of the tile, from its key's position.  At the item's end
 //     group (t, 1) hands its sums to group (t, 0), which adds them and writes.
 // Sums are fp32 in levels: the columns of a tile in pairs of chains, tiles,
 // groups.
 //
 // A wait that gives up sets the abort flag; the groups then go through the
-// rest of their products without waiting or writing, so that their named
-// barriers always meet.
+// rest of their items without waiting or writing, so that their named barriers
+// always meet.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -66,6 +70,9 @@ constexpr int kGroups = 4;    // of four warps: key tile and buffer
 constexpr int kThreadsS = 128 + 128 * kGroups;
 constexpr uint32_t kTmemColsS = 512;  // S of tile t, buffer b at 128 (2 t + b)
 constexpr uint32_t kKSlice = kKeys * 128;  // bytes of a 64-element slice of a K tile
+constexpr int kMaxRing = 8;   // slots of the K and the query ring at most
+constexpr int kLseRing = 4;   // slots of the lse ring
+constexpr uint32_t kTileBytes = 6 * 32768;  // shared memory of both tile rings
 
 struct ScoreParams {
     CUtensorMap tmap_q;  // query as [head_dim/64][tokens][heads][64], box NQ x NH rows
@@ -78,35 +85,44 @@ struct ScoreParams {
     int max_query_len, max_context_len, num_seqs, num_tokens, num_heads, num_kv_heads, G;
     int lg_nh, lg_nq;     // heads and tokens of a query tile
     int head_groups;      // G / NH
+    int rk, rq;           // slots of the K and the query ring
     unsigned num_items;   // 256-key ranges x num_seqs x num_kv_heads
     float scale_log2;
     unsigned int *err;
 };
 
-template <int D>
+// Shared memory: lse [slot][128], its flags [slot], the sums handed over
+// [tile][128], barriers; then, 1024-byte aligned, the K ring of rk tiles
+// [slice][128 keys][64] and the query ring of rq tiles [slice][rows][64].
 struct SLayout {
-    static constexpr int KB = D / 64;
-    static constexpr int RQ = D == 64 ? 6 : 3;                       // query stages
-    static constexpr size_t ktile = (size_t)KB * kKSlice;            // [slice][128 keys][64]
-    static constexpr size_t kbuf = kTiles * ktile;
-    static constexpr size_t qstage = (size_t)KB * kMaxCols * 128;    // [slice][rows][64]
-    static constexpr size_t k_off = 0;
-    static constexpr size_t q_off = 2 * kbuf;
-    static constexpr size_t tiles = q_off + RQ * qstage;
-    // before the tiles: lse [group][128], its dead-row flags [group][4], barriers
-    static constexpr size_t dead_off = kGroups * kMaxCols * 4;
-    static constexpr size_t bar_off = dead_off + kGroups * 4 * 4;
-    // k_full[2], k_free[2], q_full[RQ], q_free[RQ], s_full[2][2], s_free[2][2], done
-    static constexpr int kBars = 4 + 2 * RQ + 8 + 1;
+    static constexpr size_t dead_off = kLseRing * kMaxCols * 4;
+    static constexpr size_t part_off = dead_off + kLseRing * 4;
+    static constexpr size_t bar_off = part_off + kTiles * kKeys * 4;
+    // k_full, k_free, q_full, q_free [kMaxRing], l_full, l_free [kLseRing],
+    // s_full[2][2], s_free[2][2], done[2]
+    static constexpr int kBars = 4 * kMaxRing + 2 * kLseRing + 8 + 2;
     static constexpr size_t tmem_off = bar_off + 8 * kBars;
     static constexpr size_t flag_off = tmem_off + 4;
     static constexpr size_t small = (flag_off + 4 + 1023) / 1024 * 1024;
-    static constexpr size_t bytes = small + tiles;
+    static constexpr size_t bytes = small + kTileBytes;
+    static_assert(bar_off % 8 == 0, "barrier alignment");
     static_assert(bytes <= 232448, "dynamic shared memory of one CTA");
 };
 
 struct SBars {
-    uint64_t *k_full, *k_free, *q_full, *q_free, *s_full, *s_free, *done;
+    uint64_t *k_full, *k_free, *q_full, *q_free, *l_full, *l_free, *s_full, *s_free, *done;
+};
+
+// A place in a ring: slot and the parity of its current phase.
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next(int slots) {
+        if (++slot == slots) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
 };
 
 // One work item, worked out by every role for itself.
@@ -157,10 +173,10 @@ template <int D>
 __device__ __forceinline__ void run_score_producer(const ScoreParams &P, unsigned char *sk,
                                                    unsigned char *sq, const SBars &B,
                                                    volatile int *abort_flag, int lane) {
-    using L = SLayout<D>;
-    constexpr int KB = L::KB, RQ = L::RQ;
+    constexpr int KB = D / 64;
+    constexpr uint32_t ktile = KB * kKSlice;
     const int lg_tbr = min(P.block_shift, 6);  // a copy: one block's share, 8 .. 64 keys
-    const int units = kItemKeys >> lg_tbr;     // 4 .. 32: a lane each
+    const int units = kItemKeys >> lg_tbr;     // of an item, 4 .. 32: a lane each
     const int cols = 1 << (P.lg_nh + P.lg_nq);
     const uint32_t q_bytes = (uint32_t)cols * 128u * KB;
     const uint64_t policy = l2_evict_first_policy();
@@ -171,7 +187,8 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, unsigne
                    ? __ldg(&P.block_tables[(size_t)it.s * P.max_blocks_per_seq + (tok >> P.block_shift)])
                    : -1;
     };
-    int kc = 0, qc = 0;  // K buffers and query stages armed
+    Ring kr, qr;
+    int kn = 0, qn = 0;  // slots armed so far
     bool ok = true;
     SItem it, nx;
     int e = -1, en = -1;
@@ -190,118 +207,189 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, unsigne
             atomicOr(P.err, PA_ERRBIT_CONTEXT_LEN);
         if (!it.run) continue;
         const int tok = it.k0 + (lane << lg_tbr);
+        const int row = lane << lg_tbr;  // of the item's 256
         const bool use = lane < units && tok < it.L;
         const bool bad = use && (e < 0 || e >= P.num_blocks);
         const unsigned good = __ballot_sync(0xffffffffu, use && !bad);
         if (__any_sync(0xffffffffu, bad) && lane == 0 && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
-        const int kb = kc & 1;
-        if (lane == 0) ok = mbar_wait(&B.k_free[kb], (uint32_t)((kc >> 1) & 1) ^ 1u, abort_flag);
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        if (!ok) break;
-        if (lane == 0)
-            mbar_arrive_expect_tx(&B.k_full[kb], ((uint32_t)__popc(good) << lg_tbr) * 128u * KB);
-        __syncwarp();
-        if (use && !bad) {
-            const int row = lane << lg_tbr;  // of the item's 256
-            unsigned char *dst = sk + (size_t)kb * L::kbuf + (size_t)(row >> 7) * L::ktile +
-                                 (size_t)(row & 127) * 128;
-            const int y = ((e * P.num_kv_heads + it.hk) << P.block_shift) +
-                          (tok & ((1 << P.block_shift) - 1));
+        // lanes whose units belong to key tile 0
+        const unsigned low = units >= 32 ? 0xffffu : (1u << (units / 2)) - 1u;
+        auto load_k = [&](int t) {
+            if (lane == 0) ok = mbar_wait(&B.k_free[kr.slot], kr.phase ^ 1u, abort_flag);
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+            if (!ok) return;
+            if (lane == 0)
+                mbar_arrive_expect_tx(&B.k_full[kr.slot],
+                                      ((uint32_t)__popc(good & (t ? ~low : low)) << lg_tbr) * 128u * KB);
+            __syncwarp();
+            if (use && !bad && (row >> 7) == t) {
+                unsigned char *dst = sk + (size_t)kr.slot * ktile + (size_t)(row & 127) * 128;
+                const int y = ((e * P.num_kv_heads + it.hk) << P.block_shift) +
+                              (tok & ((1 << P.block_shift) - 1));
 #pragma unroll
-            for (int z = 0; z < KB; ++z)
-                tma_load_3d(dst + (size_t)z * kKSlice, &P.tmap_k, 0, y, z, &B.k_full[kb], policy);
-        }
-        __syncwarp();
-        ++kc;
-        if (lane == 0) {
-            for (int tt = it.tt0; ok && tt < it.tt1; ++tt)
-                for (int hg = 0; hg < P.head_groups; ++hg) {
-                    const int st = qc % RQ;
-                    ok = mbar_wait(&B.q_free[st], (uint32_t)((qc / RQ) & 1) ^ 1u, abort_flag);
-                    if (!ok) break;
-                    mbar_arrive_expect_tx(&B.q_full[st], q_bytes);
-                    asm volatile(
-                        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                        " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                            smem_u32(sq + (size_t)st * L::qstage)),
-                        "l"(&P.tmap_q), "r"(0), "r"(it.hk * P.G + (hg << P.lg_nh)),
-                        "r"(it.tok0 + (tt << P.lg_nq)), "r"(0), "r"(smem_u32(&B.q_full[st]))
-                        : "memory");
-                    ++qc;
-                }
-        }
-        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                for (int z = 0; z < KB; ++z)
+                    tma_load_3d(dst + (size_t)z * kKSlice, &P.tmap_k, 0, y, z, &B.k_full[kr.slot],
+                                policy);
+            }
+            __syncwarp();
+            kr.next(P.rk);
+            ++kn;
+        };
+        auto load_q = [&](int from, int to) {
+            if (lane == 0) {
+                for (int tt = from; ok && tt < to; ++tt)
+                    for (int hg = 0; hg < P.head_groups; ++hg) {
+                        ok = mbar_wait(&B.q_free[qr.slot], qr.phase ^ 1u, abort_flag);
+                        if (!ok) break;
+                        mbar_arrive_expect_tx(&B.q_full[qr.slot], q_bytes);
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                                smem_u32(sq + (size_t)qr.slot * q_bytes)),
+                            "l"(&P.tmap_q), "r"(0), "r"(it.hk * P.G + (hg << P.lg_nh)),
+                            "r"(it.tok0 + (tt << P.lg_nq)), "r"(0),
+                            "r"(smem_u32(&B.q_full[qr.slot]))
+                            : "memory");
+                        qr.next(P.rq);
+                        ++qn;
+                    }
+            }
+            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        };
+        const int second = first_tile(P, it, 1);
+        load_k(0);
+        if (ok) load_q(it.tt0, second);
+        if (ok && it.k0 + kKeys < it.L) load_k(1);
+        if (ok) load_q(second, it.tt1);
     }
     if (lane == 0) {
         if (!ok) {
             *abort_flag = 1;
             if (P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
         }
-        // every copy issued lands before the CTA can exit
+        // every copy issued lands before the CTA can exit: the last phase armed
+        // of every slot
         volatile int never = 0;
-        for (int i = max(0, kc - 2); i < kc; ++i)
-            mbar_drain_wait(&B.k_full[i & 1], (uint32_t)(i >> 1) & 1u, &never);
-        for (int i = max(0, qc - RQ); i < qc; ++i)
-            mbar_drain_wait(&B.q_full[i % RQ], (uint32_t)(i / RQ) & 1u, &never);
+        for (int i = max(0, kn - P.rk); i < kn; ++i)
+            mbar_drain_wait(&B.k_full[i % P.rk], (uint32_t)(i / P.rk) & 1u, &never);
+        for (int i = max(0, qn - P.rq); i < qn; ++i)
+            mbar_drain_wait(&B.q_full[i % P.rq], (uint32_t)(i / P.rq) & 1u, &never);
     }
     __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
-// warp 1, one thread: S = K Q^T
+// warps 1 and 2, one thread each: S = K Q^T for key tile t
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ __forceinline__ void run_score_mma(const ScoreParams &P, uint32_t fmt,
+__device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint32_t fmt,
                                               unsigned char *sk, unsigned char *sq, uint32_t tmem,
                                               const SBars &B, volatile int *abort_flag) {
-    using L = SLayout<D>;
-    constexpr int RQ = L::RQ;
+    constexpr int KB = D / 64;
+    constexpr uint32_t ktile = KB * kKSlice;
     const uint32_t cols = 1u << (P.lg_nh + P.lg_nq);
     const uint32_t idesc = umma_idesc_f16(fmt, 0, 0, kKeys, cols);
     const uint32_t ak = smem_u32(sk), aq = smem_u32(sq);
-    int kc = 0, qc = 0, sc[kTiles] = {0, 0};
+    Ring kr, qr, lr, sr;
     bool ok = true;
     for (unsigned r = 0; ok && item_id(r) < P.num_items; ++r) {
         const SItem it = score_item(P, item_id(r));
         if (!it.run) continue;
-        const int kb = kc & 1;
-        const int first[kTiles] = {first_tile(P, it, 0), first_tile(P, it, 1)};
-        ok = mbar_wait(&B.k_full[kb], (uint32_t)(kc >> 1) & 1u, abort_flag);
+        const int first = first_tile(P, it, t);
+        const bool two = it.k0 + kKeys < it.L;
+        Ring ks = kr;  // this key tile's slot
+        kr.next(P.rk);
+        if (t == 1) ks = kr;
+        if (two) kr.next(P.rk);
         for (int tt = it.tt0; ok && tt < it.tt1; ++tt)
-            for (int hg = 0; ok && hg < P.head_groups; ++hg, ++qc) {
-                const int st = qc % RQ;
-                ok = mbar_wait(&B.q_full[st], (uint32_t)(qc / RQ) & 1u, abort_flag);
+            for (int hg = 0; ok && hg < P.head_groups; ++hg) {
+                // Both issuers pass through every query tile: a wait by parity
+                // must never be a whole ring ahead or behind.  (The lse is
+                // waited for so that a group that has seen the product
+                // complete knows its slot's phase.)
+                ok = mbar_wait(&B.q_full[qr.slot], qr.phase, abort_flag) &&
+                     mbar_wait(&B.l_full[lr.slot], lr.phase, abort_flag);
                 if (!ok) break;
-                const uint32_t qt = aq + (uint32_t)(st * L::qstage);
-#pragma unroll
-                for (int t = 0; t < kTiles; ++t) {
-                    if (!ok || tt < first[t]) continue;
-                    const int b = sc[t] & 1;
-                    ok = mbar_wait(&B.s_free[2 * t + b], (uint32_t)((sc[t] >> 1) & 1) ^ 1u, abort_flag);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t kt = ak + (uint32_t)(kb * L::kbuf + t * L::ktile);
-#pragma unroll
-                    for (int kk = 0; kk < D / 16; ++kk) {
-                        const uint32_t in_slice = (uint32_t)((kk & 3) * 32);
-                        umma_f16(tmem + (uint32_t)(128 * (2 * t + b)),
-                                 umma_desc_sw128(kt + (uint32_t)(kk >> 2) * kKSlice + in_slice, 16, 1024),
-                                 umma_desc_sw128(qt + (uint32_t)(kk >> 2) * cols * 128u + in_slice, 16, 1024),
-                                 idesc, kk > 0 ? 1u : 0u);
-                    }
-                    umma_commit(&B.s_full[2 * t + b]);
-                    ++sc[t];
+                if (tt < first) {  // the other key tile alone: give this one's shares back
+                    mbar_arrive(&B.q_free[qr.slot]);
+                    for (int i = 0; i < 4; ++i) mbar_arrive(&B.l_free[lr.slot]);
+                    qr.next(P.rq);
+                    lr.next(kLseRing);
+                    continue;
                 }
-                umma_commit(&B.q_free[st]);
+                const int b = sr.slot;
+                ok = (tt > first || hg > 0 || mbar_wait(&B.k_full[ks.slot], ks.phase, abort_flag)) &&
+                     mbar_wait(&B.s_free[2 * t + b], sr.phase ^ 1u, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t kt = ak + (uint32_t)ks.slot * ktile;
+                const uint32_t qt = aq + (uint32_t)qr.slot * cols * 128u * KB;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t in_slice = (uint32_t)((kk & 3) * 32);
+                    umma_f16(tmem + (uint32_t)(128 * (2 * t + b)),
+                             umma_desc_sw128(kt + (uint32_t)(kk >> 2) * kKSlice + in_slice, 16, 1024),
+                             umma_desc_sw128(qt + (uint32_t)(kk >> 2) * cols * 128u + in_slice, 16, 1024),
+                             idesc, kk > 0 ? 1u : 0u);
+                }
+                umma_commit(&B.s_full[2 * t + b]);
+                umma_commit(&B.q_free[qr.slot]);
+                sr.next(2);
+                qr.next(P.rq);
+                lr.next(kLseRing);
             }
-        umma_commit(&B.k_free[kb]);
-        ++kc;
+        if (t == 0 || two) umma_commit(&B.k_free[ks.slot]);
     }
     if (!ok) {
         *abort_flag = 1;
         if (P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
     }
-    umma_commit(B.done);  // after every product issued: the teardown
+    umma_commit(&B.done[t]);  // after every product issued: the teardown
+}
+
+// ---------------------------------------------------------------------------
+// warp 3: the rows' lse
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ void run_score_lse(const ScoreParams &P, float *s_lse,
+                                              volatile int *s_dead, const SBars &B,
+                                              volatile int *abort_flag, int lane) {
+    const int cols = 1 << (P.lg_nh + P.lg_nq);
+    constexpr int kPer = kMaxCols / 32;
+    Ring lr;
+    bool ok = true;
+    for (unsigned r = 0; ok && item_id(r) < P.num_items; ++r) {
+        const SItem it = score_item(P, item_id(r));
+        if (!it.run) continue;
+        for (int tt = it.tt0; ok && tt < it.tt1; ++tt)
+            for (int hg = 0; ok && hg < P.head_groups; ++hg) {
+                float v[kPer];
+                bool any_dead = false;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    const int row = 32 * k + lane, i = (tt << P.lg_nq) + (row >> P.lg_nh);
+                    float l = -INFINITY;  // no such row, or one without a weight
+                    if (row < cols && i < it.n)
+                        l = __ldg(&P.lse[(size_t)(it.tok0 + i) * P.num_heads + it.hk * P.G +
+                                         (hg << P.lg_nh) + (row & ((1 << P.lg_nh) - 1))]);
+                    v[k] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
+                    any_dead |= row < cols && l == -INFINITY;
+                }
+                any_dead = __any_sync(0xffffffffu, any_dead);
+                if (lane == 0) ok = mbar_wait(&B.l_free[lr.slot], lr.phase ^ 1u, abort_flag);
+                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+                if (!ok) break;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) s_lse[lr.slot * kMaxCols + 32 * k + lane] = v[k];
+                if (lane == 0) s_dead[lr.slot] = any_dead;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&B.l_full[lr.slot]);
+                lr.next(kLseRing);
+            }
+    }
+    if (!ok && lane == 0) {
+        *abort_flag = 1;
+        if (P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -385,54 +473,38 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int b, float *s_lse,
-                                               volatile int *s_dead, uint32_t tmem,
-                                               const SBars &B, volatile int *abort_flag, int wq,
-                                               int lane) {
-    const int rk = 32 * wq + lane;  // this thread's key of the tile, and the row it stages
+__device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int b,
+                                               const float *s_lse, const volatile int *s_dead,
+                                               float *s_part, uint32_t tmem, const SBars &B,
+                                               volatile int *abort_flag, int wq, int lane) {
+    const int rk = 32 * wq + lane;  // this thread's key of the tile
     const int cols = 1 << (P.lg_nh + P.lg_nq);
     const uint32_t tb = tmem + (uint32_t)(128 * (2 * t + b)) + ((uint32_t)(32 * wq) << 16);
-    float *nl = s_lse + (2 * t + b) * kMaxCols;
-    float *other = s_lse + (2 * t + 1) * kMaxCols;  // where group (t, 1) leaves its sums
-    volatile int *dead = s_dead + (2 * t + b) * 4;
-    const int bar_own = 1 + 2 * t + b, bar_full = 5 + t, bar_free = 7 + t;
+    float *part = s_part + t * kKeys;
+    const int bar_full = 1 + t, bar_free = 3 + t;
     const uint64_t sc2 = pair(P.scale_log2, P.scale_log2);
-    // staged row rk of a product (token tile tt, head group hg): its negated lse in base 2, -inf
-    // for no such row or no weight
-    auto row_lse = [&](const SItem &it, int tt, int hg) {
-        const int i = (tt << P.lg_nq) + (rk >> P.lg_nh);
-        if (rk >= cols || tt >= it.tt1 || i >= it.n) return -INFINITY;
-        const int h = it.hk * P.G + (hg << P.lg_nh) + (rk & ((1 << P.lg_nh) - 1));
-        const float l = __ldg(&P.lse[(size_t)(it.tok0 + i) * P.num_heads + h]);
-        return l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-    };
-    // the next item with keys for this tile, from round r on
-    auto next_item = [&](unsigned &r, SItem &it) {
+    // the next item with keys for this tile, from round r on; `skipped`: query
+    // tiles of the items before it that have none
+    auto next_item = [&](unsigned &r, SItem &it, int &skipped) {
         for (; item_id(r) < P.num_items; ++r) {
             it = score_item(P, item_id(r));
-            if (it.run && it.k0 + t * kKeys < it.L) return true;
+            if (!it.run) continue;
+            if (it.k0 + t * kKeys < it.L) return true;
+            skipped += (it.tt1 - it.tt0) * P.head_groups;
         }
         return false;
     };
     unsigned r = 0;
     SItem nx;
-    bool live = next_item(r, nx);
-    int cnt = 0;          // products of the tile before this item
+    int q0 = 0;           // query tiles before the item
+    bool live = next_item(r, nx, q0);
+    int cnt = 0;          // products of the key tile before the item
     int taken = 0;        // products of this group
     bool gave = false;    // group (t, 1): sums handed over and not yet taken
     bool ok = true;
-    float next = 0.f;     // the row's lse of this group's next product
     float old = 0.f;      // the key's score before (group (t, 0))
     int blk = -1;         // and its block
-    int tt = 0, hg = 0;   // this group's next product
-    auto step = [&](int by) {
-        for (hg += by; hg >= P.head_groups; hg -= P.head_groups) ++tt;
-    };
-    auto prefetch = [&]() {  // of item nx, whose products start at number cnt
-        tt = first_tile(P, nx, t);
-        hg = 0;
-        step((cnt ^ b) & 1);
-        next = row_lse(nx, tt, hg);
+    auto prefetch = [&]() {  // of item nx
         const int key = nx.k0 + t * kKeys + rk;
         if (b == 0 && key < nx.L) {
             blk = __ldg(&P.block_tables[(size_t)nx.s * P.max_blocks_per_seq + (key >> P.block_shift)]);
@@ -446,56 +518,49 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int 
         const int key = it.k0 + t * kKeys + rk;
         const float old_now = old;
         const int blk_now = blk;
-        float acc = 0.f;
-        int p = (cnt ^ b) & 1;
-        cnt += np;
+        const int qp = q0 + (first - it.tt0) * P.head_groups;  // query tile of product 0
+        q0 += (it.tt1 - it.tt0) * P.head_groups;
         ++r;
-        live = next_item(r, nx);
-        for (;; p += 2) {
-            const bool last = p + 2 >= np;  // this group's last product of the item, or none at all
-            const float mine = next;
-            const int tok = tt << P.lg_nq;  // the product's first token
-            if (last) {
-                if (live) prefetch();
-                if (p >= np) break;
-            } else {
-                step(2);
-                next = row_lse(it, tt, hg);  // arrives during this product
-            }
-            if (gave) {  // the sums lie where the lse goes
-                bar_sync(bar_free, 256);
-                gave = false;
-            }
-            bar_sync(bar_own, 128);  // every thread has read the previous product's lse
-            if (rk < cols) nl[rk] = mine;
-            const bool any_dead = __any_sync(0xffffffffu, rk < cols && mine == -INFINITY);
-            if (lane == 0) dead[wq] = any_dead;
-            bar_sync(bar_own, 128);
-            const int done = taken++;
-            if (ok) ok = mbar_wait(&B.s_full[2 * t + b], (uint32_t)done & 1u, abort_flag);
+        live = next_item(r, nx, q0);
+        if (live) prefetch();
+        float acc = 0.f;
+        int tt = first, hg = 0, p = (cnt ^ b) & 1;
+        auto step = [&](int by) {
+            for (hg += by; hg >= P.head_groups; hg -= P.head_groups) ++tt;
+        };
+        step(p);
+        cnt += np;
+        for (; ok && p < np; p += 2, step(2)) {
+            const int q = qp + p, slot = q % kLseRing;
+            ok = mbar_wait(&B.s_full[2 * t + b], (uint32_t)taken & 1u, abort_flag) &&
+                 // staged before the product was issued: only orders the reads
+                 mbar_wait(&B.l_full[slot], (uint32_t)(q / kLseRing) & 1u, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) *abort_flag = 1;  // at once: no sum that lacks this product is written
-            if (ok) {
-                tc_fence_after();
-                const int lo = max(0, key - it.c - tok) << P.lg_nh;
-                const int hi = (it.n - tok) << P.lg_nh;
-                const bool all = __all_sync(0xffffffffu, lo == 0) && hi >= cols &&
-                                 !(dead[0] | dead[1] | dead[2] | dead[3]);
-                acc += all ? sum_product<true>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b])
-                           : sum_product<false>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b]);
+            if (!ok) {  // at once: no sum that lacks this product is written
+                *abort_flag = 1;
+                break;
             }
-            if (last) break;
+            ++taken;
+            tc_fence_after();
+            const float *nl = s_lse + slot * kMaxCols;
+            const int tok = tt << P.lg_nq;  // the tile's first token
+            const int lo = max(0, key - it.c - tok) << P.lg_nh;
+            const int hi = (it.n - tok) << P.lg_nh;
+            const bool all = __all_sync(0xffffffffu, lo == 0) && hi >= cols && !s_dead[slot];
+            acc += all ? sum_product<true>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b])
+                       : sum_product<false>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b]);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&B.l_free[slot]);
         }
         // the item's sums
         if (b == 1) {
             if (gave) bar_sync(bar_free, 256);
-            bar_sync(bar_own, 128);  // every thread has read the last product's lse
-            other[rk] = acc;
+            part[rk] = acc;
             bar_arrive(bar_full, 256);
             gave = true;
         } else {
             bar_sync(bar_full, 256);
-            acc += other[rk];
+            acc += part[rk];
             bar_arrive(bar_free, 256);
             if (ok && !*abort_flag && key < it.L && blk_now >= 0 && blk_now < P.num_blocks)
                 P.scores[((long long)it.s * P.num_kv_heads + it.hk) * P.score_stride + key] =
@@ -511,8 +576,7 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int 
 template <int D>
 __global__ void __launch_bounds__(kThreadsS, 1)
     prefill_scores_kernel(const __grid_constant__ ScoreParams P, uint32_t fmt) {
-    using L = SLayout<D>;
-    constexpr int RQ = L::RQ;
+    using L = SLayout;
     extern __shared__ __align__(1024) unsigned char smem[];
     pdl_trigger();
     // the swizzled tiles need 1024-byte alignment, which the start of dynamic
@@ -524,16 +588,19 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     }
     float *s_lse = reinterpret_cast<float *>(smem);
     volatile int *s_dead = reinterpret_cast<volatile int *>(smem + L::dead_off);
+    float *s_part = reinterpret_cast<float *>(smem + L::part_off);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::bar_off);
-    unsigned char *sk = smem + L::small + L::k_off, *sq = smem + L::small + L::q_off;
+    unsigned char *sk = smem + L::small, *sq = sk + (size_t)P.rk * (D / 64) * kKSlice;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(smem + L::tmem_off);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::flag_off);
     SBars B;
     B.k_full = bars;
-    B.k_free = B.k_full + 2;
-    B.q_full = B.k_free + 2;
-    B.q_free = B.q_full + RQ;
-    B.s_full = B.q_free + RQ;
+    B.k_free = B.k_full + kMaxRing;
+    B.q_full = B.k_free + kMaxRing;
+    B.q_free = B.q_full + kMaxRing;
+    B.l_full = B.q_free + kMaxRing;
+    B.l_free = B.l_full + kLseRing;
+    B.s_full = B.l_free + kLseRing;
     B.s_free = B.s_full + 4;
     B.done = B.s_free + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -542,10 +609,14 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         prefetch_tmap(&P.tmap_k);
         for (int b = 0; b < L::kBars; ++b) mbar_init(&bars[b], 1);
         for (int b = 0; b < 4; ++b) mbar_init(&B.s_free[b], kKeys);
+        // a slot of these rings is given back for each key tile: by the four
+        // warps of its group, and by its products
+        for (int b = 0; b < kLseRing; ++b) mbar_init(&B.l_free[b], 8);
+        for (int b = 0; b < kMaxRing; ++b) mbar_init(&B.q_free[b], 2);
         *abort_flag = 0;
         fence_mbar_init();
     }
-    if (warp == 2) tmem_alloc(tmem_slot, kTmemColsS);
+    if (warp == 1) tmem_alloc(tmem_slot, kTmemColsS);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -553,27 +624,29 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     pdl_wait();  // the kernels before may still write what this reads
     if (warp == 0) {
         run_score_producer<D>(P, sk, sq, B, abort_flag, lane);
-    } else if (warp == 1) {
+    } else if (warp <= 2) {
         if (lane == 0) {
-            run_score_mma<D>(P, fmt, sk, sq, tmem, B, abort_flag);
+            run_score_mma<D>(P, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
             // every product has completed before tensor memory is released
             volatile int never = 0;
-            mbar_drain_wait(B.done, 0, &never);
+            mbar_drain_wait(&B.done[warp - 1], 0, &never);
         }
         __syncwarp();
+    } else if (warp == 3) {
+        run_score_lse(P, s_lse, s_dead, B, abort_flag, lane);
     } else if (warp >= 4) {
-        run_score_sums(P, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, tmem, B, abort_flag,
-                       warp & 3, lane);
+        run_score_sums(P, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, s_part, tmem, B,
+                       abort_flag, warp & 3, lane);
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 2) tmem_dealloc(tmem, kTmemColsS);
+    if (warp == 1) tmem_dealloc(tmem, kTmemColsS);
 }
 
 template <int D>
 pa_status_t launch_scores(const ScoreParams &P, uint32_t fmt, unsigned grid, cudaStream_t stream) {
-    using L = SLayout<D>;
+    using L = SLayout;
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> attr_set[kMaxDevices];
     int dev = 0;
@@ -651,6 +724,13 @@ extern "C" pa_status_t pa_prefill_scores(
            ((1 << P.lg_nq) < max_query_len || P.lg_nh + P.lg_nq < 5))
         ++P.lg_nq;
     P.head_groups = G >> P.lg_nh;
+    // the rings: three K tiles and three full query tiles at head_dim 128; with
+    // query tiles of at most 64 rows (windows) more of both
+    const uint32_t kbytes = (uint32_t)head_dim * 256u, qbytes = (uint32_t)head_dim * 2u << (P.lg_nh + P.lg_nq);
+    P.rk = qbytes < kbytes ? 4 : 3;
+    if (head_dim == 64) P.rk *= 2;
+    P.rq = (int)((kTileBytes - (uint32_t)P.rk * kbytes) / qbytes);
+    if (P.rq > kMaxRing) P.rq = kMaxRing;
     const cuuint64_t KB = (cuuint64_t)head_dim / 64;
     {
         const cuuint64_t dims[4] = {64u, (cuuint64_t)num_heads, (cuuint64_t)num_tokens, KB};
