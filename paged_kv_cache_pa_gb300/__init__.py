@@ -118,6 +118,8 @@ def library_path() -> str:
 def load_library() -> ctypes.CDLL:
     """Load libpa_gb300.so (raises if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(_LIB_PATH):
@@ -164,7 +166,8 @@ def _dev(t, name):
 def _stream_ptr(stream, device) -> int:
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # the current stream's handle, without making a Stream object
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return int(stream.cuda_stream)
 
 

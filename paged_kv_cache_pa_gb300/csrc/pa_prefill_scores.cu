@@ -34,7 +34,7 @@
 //     query tiles', with a flag for tiles that hold rows without a weight;
 //   * warps 4..19: four groups of four, group (t, b) for the products of key
 //     tile t in buffer b, one key a thread (the lanes a warp may read go by
-//     its number modulo 4).  Each loads S from tensor memory 16 columns at a
+//     its number modulo 4).  Each loads S from tensor memory 32 columns at a
 //     time and sums 2^(x scale log2 e - lse) over the columns it may see -- a
 //     range [lo, hi) of the tile, from its key's position.  At the item's end
 //     group (t, 1) hands its sums to group (t, 0), which adds them and writes.
@@ -65,9 +65,15 @@ namespace {
 constexpr int kKeys = 128;    // keys of a tile (tensor-memory lanes)
 constexpr int kTiles = 2;     // key tiles of an item
 constexpr int kItemKeys = kKeys * kTiles;
+constexpr int kChunk = 32;    // columns a thread holds at once
 constexpr int kMaxCols = 128; // rows of a query tile
 constexpr int kGroups = 4;    // of four warps: key tile and buffer
 constexpr int kThreadsS = 128 + 128 * kGroups;
+// registers a thread: 96 at launch (640 threads), then 104 for the groups and
+// 64 for the other four warps -- no more than the same total
+constexpr int kRegsLaunch = 96, kRegsSums = 104, kRegsOther = 64;
+static_assert(128 * kGroups * kRegsSums + 128 * kRegsOther <= kThreadsS * kRegsLaunch,
+              "register reallocation within the launch's registers");
 constexpr uint32_t kTmemColsS = 512;  // S of tile t, buffer b at 128 (2 t + b)
 constexpr uint32_t kKSlice = kKeys * 128;  // bytes of a 64-element slice of a K tile
 constexpr int kMaxRing = 8;   // slots of the K and the query ring at most
@@ -418,17 +424,29 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 }
 
 // One product of this thread's key: the weights of `cols` columns of tensor
-// memory (a multiple of 32), 16 at a time, in four chains of pairs.  ALL: every
-// column is visible; else those in [lo, hi) whose row has a weight at all (a
-// row without has nl = -inf).  nl: the rows' negated lse.  The buffer is given
-// back through `bar` once all of it has been loaded.
-template <bool ALL>
+// memory (a multiple of CH) in four chains of pairs.  CH columns at a time are
+// loaded into registers, and the buffer is given back through `bar` with the
+// last load, so the next product runs while their weights are worked out.  (32
+// columns measured 135 us on 2 prompts of 4096 tokens with 32 heads on 8; 64,
+// with more registers, 139; 16 in two sets of registers 143.)  ALL: every column is visible; else those in [lo, hi) whose row has a
+// weight at all (a row without has nl = -inf).  nl: the rows' negated lse.
+template <bool ALL, int CH>
 __device__ __forceinline__ float sum_product(uint32_t taddr, int cols, const float *nl, int lo,
                                              int hi, uint64_t sc2, uint64_t *bar) {
     uint64_t a[4] = {0ull, 0ull, 0ull, 0ull};
-    auto add = [&](const uint32_t (&u)[16], int c) {
+#pragma unroll 1
+    for (int c = 0; c < cols; c += CH) {
+        uint32_t u[CH];
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
+        for (int i = 0; i < CH; i += 16)
+            tmem_ld16(taddr + (uint32_t)(c + i), *reinterpret_cast<uint32_t(*)[16]>(&u[i]));
+        tmem_wait_ld();
+        if (c + CH >= cols) {
+            tc_fence_before();
+            mbar_arrive(bar);
+        }
+#pragma unroll
+        for (int i = 0; i < CH; i += 4) {
             const float4 l4 = *reinterpret_cast<const float4 *>(nl + c + i);
             const float l[4] = {l4.x, l4.y, l4.z, l4.w};
 #pragma unroll
@@ -445,22 +463,6 @@ __device__ __forceinline__ float sum_product(uint32_t taddr, int cols, const flo
                 a[(i + k) / 2 % 4] = add2(a[(i + k) / 2 % 4], pair(p0, p1));
             }
         }
-    };
-    uint32_t ua[16], ub[16];
-    tmem_ld16(taddr, ua);
-#pragma unroll 1
-    for (int c = 0; c < cols; c += 32) {
-        tmem_wait_ld();
-        tmem_ld16(taddr + (uint32_t)(c + 16), ub);
-        add(ua, c);
-        tmem_wait_ld();
-        if (c + 32 < cols) {
-            tmem_ld16(taddr + (uint32_t)(c + 32), ua);
-        } else {  // the buffer may take the next product
-            tc_fence_before();
-            mbar_arrive(bar);
-        }
-        add(ub, c + 16);
     }
     const float2 v = unpair(add2(add2(a[0], a[1]), add2(a[2], a[3])));
     return v.x + v.y;
@@ -547,8 +549,8 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int 
             const int lo = max(0, key - it.c - tok) << P.lg_nh;
             const int hi = (it.n - tok) << P.lg_nh;
             const bool all = __all_sync(0xffffffffu, lo == 0) && hi >= cols && !s_dead[slot];
-            acc += all ? sum_product<true>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b])
-                       : sum_product<false>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b]);
+            acc += all ? sum_product<true, kChunk>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b])
+                       : sum_product<false, kChunk>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b]);
             __syncwarp();
             if (lane == 0) mbar_arrive(&B.l_free[slot]);
         }
@@ -621,22 +623,29 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    pdl_wait();  // the kernels before may still write what this reads
-    if (warp == 0) {
-        run_score_producer<D>(P, sk, sq, B, abort_flag, lane);
-    } else if (warp <= 2) {
-        if (lane == 0) {
-            run_score_mma<D>(P, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
-            // every product has completed before tensor memory is released
-            volatile int never = 0;
-            mbar_drain_wait(&B.done[warp - 1], 0, &never);
-        }
-        __syncwarp();
-    } else if (warp == 3) {
-        run_score_lse(P, s_lse, s_dead, B, abort_flag, lane);
-    } else if (warp >= 4) {
+    // each role's code follows its own register reallocation (code after a
+    // join of the two would be held to the smaller count)
+    if (warp >= 4) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
+        pdl_wait();  // the kernels before may still write what this reads
         run_score_sums(P, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, s_part, tmem, B,
                        abort_flag, warp & 3, lane);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
+        pdl_wait();
+        if (warp == 0) {
+            run_score_producer<D>(P, sk, sq, B, abort_flag, lane);
+        } else if (warp <= 2) {
+            if (lane == 0) {
+                run_score_mma<D>(P, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
+                // every product has completed before tensor memory is released
+                volatile int never = 0;
+                mbar_drain_wait(&B.done[warp - 1], 0, &never);
+            }
+            __syncwarp();
+        } else {
+            run_score_lse(P, s_lse, s_dead, B, abort_flag, lane);
+        }
     }
     tc_fence_before();
     __syncthreads();
@@ -652,6 +661,11 @@ pa_status_t launch_scores(const ScoreParams &P, uint32_t fmt, unsigned grid, cud
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
     if (!attr_set[dev].load(std::memory_order_relaxed)) {
+        // the register reallocation inside the kernel assumes exactly
+        // kRegsLaunch registers a thread at launch; anything else is refused
+        cudaFuncAttributes fa;
+        if (cudaFuncGetAttributes(&fa, prefill_scores_kernel<D>) != cudaSuccess) return PA_ERR_CUDA;
+        if (fa.numRegs != kRegsLaunch) return PA_ERR_UNSUPPORTED;
         if (cudaFuncSetAttribute(prefill_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                  (int)L::bytes) != cudaSuccess)
             return PA_ERR_CUDA;

@@ -22,7 +22,11 @@
 // two halves of its eight pairs (or two neighbouring chunks when interleaved
 // or past rotary_dim), so a rotation never leaves its thread.  A token's
 // sines and cosines are computed once a CTA, for all its heads, while its
-// first rows are in flight.
+// first rows are in flight.  A CTA takes as many tokens as give each thread
+// four rows, unless that leaves fewer than two CTAs an SM: with few rows a
+// token (grouped queries) one row a thread is one round trip to memory a CTA
+// and half the rate (4099 tokens of 12 + 2 + 2 heads of 128: 15.3 us, RGQA
+// with four rows).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -53,6 +57,7 @@ struct RotaryParams {
     int num_tokens, num_heads, num_kv_heads, block_shift;
     int lg_lpr;        // log2 of a row's threads (head_dim / 16)
     int lg_rows;       // log2 of the rows a token's threads take at once
+    int rounds;        // tokens a thread takes, one after the other
     unsigned int *err;
     pa_rotary_t rot;
 };
@@ -104,29 +109,25 @@ __device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 *cs) {
     }
 }
 
-// A CTA takes 256 / (threads a row * rows at once) tokens; thread = (token,
-// row, unit j of the row).  A token's rows are its query heads, its key heads
-// and its value heads.
+// A CTA takes `rounds` times 256 / (threads a row * rows at once) tokens; thread
+// = (token, row, unit j of the row).  A token's rows are its query heads, its
+// key heads and its value heads; a thread goes through its rows of all its
+// tokens as one list, four at a time.
 template <typename T, bool IL>
 __global__ void __launch_bounds__(kRotThreads)
     rotary_cache_write_kernel(const __grid_constant__ RotaryParams P) {
-    __shared__ float2 s_cs[kRotThreads / 4][8];  // [token][unit][pair], a unit per row thread
+    extern __shared__ __align__(16) float2 s_cs[];  // [token][pair]
     pdl_trigger();
     const int lpr = 1 << P.lg_lpr, rows_at_once = 1 << P.lg_rows;
     const int j = threadIdx.x & (lpr - 1);
     const int r0 = ((int)threadIdx.x >> P.lg_lpr) & (rows_at_once - 1);
     const int tl = (int)threadIdx.x >> (P.lg_lpr + P.lg_rows);
-    const int tokens = kRotThreads >> (P.lg_lpr + P.lg_rows);
-    const long long t = (long long)blockIdx.x * tokens + tl;
-    const bool live = t < P.num_tokens;
+    const int lanes = kRotThreads >> (P.lg_lpr + P.lg_rows);  // tokens at once
+    const int tokens = lanes * P.rounds;
+    const long long t0 = (long long)blockIdx.x * tokens;
     const int H = P.num_heads, Hkv = P.num_kv_heads, rows = H + 2 * Hkv;
     const int pairs = P.rot.rotary_dim / 2, rot_units = pairs / 8;
     pdl_wait();  // earlier kernels on the stream may still read or write what this touches
-
-    const int64_t slot = live ? P.slot_mapping[t] : -1;
-    const bool to_cache = slot >= 0 && slot < P.num_slots;  // < 0: padding
-    if (live && slot >= P.num_slots && r0 == 0 && j == 0 && P.err)
-        atomicOr(P.err, PA_ERRBIT_SLOT_OOB);
 
     // this thread's two chunks of a row
     int ca, cb;
@@ -137,61 +138,66 @@ __global__ void __launch_bounds__(kRotThreads)
         ca = j;
         cb = j + rot_units;
     }
-    const uint4 *src[3] = {P.q + (live ? t : 0) * P.q_stride, P.k + (live ? t : 0) * P.k_stride,
-                           P.v + (live ? t : 0) * P.v_stride};
     const int lg_cpr = P.lg_lpr + 1;  // log2 of a row's chunks
-    auto row_ptr = [&](int r) {
-        return r < H ? src[0] + ((size_t)r << lg_cpr)
-                     : r < H + Hkv ? src[1] + ((size_t)(r - H) << lg_cpr)
-                                   : src[2] + ((size_t)(r - H - Hkv) << lg_cpr);
+    // the thread's place in its list: token of the CTA and row
+    struct At {
+        int tok, r;
     };
-    uint4 a[kRotBatch], b[kRotBatch];
-    auto load = [&](int rb) {
-#pragma unroll
-        for (int u = 0; u < kRotBatch; ++u) {
-            const int r = rb + u * rows_at_once;
-            if (live && r < rows && (r < H || to_cache)) {
-                const uint4 *p = row_ptr(r);
-                a[u] = __ldcs(p + ca);
-                b[u] = __ldcs(p + cb);
-            }
+    auto next = [&](At &p) {
+        p.r += rows_at_once;
+        if (p.r >= rows) {
+            p.r = r0;
+            p.tok += lanes;
         }
     };
-    load(r0);
+    auto in_list = [&](const At &p) { return p.tok < tokens && t0 + p.tok < P.num_tokens; };
+    uint4 a[kRotBatch], b[kRotBatch];
+    int64_t slot[kRotBatch];
+    auto load = [&](At p) {
+#pragma unroll
+        for (int u = 0; u < kRotBatch; ++u, next(p)) {
+            if (!in_list(p)) break;
+            const long long t = t0 + p.tok;
+            const int r = p.r;
+            slot[u] = r < H ? 0 : P.slot_mapping[t];
+            const uint4 *src = r < H ? P.q + t * P.q_stride + ((size_t)r << lg_cpr)
+                               : r < H + Hkv ? P.k + t * P.k_stride + ((size_t)(r - H) << lg_cpr)
+                                             : P.v + t * P.v_stride + ((size_t)(r - H - Hkv) << lg_cpr);
+            a[u] = __ldcs(src + ca);
+            b[u] = __ldcs(src + cb);
+        }
+    };
+    At at = {tl, r0};
+    if (r0 >= rows) at.tok = tokens;  // more threads than rows
+    load(at);
 
     // sines and cosines of the CTA's tokens, once each
     for (int i = threadIdx.x; i < tokens * pairs; i += kRotThreads) {
         const int tok = i / pairs, pr = i - tok * pairs;
-        const long long tt = (long long)blockIdx.x * tokens + tok;
-        if (tt < P.num_tokens) {
-            const int64_t pos = P.positions[(size_t)P.rot.axis[pr] * P.num_tokens + tt];
+        const long long t = t0 + tok;
+        if (t < P.num_tokens) {
+            const int64_t pos = P.positions[(size_t)P.rot.axis[pr] * P.num_tokens + t];
             const uint64_t turn = (uint64_t)pos * P.rot.turns[pr];  // modulo one turn
             float s, c;
             sincospif(__ll2float_rn((long long)turn) * 0x1p-63f, &s, &c);
-            s_cs[(tok << P.lg_lpr) + (pr >> 3)][pr & 7] = make_float2(c * P.rot.scale,
-                                                                      s * P.rot.scale);
+            s_cs[i] = make_float2(c * P.rot.scale, s * P.rot.scale);
         }
     }
     __syncthreads();
-    if (!live) return;
     const bool turns = j < rot_units;
-    float2 cs[8];
-    if (turns) {
+    while (in_list(at)) {
+        At p = at;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) cs[e] = s_cs[(tl << P.lg_lpr) + j][e];
-    }
-    const size_t cache_row =
-        to_cache ? (((size_t)(slot >> P.block_shift) * Hkv) << P.block_shift) +
-                       (size_t)(slot & ((1 << P.block_shift) - 1))
-                 : 0;
-    uint4 *const q_out = P.q_out + t * P.q_out_stride;
-    for (int rb = r0; rb < rows; rb += kRotBatch * rows_at_once) {
-        if (rb != r0) load(rb);
-#pragma unroll
-        for (int u = 0; u < kRotBatch; ++u) {
-            const int r = rb + u * rows_at_once;
-            if (r >= rows || (r >= H && !to_cache)) continue;
+        for (int u = 0; u < kRotBatch; ++u, next(p)) {
+            if (!in_list(p)) break;
+            const long long t = t0 + p.tok;
+            const int r = p.r;
             if (turns && r < H + Hkv) {
+                float2 cs[8];
+#pragma unroll
+                for (int e = 0; e < 8; e += 2)
+                    *reinterpret_cast<float4 *>(&cs[e]) =
+                        *reinterpret_cast<const float4 *>(&s_cs[p.tok * pairs + 8 * j + e]);
                 if (IL) {
                     turn_neighbours<T>(a[u], cs);
                     turn_neighbours<T>(b[u], cs + 4);
@@ -201,15 +207,24 @@ __global__ void __launch_bounds__(kRotThreads)
             }
             uint4 *dst;
             if (r < H) {
-                dst = q_out + ((size_t)r << lg_cpr);
+                dst = P.q_out + t * P.q_out_stride + ((size_t)r << lg_cpr);
             } else {
+                if (slot[u] < 0) continue;  // padding
+                if (slot[u] >= P.num_slots) {
+                    if (r == H && j == 0 && P.err) atomicOr(P.err, PA_ERRBIT_SLOT_OOB);
+                    continue;
+                }
                 const int h = r < H + Hkv ? r - H : r - H - Hkv;
                 dst = (r < H + Hkv ? P.k_cache : P.v_cache) +
-                      ((cache_row + ((size_t)h << P.block_shift)) << lg_cpr);
+                      ((((((size_t)(slot[u] >> P.block_shift) * Hkv) + h) << P.block_shift) +
+                        (size_t)(slot[u] & ((1 << P.block_shift) - 1)))
+                       << lg_cpr);
             }
             dst[ca] = a[u];
             dst[cb] = b[u];
         }
+        at = p;
+        load(at);
     }
 }
 
@@ -312,17 +327,29 @@ extern "C" pa_status_t pa_rotary_cache_write(
     P.lg_rows = log2_of(rows < max_rows ? rows : max_rows);
     P.err = dev_error_word;
     P.rot = *rotary;
-    const int tokens = kRotThreads >> (P.lg_lpr + P.lg_rows);
+    // tokens a CTA: enough for four rows a thread, while two CTAs an SM are left
+    const int lanes = kRotThreads >> (P.lg_lpr + P.lg_rows);
+    const int groups = (rows + (1 << P.lg_rows) - 1) >> P.lg_rows;  // rows a thread and token
+    const int sms = device_sms();
+    if (sms <= 0) return PA_ERR_CUDA;
+    P.rounds = 1;
+    while (P.rounds * groups < kRotBatch &&
+           (long long)num_tokens >= 2ll * sms * lanes * (2 * P.rounds))
+        P.rounds *= 2;
+    const int tokens = lanes * P.rounds;
     const dim3 grid((unsigned)((num_tokens + tokens - 1) / tokens));
+    // at most 256 / 4 units of 8 pairs at once (a token has three rows at
+    // least), four rounds: 16 KB
+    const size_t smem = (size_t)tokens * (rotary->rotary_dim / 2) * sizeof(float2);
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e;
     if (dtype == PA_F16)
         e = rotary->interleaved
-                ? launch_pdl(rotary_cache_write_kernel<__half, true>, grid, dim3(kRotThreads), 0, st, P)
-                : launch_pdl(rotary_cache_write_kernel<__half, false>, grid, dim3(kRotThreads), 0, st, P);
+                ? launch_pdl(rotary_cache_write_kernel<__half, true>, grid, dim3(kRotThreads), smem, st, P)
+                : launch_pdl(rotary_cache_write_kernel<__half, false>, grid, dim3(kRotThreads), smem, st, P);
     else
         e = rotary->interleaved
-                ? launch_pdl(rotary_cache_write_kernel<__nv_bfloat16, true>, grid, dim3(kRotThreads), 0, st, P)
-                : launch_pdl(rotary_cache_write_kernel<__nv_bfloat16, false>, grid, dim3(kRotThreads), 0, st, P);
+                ? launch_pdl(rotary_cache_write_kernel<__nv_bfloat16, true>, grid, dim3(kRotThreads), smem, st, P)
+                : launch_pdl(rotary_cache_write_kernel<__nv_bfloat16, false>, grid, dim3(kRotThreads), smem, st, P);
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
