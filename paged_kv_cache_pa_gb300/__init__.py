@@ -609,7 +609,7 @@ def evict_workspace_size(num_layers: int, num_seqs: int, num_kv_heads: int, max_
 
 
 def _layer_ptrs(xs, name):
-    return ctypes.cast((ctypes.c_void_p * len(xs))(*[_dev(x, name) for x in xs]), ctypes.c_void_p)
+    return (ctypes.c_void_p * len(xs))(*[_dev(x, name) for x in xs])
 
 
 def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block_tables,
@@ -636,8 +636,9 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
         raise ValueError("need the same, non-zero number of K pools, V pools and scores")
     nb, hkv, bs, d = k_caches[0].shape
     dt = k_caches[0].dtype
+    pool = k_caches[0].shape
     for c in (*k_caches, *v_caches):
-        if c.shape != k_caches[0].shape or c.dtype != dt:
+        if c.shape != pool or c.dtype != dt:
             raise ValueError("all pools must have one shape and dtype")
     for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
                  (keep_lens, "keep_lens")):
@@ -655,11 +656,12 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
     def rows(xs, name, dtype):  # one shape and type for all layers
         if len(xs) != L:
             raise ValueError(f"need one {name} per layer")
+        first = xs[0].shape
+        ok = len(first) == 3 and first[0] == S and first[1] == hkv
         for x in xs:
-            if x.dtype != dtype or x.shape != xs[0].shape or x.dim() != 3 or \
-                    x.shape[0] != S or x.shape[1] != hkv:
+            if not ok or x.dtype != dtype or x.shape != first:
                 raise ValueError(f"{name} must be {dtype} [S][Hkv][positions] in every layer")
-        return _layer_ptrs(xs, name), xs[0].shape[2]
+        return _layer_ptrs(xs, name), first[2]
 
     sc = rows(scores, "scores", torch.float32)
     out = (None, 0) if scores_out is None else rows(scores_out, "scores_out", torch.float32)

@@ -103,12 +103,25 @@ __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
                      : "memory");
 }
-// A 32-bit word of another CTA of the cluster, at the place of `p` in this one's shared memory.
+// Another CTA of the cluster's copy of a word of this one's shared memory: read,
+// write, add.
+__device__ __forceinline__ uint32_t cluster_addr(const unsigned *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
 __device__ __forceinline__ unsigned ld_cluster(const unsigned *p, uint32_t rank) {
-    uint32_t a, v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    uint32_t v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
     return v;
+}
+__device__ __forceinline__ void st_cluster(unsigned *p, uint32_t rank, unsigned v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
+__device__ __forceinline__ void add_cluster(unsigned *p, uint32_t rank, unsigned v) {
+    asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(cluster_addr(p, rank)),
+                 "r"(v)
+                 : "memory");
 }
 
 // grid (cluster rank, unit): CS CTAs a unit, each with a contiguous segment of
@@ -117,7 +130,8 @@ template <int CS>
 __global__ void __launch_bounds__(kSelThreads)
     evict_select_kernel(const __grid_constant__ EvictParams P) {
     extern __shared__ uint4 s_key4[];  // the order keys of this CTA's segment, four a word
-    __shared__ unsigned hist[2][kBins];
+    // hist: this CTA's counts; a cluster adds them up in all_hist of its CTA 0
+    __shared__ unsigned hist[kBins], all_hist[CS > 1 ? kBins : 1];
     __shared__ unsigned s_warp[kSelThreads / 32], s_digit, s_need;
     __shared__ unsigned s_total;  // the segment's tokens above the threshold, and at it << 16
     uint32_t *const s_key = reinterpret_cast<uint32_t *>(s_key4);
@@ -155,7 +169,10 @@ __global__ void __launch_bounds__(kSelThreads)
     }
     const int seg = ((q.L + CS - 1) / CS + 3) & ~3, t0 = rank * seg;
     const int cnt = max(0, min(seg, q.L - t0));  // this CTA's tokens t0 .. t0 + cnt - 1
-    for (int i = tid; i < kBins; i += kSelThreads) hist[0][i] = 0u;
+    for (int i = tid; i < kBins; i += kSelThreads) {
+        hist[i] = 0u;
+        if (CS > 1) all_hist[i] = 0u;
+    }
     {
         int i = tid;
         for (; i + 7 * kSelThreads < cnt; i += 8 * kSelThreads) {
@@ -181,7 +198,6 @@ __global__ void __launch_bounds__(kSelThreads)
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const int bins = pass == 2 ? 1024 : 2048;
-            unsigned *h = hist[pass & 1];
             for (int j = tid; 4 * j < i1; j += kSelThreads) {
                 const uint4 k4 = s_key4[j];
                 const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -189,53 +205,69 @@ __global__ void __launch_bounds__(kSelThreads)
                 for (int u = 0; u < 4; ++u) {
                     const int i = 4 * j + u;
                     if (i >= i0 && i < i1 && ((key[u] ^ thr) & mask) == 0u)
-                        atomicAdd(&h[(key[u] >> shift) & (unsigned)(bins - 1)], 1u);
+                        atomicAdd(&hist[(key[u] >> shift) & (unsigned)(bins - 1)], 1u);
                 }
             }
+            if constexpr (CS > 1) {
+                // (the first pass: every CTA's all_hist is zero by now; later
+                // ones: cleared before the barrier that ended the last pass)
+                if (pass == 0) cluster_sync();
+                else __syncthreads();
+                for (int i = tid; i < bins; i += kSelThreads)
+                    if (hist[i]) add_cluster(&all_hist[i], 0u, hist[i]);
+                cluster_sync();
+            } else {
+                __syncthreads();
+            }
+            if (CS == 1 || rank == 0) {
+                unsigned *h = CS > 1 ? all_hist : hist;
+                // largest digits first: thread i has bins bins-1-4i .. bins-4-4i
+                unsigned c[4], sum = 0u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int b = bins - 1 - (4 * tid + k);
+                    c[k] = b >= 0 ? h[b] : 0u;
+                    sum += c[k];
+                }
+                unsigned incl = sum;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += u;
+                }
+                if (lane == 31) s_warp[wid] = incl;
+                __syncthreads();
+                unsigned before = incl - sum;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) before += w < wid ? s_warp[w] : 0u;
+                if (before < left && before + sum >= left) {  // one thread
+                    int k = 0;
+                    unsigned b4 = before;
+#pragma unroll
+                    for (int e = 0; e < 3; ++e)
+                        if (k == e && b4 + c[e] < left) {
+                            b4 += c[e];
+                            k = e + 1;
+                        }
+                    const unsigned digit = (unsigned)(bins - 1 - (4 * tid + k));
+                    if constexpr (CS > 1) {
+                        for (uint32_t r = 0; r < CS; ++r) {
+                            st_cluster(&s_digit, r, digit);
+                            st_cluster(&s_need, r, left - b4);
+                        }
+                    } else {
+                        s_digit = digit;
+                        s_need = left - b4;
+                    }
+                }
+            }
+            if (pass < 2)  // for the next pass (this one's scan has read them)
+                for (int i = tid; i < kBins; i += kSelThreads) {
+                    hist[i] = 0u;
+                    if (CS > 1) all_hist[i] = 0u;
+                }
             if (CS > 1) cluster_sync();
             else __syncthreads();
-            // largest digits first: thread i has bins bins-1-4i .. bins-4-4i
-            unsigned c[4], sum = 0u;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int b = bins - 1 - (4 * tid + k);
-                c[k] = 0u;
-                if (b >= 0) {
-                    if constexpr (CS > 1) {
-#pragma unroll
-                        for (int r = 0; r < CS; ++r) c[k] += ld_cluster(&h[b], (uint32_t)r);
-                    } else {
-                        c[k] = h[b];
-                    }
-                }
-                sum += c[k];
-            }
-            unsigned incl = sum;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += u;
-            }
-            if (lane == 31) s_warp[wid] = incl;
-            if (pass < 2)  // the other histogram: read last before the barrier above
-                for (int i = tid; i < kBins; i += kSelThreads) hist[(pass + 1) & 1][i] = 0u;
-            __syncthreads();
-            unsigned before = incl - sum;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) before += w < wid ? s_warp[w] : 0u;
-            if (before < left && before + sum >= left) {  // one thread
-                int k = 0;
-                unsigned b4 = before;
-#pragma unroll
-                for (int e = 0; e < 3; ++e)
-                    if (k == e && b4 + c[e] < left) {
-                        b4 += c[e];
-                        k = e + 1;
-                    }
-                s_digit = (unsigned)(bins - 1 - (4 * tid + k));
-                s_need = left - b4;
-            }
-            __syncthreads();
             thr |= s_digit << shift;
             mask |= (unsigned)(bins - 1) << shift;
             left = s_need;
@@ -296,6 +328,10 @@ __global__ void __launch_bounds__(kSelThreads)
         b_gt += o_gt;
         b_eq += o_eq;
     }
+    // A step's kept tokens have consecutive places: gathered in shared memory,
+    // then written out with neighbouring lanes on neighbouring places.
+    unsigned *const gathered = hist + wid * 128;
+    static_assert(kWarps * 128 <= kBins, "a step's tokens of every warp");
     for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
         const unsigned c = classify(i), own = counts(c);
         unsigned incl = own;
@@ -304,22 +340,27 @@ __global__ void __launch_bounds__(kSelThreads)
             const unsigned u = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += u;
         }
+        const unsigned first = b_gt + min(b_eq, need);
         unsigned g = b_gt + ((incl - own) & 0xffffu), e = b_eq + ((incl - own) >> 16);
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const bool above = (c >> u) & 1u, at = (c >> (16 + u)) & 1u;
-            if (above || (at && e < need)) {
-                const unsigned p = g + min(e, need);
-                idx[p] = t0 + i + u;
-                if (kept) kept[p] = t0 + i + u;
-                out[p] = score_of(s_key[i + u]);
-            }
+            if (above || (at && e < need)) gathered[g + min(e, need) - first] = (unsigned)(i + u);
             g += above;
             e += at;
         }
         const unsigned all = __shfl_sync(0xffffffffu, incl, 31);
         b_gt += all & 0xffffu;
         b_eq += all >> 16;
+        const unsigned last = b_gt + min(b_eq, need);
+        __syncwarp();
+        for (unsigned p = first + lane; p < last; p += 32) {
+            const unsigned j = gathered[p - first];
+            idx[p] = t0 + (int)j;
+            if (kept) kept[p] = t0 + (int)j;
+            out[p] = score_of(s_key[j]);
+        }
+        __syncwarp();
     }
     for (int p = q.n + rank * kSelThreads + tid; p < q.L; p += CS * kSelThreads) out[p] = 0.f;
     if (CS > 1) cluster_sync();  // no CTA leaves while another may read its counts
