@@ -23,15 +23,15 @@
 //   * warp 0 (producer): K tiles into a ring of 128-key slots, block by block
 //     (tiled bulk copies, TMA), and query tiles into another; it runs ahead
 //     into the next item;
-//   * warps 1 and 2 (one thread each): S_t = K_t Q^T (M = 128 keys, N = the
+//   * warps 1 and 2: S_t = K_t Q^T (M = 128 keys, N = the
 //     tile's rows, K = head_dim) for key tile 0 and 1 into one of two
 //     tensor-memory buffers each (two issuers: the waits of one fall into the
 //     other's products); causal: a key tile starts with the query tile that
 //     holds the first token to see its first key, so the second tile's copy
 //     has time while the first one works alone.  Warp 1 allocates tensor
 //     memory;
-//   * warp 3 brings the rows' lse (base 2, negated) into a ring beside the
-//     query tiles', with a flag for tiles that hold rows without a weight;
+//   * warp 3 brings the rows' lse (base 2, negated) beside the query tiles of
+//     the ring, with a flag for tiles that hold rows without a weight;
 //   * warps 4..19: four groups of four, group (t, b) for the products of key
 //     tile t in buffer b, one key a thread (the lanes a warp may read go by
 //     its number modulo 4).  Each loads S from tensor memory 32 columns at a
@@ -77,7 +77,6 @@ static_assert(128 * kGroups * kRegsSums + 128 * kRegsOther <= kThreadsS * kRegsL
 constexpr uint32_t kTmemColsS = 512;  // S of tile t, buffer b at 128 (2 t + b)
 constexpr uint32_t kKSlice = kKeys * 128;  // bytes of a 64-element slice of a K tile
 constexpr int kMaxRing = 8;   // slots of the K and the query ring at most
-constexpr int kLseRing = 4;   // slots of the lse ring
 constexpr uint32_t kTileBytes = 6 * 32768;  // shared memory of both tile rings
 
 struct ScoreParams {
@@ -101,12 +100,12 @@ struct ScoreParams {
 // [tile][128], barriers; then, 1024-byte aligned, the K ring of rk tiles
 // [slice][128 keys][64] and the query ring of rq tiles [slice][rows][64].
 struct SLayout {
-    static constexpr size_t dead_off = kLseRing * kMaxCols * 4;
-    static constexpr size_t part_off = dead_off + kLseRing * 4;
+    static constexpr size_t dead_off = kMaxRing * kMaxCols * 4;
+    static constexpr size_t part_off = dead_off + kMaxRing * 4;
     static constexpr size_t bar_off = part_off + kTiles * kKeys * 4;
-    // k_full, k_free, q_full, q_free [kMaxRing], l_full, l_free [kLseRing],
-    // s_full[2][2], s_free[2][2], done[2]
-    static constexpr int kBars = 4 * kMaxRing + 2 * kLseRing + 8 + 2;
+    // k_full, k_free, q_full, q_free, l_full, l_free [kMaxRing], s_full[2][2],
+    // s_free[2][2], done[2]
+    static constexpr int kBars = 6 * kMaxRing + 8 + 2;
     static constexpr size_t tmem_off = bar_off + 8 * kBars;
     static constexpr size_t flag_off = tmem_off + 4;
     static constexpr size_t small = (flag_off + 4 + 1023) / 1024 * 1024;
@@ -285,8 +284,19 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, unsigne
 }
 
 // ---------------------------------------------------------------------------
-// warps 1 and 2, one thread each: S = K Q^T for key tile t
+// warps 1 and 2: S = K Q^T for key tile t.  The whole warp goes through the
+// waits and one elected lane issues: an issuer's own instructions, each behind
+// the one before, take longer than the products if they are many, and values
+// that are the same in the warp stay in uniform registers, where the products
+// want their descriptors.
 // ---------------------------------------------------------------------------
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0u;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 template <int D>
 __device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint32_t fmt,
                                               unsigned char *sk, unsigned char *sq, uint32_t tmem,
@@ -295,62 +305,75 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint3
     constexpr uint32_t ktile = KB * kKSlice;
     const uint32_t cols = 1u << (P.lg_nh + P.lg_nq);
     const uint32_t idesc = umma_idesc_f16(fmt, 0, 0, kKeys, cols);
-    const uint32_t ak = smem_u32(sk), aq = smem_u32(sq);
-    Ring kr, qr, lr, sr;
+    const uint32_t q_bytes = cols * 128u * KB;
+    const uint64_t dk0 = umma_desc_sw128(smem_u32(sk), 16, 1024);
+    const uint64_t dq0 = umma_desc_sw128(smem_u32(sq), 16, 1024);
+    const uint32_t q_slice16 = cols * 128u / 16u;  // (head_dim 128: one further slice)
+    Ring kr, qr, sr;
     bool ok = true;
+    // a whole warp's wait
+    auto wait = [&](uint64_t *bar, uint32_t phase) {
+        ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag));
+        return ok;
+    };
     for (unsigned r = 0; ok && item_id(r) < P.num_items; ++r) {
         const SItem it = score_item(P, item_id(r));
         if (!it.run) continue;
-        const int first = first_tile(P, it, t);
         const bool two = it.k0 + kKeys < it.L;
         Ring ks = kr;  // this key tile's slot
         kr.next(P.rk);
         if (t == 1) ks = kr;
         if (two) kr.next(P.rk);
-        for (int tt = it.tt0; ok && tt < it.tt1; ++tt)
-            for (int hg = 0; ok && hg < P.head_groups; ++hg) {
-                // Both issuers pass through every query tile: a wait by parity
-                // must never be a whole ring ahead or behind.  (The lse is
-                // waited for so that a group that has seen the product
-                // complete knows its slot's phase.)
-                ok = mbar_wait(&B.q_full[qr.slot], qr.phase, abort_flag) &&
-                     mbar_wait(&B.l_full[lr.slot], lr.phase, abort_flag);
-                if (!ok) break;
-                if (tt < first) {  // the other key tile alone: give this one's shares back
-                    mbar_arrive(&B.q_free[qr.slot]);
-                    for (int i = 0; i < 4; ++i) mbar_arrive(&B.l_free[lr.slot]);
-                    qr.next(P.rq);
-                    lr.next(kLseRing);
-                    continue;
-                }
-                const int b = sr.slot;
-                ok = (tt > first || hg > 0 || mbar_wait(&B.k_full[ks.slot], ks.phase, abort_flag)) &&
-                     mbar_wait(&B.s_free[2 * t + b], sr.phase ^ 1u, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t kt = ak + (uint32_t)ks.slot * ktile;
-                const uint32_t qt = aq + (uint32_t)qr.slot * cols * 128u * KB;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t in_slice = (uint32_t)((kk & 3) * 32);
-                    umma_f16(tmem + (uint32_t)(128 * (2 * t + b)),
-                             umma_desc_sw128(kt + (uint32_t)(kk >> 2) * kKSlice + in_slice, 16, 1024),
-                             umma_desc_sw128(qt + (uint32_t)(kk >> 2) * cols * 128u + in_slice, 16, 1024),
-                             idesc, kk > 0 ? 1u : 0u);
-                }
-                umma_commit(&B.s_full[2 * t + b]);
-                umma_commit(&B.q_free[qr.slot]);
-                sr.next(2);
-                qr.next(P.rq);
-                lr.next(kLseRing);
+        const int first = first_tile(P, it, t);
+        // Both issuers pass through every query tile (a wait by parity must
+        // never be a whole ring ahead or behind), and give back their share of
+        // those that are the other key tile's alone.
+        int n = (first - it.tt0) * P.head_groups;
+        for (; n > 0; --n) {
+            if (!wait(&B.q_full[qr.slot], qr.phase) || !wait(&B.l_full[qr.slot], qr.phase)) break;
+            if (elect_one()) {
+                mbar_arrive(&B.q_free[qr.slot]);
+                for (int i = 0; i < 4; ++i) mbar_arrive(&B.l_free[qr.slot]);
             }
-        if (t == 0 || two) umma_commit(&B.k_free[ks.slot]);
+            qr.next(P.rq);
+        }
+        n = (it.tt1 - first) * P.head_groups;
+        if (!ok || n == 0) continue;
+        if (!wait(&B.k_full[ks.slot], ks.phase)) break;
+        const uint32_t dk = uniform((uint32_t)dk0 + (uint32_t)ks.slot * (ktile / 16u));
+        for (; n > 0; --n) {
+            if (!wait(&B.q_full[qr.slot], qr.phase)) break;
+            if (!wait(&B.s_free[2 * t + sr.slot], sr.phase ^ 1u)) break;
+            tc_fence_after();
+            const uint32_t dq = uniform((uint32_t)dq0 + (uint32_t)qr.slot * (q_bytes / 16u));
+            const uint32_t ts = uniform(tmem + (uint32_t)(128 * (2 * t + sr.slot)));
+            if (elect_one()) {
+                // a step of 16 elements is 32 bytes inside a slice; the offsets
+                // (16-byte units) never carry out of the address field
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+                    umma_f16(ts,
+                             (dk0 & 0xffffffff00000000ull) |
+                                 (dk + (uint32_t)((kk >> 2) * (kKSlice / 16) + (kk & 3) * 2)),
+                             (dq0 & 0xffffffff00000000ull) |
+                                 (dq + (uint32_t)((kk & 3) * 2) + ((kk >> 2) ? q_slice16 : 0u)),
+                             idesc, kk > 0 ? 1u : 0u);
+                umma_commit(&B.s_full[2 * t + sr.slot]);
+                umma_commit(&B.q_free[qr.slot]);
+                if (n == 1) umma_commit(&B.k_free[ks.slot]);
+            }
+            __syncwarp();
+            sr.next(2);
+            qr.next(P.rq);
+        }
     }
     if (!ok) {
         *abort_flag = 1;
-        if (P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
+        if (P.err && elect_one()) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
     }
-    umma_commit(&B.done[t]);  // after every product issued: the teardown
+    // after every product issued (by the same lane): the teardown
+    if (elect_one()) umma_commit(&B.done[t]);
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -363,34 +386,60 @@ __device__ __forceinline__ void run_score_lse(const ScoreParams &P, float *s_lse
     constexpr int kPer = kMaxCols / 32;
     Ring lr;
     bool ok = true;
-    for (unsigned r = 0; ok && item_id(r) < P.num_items; ++r) {
-        const SItem it = score_item(P, item_id(r));
-        if (!it.run) continue;
-        for (int tt = it.tt0; ok && tt < it.tt1; ++tt)
-            for (int hg = 0; ok && hg < P.head_groups; ++hg) {
-                float v[kPer];
-                bool any_dead = false;
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) {
-                    const int row = 32 * k + lane, i = (tt << P.lg_nq) + (row >> P.lg_nh);
-                    float l = -INFINITY;  // no such row, or one without a weight
-                    if (row < cols && i < it.n)
-                        l = __ldg(&P.lse[(size_t)(it.tok0 + i) * P.num_heads + it.hk * P.G +
-                                         (hg << P.lg_nh) + (row & ((1 << P.lg_nh) - 1))]);
-                    v[k] = l == -INFINITY ? -INFINITY : -l * 1.4426950408889634f;
-                    any_dead |= row < cols && l == -INFINITY;
-                }
-                any_dead = __any_sync(0xffffffffu, any_dead);
-                if (lane == 0) ok = mbar_wait(&B.l_free[lr.slot], lr.phase ^ 1u, abort_flag);
-                ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-                if (!ok) break;
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) s_lse[lr.slot * kMaxCols + 32 * k + lane] = v[k];
-                if (lane == 0) s_dead[lr.slot] = any_dead;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&B.l_full[lr.slot]);
-                lr.next(kLseRing);
+    // the next query tile, whose lse is on its way
+    unsigned r = 0;
+    SItem it;
+    int tt = 0, hg = 0;
+    auto next_item = [&]() {  // the first item with work from round r on
+        for (; item_id(r) < P.num_items; ++r) {
+            it = score_item(P, item_id(r));
+            if (it.run) {
+                tt = it.tt0;
+                hg = 0;
+                return true;
             }
+        }
+        return false;
+    };
+    float l[kPer];
+    auto load = [&]() {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            const int row = 32 * k + lane, i = (tt << P.lg_nq) + (row >> P.lg_nh);
+            l[k] = -INFINITY;  // no such row, or one without a weight
+            if (row < cols && i < it.n)
+                l[k] = __ldg(&P.lse[(size_t)(it.tok0 + i) * P.num_heads + it.hk * P.G +
+                                    (hg << P.lg_nh) + (row & ((1 << P.lg_nh) - 1))]);
+        }
+    };
+    bool live = next_item();
+    if (live) load();
+    while (live) {
+        float v[kPer];
+        bool any_dead = false;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) {
+            v[k] = l[k] == -INFINITY ? -INFINITY : -l[k] * 1.4426950408889634f;
+            any_dead |= 32 * k + lane < cols && l[k] == -INFINITY;
+        }
+        any_dead = __any_sync(0xffffffffu, any_dead);
+        if (++hg == P.head_groups) {
+            hg = 0;
+            if (++tt == it.tt1) {
+                ++r;
+                live = next_item();
+            }
+        }
+        if (live) load();
+        if (lane == 0) ok = mbar_wait(&B.l_free[lr.slot], lr.phase ^ 1u, abort_flag);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        if (!ok) break;
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) s_lse[lr.slot * kMaxCols + 32 * k + lane] = v[k];
+        if (lane == 0) s_dead[lr.slot] = any_dead;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.l_full[lr.slot]);
+        lr.next(P.rq);
     }
     if (!ok && lane == 0) {
         *abort_flag = 1;
@@ -532,11 +581,13 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int 
         };
         step(p);
         cnt += np;
-        for (; ok && p < np; p += 2, step(2)) {
-            const int q = qp + p, slot = q % kLseRing;
+        unsigned q = (unsigned)(qp + p);  // its query tile, counted from the CTA's first
+        for (; ok && p < np; p += 2, q += 2, step(2)) {
+            const int slot = (int)(q % (unsigned)P.rq);
             ok = mbar_wait(&B.s_full[2 * t + b], (uint32_t)taken & 1u, abort_flag) &&
-                 // staged before the product was issued: only orders the reads
-                 mbar_wait(&B.l_full[slot], (uint32_t)(q / kLseRing) & 1u, abort_flag);
+                 // (the slot's phase before has completed: this group has read the
+                 // tile before last, or the issuer has seen the last one staged)
+                 mbar_wait(&B.l_full[slot], (q / (unsigned)P.rq) & 1u, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {  // at once: no sum that lacks this product is written
                 *abort_flag = 1;
@@ -601,8 +652,8 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     B.q_full = B.k_free + kMaxRing;
     B.q_free = B.q_full + kMaxRing;
     B.l_full = B.q_free + kMaxRing;
-    B.l_free = B.l_full + kLseRing;
-    B.s_full = B.l_free + kLseRing;
+    B.l_free = B.l_full + kMaxRing;
+    B.s_full = B.l_free + kMaxRing;
     B.s_free = B.s_full + 4;
     B.done = B.s_free + 4;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -611,10 +662,12 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         prefetch_tmap(&P.tmap_k);
         for (int b = 0; b < L::kBars; ++b) mbar_init(&bars[b], 1);
         for (int b = 0; b < 4; ++b) mbar_init(&B.s_free[b], kKeys);
-        // a slot of these rings is given back for each key tile: by the four
-        // warps of its group, and by its products
-        for (int b = 0; b < kLseRing; ++b) mbar_init(&B.l_free[b], 8);
-        for (int b = 0; b < kMaxRing; ++b) mbar_init(&B.q_free[b], 2);
+        // a query slot is given back for each key tile, the tile by its products
+        // and the lse by the four warps of its group
+        for (int b = 0; b < kMaxRing; ++b) {
+            mbar_init(&B.q_free[b], 2);
+            mbar_init(&B.l_free[b], 8);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -636,12 +689,10 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         if (warp == 0) {
             run_score_producer<D>(P, sk, sq, B, abort_flag, lane);
         } else if (warp <= 2) {
-            if (lane == 0) {
-                run_score_mma<D>(P, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
-                // every product has completed before tensor memory is released
-                volatile int never = 0;
-                mbar_drain_wait(&B.done[warp - 1], 0, &never);
-            }
+            run_score_mma<D>(P, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
+            // every product has completed before tensor memory is released
+            volatile int never = 0;
+            mbar_drain_wait(&B.done[warp - 1], 0, &never);
             __syncwarp();
         } else {
             run_score_lse(P, s_lse, s_dead, B, abort_flag, lane);
