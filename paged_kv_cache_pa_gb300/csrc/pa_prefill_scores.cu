@@ -581,13 +581,27 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int 
         };
         step(p);
         cnt += np;
-        unsigned q = (unsigned)(qp + p);  // its query tile, counted from the CTA's first
-        for (; ok && p < np; p += 2, q += 2, step(2)) {
-            const int slot = (int)(q % (unsigned)P.rq);
-            ok = mbar_wait(&B.s_full[2 * t + b], (uint32_t)taken & 1u, abort_flag) &&
-                 // (the slot's phase before has completed: this group has read the
-                 // tile before last, or the issuer has seen the last one staged)
-                 mbar_wait(&B.l_full[slot], (q / (unsigned)P.rq) & 1u, abort_flag);
+        // the ring's slot of its query tile
+        int slot = (int)((unsigned)(qp + p) % (unsigned)P.rq);
+        uint32_t phase = ((unsigned)(qp + p) / (unsigned)P.rq) & 1u;
+        auto slot_step = [&]() {
+            slot += 2;
+            if (slot >= P.rq) {
+                slot -= P.rq;
+                phase ^= 1u;
+            }
+        };
+        const int p_first = p;
+        for (; ok && p < np; p += 2, step(2), slot_step()) {
+            // The lse is there by now or soon; waiting for it first hides that
+            // wait behind the product's.  That its slot's phase before has
+            // completed is known where this group has read the tile before
+            // last; at the start of key tile 1's part of an item it is known
+            // with the product, whose issuer has seen the last tile staged.
+            const bool late = t == 1 && p == p_first;
+            if (!late) ok = mbar_wait(&B.l_full[slot], phase, abort_flag);
+            ok = ok && mbar_wait(&B.s_full[2 * t + b], (uint32_t)taken & 1u, abort_flag);
+            if (late) ok = ok && mbar_wait(&B.l_full[slot], phase, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) {  // at once: no sum that lacks this product is written
                 *abort_flag = 1;
