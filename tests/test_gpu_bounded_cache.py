@@ -1,0 +1,209 @@
+"""The bounded cache as a server runs it: rotary writes, prompt attention with
+scores, a fork, decode steps with scores, eviction in place with the block
+manager's copies, and decode steps after it.  A list of rows per (layer,
+sequence, head) follows along in 64 bits; every output and score is compared
+with it (tolerances: cachelib)."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import paged_kv_cache_pa_gb300 as pa
+from cachelib import logits64, weights64
+from paged_kv_cache_pa_gb300.manager import BlockManager
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+class Server:
+    def __init__(self, layers, H, Hkv, D, dtype, block, blocks, rows, max_len):
+        g = torch.Generator(device=DEV).manual_seed(1)
+        self.g, self.H, self.Hkv, self.D, self.dtype, self.B = g, H, Hkv, D, dtype, block
+        self.layers, self.max_len, self.scale = layers, max_len, D ** -0.5
+        pool = (blocks, Hkv, block, D)
+        self.k = [torch.full(pool, float("nan"), dtype=dtype, device=DEV) for _ in range(layers)]
+        self.v = [torch.full(pool, float("nan"), dtype=dtype, device=DEV) for _ in range(layers)]
+        self.scores = [torch.zeros(rows, Hkv, max_len, device=DEV) for _ in range(layers)]
+        self.bm = BlockManager(blocks, 0, block)
+        self.err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        self.rotary = pa.Rotary([10000.0 ** (-i / (D // 2)) for i in range(D // 2)],
+                                axes=[min(2, 3 * i // (D // 2)) for i in range(D // 2)])
+        # the follower: rows and scores of every (layer, batch row, head)
+        self.ref = [[[([], [], []) for _ in range(Hkv)] for _ in range(rows)] for _ in range(layers)]
+
+    def randn(self, *shape):
+        return torch.randn(shape, generator=self.g, device=DEV).to(self.dtype)
+
+    def copies(self):
+        pairs = self.bm.take_copies()
+        if len(pairs):
+            pa.copy_blocks(self.k, self.v, torch.as_tensor(pairs, device=DEV), error_word=self.err)
+
+    def batch(self, seqs):
+        t, n = self.bm.build_batch(seqs, -(-self.max_len // self.B))
+        return torch.as_tensor(t, device=DEV), torch.as_tensor(n, device=DEV), n.tolist()
+
+    def write(self, layer, rows, counts, slots, positions):
+        """New tokens of the batch rows; returns the turned queries."""
+        T, H, Hkv, D = sum(counts), self.H, self.Hkv, self.D
+        qkv = self.randn(T, (H + 2 * Hkv) * D)
+        q, k, v = (x.view(T, -1, D) for x in qkv.split([H * D, Hkv * D, Hkv * D], 1))
+        out = pa.rotary_cache_write(q, k, v, positions, self.rotary, self.k[layer], self.v[layer], slots,
+                                    error_word=self.err)
+        blk, off, i = slots // self.B, slots % self.B, 0
+        for row, n in zip(rows, counts):
+            for h in range(Hkv):
+                rk, rv, rs = self.ref[layer][row][h]
+                rk.extend(self.k[layer][blk[i:i + n], h, off[i:i + n]].clone())
+                rv.extend(self.v[layer][blk[i:i + n], h, off[i:i + n]].clone())
+                rs.extend([0.0] * n)
+            i += n
+        return out
+
+    def follow(self, layer, row, q, out, first):
+        """Queries q [n][H][D] whose last sees every row; compare out, add the weights."""
+        n, G = q.shape[0], self.H // self.Hkv
+        for h in range(self.Hkv):
+            rk, rv, rs = self.ref[layer][row][h]
+            k, v = torch.stack(rk), torch.stack(rv).double()
+            L = len(rk)
+            hide = torch.ones(n, L, dtype=torch.bool, device=DEV).triu(L - n + 1)
+            add, tol = torch.zeros(L, dtype=torch.float64, device=DEV), torch.zeros(L, dtype=torch.float64, device=DEV)
+            for g in range(G):
+                x, e = logits64(q[:, h * G + g], k, self.scale)
+                p, pe = weights64(x.masked_fill(hide, -np.inf), e.masked_fill(hide, 0.0))
+                o = p @ v
+                lim = pe @ v.abs() + 2.0 ** -10 * (p @ v.abs()) + 2.0 ** -8 * o.abs() + 1e-6
+                assert bool(((out[:, h * G + g].double() - o).abs() <= lim).all())
+                add += p.sum(0)
+                tol += pe.sum(0) + n * 2.0 ** -22 * p.sum(0)
+            want = torch.tensor(rs, dtype=torch.float64, device=DEV) + add
+            got = self.scores[layer][row, h, :L].double()
+            assert bool(((got - want).abs() <= tol + 2.0 ** -23 * want + 1e-7).all())
+            assert not self.scores[layer][row, h, L:].any()
+            self.ref[layer][row][h] = (rk, rv, got.tolist())
+
+    def prompt(self, row, seq, n):
+        slots = torch.as_tensor(self.bm.append(seq, n), device=DEV)
+        self.copies()
+        tables, lens, _ = self.batch([seq])
+        qsl = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        pos = torch.stack([torch.arange(n), torch.arange(n) // 7, torch.arange(n) % 7]).to(DEV)
+        for layer in range(self.layers):
+            q = self.write(layer, [row], [n], slots, pos)
+            lse = torch.empty(n, self.H, device=DEV)
+            out = pa.prefill_attention(q, self.k[layer], self.v[layer], tables, qsl, lens, n, self.max_len, self.scale,
+                                       lse=lse, error_word=self.err)
+            pa.prefill_scores(q, lse, self.k[layer], tables, qsl, lens, n, self.max_len, self.scale,
+                              self.scores[layer][row:row + 1], error_word=self.err)
+            self.follow(layer, row, q, out, 0)
+
+    def step(self, seqs, positions):
+        slots = torch.as_tensor(np.concatenate([self.bm.append(s, 1) for s in seqs]), device=DEV)
+        self.copies()
+        tables, lens, _ = self.batch(seqs)
+        S = len(seqs)
+        pos = torch.tensor([positions] * 3, device=DEV)
+        for layer in range(self.layers):
+            q = self.write(layer, range(S), [1] * S, slots, pos)
+            out = pa.decode_attention_scored(q, self.k[layer], self.v[layer], tables, lens, self.max_len, self.scale,
+                                             self.scores[layer], error_word=self.err)
+            for row in range(S):
+                self.follow(layer, row, q[row:row + 1], out[row:row + 1], 0)
+
+    def evict(self, seqs, budget, sink, recent):
+        tables0, lens0, host = self.batch(seqs)
+        keep = [min(n, budget) for n in host]
+        for s, n in zip(seqs, keep):
+            self.bm.make_private(s, n)
+        self.copies()
+        tables, lens, _ = self.batch(seqs)
+        kept = [torch.full((len(seqs), self.Hkv, budget), -1, dtype=torch.int32, device=DEV) for _ in self.k]
+        new = pa.evict_tokens(self.k, self.v, self.scores, tables, lens,
+                              torch.full_like(lens, budget), self.max_len, budget, num_sink=sink, num_recent=recent,
+                              kept=kept, error_word=self.err)
+        assert new.tolist() == keep
+        for s, n in zip(seqs, keep):
+            self.bm.shrink(s, n)
+        for layer in range(self.layers):
+            for row, n in enumerate(keep):
+                for h in range(self.Hkv):
+                    rk, rv, rs = self.ref[layer][row][h]
+                    idx = kept[layer][row, h, :n].tolist()
+                    assert idx == sorted(set(idx))
+                    L = len(rk)
+                    r = min(recent, n)
+                    a = min(sink, n - r)
+                    assert idx[:a] == list(range(a)) and idx[n - r:] == list(range(L - r, L))
+                    if n < L:
+                        mid = idx[a:n - r]
+                        gone = sorted(set(range(a, L - r)) - set(mid))
+                        assert min(rs[i] for i in mid) >= max(rs[i] for i in gone)
+                    self.ref[layer][row][h] = tuple([x[i] for i in idx] for x in (rk, rv, rs))
+
+
+@pytest.mark.parametrize("H,Hkv,D,dtype,block", [(4, 2, 64, torch.bfloat16, 8), (6, 1, 128, torch.float16, 16),
+                                                 (2, 2, 128, torch.bfloat16, 32)])
+def test_prompts_forks_decode_evict_decode(H, Hkv, D, dtype, block):
+    srv = Server(2, H, Hkv, D, dtype, block, 40 * 16 // block, 3, 160)
+    a = srv.bm.new_sequence()
+    srv.prompt(0, a, 90)
+    b = srv.bm.fork(a)                       # shares every block; its scores are its own from here
+    for layer in range(2):
+        srv.scores[layer][1].copy_(srv.scores[layer][0])
+        srv.ref[layer][1] = [tuple(list(x) for x in t) for t in srv.ref[layer][0]]
+    c = srv.bm.new_sequence()
+    srv.prompt(2, c, 33)
+    seqs, pos = [a, b, c], [90, 90, 33]
+    for _ in range(3):
+        srv.step(seqs, pos)
+        pos = [p + 1 for p in pos]
+    srv.evict(seqs, 48, 4, 16)               # two shrink, one (36 tokens) stays
+    assert [srv.bm.seq_len(s) for s in seqs] == [48, 48, 36]
+    for _ in range(14):
+        srv.step(seqs, pos)
+        pos = [p + 1 for p in pos]
+    srv.evict(seqs, 40, 0, 8)                # now all three
+    assert [srv.bm.seq_len(s) for s in seqs] == [40, 40, 40]
+    for _ in range(2):
+        srv.step(seqs, pos)
+        pos = [p + 1 for p in pos]
+    assert int(srv.err.item()) == 0
+    for s in seqs:
+        srv.bm.free(s)
+    assert srv.bm.num_free_gpu == 40 * 16 // block
+
+
+def test_scores_of_a_window_choose_what_a_prompt_keeps():
+    """A window of the last queries scores the prompt, which is then written out of place."""
+    H, Hkv, D, n, W, keep = 8, 2, 64, 500, 32, 100
+    srv = Server(1, H, Hkv, D, torch.float16, 16, 64, 1, 512)
+    seq = srv.bm.new_sequence()
+    slots = torch.as_tensor(srv.bm.append(seq, n), device=DEV)
+    tables, lens, _ = srv.batch([seq])
+    pos = torch.arange(n, device=DEV).repeat(3, 1)
+    q = srv.write(0, [0], [n], slots, pos)
+    lse = torch.empty(n, H, device=DEV)
+    pa.prefill_attention(q, srv.k[0], srv.v[0], tables, torch.tensor([0, n], dtype=torch.int32, device=DEV), lens, n,
+                         512, srv.scale, lse=lse)
+    pa.prefill_scores(q[-W:], lse[-W:], srv.k[0], tables, torch.tensor([0, W], dtype=torch.int32, device=DEV), lens, W,
+                      512, srv.scale, srv.scores[0])
+    total = srv.scores[0].double().sum()
+    assert abs(float(total) - W * H) < 1e-4 * W * H  # every row's weights sum to one
+    fork = srv.bm.fork(seq)                  # the kept tokens go to blocks of their own
+    srv.bm.make_private(fork, keep)
+    pairs = srv.bm.take_copies()
+    dst = torch.as_tensor(pairs[None, :, 1].astype(np.int32).copy(), device=DEV)
+    out = [torch.zeros_like(srv.scores[0])]
+    kept = [torch.empty(1, Hkv, keep, dtype=torch.int32, device=DEV)]
+    before = srv.k[0][pairs[:, 0]].view(torch.int16).clone()
+    pa.evict_tokens(srv.k, srv.v, srv.scores, tables, lens, torch.tensor([keep], dtype=torch.int32, device=DEV), 512,
+                    keep, num_sink=4, num_recent=W, dst_block_tables=dst, scores_out=out, kept=kept)
+    assert torch.equal(srv.k[0][pairs[:, 0]].view(torch.int16), before)  # the prompt is as it was
+    for h in range(Hkv):
+        idx = kept[0][0, h].long()
+        s = srv.scores[0][0, h]
+        want = torch.sort(torch.cat([torch.arange(4, device=DEV), torch.arange(n - W, n, device=DEV),
+                                     4 + torch.topk(s[4:n - W], keep - 4 - W).indices])).values
+        assert torch.equal(idx, want) and torch.equal(out[0][0, h, :keep], s[want])
