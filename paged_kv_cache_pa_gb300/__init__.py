@@ -144,27 +144,42 @@ def _check(status: int, op: str) -> None:
         raise PaError(status, op)
 
 
+_torch_module = None
+
+
+def _torch():
+    """torch, imported with the first call (an import statement in every call
+    costs more than this)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_DTYPE_CODES = {}
+
+
 def _dtype_code(dt) -> int:
-    import torch
-    if dt == torch.float16:
-        return PA_F16
-    if dt == torch.bfloat16:
-        return PA_BF16
-    if dt == torch.float32:
-        return PA_F32
-    raise TypeError(f"unsupported dtype {dt}")
+    if not _DTYPE_CODES:
+        torch = _torch()
+        _DTYPE_CODES.update({torch.float16: PA_F16, torch.bfloat16: PA_BF16,
+                             torch.float32: PA_F32})
+    code = _DTYPE_CODES.get(dt)
+    if code is None:
+        raise TypeError(f"unsupported dtype {dt}")
+    return code
 
 
 def _dev(t, name):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    if t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda
+                     else f"{name} must be contiguous")
 
 
 def _stream_ptr(stream, device) -> int:
-    import torch
+    torch = _torch()
     if stream is None:
         # the current stream's handle, without making a Stream object
         return torch._C._cuda_getCurrentRawStream(device.index)
@@ -179,7 +194,7 @@ def cache_write(key, value, k_cache, v_cache, slot_mapping, error_word=None,
                 stream=None) -> None:
     """Write key[t] / value[t] ([T][Hkv][D]) into pool slot slot_mapping[t]
     (int64; < 0 skips).  Pools: [num_blocks][Hkv][block_size][D]."""
-    import torch
+    torch = _torch()
     if slot_mapping.dtype != torch.int64:
         raise TypeError("slot_mapping must be int64")
     nb, hkv, bs, d = k_cache.shape
@@ -244,11 +259,11 @@ def _rows(t, name):
     dense and whose tokens may be apart (a slice of a projection's rows)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    _, h, d = t.shape
-    st = t.stride()
-    if st[2] != 1 or (h > 1 and st[1] != d):
+    n, h, d = t.shape
+    token, head, element = t.stride()
+    if element != 1 or (h > 1 and head != d):
         raise ValueError(f"{name} must have dense heads")
-    return t.data_ptr(), (st[0] if t.shape[0] > 1 else h * d)
+    return t.data_ptr(), (token if n > 1 else h * d)
 
 
 def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_cache,
@@ -259,13 +274,14 @@ def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_
     are free (slices of one projection's rows).  Returns the turned query:
     ``query_out``, ``query`` itself for an update in place, or a new dense
     tensor."""
-    import torch
+    torch = _torch()
     nb, hkv, bs, d = k_cache.shape
     T, H, D = query.shape
-    if tuple(key.shape) != (T, hkv, d) or key.shape != value.shape or D != d:
+    new, dt = (T, hkv, d), query.dtype
+    if key.shape != new or value.shape != new or D != d:
         raise ValueError("shape mismatch between query/key/value and the pools")
-    if v_cache.shape != k_cache.shape or not (
-            query.dtype == key.dtype == value.dtype == k_cache.dtype == v_cache.dtype):
+    if v_cache.shape != (nb, hkv, bs, d) or not (
+            dt == key.dtype == value.dtype == k_cache.dtype == v_cache.dtype):
         raise ValueError("pools, query, key and value must have one dtype, the pools one shape")
     if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
         raise TypeError("slot_mapping and positions must be int64")
@@ -275,14 +291,14 @@ def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_
             (positions.shape[0] if positions.dim() == 2 else 1) < rotary.num_axes:
         raise ValueError("positions must be [axes][T] with an axis for each the frequencies name")
     if query_out is None:
-        query_out = torch.empty(T, H, D, dtype=query.dtype, device=query.device)
-    elif query_out.shape != query.shape or query_out.dtype != query.dtype:
+        query_out = torch.empty(T, H, D, dtype=dt, device=query.device)
+    elif query_out is not query and (query_out.shape != (T, H, D) or query_out.dtype != dt):
         raise ValueError("query_out must match the query")
     st = load_library().pa_rotary_cache_write(
         *_rows(query_out, "query_out"), *_rows(query, "query"), *_rows(key, "key"),
         *_rows(value, "value"), _dev(positions, "positions"), rotary._ptr,
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"),
-        T, nb, bs, H, hkv, d, _dtype_code(query.dtype), _opt_ptr(error_word, "error_word"),
+        T, nb, bs, H, hkv, d, _dtype_code(dt), _opt_ptr(error_word, "error_word"),
         _stream_ptr(stream, query.device))
     _check(st, "pa_rotary_cache_write")
     return query_out
@@ -315,7 +331,7 @@ def decode_attention(query, k_cache, v_cache, block_tables, context_lens,
     ``out_dtype`` / ``out`` says the input dtype).  ``workspace`` (uint8, >=
     decode_workspace_size bytes) is allocated here when not given.  Pools
     are [num_blocks][Hkv][block_size][D]."""
-    import torch
+    torch = _torch()
     S, H, D = query.shape
     nb, hkv, bs, d2 = k_cache.shape
     if d2 != D or v_cache.shape != k_cache.shape:
@@ -350,7 +366,7 @@ def decode_attention_contiguous(query, k_cache, v_cache, context_lens, max_conte
     """Decode attention over a contiguous (unpaged) cache
     k_cache / v_cache [S][Hkv][max_rows][D] (max_rows a multiple of 16); the
     baseline that measures what the block table costs."""
-    import torch
+    torch = _torch()
     S, H, D = query.shape
     s2, hkv, rows, d2 = k_cache.shape
     if s2 != S or d2 != D or v_cache.shape != k_cache.shape:
@@ -380,12 +396,13 @@ def decode_scored_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: in
 
 def _score_rows(scores, rows, name="scores"):
     """Pointer and row stride of fp32 scores [..rows..][stride]."""
-    import torch
+    torch = _torch()
     if scores.dtype != torch.float32:
         raise TypeError(f"{name} must be float32")
-    if scores.dim() != 3 or tuple(scores.shape[:2]) != rows:
+    shape = scores.shape
+    if len(shape) != 3 or shape[:2] != rows:
         raise ValueError(f"{name} must be [S][Hkv][positions]")
-    return _dev(scores, name), scores.shape[2]
+    return _dev(scores, name), shape[2]
 
 
 def decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
@@ -396,7 +413,7 @@ def decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
     [S][Hkv][>= max_context_len], row s for the batch's sequence s).
     ``workspace`` (uint8, >= decode_scored_workspace_size bytes) is allocated
     here when not given.  Returns ``out``."""
-    import torch
+    torch = _torch()
     S, H, D = query.shape
     nb, hkv, bs, d2 = k_cache.shape
     if d2 != D or v_cache.shape != k_cache.shape:
@@ -430,7 +447,7 @@ def copy_blocks(k_caches: Sequence, v_caches: Sequence, block_pairs, error_word=
                 stream=None) -> None:
     """For every layer: pools[dst] = pools[src] for each (src, dst) row of
     block_pairs (int64 [P][2], on the device)."""
-    import torch
+    torch = _torch()
     if len(k_caches) != len(v_caches) or not k_caches:
         raise ValueError("need the same, non-zero number of K and V pools")
     if block_pairs.dtype != torch.int64:
@@ -469,7 +486,7 @@ def swap_blocks(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_caches: Se
     of block_pairs (int64 [P][2], on the device).  Pools are
     [num_blocks][Hkv][block_size][D]; either side may be device memory or
     pinned host memory (the CPU swap space)."""
-    import torch
+    torch = _torch()
     L = len(dst_k_caches)
     if not (L == len(dst_v_caches) == len(src_k_caches) == len(src_v_caches)) or not L:
         raise ValueError("need the same, non-zero number of pools on each side")
@@ -513,7 +530,7 @@ def prefill_attention(query, k_cache, v_cache, block_tables, query_start_loc, co
     prefill_workspace_size bytes) is allocated here when not given.  ``lse``
     (fp32 [T][H], optional) gets each row's log-sum-exp.  Returns out
     [T][H][D]."""
-    import torch
+    torch = _torch()
     T, H, D = query.shape
     nb, hkv, bs, d2 = k_cache.shape
     if d2 != D or v_cache.shape != k_cache.shape:
@@ -549,7 +566,7 @@ def prefill_attention(query, k_cache, v_cache, block_tables, query_start_loc, co
 
 
 def _lse_ptr(lse, T, H):
-    import torch
+    torch = _torch()
     if lse.dtype != torch.float32 or tuple(lse.shape) != (T, H):
         raise ValueError("lse must be float32 [T][H]")
     return _dev(lse, "lse")
@@ -572,7 +589,7 @@ def prefill_scores(query, lse, k_cache, block_tables, query_start_loc, context_l
     log-sum-exp (prefill_attention's).  ``workspace`` (uint8, >=
     prefill_scores_workspace_size bytes) is allocated here when not given.
     Returns ``scores``."""
-    import torch
+    torch = _torch()
     T, H, D = query.shape
     nb, hkv, bs, d2 = k_cache.shape
     if d2 != D or k_cache.dtype != query.dtype:
@@ -630,7 +647,7 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
     positions.  max_keep_len bounds the lengths left.  ``workspace`` (uint8,
     >= evict_workspace_size bytes) is allocated here when not given.  Returns
     new_lens, int32 [S]."""
-    import torch
+    torch = _torch()
     L = len(k_caches)
     if not L or len(v_caches) != L or len(scores) != L:
         raise ValueError("need the same, non-zero number of K pools, V pools and scores")
