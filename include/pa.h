@@ -329,6 +329,9 @@ pa_status_t pa_decode_attention_ex(void *out, pa_dtype_t out_dtype, const void *
                                    unsigned int *dev_error_word, pa_stream_t stream);
 
 /*
+ * (Workspaces of this and the following bounded-cache calls: calls on one
+ * stream may share one, whatever their sizes.)
+ *
  * pa_decode_scored_workspace_size -- bytes of device workspace
  * pa_decode_attention_scored needs for these sizes: that of
  * pa_decode_attention without shared prefixes, and a logit
@@ -701,9 +704,11 @@ size_t pa_evict_workspace_size(int num_layers, int num_seqs, int num_kv_heads,
  *               in place, into the first ceil(n / block_size) blocks of
  *               block_tables, which no other sequence may then share (make
  *               them private first, pa_bm_seq_make_private); blocks behind
- *               those are only read
+ *               those are only read.  Either way a block that is written is
+ *               named once (two sequences that write one block race)
  * context_lens, keep_lens  device int32 [num_seqs]
- * new_lens      device int32 [num_seqs]; other memory than both
+ * new_lens      device int32 [num_seqs]; other memory than both; may be the
+ *               context_lens of the next call on the stream
  * max_context_len  host-known bound on context_lens, <= block_size *
  *               max_blocks_per_seq
  * max_keep_len  host-known bound on n, <= max_context_len

@@ -266,11 +266,19 @@ pa_status_t pa_bm_seq_make_private(pa_block_manager_t *bm, int64_t seq, int num_
     int shared = 0;
     for (size_t i = 0; i < nb; ++i) shared += bm->gpu.refs(s->table[i]) > 1;
     if (shared > bm->gpu.num_free()) return PA_ERR_NO_BLOCKS;
+    // room for the pairs first, so that nothing has changed if there is none
+    const size_t queued = bm->copies.size();
+    try {
+        bm->copies.resize(queued + shared);
+    } catch (const std::bad_alloc &) {
+        return PA_ERR_NO_BLOCKS;
+    }
+    size_t next = queued;
     for (size_t i = 0; i < nb; ++i) {
         const int old = s->table[i];
         if (bm->gpu.refs(old) <= 1) continue;
         const int fresh = bm->gpu.alloc();
-        bm->copies.emplace_back(old, fresh);
+        bm->copies[next++] = {old, fresh};
         bm->gpu.release(old);
         s->table[i] = fresh;
     }

@@ -823,7 +823,6 @@ extern "C" pa_status_t pa_decode_attention_scored(
     pa_stream_t stream) {
     PA_NVTX_RANGE("pa_decode_attention_scored");
     if (score_stride < max_context_len) return PA_ERR_INVALID_ARG;
-    if (num_kv_heads > 65535) return PA_ERR_UNSUPPORTED;
     if (num_seqs > 0 && (!scores || !aligned(scores, 4))) return PA_ERR_INVALID_ARG;
     return decode_impl(out, out_dtype, query, k_cache, v_cache, block_tables, max_blocks_per_seq,
                        0, context_lens, max_context_len, num_seqs, num_heads, num_kv_heads,

@@ -136,8 +136,11 @@ __global__ void __launch_bounds__(kSelThreads)
     __shared__ unsigned s_total;  // the segment's tokens above the threshold, and at it << 16
     uint32_t *const s_key = reinterpret_cast<uint32_t *>(s_key4);
     constexpr int kWarps = kSelThreads / 32;
-    pdl_trigger();
     pdl_wait();  // earlier kernels may still write what this reads, or read what it writes
+    // The move kernel may be set up now.  Without one the next call's kernels
+    // come next, and those read new_lens (as their context lengths) as soon as
+    // they start: then nothing is let through before this grid has ended.
+    if (P.max_chunks) pdl_trigger();
     const unsigned unit = blockIdx.x / CS;
     const int rank = CS > 1 ? (int)cluster_rank() : 0;
     const int hk = (int)(unit % (unsigned)P.num_kv_heads);
@@ -391,7 +394,8 @@ template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveThreads)
     evict_move_kernel(const __grid_constant__ EvictParams P) {
     __shared__ int s_chunk;
-    pdl_trigger();
+    // (no dependent is let through early: the next call's plan may write to a
+    // workspace that it shares with this one as soon as it starts)
     pdl_wait();
     const unsigned unit = blockIdx.x / (unsigned)P.max_chunks;
     int chunk = (int)(blockIdx.x - unit * (unsigned)P.max_chunks);

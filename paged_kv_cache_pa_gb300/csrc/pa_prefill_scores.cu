@@ -645,7 +645,6 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     prefill_scores_kernel(const __grid_constant__ ScoreParams P, uint32_t fmt) {
     using L = SLayout;
     extern __shared__ __align__(1024) unsigned char smem[];
-    pdl_trigger();
     // the swizzled tiles need 1024-byte alignment, which the start of dynamic
     // shared memory has
     if (smem_u32(smem) & 1023u) {
@@ -700,6 +699,7 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         pdl_wait();
+        pdl_trigger();  // (after the wait: what follows may start before this grid ends, not before those)
         if (warp == 0) {
             run_score_producer<D>(P, sk, sq, B, abort_flag, lane);
         } else if (warp <= 2) {

@@ -117,7 +117,6 @@ template <typename T, bool IL>
 __global__ void __launch_bounds__(kRotThreads)
     rotary_cache_write_kernel(const __grid_constant__ RotaryParams P) {
     extern __shared__ __align__(16) float2 s_cs[];  // [token][pair]
-    pdl_trigger();
     const int lpr = 1 << P.lg_lpr, rows_at_once = 1 << P.lg_rows;
     const int j = threadIdx.x & (lpr - 1);
     const int r0 = ((int)threadIdx.x >> P.lg_lpr) & (rows_at_once - 1);
@@ -128,6 +127,7 @@ __global__ void __launch_bounds__(kRotThreads)
     const int H = P.num_heads, Hkv = P.num_kv_heads, rows = H + 2 * Hkv;
     const int pairs = P.rot.rotary_dim / 2, rot_units = pairs / 8;
     pdl_wait();  // earlier kernels on the stream may still read or write what this touches
+    pdl_trigger();  // (after the wait: what follows may start before this grid ends, not before those)
 
     // this thread's two chunks of a row
     int ca, cb;

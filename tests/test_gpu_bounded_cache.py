@@ -207,3 +207,127 @@ def test_scores_of_a_window_choose_what_a_prompt_keeps():
         want = torch.sort(torch.cat([torch.arange(4, device=DEV), torch.arange(n - W, n, device=DEV),
                                      4 + torch.topk(s[4:n - W], keep - 4 - W).indices])).values
         assert torch.equal(idx, want) and torch.equal(out[0][0, h, :keep], s[want])
+
+
+@pytest.mark.parametrize("keep", [300, 0])
+@pytest.mark.parametrize("H", [2, 12])
+def test_new_lengths_go_straight_into_the_next_calls(H, keep):
+    """new_lens is the next calls' context_lens: they must see it although they are set up
+    while the eviction still runs (keep 0: there is nothing to move)."""
+    from cachelib import Cache
+    Hkv, S, L = 2, 48, 1500
+    q = torch.randn(S, H, 64, device=DEV).to(torch.float16)
+    want = None
+    for i in range(12):
+        c = Cache([L] * S, Hkv, 64, torch.float16, 16, seed=21)
+        sc = torch.rand(S, Hkv, L, generator=torch.Generator(device=DEV).manual_seed(3), device=DEV)
+        budget = torch.full((S,), keep, dtype=torch.int32, device=DEV)
+        new = torch.full((S,), L, dtype=torch.int32, device=DEV)  # what a reader too early would see
+        torch.cuda.synchronize()
+        pa.evict_tokens(c.k, c.v, [sc], c.tables, c.lens, budget, L, keep, new_lens=new)
+        if i == 0:
+            torch.cuda.synchronize()
+        out = pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, new, L, 0.125, sc)
+        plain = pa.decode_attention(q, c.k[0], c.v[0], c.tables, new, L, 0.125)
+        chunk = pa.prefill_attention(q[:, :H], c.k[0], c.v[0], c.tables,
+                                     torch.arange(S + 1, dtype=torch.int32, device=DEV), new, 1, L, 0.125) if keep else plain
+        got = [x.clone() for x in (out, plain, chunk, sc, new)]
+        if want is None:
+            want = got
+            assert new.tolist() == [keep] * S and (bool(out.any()) == (keep > 0))
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), i
+
+
+def test_pools_past_32_bit_offsets():
+    """Blocks whose elements lie past 2^32 of a pool."""
+    Hkv, B, D, nb = 8, 64, 128, 70000       # 4.6e9 elements
+    k, v = (torch.empty(nb, Hkv, B, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    H, n = 16, 200
+    hi = [nb - 1, 3, nb - 2, nb - 3]
+    tables = torch.tensor([hi], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    small = torch.tensor([[0, 1, 2, 3]], dtype=torch.int32, device=DEV)
+    ks, vs = (torch.empty(8, Hkv, B, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    g = torch.Generator(device=DEV).manual_seed(4)
+    qkv = torch.randn(n, (H + 2 * Hkv) * D, generator=g, device=DEV).to(torch.bfloat16)
+    q, kn, vn = (x.view(n, -1, D) for x in qkv.split([H * D, Hkv * D, Hkv * D], 1))
+    rot, pos = pa.Rotary([0.1] * 64), torch.arange(n, device=DEV)
+    t = torch.arange(n, device=DEV)
+    res = []
+    for kc, vc, tab in ((k, v, tables), (ks, vs, small)):
+        slots = tab[0].long()[t // B] * B + t % B
+        qo = pa.rotary_cache_write(q, kn, vn, pos, rot, kc, vc, slots)
+        qsl = torch.tensor([0, n], dtype=torch.int32, device=DEV)
+        lse = torch.empty(n, H, device=DEV)
+        out = pa.prefill_attention(qo, kc, vc, tab, qsl, lens, n, 256, 0.09, lse=lse)
+        sc = torch.zeros(1, Hkv, 256, device=DEV)
+        pa.prefill_scores(qo, lse, kc, tab, qsl, lens, n, 256, 0.09, sc)
+        dec = pa.decode_attention_scored(qo[-1:], kc, vc, tab, lens, 256, 0.09, sc)
+        new = pa.evict_tokens([kc], [vc], [sc], tab, lens, torch.tensor([90], dtype=torch.int32, device=DEV), 256, 90,
+                              num_sink=2, num_recent=10)
+        rows = [c[tab[0].long()[t[:90] // B], :, t[:90] % B].view(torch.int16) for c in (kc, vc)]
+        res.append([qo.view(torch.int16), out, lse, sc, dec, new, *rows])
+    for a, b in zip(*res):
+        assert torch.equal(a, b)
+
+
+def test_scores_at_any_4_byte_address():
+    from cachelib import Cache
+    c = Cache([300, 90], 2, 64, torch.float16, 16, seed=5, spare=30)
+    q = torch.randn(2, 8, 64, device=DEV).to(torch.float16)
+    flat = torch.zeros(2 * 2 * 300 + 1, device=DEV)
+    odd, even = flat[1:].view(2, 2, 300), torch.zeros(2, 2, 300, device=DEV)
+    for sc in (odd, even):
+        pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, 300, 0.1, sc)
+        pa.prefill_scores(q, torch.full((2, 8), 6.0, device=DEV), c.k[0], c.tables,
+                          torch.tensor([0, 1, 2], dtype=torch.int32, device=DEV), c.lens, 1, 300, 0.1, sc)
+    assert odd.data_ptr() % 8 == 4 and torch.equal(odd, even)
+    res = []
+    for sc in (odd, even):
+        k = [c.k[0].clone()]
+        pa.evict_tokens(k, [c.v[0].clone()], [sc], c.tables, c.lens,
+                        torch.tensor([100, 50], dtype=torch.int32, device=DEV), 300, 100)
+        res.append((sc.clone(), k[0].view(torch.int16)))
+    assert torch.equal(res[0][0], res[1][0]) and torch.equal(res[0][1], res[1][1])
+
+
+def test_one_workspace_for_calls_of_all_sizes():
+    """Calls of different sizes back to back on one workspace: none may write to it before the
+    one before has read it."""
+    from cachelib import Cache
+    g = torch.Generator(device=DEV).manual_seed(6)
+    jobs = []
+    for i, (S, L, H, Hkv) in enumerate([(3, 3000, 12, 2), (90, 300, 4, 4), (1, 9000, 6, 1), (40, 700, 8, 2)]):
+        c = Cache([L - 7 * s % L for s in range(S)], Hkv, 64, torch.float16, 16, seed=i)
+        q = torch.randn(S, H, 64, generator=g, device=DEV).to(torch.float16)
+        jobs.append((c, q, torch.rand(S, Hkv, L, generator=g, device=DEV)))
+    ws = torch.empty(64 << 20, dtype=torch.uint8, device=DEV)
+
+    def go(workspace, sync):
+        res = []
+        for c, q, sc in jobs:
+            S, L = q.shape[0], c.max_len
+            k, v, s1 = c.k[0].clone(), c.v[0].clone(), sc.clone()
+            s2, new = torch.zeros_like(sc), torch.empty(S, dtype=torch.int32, device=DEV)
+            o1, o2 = (torch.empty(S, q.shape[1], 64, device=DEV) for _ in range(2))
+            keep = torch.full((S,), L // 3, dtype=torch.int32, device=DEV)
+            torch.cuda.synchronize()
+            res.append((c, q, k, v, s1, s2, new, o1, o2, keep, S, L))
+        for c, q, k, v, s1, s2, new, o1, o2, keep, S, L in res:
+            for step in range(3):
+                if step != 1:
+                    pa.decode_attention_scored(q, k, v, c.tables, c.lens if step == 0 else new, L, 0.1, s1,
+                                               out=o1 if step == 0 else o2, workspace=workspace)
+                else:
+                    pa.evict_tokens([k], [v], [s1], c.tables, c.lens, keep, L, L // 3, num_recent=5, new_lens=new,
+                                    workspace=workspace)
+                if sync:
+                    torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return [t for r in res for t in (r[2].view(torch.int16), r[4], r[6], r[7], r[8])]
+
+    want = go(None, True)
+    for _ in range(5):
+        for a, b in zip(go(ws, False), want):
+            assert torch.equal(a, b)
