@@ -316,9 +316,19 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint3
         ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag));
         return ok;
     };
-    for (unsigned r = 0; ok && item_id(r) < P.num_items; ++r) {
-        const SItem it = score_item(P, item_id(r));
-        if (!it.run) continue;
+    unsigned r = 0;
+    auto next_item = [&]() {  // the next item with work, from round r on; not run: none left
+        SItem it;
+        it.run = false;
+        while (item_id(r) < P.num_items) {
+            it = score_item(P, item_id(r++));
+            if (it.run) break;
+        }
+        return it;
+    };
+    SItem nx = next_item();
+    while (ok && nx.run) {
+        const SItem it = nx;
         const bool two = it.k0 + kKeys < it.L;
         Ring ks = kr;  // this key tile's slot
         kr.next(P.rk);
@@ -337,8 +347,12 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint3
             }
             qr.next(P.rq);
         }
-        n = (it.tt1 - first) * P.head_groups;
-        if (!ok || n == 0) continue;
+        const int total = (it.tt1 - first) * P.head_groups;
+        n = total;
+        if (!ok || n == 0) {
+            nx = next_item();
+            continue;
+        }
         if (!wait(&B.k_full[ks.slot], ks.phase)) break;
         const uint32_t dk = uniform((uint32_t)dk0 + (uint32_t)ks.slot * (ktile / 16u));
         for (; n > 0; --n) {
@@ -363,6 +377,7 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint3
                 if (n == 1) umma_commit(&B.k_free[ks.slot]);
             }
             __syncwarp();
+            if (n == total) nx = next_item();  // while the products run
             sr.next(2);
             qr.next(P.rq);
         }
@@ -675,8 +690,8 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         prefetch_tmap(&P.tmap_k);
         for (int b = 0; b < L::kBars; ++b) mbar_init(&bars[b], 1);
         for (int b = 0; b < 4; ++b) mbar_init(&B.s_free[b], kKeys);
-        // a query slot is given back for each key tile, the tile by its products
-        // and the lse by the four warps of its group
+        // a query slot is given back for each key tile: the query rows by the
+        // product's completion, the lse by the four warps of the group
         for (int b = 0; b < kMaxRing; ++b) {
             mbar_init(&B.q_free[b], 2);
             mbar_init(&B.l_free[b], 8);
