@@ -31,7 +31,10 @@
 namespace pa {
 namespace {
 
-constexpr int kSelThreads = 512;
+// Threads of a select CTA: one of several on an SM, or one that has the SM (a
+// long sequence's cluster).  131072 tokens over 8 CTAs: 24 us with 512, LONGSEL
+// with 1024.
+constexpr int kSelThreads = 512, kSelThreadsLong = 1024;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveBatch = 8;  // 16-byte pieces a thread has in flight
 
@@ -126,16 +129,17 @@ __device__ __forceinline__ void add_cluster(unsigned *p, uint32_t rank, unsigned
 
 // grid (cluster rank, unit): CS CTAs a unit, each with a contiguous segment of
 // its tokens in shared memory.
-template <int CS>
-__global__ void __launch_bounds__(kSelThreads)
+template <int CS, int THREADS>
+__global__ void __launch_bounds__(THREADS)
     evict_select_kernel(const __grid_constant__ EvictParams P) {
     extern __shared__ uint4 s_key4[];  // the order keys of this CTA's segment, four a word
     // hist: this CTA's counts; a cluster adds them up in all_hist of its CTA 0
-    __shared__ unsigned hist[kBins], all_hist[CS > 1 ? kBins : 1];
-    __shared__ unsigned s_warp[kSelThreads / 32], s_digit, s_need;
+    // (hist also holds a step's kept tokens of every warp, 128 each)
+    __shared__ unsigned hist[THREADS * 4 > kBins ? THREADS * 4 : kBins], all_hist[CS > 1 ? kBins : 1];
+    __shared__ unsigned s_warp[THREADS / 32], s_digit, s_need;
     __shared__ unsigned s_total;  // the segment's tokens above the threshold, and at it << 16
     uint32_t *const s_key = reinterpret_cast<uint32_t *>(s_key4);
-    constexpr int kWarps = kSelThreads / 32;
+    constexpr int kWarps = THREADS / 32;
     pdl_wait();  // earlier kernels may still write what this reads, or read what it writes
     // The move kernel may be set up now.  Without one the next call's kernels
     // come next, and those read new_lens (as their context lengths) as soon as
@@ -161,10 +165,10 @@ __global__ void __launch_bounds__(kSelThreads)
     if (P.in_place) {  // the move kernel's order of chunks
         if (tid == 0 && rank == 0) P.ticket[unit] = 0u;
         unsigned *flags = P.flags + (size_t)unit * P.max_chunks;
-        for (int i = rank * kSelThreads + tid; i < P.max_chunks; i += CS * kSelThreads) flags[i] = 0u;
+        for (int i = rank * THREADS + tid; i < P.max_chunks; i += CS * THREADS) flags[i] = 0u;
     }
     if (q.n == q.L) {  // everything stays where it is (the move needs no list)
-        for (int t = rank * kSelThreads + tid; t < q.L; t += CS * kSelThreads) {
+        for (int t = rank * THREADS + tid; t < q.L; t += CS * THREADS) {
             if (kept) kept[t] = t;
             if (out != sc) out[t] = sc[t];
         }
@@ -172,20 +176,20 @@ __global__ void __launch_bounds__(kSelThreads)
     }
     const int seg = ((q.L + CS - 1) / CS + 3) & ~3, t0 = rank * seg;
     const int cnt = max(0, min(seg, q.L - t0));  // this CTA's tokens t0 .. t0 + cnt - 1
-    for (int i = tid; i < kBins; i += kSelThreads) {
+    for (int i = tid; i < kBins; i += THREADS) {
         hist[i] = 0u;
         if (CS > 1) all_hist[i] = 0u;
     }
     {
         int i = tid;
-        for (; i + 7 * kSelThreads < cnt; i += 8 * kSelThreads) {
+        for (; i + 7 * THREADS < cnt; i += 8 * THREADS) {
             float x[8];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) x[u] = sc[t0 + i + u * kSelThreads];
+            for (int u = 0; u < 8; ++u) x[u] = sc[t0 + i + u * THREADS];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s_key[i + u * kSelThreads] = order_key(x[u]);
+            for (int u = 0; u < 8; ++u) s_key[i + u * THREADS] = order_key(x[u]);
         }
-        for (; i < cnt; i += kSelThreads) s_key[i] = order_key(sc[t0 + i]);
+        for (; i < cnt; i += THREADS) s_key[i] = order_key(sc[t0 + i]);
     }
     __syncthreads();
     const int m0 = q.sink, m1 = q.L - q.recent;  // the middle
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kSelThreads)
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const int bins = pass == 2 ? 1024 : 2048;
-            for (int j = tid; 4 * j < i1; j += kSelThreads) {
+            for (int j = tid; 4 * j < i1; j += THREADS) {
                 const uint4 k4 = s_key4[j];
                 const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
@@ -216,7 +220,7 @@ __global__ void __launch_bounds__(kSelThreads)
                 // ones: cleared before the barrier that ended the last pass)
                 if (pass == 0) cluster_sync();
                 else __syncthreads();
-                for (int i = tid; i < bins; i += kSelThreads)
+                for (int i = tid; i < bins; i += THREADS)
                     if (hist[i]) add_cluster(&all_hist[i], 0u, hist[i]);
                 cluster_sync();
             } else {
@@ -224,11 +228,12 @@ __global__ void __launch_bounds__(kSelThreads)
             }
             if (CS == 1 || rank == 0) {
                 unsigned *h = CS > 1 ? all_hist : hist;
-                // largest digits first: thread i has bins bins-1-4i .. bins-4-4i
-                unsigned c[4], sum = 0u;
+                // largest digits first: thread i has BPT bins from bins - 1 - BPT i down
+                constexpr int BPT = kBins / THREADS;
+                unsigned c[BPT], sum = 0u;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int b = bins - 1 - (4 * tid + k);
+                for (int k = 0; k < BPT; ++k) {
+                    const int b = bins - 1 - (BPT * tid + k);
                     c[k] = b >= 0 ? h[b] : 0u;
                     sum += c[k];
                 }
@@ -247,12 +252,12 @@ __global__ void __launch_bounds__(kSelThreads)
                     int k = 0;
                     unsigned b4 = before;
 #pragma unroll
-                    for (int e = 0; e < 3; ++e)
+                    for (int e = 0; e < BPT - 1; ++e)
                         if (k == e && b4 + c[e] < left) {
                             b4 += c[e];
                             k = e + 1;
                         }
-                    const unsigned digit = (unsigned)(bins - 1 - (4 * tid + k));
+                    const unsigned digit = (unsigned)(bins - 1 - (BPT * tid + k));
                     if constexpr (CS > 1) {
                         for (uint32_t r = 0; r < CS; ++r) {
                             st_cluster(&s_digit, r, digit);
@@ -265,7 +270,7 @@ __global__ void __launch_bounds__(kSelThreads)
                 }
             }
             if (pass < 2)  // for the next pass (this one's scan has read them)
-                for (int i = tid; i < kBins; i += kSelThreads) {
+                for (int i = tid; i < kBins; i += THREADS) {
                     hist[i] = 0u;
                     if (CS > 1) all_hist[i] = 0u;
                 }
@@ -291,6 +296,13 @@ __global__ void __launch_bounds__(kSelThreads)
         const uint4 k4 = s_key4[i >> 2];
         const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
         unsigned c = 0u;
+        if (i >= f0 && i + 4 <= f1 && i + 4 <= w1) {  // all in the middle
+            if (!some) return 0u;
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                c |= (key[u] > thr ? 1u << u : 0u) | (key[u] == thr ? 0x10000u << u : 0u);
+            return c;
+        }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
             const bool in = i + u < w1, fixed = i + u < f0 || i + u >= f1;
@@ -334,7 +346,6 @@ __global__ void __launch_bounds__(kSelThreads)
     // A step's kept tokens have consecutive places: gathered in shared memory,
     // then written out with neighbouring lanes on neighbouring places.
     unsigned *const gathered = hist + wid * 128;
-    static_assert(kWarps * 128 <= kBins, "a step's tokens of every warp");
     for (int i = w0 + 4 * lane; i - 4 * lane < w1; i += 128) {
         const unsigned c = classify(i), own = counts(c);
         unsigned incl = own;
@@ -365,7 +376,7 @@ __global__ void __launch_bounds__(kSelThreads)
         }
         __syncwarp();
     }
-    for (int p = q.n + rank * kSelThreads + tid; p < q.L; p += CS * kSelThreads) out[p] = 0.f;
+    for (int p = q.n + rank * THREADS + tid; p < q.L; p += CS * THREADS) out[p] = 0.f;
     if (CS > 1) cluster_sync();  // no CTA leaves while another may read its counts
 }
 
@@ -488,7 +499,8 @@ constexpr long long kMaxSegment = 48 * 1024;
 
 template <int CS>
 cudaError_t launch_select(const EvictParams &P, unsigned units, size_t smem, cudaStream_t stream) {
-    auto kern = evict_select_kernel<CS>;
+    constexpr int kThreads = CS > 1 ? kSelThreadsLong : kSelThreads;
+    auto kern = evict_select_kernel<CS, kThreads>;
     constexpr int kMaxDevices = 64;
     static std::atomic<bool> attr_set[kMaxDevices];
     int dev = 0;
@@ -502,7 +514,7 @@ cudaError_t launch_select(const EvictParams &P, unsigned units, size_t smem, cud
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(units * CS);
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
