@@ -25,7 +25,7 @@
 // first rows are in flight.  A CTA takes as many tokens as give each thread
 // four rows, unless that leaves fewer than two CTAs an SM: with few rows a
 // token (grouped queries) one row a thread is one round trip to memory a CTA
-// and half the rate (4099 tokens of 12 + 2 + 2 heads of 128: 15.3 us, RGQA
+// and half the rate (4099 tokens of 12 + 2 + 2 heads of 128: 15.3 us, 11.9
 // with four rows).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
