@@ -494,7 +494,8 @@ size_t pa_prefill_scores_workspace_size(int num_seqs, int num_heads, int num_kv_
  * score_stride  >= max_context_len
  * head_dim 64 or 128 (PA_ERR_UNSUPPORTED otherwise); num_seqs and
  * num_kv_heads at most 65535.  Lengths, tables and limits are those of
- * pa_prefill_attention.
+ * pa_prefill_attention; query_start_loc and context_lens are read as soon as
+ * the kernel starts (as pa_decode_attention reads its lengths).
  * workspace     device, >= pa_prefill_scores_workspace_size(...) bytes,
  *               256-byte aligned; calls in flight at once must not share one
  * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence

@@ -18,7 +18,12 @@
 // largest power of two that divides it) times NQ tokens, one TMA box.  The
 // kernel is persistent, one CTA per SM; items are numbered from the first keys
 // on (with whole prompts those see the most queries) and dealt out forth and
-// back, so every CTA's share is about as heavy and no list is needed.
+// back, so every CTA's share is about as heavy.  Each CTA works the numbering
+// out for itself in shared memory, from the lengths: only ranges that hold
+// keys are numbered (sequences ordered by their number of ranges, so range k's
+// are the first of them), and an item's sequence is at hand without a trip to
+// memory.  Batches past kMaxTableSeqs sequences or kMaxTableRanges ranges number
+// every range up to the longest and pass over the empty ones.
 // Twenty warps:
 //   * warp 0 (producer): K tiles into a ring of 128-key slots, block by block
 //     (tiled bulk copies, TMA), and query tiles into another; it runs ahead
@@ -78,6 +83,7 @@ constexpr uint32_t kTmemColsS = 512;  // S of tile t, buffer b at 128 (2 t + b)
 constexpr uint32_t kKSlice = kKeys * 128;  // bytes of a 64-element slice of a K tile
 constexpr int kMaxRing = 8;   // slots of the K and the query ring at most
 constexpr uint32_t kTileBytes = 6 * 32768;  // shared memory of both tile rings
+constexpr int kMaxTableSeqs = 512, kMaxTableRanges = 2047;
 
 struct ScoreParams {
     CUtensorMap tmap_q;  // query as [head_dim/64][tokens][heads][64], box NQ x NH rows
@@ -92,12 +98,22 @@ struct ScoreParams {
     int head_groups;      // G / NH
     int rk, rq;           // slots of the K and the query ring
     unsigned num_items;   // 256-key ranges x num_seqs x num_kv_heads
+    int ranges;           // 256-key ranges of the longest context
+    int table;            // 1: items are numbered by the table in shared memory
     float scale_log2;
     unsigned int *err;
 };
 
+// The numbering of the items in shared memory.
+struct STable {
+    int tok0[kMaxTableSeqs], n[kMaxTableSeqs], L[kMaxTableSeqs];  // of each sequence
+    unsigned short ranges[kMaxTableSeqs];  // its 256-key ranges (0: no work)
+    unsigned short order[kMaxTableSeqs];   // sequences by ranges, most first
+    unsigned first[kMaxTableRanges + 1];   // first item of range k; [ranges]: all items
+};
+
 // Shared memory: lse [slot][128], its flags [slot], the sums handed over
-// [tile][128], barriers; then, 1024-byte aligned, the K ring of rk tiles
+// [tile][128], barriers, the items' table; then, 1024-byte aligned, the K ring of rk tiles
 // [slice][128 keys][64] and the query ring of rq tiles [slice][rows][64].
 struct SLayout {
     static constexpr size_t dead_off = kMaxRing * kMaxCols * 4;
@@ -108,7 +124,8 @@ struct SLayout {
     static constexpr int kBars = 6 * kMaxRing + 8 + 2;
     static constexpr size_t tmem_off = bar_off + 8 * kBars;
     static constexpr size_t flag_off = tmem_off + 4;
-    static constexpr size_t small = (flag_off + 4 + 1023) / 1024 * 1024;
+    static constexpr size_t table_off = (flag_off + 4 + 15) / 16 * 16;
+    static constexpr size_t small = (table_off + sizeof(STable) + 1023) / 1024 * 1024;
     static constexpr size_t bytes = small + kTileBytes;
     static_assert(bar_off % 8 == 0, "barrier alignment");
     static_assert(bytes <= 232448, "dynamic shared memory of one CTA");
@@ -139,30 +156,111 @@ struct SItem {
     bool ok, run;
 };
 
-__device__ __forceinline__ SItem score_item(const ScoreParams &P, unsigned id) {
-    SItem it;
-    const unsigned per = (unsigned)P.num_seqs * (unsigned)P.num_kv_heads;
-    const unsigned range = id / per, rest = id - range * per;
-    it.s = (int)(rest / (unsigned)P.num_kv_heads);
-    it.hk = (int)(rest - (unsigned)it.s * (unsigned)P.num_kv_heads);
-    const int a = __ldg(&P.query_start_loc[it.s]), b = __ldg(&P.query_start_loc[it.s + 1]);
-    it.L = __ldg(&P.context_lens[it.s]);
-    it.n = b - a;
-    it.tok0 = a;
-    it.ok = a >= 0 && b <= P.num_tokens && it.n >= 0 && it.n <= P.max_query_len &&
-            it.L >= it.n && it.L <= P.max_context_len;
-    it.c = it.L - it.n;
-    it.k0 = (int)range * kItemKeys;
-    it.run = it.ok && it.n > 0 && it.k0 < it.L;
-    it.tt0 = max(0, it.k0 - it.c) >> P.lg_nq;
-    it.tt1 = (it.n + (1 << P.lg_nq) - 1) >> P.lg_nq;
-    return it;
+__device__ __forceinline__ bool lengths_ok(const ScoreParams &P, int a, int b, int L) {
+    const int n = b - a;
+    return a >= 0 && b <= P.num_tokens && n >= 0 && n <= P.max_query_len && L >= n &&
+           L <= P.max_context_len;
 }
 
-// Item of the CTA's round r: forth and back over the CTAs.
-__device__ __forceinline__ unsigned item_id(unsigned r) {
-    return r * gridDim.x + ((r & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+// Fill the table (every thread of the CTA).
+__device__ __forceinline__ void number_items(const ScoreParams &P, STable &T) {
+    const int tid = threadIdx.x, S = P.num_seqs;
+    for (int s = tid; s < S; s += kThreadsS) {
+        const int a = __ldg(&P.query_start_loc[s]), b = __ldg(&P.query_start_loc[s + 1]);
+        const int L = __ldg(&P.context_lens[s]);
+        const bool ok = lengths_ok(P, a, b, L);
+        if (!ok && blockIdx.x == 0 && P.err) atomicOr(P.err, PA_ERRBIT_CONTEXT_LEN);
+        T.tok0[s] = a;
+        T.n[s] = b - a;
+        T.L[s] = L;
+        T.ranges[s] = ok && b > a ? (unsigned short)((L + kItemKeys - 1) / kItemKeys) : 0;
+    }
+    __syncthreads();
+    for (int s = tid; s < S; s += kThreadsS) {
+        const int mine = T.ranges[s];
+        int place = 0;
+        for (int j = 0; j < S; ++j) {
+            const int r = T.ranges[j];
+            place += r > mine || (r == mine && j < s);
+        }
+        T.order[place] = (unsigned short)s;
+    }
+    __syncthreads();
+    for (int k = tid; k < P.ranges; k += kThreadsS) {  // sequences with more than k ranges
+        int lo = 0, hi = S;
+        while (lo < hi) {
+            const int mid = (lo + hi) / 2;
+            if (T.ranges[T.order[mid]] > k) lo = mid + 1;
+            else hi = mid;
+        }
+        T.first[k + 1] = (unsigned)lo * (unsigned)P.num_kv_heads;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        unsigned carry = 0u;
+        if (tid == 0) T.first[0] = 0u;
+        for (int k0 = 1; k0 <= P.ranges; k0 += 32) {
+            const int k = k0 + tid;
+            unsigned v = k <= P.ranges ? T.first[k] : 0u;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned u = __shfl_up_sync(0xffffffffu, v, o);
+                if (tid >= o) v += u;
+            }
+            v += carry;
+            if (k <= P.ranges) T.first[k] = v;
+            carry = __shfl_sync(0xffffffffu, v, 31);
+        }
+    }
+    __syncthreads();
 }
+
+// A role's way through the CTA's items, round by round: forth and back over the
+// CTAs, in ascending numbers.
+struct Items {
+    const ScoreParams &P;
+    const STable &T;
+    unsigned total;
+    int range = 0;  // of the last item taken from the table
+    __device__ __forceinline__ Items(const ScoreParams &params, const STable &table)
+        : P(params), T(table), total(params.table ? table.first[params.ranges] : params.num_items) {}
+    __device__ __forceinline__ unsigned id(unsigned r) const {
+        return r * gridDim.x + ((r & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+    }
+    __device__ __forceinline__ bool has(unsigned r) const { return id(r) < total; }
+    // the item of round r (rounds in ascending order)
+    __device__ __forceinline__ SItem get(unsigned r) {
+        SItem it;
+        const unsigned i = id(r), Hkv = (unsigned)P.num_kv_heads;
+        if (P.table) {
+            while (i >= T.first[range + 1]) ++range;
+            const unsigned rest = i - T.first[range], place = rest / Hkv;
+            it.s = T.order[place];
+            it.hk = (int)(rest - place * Hkv);
+            it.tok0 = T.tok0[it.s];
+            it.n = T.n[it.s];
+            it.L = T.L[it.s];
+            it.ok = true;
+        } else {
+            const unsigned per = (unsigned)P.num_seqs * Hkv;
+            range = (int)(i / per);
+            const unsigned rest = i - (unsigned)range * per;
+            it.s = (int)(rest / Hkv);
+            it.hk = (int)(rest - (unsigned)it.s * Hkv);
+            const int a = __ldg(&P.query_start_loc[it.s]), b = __ldg(&P.query_start_loc[it.s + 1]);
+            it.L = __ldg(&P.context_lens[it.s]);
+            it.n = b - a;
+            it.tok0 = a;
+            it.ok = lengths_ok(P, a, b, it.L);
+        }
+        it.c = it.L - it.n;
+        it.k0 = range * kItemKeys;
+        it.run = it.ok && it.n > 0 && it.k0 < it.L;
+        it.tt0 = max(0, it.k0 - it.c) >> P.lg_nq;
+        it.tt1 = (it.n + (1 << P.lg_nq) - 1) >> P.lg_nq;
+        return it;
+    }
+};
 
 // First token tile that key tile t has a product with (the tile that holds the
 // first token to see the tile's first key); tt1 if it has no keys.
@@ -175,7 +273,7 @@ __device__ __forceinline__ int first_tile(const ScoreParams &P, const SItem &it,
 // warp 0: K and query copies
 // ---------------------------------------------------------------------------
 template <int D>
-__device__ __forceinline__ void run_score_producer(const ScoreParams &P, unsigned char *sk,
+__device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items items, unsigned char *sk,
                                                    unsigned char *sq, const SBars &B,
                                                    volatile int *abort_flag, int lane) {
     constexpr int KB = D / 64;
@@ -197,15 +295,15 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, unsigne
     bool ok = true;
     SItem it, nx;
     int e = -1, en = -1;
-    if (item_id(0) < P.num_items) {
-        nx = score_item(P, item_id(0));
+    if (items.has(0)) {
+        nx = items.get(0);
         en = entry(nx);
     }
-    for (unsigned r = 0; ok && item_id(r) < P.num_items; ++r) {
+    for (unsigned r = 0; ok && items.has(r); ++r) {
         it = nx;
         e = en;
-        if (item_id(r + 1) < P.num_items) {  // its table entries arrive meanwhile
-            nx = score_item(P, item_id(r + 1));
+        if (items.has(r + 1)) {  // its table entries arrive meanwhile
+            nx = items.get(r + 1);
             en = entry(nx);
         }
         if (!it.ok && it.k0 == 0 && it.hk == 0 && lane == 0 && P.err)
@@ -298,7 +396,7 @@ __device__ __forceinline__ bool elect_one() {
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
 template <int D>
-__device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint32_t fmt,
+__device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items items, int t, uint32_t fmt,
                                               unsigned char *sk, unsigned char *sq, uint32_t tmem,
                                               const SBars &B, volatile int *abort_flag) {
     constexpr int KB = D / 64;
@@ -320,8 +418,8 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint3
     auto next_item = [&]() {  // the next item with work, from round r on; not run: none left
         SItem it;
         it.run = false;
-        while (item_id(r) < P.num_items) {
-            it = score_item(P, item_id(r++));
+        while (items.has(r)) {
+            it = items.get(r++);
             if (it.run) break;
         }
         return it;
@@ -394,7 +492,7 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, int t, uint3
 // ---------------------------------------------------------------------------
 // warp 3: the rows' lse
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void run_score_lse(const ScoreParams &P, float *s_lse,
+__device__ __forceinline__ void run_score_lse(const ScoreParams &P, Items items, float *s_lse,
                                               volatile int *s_dead, const SBars &B,
                                               volatile int *abort_flag, int lane) {
     const int cols = 1 << (P.lg_nh + P.lg_nq);
@@ -406,8 +504,8 @@ __device__ __forceinline__ void run_score_lse(const ScoreParams &P, float *s_lse
     SItem it;
     int tt = 0, hg = 0;
     auto next_item = [&]() {  // the first item with work from round r on
-        for (; item_id(r) < P.num_items; ++r) {
-            it = score_item(P, item_id(r));
+        for (; items.has(r); ++r) {
+            it = items.get(r);
             if (it.run) {
                 tt = it.tt0;
                 hg = 0;
@@ -539,7 +637,7 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int b,
+__device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items items, int t, int b,
                                                const float *s_lse, const volatile int *s_dead,
                                                float *s_part, uint32_t tmem, const SBars &B,
                                                volatile int *abort_flag, int wq, int lane) {
@@ -552,8 +650,8 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, int t, int 
     // the next item with keys for this tile, from round r on; `skipped`: query
     // tiles of the items before it that have none
     auto next_item = [&](unsigned &r, SItem &it, int &skipped) {
-        for (; item_id(r) < P.num_items; ++r) {
-            it = score_item(P, item_id(r));
+        for (; items.has(r); ++r) {
+            it = items.get(r);
             if (!it.run) continue;
             if (it.k0 + t * kKeys < it.L) return true;
             skipped += (it.tt1 - it.tt0) * P.head_groups;
@@ -700,31 +798,33 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, kTmemColsS);
+    STable &table = *reinterpret_cast<STable *>(smem + L::table_off);
+    if (P.table) number_items(P, table);  // (from the lengths alone: before the wait)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    pdl_wait();     // the kernels before may still write what this reads
+    pdl_trigger();  // (after the wait: what follows may start before this grid ends, not before those)
+    const Items items(P, table);
     // each role's code follows its own register reallocation (code after a
     // join of the two would be held to the smaller count)
     if (warp >= 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
-        pdl_wait();  // the kernels before may still write what this reads
-        run_score_sums(P, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, s_part, tmem, B,
+        run_score_sums(P, items, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, s_part, tmem, B,
                        abort_flag, warp & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
-        pdl_wait();
-        pdl_trigger();  // (after the wait: what follows may start before this grid ends, not before those)
         if (warp == 0) {
-            run_score_producer<D>(P, sk, sq, B, abort_flag, lane);
+            run_score_producer<D>(P, items, sk, sq, B, abort_flag, lane);
         } else if (warp <= 2) {
-            run_score_mma<D>(P, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
+            run_score_mma<D>(P, items, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
             // every product has completed before tensor memory is released
             volatile int never = 0;
             mbar_drain_wait(&B.done[warp - 1], 0, &never);
             __syncwarp();
         } else {
-            run_score_lse(P, s_lse, s_dead, B, abort_flag, lane);
+            run_score_lse(P, items, s_lse, s_dead, B, abort_flag, lane);
         }
     }
     tc_fence_before();
@@ -862,6 +962,8 @@ extern "C" pa_status_t pa_prefill_scores(
         num_kv_heads;
     if (items >= (1ull << 31)) return PA_ERR_UNSUPPORTED;
     P.num_items = (unsigned)items;
+    P.ranges = (int)((max_context_len + (long long)kItemKeys - 1) / kItemKeys);
+    P.table = num_seqs <= kMaxTableSeqs && P.ranges <= kMaxTableRanges ? 1 : 0;
     const unsigned grid = items < (unsigned long long)sms ? (unsigned)items : (unsigned)sms;
     const uint32_t fmt = dtype == PA_BF16 ? 1u : 0u;
     cudaStream_t st = (cudaStream_t)stream;

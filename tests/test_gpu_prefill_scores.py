@@ -116,6 +116,19 @@ def test_longer_ones(H, Hkv, D, new, lens):
     _check_scores(c, q, starts, qsl, new, lse, D ** -0.5, stride=c.max_len + 5)
 
 
+@pytest.mark.parametrize("S", [100, 512, 513])
+def test_many_ragged_sequences(S):
+    """Past 512 sequences the items are numbered without the table."""
+    rng = np.random.default_rng(S)
+    lens = rng.integers(1, 700, S)
+    lens[S // 2] = 1500
+    new = [int(rng.integers(0, min(n, 40) + 1)) for n in lens]
+    c = Cache(lens, 1, 64, torch.float16, 32, seed=S)
+    q, qsl, starts = _batch(c, new, 2, 64)
+    _, lse = _attend(c, q, qsl, new, 0.125)
+    _check_scores(c, q, starts, qsl, new, lse, 0.125)
+
+
 def test_split_items_give_the_lse_too():
     """One long prompt on few heads: its heaviest items are split and merged."""
     c = Cache([6000], 1, 64, torch.float16, 16, seed=5)
