@@ -224,3 +224,16 @@ def test_captured_and_replayed():
     torch.cuda.synchronize()
     assert torch.equal(_bits(k1), _bits(k2)) and torch.equal(_bits(v1), _bits(v2))
     assert torch.equal(o1, o2) and n1.tolist() == n2.tolist() == [100, 150]
+
+
+@pytest.mark.parametrize("D,run,gap", [(64, 100, 1), (128, 1, 100), (128, 500, 130), (256, 33, 31)])
+def test_in_place_runs_of_kept_tokens(D, run, gap):
+    """Runs of kept tokens between gaps: new rows reach the old rows of chunks
+    right before and far before their own."""
+    L = [20000, 4097, 130]
+    c = Cache(L, 2, D, torch.bfloat16, 16, seed=run, layers=2)
+    sc = _scores(2, len(L), 2, 20000, seed=gap)
+    t = torch.arange(20000, device=DEV) % (run + gap)
+    sc += (t < run).float()
+    keep = [int((t[:n] < run).sum()) for n in L]
+    _check(c, sc, keep, 0, 0)
