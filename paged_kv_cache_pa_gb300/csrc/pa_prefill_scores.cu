@@ -43,16 +43,21 @@
 //     range [lo, hi) of the tile, from its key's position.  At the item's end
 //     group (t, 1) hands its sums to group (t, 0), which adds them and writes.
 // Sums are fp32 in levels: the columns of a tile in pairs of chains, tiles,
-// groups.
+// groups, CTAs.
+//
+// Few items (one prompt) leave most SMs idle and end with the longest, so a
+// cluster of 2, 4 or 8 CTAs shares each: the query tiles in equal parts one
+// after the other, and the first CTA's group (t, 0) adds the others' sums, in
+// their order, through distributed shared memory.  One prompt, 32 heads on 8 of
+// 128, with clusters and without: 4096 tokens 70 and 119 us, 1024 tokens 21 and
+// 39 us.
 //
 // Bound: 2 prompts of 4096 tokens, 32 heads on 8 of 128, bf16, take 122 us; the
-// products alone are 73 us at the rate of a large bf16 matrix product, and the
-// exponentials 60 us at one a lane, four cycles and scheduler.  Measured apart,
-// the weights without products take about 100 us and the products without
-// weights about 100: what is left is that the two do not overlap fully with
-// two buffers a key tile (tensor memory is full).  Query tiles of 256 rows,
-// one buffer a key tile, took 135 to 145 us.  A window of few queries is bound by
-// the steps of an item one after the other (5 us for 64 KB of K).
+// products are 73 us at the rate of a large bf16 matrix product.  A scheduler
+// spends about eight cycles on a warp's column of weights, four of them on the
+// exponential (58 us in all at four).  Query tiles of 256 rows with one buffer a
+// key tile took 134 to 151 us.  A window of few queries is bound by the steps
+// of an item one after the other.
 //
 // A wait that gives up sets the abort flag; the groups then go through the
 // rest of their items without waiting or writing, so that their named barriers
@@ -91,6 +96,7 @@ constexpr uint32_t kTmemColsS = 512;  // S of tile t, buffer b at 128 (2 t + b)
 constexpr uint32_t kKSlice = kKeys * 128;  // bytes of a 64-element slice of a K tile
 constexpr int kMaxRing = 8;   // slots of the K and the query ring at most
 constexpr uint32_t kTileBytes = 6 * 32768;  // shared memory of both tile rings
+constexpr int kMaxParts = 8;  // CTAs that share one item at most (a cluster)
 constexpr int kMaxTableSeqs = 512, kMaxTableRanges = 2047;  // sizes of the items' table
 
 struct ScoreParams {
@@ -108,6 +114,7 @@ struct ScoreParams {
     unsigned num_items;   // 256-key ranges x num_seqs x num_kv_heads
     int ranges;           // 256-key ranges of the longest context
     int table;            // 1: items are numbered by the table in shared memory
+    int lg_parts;         // log2 of the CTAs that share an item
     float scale_log2;
     unsigned int *err;
 };
@@ -129,19 +136,23 @@ struct SLayout {
     static constexpr size_t part_off = dead_off + kMaxRing * 4;
     static constexpr size_t bar_off = part_off + kTiles * kKeys * 4;
     // k_full, k_free, q_full, q_free, l_full, l_free [kMaxRing], s_full[2][2],
-    // s_free[2][2], done[2]
-    static constexpr int kBars = 6 * kMaxRing + 8 + 2;
+    // s_free[2][2], done[2], c_full[2], c_free[2]
+    static constexpr int kBars = 6 * kMaxRing + 8 + 2 + 4;
     static constexpr size_t tmem_off = bar_off + 8 * kBars;
     static constexpr size_t flag_off = tmem_off + 4;
     static constexpr size_t table_off = (flag_off + 4 + 15) / 16 * 16;
-    static constexpr size_t small = (table_off + sizeof(STable) + 1023) / 1024 * 1024;
+    // an item shared by a cluster: in its first CTA the sums of the others
+    static constexpr size_t comb_off = (table_off + sizeof(STable) + 15) / 16 * 16;
+    static constexpr size_t small =
+        (comb_off + (kMaxParts - 1) * kItemKeys * 4 + 1023) / 1024 * 1024;
     static constexpr size_t bytes = small + kTileBytes;
     static_assert(bar_off % 8 == 0, "barrier alignment");
     static_assert(bytes <= 232448, "dynamic shared memory of one CTA");
 };
 
 struct SBars {
-    uint64_t *k_full, *k_free, *q_full, *q_free, *l_full, *l_free, *s_full, *s_free, *done;
+    uint64_t *k_full, *k_free, *q_full, *q_free, *l_full, *l_free, *s_full, *s_free, *done, *c_full,
+        *c_free;
 };
 
 // A place in a ring: slot and the parity of its current phase.
@@ -162,7 +173,7 @@ struct SItem {
     int n, L, c, tok0;  // new tokens, context length, cached before, first query row
     int k0;             // first key
     int tt0, tt1;       // token tiles that see some key of the item
-    bool ok, run;
+    bool ok, any, run;  // lengths in order; work in the item; in this CTA's part
 };
 
 __device__ __forceinline__ bool lengths_ok(const ScoreParams &P, int a, int b, int L) {
@@ -225,7 +236,9 @@ __device__ __forceinline__ void number_items(const ScoreParams &P, STable &T) {
 }
 
 // A role's way through the CTA's items, round by round: forth and back over the
-// CTAs, in ascending numbers.
+// CTAs, in ascending numbers.  SPLIT: the CTAs of a cluster go the same way,
+// each with a part of every item's query tiles.
+template <bool SPLIT>
 struct Items {
     const ScoreParams &P;
     const STable &T;
@@ -234,7 +247,9 @@ struct Items {
     __device__ __forceinline__ Items(const ScoreParams &params, const STable &table)
         : P(params), T(table), total(params.table ? table.first[params.ranges] : params.num_items) {}
     __device__ __forceinline__ unsigned id(unsigned r) const {
-        return r * gridDim.x + ((r & 1u) ? gridDim.x - 1u - blockIdx.x : blockIdx.x);
+        const unsigned ways = SPLIT ? gridDim.x >> P.lg_parts : gridDim.x;
+        const unsigned way = SPLIT ? blockIdx.x >> P.lg_parts : blockIdx.x;
+        return r * ways + ((r & 1u) ? ways - 1u - way : way);
     }
     __device__ __forceinline__ bool has(unsigned r) const { return id(r) < total; }
     // the item of round r (rounds in ascending order)
@@ -264,25 +279,33 @@ struct Items {
         }
         it.c = it.L - it.n;
         it.k0 = range * kItemKeys;
-        it.run = it.ok && it.n > 0 && it.k0 < it.L;
+        it.any = it.run = it.ok && it.n > 0 && it.k0 < it.L;
         it.tt0 = max(0, it.k0 - it.c) >> P.lg_nq;
         it.tt1 = (it.n + (1 << P.lg_nq) - 1) >> P.lg_nq;
+        if (SPLIT) {
+            const int tiles = it.tt1 - it.tt0, part = (int)blockIdx.x & ((1 << P.lg_parts) - 1);
+            it.tt1 = it.tt0 + ((tiles * (part + 1)) >> P.lg_parts);
+            it.tt0 += (tiles * part) >> P.lg_parts;
+            it.run = it.run && it.tt0 < it.tt1;
+        }
         return it;
     }
 };
 
 // First token tile that key tile t has a product with (the tile that holds the
-// first token to see the tile's first key); tt1 if it has no keys.
+// first token to see the tile's first key); tt1 if there is none.
+template <bool SPLIT>
 __device__ __forceinline__ int first_tile(const ScoreParams &P, const SItem &it, int t) {
     const int key = it.k0 + t * kKeys;
-    return key < it.L ? max(0, key - it.c) >> P.lg_nq : it.tt1;
+    const int tile = key < it.L ? max(0, key - it.c) >> P.lg_nq : it.tt1;
+    return SPLIT ? min(max(tile, it.tt0), it.tt1) : tile;
 }
 
 // ---------------------------------------------------------------------------
 // warp 0: K and query copies
 // ---------------------------------------------------------------------------
-template <int D>
-__device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items items, unsigned char *sk,
+template <int D, bool SPLIT>
+__device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items<SPLIT> items, unsigned char *sk,
                                                    unsigned char *sq, const SBars &B,
                                                    volatile int *abort_flag, int lane) {
     constexpr int KB = D / 64;
@@ -368,10 +391,10 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items i
             }
             ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         };
-        const int second = first_tile(P, it, 1);
+        const int second = first_tile<SPLIT>(P, it, 1);
         load_k(0);
         if (ok) load_q(it.tt0, second);
-        if (ok && it.k0 + kKeys < it.L) load_k(1);
+        if (ok && second < it.tt1) load_k(1);
         if (ok) load_q(second, it.tt1);
     }
     if (lane == 0) {
@@ -404,8 +427,8 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
 
-template <int D>
-__device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items items, int t, uint32_t fmt,
+template <int D, bool SPLIT>
+__device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT> items, int t, uint32_t fmt,
                                               unsigned char *sk, unsigned char *sq, uint32_t tmem,
                                               const SBars &B, volatile int *abort_flag) {
     constexpr int KB = D / 64;
@@ -436,12 +459,12 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items items,
     SItem nx = next_item();
     while (ok && nx.run) {
         const SItem it = nx;
-        const bool two = it.k0 + kKeys < it.L;
+        const bool two = first_tile<SPLIT>(P, it, 1) < it.tt1;
         Ring ks = kr;  // this key tile's slot
         kr.next(P.rk);
         if (t == 1) ks = kr;
         if (two) kr.next(P.rk);
-        const int first = first_tile(P, it, t);
+        const int first = first_tile<SPLIT>(P, it, t);
         // Both issuers pass through every query tile (a wait by parity must
         // never be a whole ring ahead or behind), and give back their share of
         // those that are the other key tile's alone.
@@ -501,7 +524,8 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items items,
 // ---------------------------------------------------------------------------
 // warp 3: the rows' lse
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ void run_score_lse(const ScoreParams &P, Items items, float *s_lse,
+template <bool SPLIT>
+__device__ __forceinline__ void run_score_lse(const ScoreParams &P, Items<SPLIT> items, float *s_lse,
                                               volatile int *s_dead, const SBars &B,
                                               volatile int *abort_flag, int lane) {
     const int cols = 1 << (P.lg_nh + P.lg_nq);
@@ -647,10 +671,44 @@ __device__ __forceinline__ void bar_arrive(int id, int threads) {
     asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-__device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items items, int t, int b,
+// Another CTA of the cluster's copy of a place in shared memory; a store to one,
+// an arrival at one, and the wait for such arrivals.
+__device__ __forceinline__ uint32_t cluster_addr(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void st_cluster(float *p, uint32_t rank, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(cluster_addr(p, rank)), "f"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint64_t *bar, uint32_t rank) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
+                     cluster_addr(bar, rank))
+                 : "memory");
+}
+__device__ __forceinline__ bool wait_cluster(uint64_t *bar, uint32_t parity, volatile int *abort) {
+    if (!mbar_wait(bar, parity, abort)) return false;
+    uint32_t done;  // (the phase has completed: seen once more, for the cluster's order)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return done != 0u;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+                     : "memory");
+}
+
+template <bool SPLIT>
+__device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT> items, int t, int b,
                                                const float *s_lse, const volatile int *s_dead,
-                                               float *s_part, uint32_t tmem, const SBars &B,
-                                               volatile int *abort_flag, int wq, int lane) {
+                                               float *s_part, float *comb, uint32_t tmem,
+                                               const SBars &B, volatile int *abort_flag, int wq,
+                                               int lane) {
     const int rk = 32 * wq + lane;  // this thread's key of the tile
     const int cols = 1 << (P.lg_nh + P.lg_nq);
     const uint32_t tb = tmem + (uint32_t)(128 * (2 * t + b)) + ((uint32_t)(32 * wq) << 16);
@@ -662,7 +720,7 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items items
     auto next_item = [&](unsigned &r, SItem &it, int &skipped) {
         for (; items.has(r); ++r) {
             it = items.get(r);
-            if (!it.run) continue;
+            if (!it.any) continue;  // (a part without a product hands over zeros)
             if (it.k0 + t * kKeys < it.L) return true;
             skipped += (it.tt1 - it.tt0) * P.head_groups;
         }
@@ -675,12 +733,14 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items items
     int cnt = 0;          // products of the key tile before the item
     int taken = 0;        // products of this group
     bool gave = false;    // group (t, 1): sums handed over and not yet taken
+    const unsigned part_id = SPLIT ? blockIdx.x & ((1u << P.lg_parts) - 1u) : 0u;
+    unsigned shared = 0u;  // items put together in the cluster
     bool ok = true;
     float old = 0.f;      // the key's score before (group (t, 0))
     int blk = -1;         // and its block
     auto prefetch = [&]() {  // of item nx
         const int key = nx.k0 + t * kKeys + rk;
-        if (b == 0 && key < nx.L) {
+        if (b == 0 && part_id == 0u && key < nx.L) {
             blk = __ldg(&P.block_tables[(size_t)nx.s * P.max_blocks_per_seq + (key >> P.block_shift)]);
             old = P.scores[((long long)nx.s * P.num_kv_heads + nx.hk) * P.score_stride + key];
         }
@@ -688,7 +748,7 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items items
     if (live) prefetch();
     while (live) {
         const SItem it = nx;
-        const int first = first_tile(P, it, t), np = (it.tt1 - first) * P.head_groups;
+        const int first = first_tile<SPLIT>(P, it, t), np = (it.tt1 - first) * P.head_groups;
         const int key = it.k0 + t * kKeys + rk;
         const float old_now = old;
         const int blk_now = blk;
@@ -752,6 +812,28 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items items
             bar_sync(bar_full, 256);
             acc += part[rk];
             bar_arrive(bar_free, 256);
+            if (SPLIT && part_id) {  // to the cluster's first CTA
+                if (shared) ok = ok && wait_cluster(&B.c_free[t], (shared - 1u) & 1u, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    st_cluster(comb + (part_id - 1u) * kItemKeys + t * kKeys + rk, 0u, acc);
+                    __syncwarp();
+                    if (lane == 0) arrive_cluster(&B.c_full[t], 0u);
+                }
+                ++shared;
+                continue;
+            }
+            if (SPLIT) {
+                ok = ok && wait_cluster(&B.c_full[t], shared & 1u, abort_flag);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok) {
+                    const unsigned parts = 1u << P.lg_parts;
+                    for (unsigned i = 0; i + 1u < parts; ++i) acc += comb[i * kItemKeys + t * kKeys + rk];
+                    __syncwarp();
+                    if (lane > 0 && lane < (int)parts) arrive_cluster(&B.c_free[t], (uint32_t)lane);
+                }
+                ++shared;
+            }
             if (ok && !*abort_flag && key < it.L && blk_now >= 0 && blk_now < P.num_blocks)
                 P.scores[((long long)it.s * P.num_kv_heads + it.hk) * P.score_stride + key] =
                     old_now + acc;
@@ -763,7 +845,8 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items items
     }
 }
 
-template <int D>
+// SPLIT: the CTAs of a cluster share one item.
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(kThreadsS, 1)
     prefill_scores_kernel(const __grid_constant__ ScoreParams P, uint32_t fmt) {
     using L = SLayout;
@@ -792,6 +875,8 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     B.s_full = B.l_free + kMaxRing;
     B.s_free = B.s_full + 4;
     B.done = B.s_free + 4;
+    B.c_full = B.done + 2;
+    B.c_free = B.c_full + 2;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         prefetch_tmap(&P.tmap_q);
@@ -804,67 +889,123 @@ __global__ void __launch_bounds__(kThreadsS, 1)
             mbar_init(&B.q_free[b], 2);
             mbar_init(&B.l_free[b], 8);
         }
+        for (int t = 0; SPLIT && t < kTiles; ++t) {  // (a warp arrives once)
+            mbar_init(&B.c_full[t], 4u * ((1u << P.lg_parts) - 1u));
+            mbar_init(&B.c_free[t], 4);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, kTmemColsS);
     STable &table = *reinterpret_cast<STable *>(smem + L::table_off);
+    float *comb = reinterpret_cast<float *>(smem + L::comb_off);
     if (P.table) number_items(P, table);  // (from the lengths alone: before the wait)
     tc_fence_before();
     __syncthreads();
+    if (SPLIT) cluster_sync();  // every CTA has started, its barriers set up
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
     pdl_wait();     // the kernels before may still write what this reads
     pdl_trigger();  // (after the wait: what follows may start before this grid ends, not before those)
-    const Items items(P, table);
+    const Items<SPLIT> items(P, table);
     // each role's code follows its own register reallocation (code after a
     // join of the two would be held to the smaller count)
     if (warp >= 4) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSums));
-        run_score_sums(P, items, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, s_part, tmem, B,
-                       abort_flag, warp & 3, lane);
+        run_score_sums<SPLIT>(P, items, (warp - 4) >> 3, ((warp - 4) >> 2) & 1, s_lse, s_dead, s_part,
+                              comb, tmem, B, abort_flag, warp & 3, lane);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == 0) {
-            run_score_producer<D>(P, items, sk, sq, B, abort_flag, lane);
+            run_score_producer<D, SPLIT>(P, items, sk, sq, B, abort_flag, lane);
         } else if (warp <= 2) {
-            run_score_mma<D>(P, items, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
+            run_score_mma<D, SPLIT>(P, items, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
             // every product has completed before tensor memory is released
             volatile int never = 0;
             mbar_drain_wait(&B.done[warp - 1], 0, &never);
             __syncwarp();
         } else {
-            run_score_lse(P, items, s_lse, s_dead, B, abort_flag, lane);
+            run_score_lse<SPLIT>(P, items, s_lse, s_dead, B, abort_flag, lane);
         }
     }
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     if (warp == 1) tmem_dealloc(tmem, kTmemColsS);
+    if (SPLIT) cluster_sync();  // no CTA leaves while another may still write to it
 }
 
-template <int D>
-pa_status_t launch_scores(const ScoreParams &P, uint32_t fmt, unsigned grid, cudaStream_t stream) {
-    using L = SLayout;
-    constexpr int kMaxDevices = 64;
-    static std::atomic<bool> attr_set[kMaxDevices];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
-    if (!attr_set[dev].load(std::memory_order_relaxed)) {
-        // the register reallocation inside the kernel assumes exactly
-        // kRegsLaunch registers a thread at launch; anything else is refused
-        cudaFuncAttributes fa;
-        if (cudaFuncGetAttributes(&fa, prefill_scores_kernel<D>) != cudaSuccess) return PA_ERR_CUDA;
-        if (fa.numRegs != kRegsLaunch) return PA_ERR_UNSUPPORTED;
-        if (cudaFuncSetAttribute(prefill_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 (int)L::bytes) != cudaSuccess)
-            return PA_ERR_CUDA;
-        attr_set[dev].store(true, std::memory_order_relaxed);
+constexpr int kMaxLgParts = 3;
+static_assert(1 << kMaxLgParts == kMaxParts, "parts of an item");
+
+// A launch of either form; lg: log2 of the CTAs of a cluster.
+struct ScoreLaunch {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    ScoreLaunch(unsigned grid, int lg, cudaStream_t stream) {
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(kThreadsS);
+        cfg.dynamicSmemBytes = SLayout::bytes;
+        cfg.stream = stream;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 1u << lg;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = lg ? 2 : 1;
     }
-    return launch_pdl(prefill_scores_kernel<D>, dim3(grid), dim3(kThreadsS), L::bytes, stream, P,
-                      fmt) == cudaSuccess
+};
+
+template <int D, bool SPLIT>
+pa_status_t set_up_scores() {
+    // the register reallocation inside the kernel assumes exactly kRegsLaunch
+    // registers a thread at launch; anything else is refused
+    cudaFuncAttributes fa;
+    if (cudaFuncGetAttributes(&fa, prefill_scores_kernel<D, SPLIT>) != cudaSuccess) return PA_ERR_CUDA;
+    if (fa.numRegs != kRegsLaunch) return PA_ERR_UNSUPPORTED;
+    return cudaFuncSetAttribute(prefill_scores_kernel<D, SPLIT>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)SLayout::bytes) == cudaSuccess
                ? PA_OK
                : PA_ERR_CUDA;
+}
+
+// tiles: token tiles of the longest sequence of queries.
+template <int D>
+pa_status_t launch_scores(ScoreParams &P, uint32_t fmt, int tiles, int sms, cudaStream_t stream) {
+    constexpr int kMaxDevices = 64;
+    static std::atomic<bool> ready[kMaxDevices];
+    static std::atomic<int> clusters[kMaxDevices][kMaxLgParts + 1];  // that run at once
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PA_ERR_CUDA;
+    if (!ready[dev].load(std::memory_order_acquire)) {
+        pa_status_t e = set_up_scores<D, false>();
+        if (e == PA_OK) e = set_up_scores<D, true>();
+        if (e != PA_OK) return e;
+        for (int lg = 1; lg <= kMaxLgParts; ++lg) {
+            const ScoreLaunch one(1u << lg, lg, stream);
+            int n = 0;
+            if (cudaOccupancyMaxActiveClusters(&n, prefill_scores_kernel<D, true>, &one.cfg) != cudaSuccess)
+                return PA_ERR_CUDA;
+            clusters[dev][lg].store(n, std::memory_order_relaxed);
+        }
+        ready[dev].store(true, std::memory_order_release);
+    }
+    // Few items are shared, while the GPU then has about two of them a CTA and
+    // a CTA two token tiles of the longest.
+    P.lg_parts = 0;
+    for (int lg = 1; lg <= kMaxLgParts; ++lg)
+        if (tiles >= 2 << lg && (unsigned long long)P.num_items << lg <= 2ull * (unsigned)sms &&
+            clusters[dev][lg].load(std::memory_order_relaxed) > 0)
+            P.lg_parts = lg;
+    const unsigned ways = P.lg_parts ? (unsigned)clusters[dev][P.lg_parts].load(std::memory_order_relaxed)
+                                     : (unsigned)sms;
+    const ScoreLaunch l((P.num_items < ways ? P.num_items : ways) << P.lg_parts, P.lg_parts, stream);
+    const cudaError_t e = P.lg_parts ? cudaLaunchKernelEx(&l.cfg, prefill_scores_kernel<D, true>, P, fmt)
+                                     : cudaLaunchKernelEx(&l.cfg, prefill_scores_kernel<D, false>, P, fmt);
+    return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
 
 }  // namespace
@@ -974,8 +1115,9 @@ extern "C" pa_status_t pa_prefill_scores(
     P.num_items = (unsigned)items;
     P.ranges = (int)((max_context_len + (long long)kItemKeys - 1) / kItemKeys);
     P.table = num_seqs <= kMaxTableSeqs && P.ranges <= kMaxTableRanges ? 1 : 0;
-    const unsigned grid = items < (unsigned long long)sms ? (unsigned)items : (unsigned)sms;
+    const int tiles = (int)((max_query_len + (1ll << P.lg_nq) - 1) >> P.lg_nq);
     const uint32_t fmt = dtype == PA_BF16 ? 1u : 0u;
     cudaStream_t st = (cudaStream_t)stream;
-    return head_dim == 64 ? launch_scores<64>(P, fmt, grid, st) : launch_scores<128>(P, fmt, grid, st);
+    return head_dim == 64 ? launch_scores<64>(P, fmt, tiles, sms, st)
+                          : launch_scores<128>(P, fmt, tiles, sms, st);
 }

@@ -232,3 +232,39 @@ def test_repeatable_captured_and_replayed():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(l2, lse) and torch.equal(sc, want + want)
+
+
+@pytest.mark.parametrize("H,Hkv,D,new,lens", [
+    (8, 1, 128, [1024], [1024]), (1, 1, 64, [2000], [2001]), (6, 2, 64, [700, 3, 64], [700, 2000, 300]),
+    (32, 8, 128, [500], [1024]), (4, 4, 128, [257, 0, 1, 640], [257, 100, 700, 641]), (24, 8, 64, [300], [333]),
+    (8, 8, 64, [4000], [4100]), (4, 4, 64, [3000, 200], [4096, 1500]), (16, 2, 128, [1500], [1500])])
+def test_few_items_shared_by_several_blocks_of_threads(H, Hkv, D, new, lens):
+    """Few items of many queries: clusters share them, some with parts that are
+    empty, and the sums do not depend on timing."""
+    c = Cache(lens, Hkv, D, torch.bfloat16, 16, seed=D + H)
+    q, qsl, starts = _batch(c, new, H, D)
+    _, lse = _attend(c, q, qsl, new, D ** -0.5)
+    _check_scores(c, q, starts, qsl, new, lse, D ** -0.5, stride=c.max_len + 5)
+    runs = [pa.prefill_scores(q, lse, c.k[0], c.tables, qsl, c.lens, max(new), c.max_len, D ** -0.5,
+                              torch.zeros(len(lens), Hkv, c.max_len, device=DEV)) for _ in range(3)]
+    assert torch.equal(runs[0], runs[1]) and torch.equal(runs[0], runs[2])
+
+
+def test_shared_items_with_bad_lengths_and_blocks():
+    lens, new = [900, 500, 700], [900, 400, 600]
+    c = Cache(lens, 1, 64, torch.float16, 16, seed=9)
+    q, qsl, starts = _batch(c, new, 4, 64)
+    _, lse = _attend(c, q, qsl, new, 0.125)
+    tables = c.tables.clone()
+    tables[2, 3] = -1  # tokens 48 .. 63 of the last sequence
+    lens_bad = c.lens.clone()
+    lens_bad[1] = 399  # fewer than its new tokens
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    good = pa.prefill_scores(q, lse, c.k[0], c.tables, qsl, c.lens, 900, 900, 0.125, torch.zeros(3, 1, 900, device=DEV))
+    got = pa.prefill_scores(q, lse, c.k[0], tables, qsl, lens_bad, 900, 900, 0.125, torch.zeros(3, 1, 900, device=DEV),
+                            error_word=err)
+    torch.cuda.synchronize()
+    assert int(err.item()) == pa.ERRBIT_CONTEXT_LEN | pa.ERRBIT_BLOCK_OOB
+    assert torch.equal(got[0], good[0]) and not got[1].any()
+    assert not got[2, 0, 48:64].any()
+    assert torch.equal(got[2, 0, :48], good[2, 0, :48]) and torch.equal(got[2, 0, 64:], good[2, 0, 64:])
