@@ -14,28 +14,29 @@
 //
 // How.  A work item is 256 keys of one (sequence, KV head): two tiles of 128
 // keys that share every query tile, which halves the query traffic from L2.  A
-// query tile is up to 128 (token, head) rows: NH heads of the group (the
-// largest power of two that divides it) times NQ tokens, one TMA box.  The
-// kernel is persistent, one CTA per SM; items are numbered from the first keys
-// on (with whole prompts those see the most queries) and dealt out forth and
-// back, so every CTA's share is about as heavy.  Each CTA works the numbering
-// out for itself in shared memory, from the lengths: only ranges that hold
-// keys are numbered (sequences ordered by their number of ranges, so range k's
-// are the first of them), and an item's sequence is at hand without a trip to
-// memory.  Batches past kMaxTableSeqs sequences or kMaxTableRanges ranges number
-// every range up to the longest and pass over the empty ones.
+// query tile is up to 128 (token, head) rows, NH heads of the group times NQ
+// tokens, one TMA box.  The kernel is persistent, one CTA per SM; items are
+// numbered from the first keys on (with whole prompts those see the most
+// queries) and dealt out forth and back, so every CTA's share is about as
+// heavy.  Each CTA works the numbering out for itself in shared memory, from
+// the lengths: only ranges that hold keys are numbered (sequences ordered by
+// their number of ranges, so range k's are the first of them), and an item's
+// sequence is at hand without a trip to memory.  Batches past kMaxTableSeqs
+// sequences or kMaxTableRanges ranges number every range up to the longest and
+// pass over the empty ones.
 // Twenty warps:
-//   * warp 0 (producer): K tiles into a ring of 128-key slots, block by block
-//     (tiled bulk copies, TMA), and query tiles into another; it runs ahead
-//     into the next item;
+//   * warp 0: K tiles into a ring of 128-key slots, block by block (tiled bulk
+//     copies, TMA, one for a block's share: a warp issues one in about 60
+//     cycles, which counts with small blocks); it runs ahead into the next
+//     items;
 //   * warps 1 and 2: S_t = K_t Q^T (M = 128 keys, N = the tile's rows,
 //     K = head_dim) for key tile 0 and 1 into one of two tensor-memory buffers
 //     each (two issuers: the waits of one fall into the other's products);
 //     causal: a key tile starts with the query tile that holds the first token
 //     to see its first key, so the second tile's copy has time while the first
 //     one works alone.  Warp 1 allocates tensor memory;
-//   * warp 3 brings the rows' lse (base 2, negated) beside the query tiles of
-//     the ring, with a flag for tiles that hold rows without a weight;
+//   * warp 3: query tiles into another ring, and beside them the rows' lse
+//     (base 2, negated), with a flag for tiles that hold rows without a weight;
 //   * warps 4..19: four groups of four, group (t, b) for the products of key
 //     tile t in buffer b, one key a thread (the lanes a warp may read go by
 //     its number modulo 4).  Each loads S from tensor memory 32 columns at a
@@ -49,15 +50,19 @@
 // cluster of 2, 4 or 8 CTAs shares each: the query tiles in equal parts one
 // after the other, and the first CTA's group (t, 0) adds the others' sums, in
 // their order, through distributed shared memory.  One prompt, 32 heads on 8 of
-// 128, with clusters and without: 4096 tokens 70 and 119 us, 1024 tokens 21 and
+// 128, with clusters and without: 4096 tokens 68 and 119 us, 1024 tokens 21 and
 // 39 us.
 //
-// Bound: 2 prompts of 4096 tokens, 32 heads on 8 of 128, bf16, take 122 us; the
-// products are 73 us at the rate of a large bf16 matrix product.  A scheduler
-// spends about eight cycles on a warp's column of weights, four of them on the
-// exponential (58 us in all at four).  Query tiles of 256 rows with one buffer a
-// key tile took 134 to 151 us.  A window of few queries is bound by the steps
-// of an item one after the other.
+// Bound: 2 prompts of 4096 tokens, 32 heads on 8 of 128, bf16, take 120 us; the
+// products are 73 us at the rate of a large bf16 matrix product, and the sums 80
+// at the 5.5 cycles a column that four busy warps of a scheduler take (four of
+// them the exponential).  What keeps the two from overlapping is a buffer's
+// turn: product, hand-over, the sums of all but its last columns, hand-over
+// back, about 3500 cycles for two query tiles whose sums take 2800; tensor
+// memory is full with two buffers a key tile.  (Query tiles of 256 rows with
+// one buffer: 134 to 151 us.)  Windows of few queries are bound by the steps of
+// an item one after the other: 8 of 32 queries on 3000 to 16384 tokens, 12
+// heads on 2, take 18.6 us for 39 MB.
 //
 // A wait that gives up sets the abort flag; the groups then go through the
 // rest of their items without waiting or writing, so that their named barriers
@@ -101,16 +106,19 @@ constexpr int kMaxTableSeqs = 512, kMaxTableRanges = 2047;  // sizes of the item
 
 struct ScoreParams {
     CUtensorMap tmap_q;  // query as [head_dim/64][tokens][heads][64], box NQ x NH rows
-    CUtensorMap tmap_k;  // pool rows as [head_dim/64][rows][64], box min(block, 64) rows
+    // pool rows as [rows/8][head_dim/64][8][64], box min(block, 64) rows: the two
+    // 64-element slices of eight keys lie one after the other in a K tile
+    CUtensorMap tmap_k;
     const float *lse;
     const int32_t *block_tables, *query_start_loc, *context_lens;
     float *scores;
     long long score_stride;
     int max_blocks_per_seq, block_shift, num_blocks;
     int max_query_len, max_context_len, num_seqs, num_tokens, num_heads, num_kv_heads, G;
-    int lg_nh, lg_nq;     // heads and tokens of a query tile
+    int nh, lg_nq;        // heads and log2 of the tokens of a query tile
     int head_groups;      // G / NH
     int rk, rq;           // slots of the K and the query ring
+    unsigned rq_inv, kv_inv;  // small_inverse of rq and num_kv_heads
     unsigned num_items;   // 256-key ranges x num_seqs x num_kv_heads
     int ranges;           // 256-key ranges of the longest context
     int table;            // 1: items are numbered by the table in shared memory
@@ -167,6 +175,15 @@ struct Ring {
     }
 };
 
+// x / d for x below 2^31, by a multiplication: with inv = floor(2^32 / d) the
+// high word of x inv is the quotient or one less.  (Every role works out every
+// item.)
+inline unsigned small_inverse(unsigned d) { return d == 1u ? 0xffffffffu : (unsigned)((1ull << 32) / d); }
+__device__ __forceinline__ unsigned small_div(unsigned x, unsigned d, unsigned inv) {
+    const unsigned q = __umulhi(x, inv);
+    return x - q * d >= d ? q + 1u : q;
+}
+
 // One work item, worked out by every role for itself.
 struct SItem {
     int s, hk;
@@ -182,9 +199,44 @@ __device__ __forceinline__ bool lengths_ok(const ScoreParams &P, int a, int b, i
            L <= P.max_context_len;
 }
 
-// Fill the table (every thread of the CTA).
+// Fill the table (every thread of the CTA; ready after a barrier).  Up to 32
+// sequences: every warp reads the lengths, a lane a sequence, and no step waits
+// for another warp's (done after 1700 cycles instead of 3400).
 __device__ __forceinline__ void number_items(const ScoreParams &P, STable &T) {
     const int tid = threadIdx.x, S = P.num_seqs;
+    if (S <= 32) {
+        const int s = tid & 31;
+        int a = 0, b = 0, L = 0;
+        if (s < S) {
+            a = __ldg(&P.query_start_loc[s]);
+            b = __ldg(&P.query_start_loc[s + 1]);
+            L = __ldg(&P.context_lens[s]);
+        }
+        const bool ok = lengths_ok(P, a, b, L);
+        const int mine = s < S && ok && b > a ? (L + kItemKeys - 1) / kItemKeys : 0;
+        if (tid < S) {
+            if (!ok && blockIdx.x == 0 && P.err) atomicOr(P.err, PA_ERRBIT_CONTEXT_LEN);
+            T.tok0[s] = a;
+            T.n[s] = b - a;
+            T.L[s] = L;
+        }
+        int place = 0;
+        unsigned before = 0u;  // items of the ranges before range tid
+        for (int j = 0; j < S; ++j) {
+            const int r = __shfl_sync(0xffffffffu, mine, j);
+            place += r > mine || (r == mine && j < s);
+            before += (unsigned)min(r, tid);
+        }
+        if (tid < S) T.order[place] = (unsigned short)s;
+        if (tid <= P.ranges) T.first[tid] = before * (unsigned)P.num_kv_heads;
+        for (int k0 = kThreadsS; k0 <= P.ranges; k0 += kThreadsS) {  // (whole warps)
+            before = 0u;
+            for (int j = 0; j < S; ++j)
+                before += (unsigned)min(__shfl_sync(0xffffffffu, mine, j), k0 + tid);
+            if (k0 + tid <= P.ranges) T.first[k0 + tid] = before * (unsigned)P.num_kv_heads;
+        }
+        return;
+    }
     for (int s = tid; s < S; s += kThreadsS) {
         const int a = __ldg(&P.query_start_loc[s]), b = __ldg(&P.query_start_loc[s + 1]);
         const int L = __ldg(&P.context_lens[s]);
@@ -232,7 +284,6 @@ __device__ __forceinline__ void number_items(const ScoreParams &P, STable &T) {
             carry = __shfl_sync(0xffffffffu, v, 31);
         }
     }
-    __syncthreads();
 }
 
 // A role's way through the CTA's items, round by round: forth and back over the
@@ -252,13 +303,17 @@ struct Items {
         return r * ways + ((r & 1u) ? ways - 1u - way : way);
     }
     __device__ __forceinline__ bool has(unsigned r) const { return id(r) < total; }
-    // the item of round r (rounds in ascending order)
+    // the item of round r (rounds in ascending order; the whole warp)
     __device__ __forceinline__ SItem get(unsigned r) {
         SItem it;
         const unsigned i = id(r), Hkv = (unsigned)P.num_kv_heads;
         if (P.table) {
-            while (i >= T.first[range + 1]) ++range;
-            const unsigned rest = i - T.first[range], place = rest / Hkv;
+            for (int n = 32; n == 32;) {  // on by the ranges that end at or before i
+                const int k = range + 1 + (int)(threadIdx.x & 31);
+                n = __popc(__ballot_sync(0xffffffffu, k <= P.ranges && T.first[k] <= i));
+                range += n;
+            }
+            const unsigned rest = i - T.first[range], place = small_div(rest, Hkv, P.kv_inv);
             it.s = T.order[place];
             it.hk = (int)(rest - place * Hkv);
             it.tok0 = T.tok0[it.s];
@@ -302,18 +357,15 @@ __device__ __forceinline__ int first_tile(const ScoreParams &P, const SItem &it,
 }
 
 // ---------------------------------------------------------------------------
-// warp 0: K and query copies
+// warp 0: K copies
 // ---------------------------------------------------------------------------
 template <int D, bool SPLIT>
 __device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items<SPLIT> items, unsigned char *sk,
-                                                   unsigned char *sq, const SBars &B,
-                                                   volatile int *abort_flag, int lane) {
+                                                   const SBars &B, volatile int *abort_flag, int lane) {
     constexpr int KB = D / 64;
     constexpr uint32_t ktile = KB * kKSlice;
     const int lg_tbr = min(P.block_shift, 6);  // a copy: one block's share, 8 .. 64 keys
     const int units = kItemKeys >> lg_tbr;     // of an item, 4 .. 32: a lane each
-    const int cols = 1 << (P.lg_nh + P.lg_nq);
-    const uint32_t q_bytes = (uint32_t)cols * 128u * KB;
     const uint64_t policy = l2_evict_first_policy();
     // this lane's unit of an item: the block it lies in, -1 past the last key
     auto entry = [&](const SItem &it) {
@@ -322,8 +374,8 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items<S
                    ? __ldg(&P.block_tables[(size_t)it.s * P.max_blocks_per_seq + (tok >> P.block_shift)])
                    : -1;
     };
-    Ring kr, qr;
-    int kn = 0, qn = 0;  // slots armed so far
+    Ring kr;
+    int kn = 0;  // slots armed so far
     bool ok = true;
     SItem it, nx;
     int e = -1, en = -1;
@@ -358,44 +410,17 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items<S
                                       ((uint32_t)__popc(good & (t ? ~low : low)) << lg_tbr) * 128u * KB);
             __syncwarp();
             if (use && !bad && (row >> 7) == t) {
-                unsigned char *dst = sk + (size_t)kr.slot * ktile + (size_t)(row & 127) * 128;
                 const int y = ((e * P.num_kv_heads + it.hk) << P.block_shift) +
                               (tok & ((1 << P.block_shift) - 1));
-#pragma unroll
-                for (int z = 0; z < KB; ++z)
-                    tma_load_3d(dst + (size_t)z * kKSlice, &P.tmap_k, 0, y, z, &B.k_full[kr.slot],
-                                policy);
+                tma_load_4d(sk + (size_t)kr.slot * ktile + (size_t)(row & 127) * (128 * KB),
+                            &P.tmap_k, 0, 0, 0, y >> 3, &B.k_full[kr.slot], policy);
             }
             __syncwarp();
             kr.next(P.rk);
             ++kn;
         };
-        auto load_q = [&](int from, int to) {
-            if (lane == 0) {
-                for (int tt = from; ok && tt < to; ++tt)
-                    for (int hg = 0; hg < P.head_groups; ++hg) {
-                        ok = mbar_wait(&B.q_free[qr.slot], qr.phase ^ 1u, abort_flag);
-                        if (!ok) break;
-                        mbar_arrive_expect_tx(&B.q_full[qr.slot], q_bytes);
-                        asm volatile(
-                            "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
-                            " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
-                                smem_u32(sq + (size_t)qr.slot * q_bytes)),
-                            "l"(&P.tmap_q), "r"(0), "r"(it.hk * P.G + (hg << P.lg_nh)),
-                            "r"(it.tok0 + (tt << P.lg_nq)), "r"(0),
-                            "r"(smem_u32(&B.q_full[qr.slot]))
-                            : "memory");
-                        qr.next(P.rq);
-                        ++qn;
-                    }
-            }
-            ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
-        };
-        const int second = first_tile<SPLIT>(P, it, 1);
         load_k(0);
-        if (ok) load_q(it.tt0, second);
-        if (ok && second < it.tt1) load_k(1);
-        if (ok) load_q(second, it.tt1);
+        if (ok && first_tile<SPLIT>(P, it, 1) < it.tt1) load_k(1);
     }
     if (lane == 0) {
         if (!ok) {
@@ -407,8 +432,6 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items<S
         volatile int never = 0;
         for (int i = max(0, kn - P.rk); i < kn; ++i)
             mbar_drain_wait(&B.k_full[i % P.rk], (uint32_t)(i / P.rk) & 1u, &never);
-        for (int i = max(0, qn - P.rq); i < qn; ++i)
-            mbar_drain_wait(&B.q_full[i % P.rq], (uint32_t)(i / P.rq) & 1u, &never);
     }
     __syncwarp();
 }
@@ -433,10 +456,10 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
                                               const SBars &B, volatile int *abort_flag) {
     constexpr int KB = D / 64;
     constexpr uint32_t ktile = KB * kKSlice;
-    const uint32_t cols = 1u << (P.lg_nh + P.lg_nq);
+    const uint32_t cols = (uint32_t)P.nh << P.lg_nq;
     const uint32_t idesc = umma_idesc_f16(fmt, 0, 0, kKeys, cols);
     const uint32_t q_bytes = cols * 128u * KB;
-    const uint64_t dk0 = umma_desc_sw128(smem_u32(sk), 16, 1024);
+    const uint64_t dk0 = umma_desc_sw128(smem_u32(sk), 16, 1024 * KB);
     const uint64_t dq0 = umma_desc_sw128(smem_u32(sq), 16, 1024);
     const uint32_t q_slice16 = cols * 128u / 16u;  // (head_dim 128: one further slice)
     Ring kr, qr, sr;
@@ -498,7 +521,7 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
                 for (int kk = 0; kk < D / 16; ++kk)
                     umma_f16(ts,
                              (dk0 & 0xffffffff00000000ull) |
-                                 (dk + (uint32_t)((kk >> 2) * (kKSlice / 16) + (kk & 3) * 2)),
+                                 (dk + (uint32_t)((kk >> 2) * (1024 / 16) + (kk & 3) * 2)),
                              (dq0 & 0xffffffff00000000ull) |
                                  (dq + (uint32_t)((kk & 3) * 2) + ((kk >> 2) ? q_slice16 : 0u)),
                              idesc, kk > 0 ? 1u : 0u);
@@ -507,7 +530,7 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
                 if (n == 1) umma_commit(&B.k_free[ks.slot]);
             }
             __syncwarp();
-            if (n == total) nx = next_item();  // while the products run
+            if (n == 1) nx = next_item();  // while the products run
             sr.next(2);
             qr.next(P.rq);
         }
@@ -522,15 +545,18 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
 }
 
 // ---------------------------------------------------------------------------
-// warp 3: the rows' lse
+// warp 3: query copies and the rows' lse
 // ---------------------------------------------------------------------------
-template <bool SPLIT>
-__device__ __forceinline__ void run_score_lse(const ScoreParams &P, Items<SPLIT> items, float *s_lse,
+template <int D, bool SPLIT>
+__device__ __forceinline__ void run_score_rows(const ScoreParams &P, Items<SPLIT> items,
+                                              unsigned char *sq, float *s_lse,
                                               volatile int *s_dead, const SBars &B,
                                               volatile int *abort_flag, int lane) {
-    const int cols = 1 << (P.lg_nh + P.lg_nq);
+    const int cols = P.nh << P.lg_nq;
+    const uint32_t q_bytes = (uint32_t)cols * (2u * D);
     constexpr int kPer = kMaxCols / 32;
     Ring lr;
+    int qn = 0;  // query slots armed so far
     bool ok = true;
     // the next query tile, whose lse is on its way
     unsigned r = 0;
@@ -548,19 +574,50 @@ __device__ __forceinline__ void run_score_lse(const ScoreParams &P, Items<SPLIT>
         return false;
     };
     float l[kPer];
+    int tok[kPer], head[kPer];  // of this lane's rows in a tile
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        tok[k] = (32 * k + lane) / P.nh;
+        head[k] = 32 * k + lane - tok[k] * P.nh;
+    }
     auto load = [&]() {
 #pragma unroll
         for (int k = 0; k < kPer; ++k) {
-            const int row = 32 * k + lane, i = (tt << P.lg_nq) + (row >> P.lg_nh);
+            const int i = (tt << P.lg_nq) + tok[k];
             l[k] = -INFINITY;  // no such row, or one without a weight
-            if (row < cols && i < it.n)
-                l[k] = __ldg(&P.lse[(size_t)(it.tok0 + i) * P.num_heads + it.hk * P.G +
-                                    (hg << P.lg_nh) + (row & ((1 << P.lg_nh) - 1))]);
+            if (32 * k + lane < cols && i < it.n)
+                l[k] = __ldg(&P.lse[(size_t)(it.tok0 + i) * P.num_heads + it.hk * P.G + hg * P.nh +
+                                    head[k]]);
         }
     };
+    Ring qr;
+    auto copy = [&]() {  // the tile's rows; false if the wait for its slot gave up
+        if (lane == 0) {
+            ok = mbar_wait(&B.q_free[qr.slot], qr.phase ^ 1u, abort_flag);
+            if (ok) {
+                mbar_arrive_expect_tx(&B.q_full[qr.slot], q_bytes);
+                asm volatile(
+                    "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                    " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                        smem_u32(sq + (size_t)qr.slot * q_bytes)),
+                    "l"(&P.tmap_q), "r"(0), "r"(it.hk * P.G + hg * P.nh),
+                    "r"(it.tok0 + (tt << P.lg_nq)), "r"(0), "r"(smem_u32(&B.q_full[qr.slot]))
+                    : "memory");
+                ++qn;
+            }
+        }
+        qr.next(P.rq);
+        ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
+        return ok;
+    };
+    // a tile's rows are on their way before the slot of the tile before it has
+    // its lse (that slot's sums may still be at work)
     bool live = next_item();
-    if (live) load();
-    while (live) {
+    if (live) {
+        load();
+        copy();
+    }
+    while (live && ok) {
         float v[kPer];
         bool any_dead = false;
 #pragma unroll
@@ -576,7 +633,10 @@ __device__ __forceinline__ void run_score_lse(const ScoreParams &P, Items<SPLIT>
                 live = next_item();
             }
         }
-        if (live) load();
+        if (live) {
+            load();
+            if (!copy()) break;
+        }
         if (lane == 0) ok = mbar_wait(&B.l_free[lr.slot], lr.phase ^ 1u, abort_flag);
         ok = __shfl_sync(0xffffffffu, (int)ok, 0) != 0;
         if (!ok) break;
@@ -587,10 +647,18 @@ __device__ __forceinline__ void run_score_lse(const ScoreParams &P, Items<SPLIT>
         if (lane == 0) mbar_arrive(&B.l_full[lr.slot]);
         lr.next(P.rq);
     }
-    if (!ok && lane == 0) {
-        *abort_flag = 1;
-        if (P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
+    if (lane == 0) {
+        if (!ok) {
+            *abort_flag = 1;
+            if (P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
+        }
+        // every copy issued lands before the CTA can exit: the last phase armed
+        // of every slot
+        volatile int never = 0;
+        for (int i = max(0, qn - P.rq); i < qn; ++i)
+            mbar_drain_wait(&B.q_full[i % P.rq], (uint32_t)(i / P.rq) & 1u, &never);
     }
+    __syncwarp();
 }
 
 // ---------------------------------------------------------------------------
@@ -710,7 +778,7 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
                                                const SBars &B, volatile int *abort_flag, int wq,
                                                int lane) {
     const int rk = 32 * wq + lane;  // this thread's key of the tile
-    const int cols = 1 << (P.lg_nh + P.lg_nq);
+    const int cols = P.nh << P.lg_nq;
     const uint32_t tb = tmem + (uint32_t)(128 * (2 * t + b)) + ((uint32_t)(32 * wq) << 16);
     float *part = s_part + t * kKeys;
     const int bar_full = 1 + t, bar_free = 3 + t;
@@ -754,9 +822,6 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
         const int blk_now = blk;
         const int qp = q0 + (first - it.tt0) * P.head_groups;  // query tile of product 0
         q0 += (it.tt1 - it.tt0) * P.head_groups;
-        ++r;
-        live = next_item(r, nx, q0);
-        if (live) prefetch();
         float acc = 0.f;
         int tt = first, hg = 0, p = (cnt ^ b) & 1;
         auto step = [&](int by) {
@@ -765,8 +830,9 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
         step(p);
         cnt += np;
         // the ring's slot of its query tile
-        int slot = (int)((unsigned)(qp + p) % (unsigned)P.rq);
-        uint32_t phase = ((unsigned)(qp + p) / (unsigned)P.rq) & 1u;
+        const unsigned turn = small_div((unsigned)(qp + p), (unsigned)P.rq, P.rq_inv);
+        int slot = qp + p - (int)turn * P.rq;
+        uint32_t phase = turn & 1u;
         auto slot_step = [&]() {
             slot += 2;
             if (slot >= P.rq) {
@@ -794,8 +860,8 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
             tc_fence_after();
             const float *nl = s_lse + slot * kMaxCols;
             const int tok = tt << P.lg_nq;  // the tile's first token
-            const int lo = max(0, key - it.c - tok) << P.lg_nh;
-            const int hi = (it.n - tok) << P.lg_nh;
+            const int lo = max(0, key - it.c - tok) * P.nh;
+            const int hi = (it.n - tok) * P.nh;
             const bool all = __all_sync(0xffffffffu, lo == 0) && hi >= cols && !s_dead[slot];
             acc += all ? sum_product<true, kChunk>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b])
                        : sum_product<false, kChunk>(tb, cols, nl, lo, hi, sc2, &B.s_free[2 * t + b]);
@@ -821,9 +887,7 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
                     if (lane == 0) arrive_cluster(&B.c_full[t], 0u);
                 }
                 ++shared;
-                continue;
-            }
-            if (SPLIT) {
+            } else if (SPLIT) {
                 ok = ok && wait_cluster(&B.c_full[t], shared & 1u, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
                 if (ok) {
@@ -834,10 +898,14 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
                 }
                 ++shared;
             }
-            if (ok && !*abort_flag && key < it.L && blk_now >= 0 && blk_now < P.num_blocks)
+            if (part_id == 0u && ok && !*abort_flag && key < it.L && blk_now >= 0 &&
+                blk_now < P.num_blocks)
                 P.scores[((long long)it.s * P.num_kv_heads + it.hk) * P.score_stride + key] =
                     old_now + acc;
         }
+        ++r;
+        live = next_item(r, nx, q0);
+        if (live) prefetch();
     }
     if (!ok) {
         *abort_flag = 1;
@@ -917,7 +985,7 @@ __global__ void __launch_bounds__(kThreadsS, 1)
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsOther));
         if (warp == 0) {
-            run_score_producer<D, SPLIT>(P, items, sk, sq, B, abort_flag, lane);
+            run_score_producer<D, SPLIT>(P, items, sk, B, abort_flag, lane);
         } else if (warp <= 2) {
             run_score_mma<D, SPLIT>(P, items, warp - 1, fmt, sk, sq, tmem, B, abort_flag);
             // every product has completed before tensor memory is released
@@ -925,7 +993,7 @@ __global__ void __launch_bounds__(kThreadsS, 1)
             mbar_drain_wait(&B.done[warp - 1], 0, &never);
             __syncwarp();
         } else {
-            run_score_lse<SPLIT>(P, items, s_lse, s_dead, B, abort_flag, lane);
+            run_score_rows<D, SPLIT>(P, items, sq, s_lse, s_dead, B, abort_flag, lane);
         }
     }
     tc_fence_before();
@@ -1060,35 +1128,47 @@ extern "C" pa_status_t pa_prefill_scores(
     ScoreParams P;
     std::memset(&P, 0, sizeof(P));
     const int G = num_heads / num_kv_heads;
-    // A query tile: NH heads, the largest power of two that divides the group
-    // (at most 128), and NQ tokens, as many as make 128 rows but no more than
-    // the longest sequence of queries needs (at least 32 rows, one step of a
-    // thread's loads).
-    while (P.lg_nh < 7 && G % (2 << P.lg_nh) == 0) ++P.lg_nh;
-    while (P.lg_nh + P.lg_nq < 7 &&
-           ((1 << P.lg_nq) < max_query_len || P.lg_nh + P.lg_nq < 5))
-        ++P.lg_nq;
-    P.head_groups = G >> P.lg_nh;
+    // A query tile: NH heads, a divisor of the group, and NQ tokens, a power of
+    // two; 32 to 128 rows in steps of 32, a thread's loads.  The fewest columns
+    // for the longest sequence of queries, a tile's fixed cost counted as 32
+    // (8 windows of 32 queries, 12 heads on 2: 18.6 us with two tiles of 16
+    // tokens by 6 heads, 20.2 with three of 32 by 2).
+    long long best = -1;
+    for (int nh = G < kMaxCols ? G : kMaxCols; nh >= 1; --nh) {
+        if (G % nh) continue;
+        for (int lg = 7; lg >= 0; --lg) {
+            const int cols = nh << lg;
+            if (cols > kMaxCols || cols % kChunk) continue;
+            const long long cost = ((max_query_len + (1ll << lg) - 1) >> lg) * (G / nh) * (cols + 32);
+            if (best >= 0 && cost >= best) continue;
+            best = cost;
+            P.nh = nh;
+            P.lg_nq = lg;
+        }
+    }
+    P.head_groups = G / P.nh;
     // the rings: three K tiles and three full query tiles at head_dim 128; with
     // query tiles of at most 64 rows (windows) more of both
-    const uint32_t kbytes = (uint32_t)head_dim * 256u, qbytes = (uint32_t)head_dim * 2u << (P.lg_nh + P.lg_nq);
+    const uint32_t kbytes = (uint32_t)head_dim * 256u, qbytes = (uint32_t)head_dim * 2u * P.nh << P.lg_nq;
     P.rk = qbytes < kbytes ? 4 : 3;
     if (head_dim == 64) P.rk *= 2;
     P.rq = (int)((kTileBytes - (uint32_t)P.rk * kbytes) / qbytes);
     if (P.rq > kMaxRing) P.rq = kMaxRing;
+    P.rq_inv = small_inverse((unsigned)P.rq);
+    P.kv_inv = small_inverse((unsigned)num_kv_heads);
     const cuuint64_t KB = (cuuint64_t)head_dim / 64;
     {
         const cuuint64_t dims[4] = {64u, (cuuint64_t)num_heads, (cuuint64_t)num_tokens, KB};
         const cuuint64_t strides[3] = {(cuuint64_t)head_dim * 2,
                                        (cuuint64_t)num_heads * head_dim * 2, 128u};
-        const cuuint32_t box[4] = {64u, 1u << P.lg_nh, 1u << P.lg_nq, (cuuint32_t)KB};
+        const cuuint32_t box[4] = {64u, (cuuint32_t)P.nh, 1u << P.lg_nq, (cuuint32_t)KB};
         if (!encode_tiled(&P.tmap_q, query, dtype, 4, dims, strides, box)) return PA_ERR_CUDA;
     }
     {
-        const cuuint64_t dims[3] = {64u, (cuuint64_t)pool_rows, KB};
-        const cuuint64_t strides[2] = {(cuuint64_t)head_dim * 2, 128u};
-        const cuuint32_t box[3] = {64u, (cuuint32_t)(block_size < 64 ? block_size : 64), 1u};
-        if (!encode_tiled(&P.tmap_k, k_cache, dtype, 3, dims, strides, box)) return PA_ERR_CUDA;
+        const cuuint64_t dims[4] = {64u, 8u, KB, (cuuint64_t)pool_rows / 8};
+        const cuuint64_t strides[3] = {(cuuint64_t)head_dim * 2, 128u, (cuuint64_t)head_dim * 16};
+        const cuuint32_t box[4] = {64u, 8u, (cuuint32_t)KB, (cuuint32_t)(block_size < 64 ? block_size : 64) / 8};
+        if (!encode_tiled(&P.tmap_k, k_cache, dtype, 4, dims, strides, box)) return PA_ERR_CUDA;
     }
     P.lse = lse;
     P.block_tables = block_tables;

@@ -268,3 +268,25 @@ def test_shared_items_with_bad_lengths_and_blocks():
     assert torch.equal(got[0], good[0]) and not got[1].any()
     assert not got[2, 0, 48:64].any()
     assert torch.equal(got[2, 0, :48], good[2, 0, :48]) and torch.equal(got[2, 0, 64:], good[2, 0, 64:])
+
+
+@pytest.mark.parametrize("S", [40, 600])
+def test_many_items_for_each_block_of_threads(S):
+    """More items than a CTA lists ahead (with and without the numbering table)."""
+    lens, new = [9000] + [700] * (S - 1), [3] + [2] * (S - 1)
+    if S == 40:  # 40 sequences of up to 9000 tokens, 64 heads: more than 200 items a CTA
+        lens = [9000 - 64 * s for s in range(S)]
+    c = Cache(lens, 64, 64, torch.float16, 64, seed=S)
+    q, qsl, starts = _batch(c, new, 64, 64)
+    _, lse = _attend(c, q, qsl, new, 0.125)
+    scores = pa.prefill_scores(q, lse, c.k[0], c.tables, qsl, c.lens, 3, c.max_len, 0.125,
+                               torch.zeros(S, 64, c.max_len, device=DEV))
+    for s in {0, 1, S // 2, S - 1}:
+        for h in (0, 17, 63):
+            w, tol = _want(c, q, starts, new, lse, 0.125, s, h, 1)
+            d = (scores[s, h, :lens[s]].double() - w).abs()
+            assert bool((d <= tol + 2 * 2.0 ** -24 * (w + 1) + 1e-30).all()), (s, h, float(d.max()))
+    assert not scores[1, :, lens[1]:].any()
+    per_row = scores.sum((1, 2), dtype=torch.float64).cpu()
+    want = torch.tensor(new, dtype=torch.float64) * 64  # every row's weights sum to one
+    assert float((per_row - want).abs().max()) < 1e-3
