@@ -3,6 +3,10 @@ scores, a fork, decode steps with scores, eviction in place with the block
 manager's copies, and decode steps after it.  A list of rows per (layer,
 sequence, head) follows along in 64 bits; every output and score is compared
 with it (tolerances: cachelib)."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -331,3 +335,63 @@ def test_one_workspace_for_calls_of_all_sizes():
     for _ in range(5):
         for a, b in zip(go(ws, False), want):
             assert torch.equal(a, b)
+
+
+FIRST_CALLS = """
+import sys
+sys.path[:0] = [{root!r}, {tests!r}]
+import torch
+import paged_kv_cache_pa_gb300 as pa
+from cachelib import Cache
+D, H, Hkv, L = 128, 8, 2, 1000
+c = Cache([L, 300], Hkv, D, torch.bfloat16, 16, seed=1)
+q = torch.randn(1300, H, D, device="cuda:0").bfloat16()
+one = q[:2].contiguous()
+qsl = torch.tensor([0, L, 1300], dtype=torch.int32, device="cuda:0")
+pos = torch.arange(2, device="cuda:0") + 400
+slots = torch.tensor([-1, -1], device="cuda:0")
+keep = torch.tensor([500, 100], dtype=torch.int32, device="cuda:0")
+rotary = pa.Rotary([1.0 / (i + 1) for i in range(64)])
+kv = one[:, :Hkv].contiguous()
+ws = [torch.empty(64 << 20, dtype=torch.uint8, device="cuda:0") for _ in range(4)]
+new = torch.empty(2, dtype=torch.int32, device="cuda:0")
+out, lse, sc = torch.empty_like(q), torch.empty(1300, H, device="cuda:0"), torch.zeros(2, Hkv, L, device="cuda:0")
+out1, rot = torch.empty_like(one), torch.empty_like(one)
+
+def calls():
+    pa.rotary_cache_write(one, kv, kv, pos, rotary, c.k[0], c.v[0], slots, query_out=rot)
+    pa.prefill_attention(q, c.k[0], c.v[0], c.tables, qsl, c.lens, L, L, 0.1, out=out, workspace=ws[0], lse=lse)
+    pa.prefill_scores(q, lse, c.k[0], c.tables, qsl, c.lens, L, L, 0.1, sc, workspace=ws[1])
+    pa.decode_attention_scored(rot, c.k[0], c.v[0], c.tables, c.lens, L, 0.1, sc, out=out1, workspace=ws[2])
+    pa.evict_tokens(c.k, c.v, [sc], c.tables, c.lens, keep, L, 500, num_recent=9, new_lens=new, workspace=ws[3])
+
+k0, v0 = c.k[0].clone(), c.v[0].clone()
+results = []
+def collect():
+    torch.cuda.synchronize()
+    results.append([t.view(torch.int16).clone() if t.dtype == torch.bfloat16 else t.clone()
+                    for t in (rot, out, lse, sc, out1, new, c.k[0], c.v[0])])
+    c.k[0].copy_(k0); c.v[0].copy_(v0); sc.zero_(); new.zero_(); out.zero_(); out1.zero_()
+    torch.cuda.synchronize()
+
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):  # the process's first calls of the library
+    calls()
+torch.cuda.synchronize()
+for _ in range(3):
+    g.replay()
+    collect()
+calls()
+collect()
+assert results[0][5].tolist() == [500, 100]
+for r in results[1:]:
+    assert all(torch.equal(a, b) for a, b in zip(r, results[0]))
+print("the same")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    tests = os.path.dirname(os.path.abspath(__file__))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests)],
+                       capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip().endswith("the same"), r.stdout[-2000:] + r.stderr[-4000:]

@@ -18,7 +18,8 @@ for p in (ROOT, HERE):
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
-CASES = ["decode_scored_g1", "decode_scored_g6", "prefill_scores_64", "prefill_scores_128", "evict_in_place"]
+CASES = ["decode_scored_g1", "decode_scored_g6", "prefill_scores_64", "prefill_scores_128", "prefill_scores_many_128",
+         "evict_in_place"]
 
 
 def _run(case, err):
@@ -34,12 +35,13 @@ def _run(case, err):
         return c, sc, H
     if case.startswith("prefill"):
         D = int(case.rsplit("_", 1)[1])
-        c = Cache([900, 600, 300], 2, D, torch.float16, seed=1)
-        new = [900, 200, 64]
+        times = 20 if "many" in case else 1  # more items than are shared by clusters
+        c = Cache([900, 600, 300] * times, 2, D, torch.float16, seed=1)
+        new = [900, 200, 64] * times
         q = torch.randn(sum(new), 6, D, generator=g, device=DEV).to(torch.float16)
         lse = torch.full((sum(new), 6), 7.0, device=DEV)
-        qsl = torch.tensor([0, 900, 1100, 1164], dtype=torch.int32, device=DEV)
-        sc = torch.zeros(3, 2, 900, device=DEV)
+        qsl = torch.tensor([0] + new, device=DEV).cumsum(0).int()
+        sc = torch.zeros(len(new), 2, 900, device=DEV)
         pa.prefill_scores(q, lse, c.k[0], c.tables, qsl, c.lens, 900, 900, D ** -0.5, sc, error_word=err)
         return c, sc, (q, new)
     c = Cache([40000], 4, 128, torch.float16, seed=1)
