@@ -34,6 +34,7 @@ Build the library with ``python -m paged_kv_cache_pa_gb300.build``.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -254,16 +255,19 @@ class Rotary:
         return self._struct.num_axes
 
 
-def _rows(t, name):
-    """Pointer and token stride (elements) of [T][heads][D] whose heads are
-    dense and whose tokens may be apart (a slice of a projection's rows)."""
+def _rows(t, name, row):
+    """Pointer and token stride (elements) of [T][heads][D], row = heads * D,
+    whose heads are dense and whose tokens may be apart (a slice of a
+    projection's rows)."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if t.is_contiguous():
+        return t.data_ptr(), row
     n, h, d = t.shape
     token, head, element = t.stride()
     if element != 1 or (h > 1 and head != d):
         raise ValueError(f"{name} must have dense heads")
-    return t.data_ptr(), (token if n > 1 else h * d)
+    return t.data_ptr(), (token if n > 1 else row)
 
 
 def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_cache,
@@ -295,8 +299,8 @@ def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_
     elif query_out is not query and (query_out.shape != (T, H, D) or query_out.dtype != dt):
         raise ValueError("query_out must match the query")
     st = load_library().pa_rotary_cache_write(
-        *_rows(query_out, "query_out"), *_rows(query, "query"), *_rows(key, "key"),
-        *_rows(value, "value"), _dev(positions, "positions"), rotary._ptr,
+        *_rows(query_out, "query_out", H * D), *_rows(query, "query", H * D),
+        *_rows(key, "key", hkv * D), *_rows(value, "value", hkv * D), _dev(positions, "positions"), rotary._ptr,
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"),
         T, nb, bs, H, hkv, d, _dtype_code(dt), _opt_ptr(error_word, "error_word"),
         _stream_ptr(stream, query.device))
@@ -625,8 +629,16 @@ def evict_workspace_size(num_layers: int, num_seqs: int, num_kv_heads: int, max_
                                                       max_context_len, max_keep_len))
 
 
-def _layer_ptrs(xs, name):
-    return (ctypes.c_void_p * len(xs))(*[_dev(x, name) for x in xs])
+def _layer_ptrs(xs, name, num_layers, shape, dtype):
+    """Pointers of one tensor a layer, all of one shape and dtype."""
+    if len(xs) != num_layers:
+        raise ValueError(f"need one {name} per layer")
+    ptrs = []
+    for x in xs:
+        if x.shape != shape or x.dtype != dtype:
+            raise ValueError(f"{name} must be {dtype} {list(shape)} in every layer")
+        ptrs.append(_dev(x, name))
+    return ptrs
 
 
 def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block_tables,
@@ -651,38 +663,38 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
     L = len(k_caches)
     if not L or len(v_caches) != L or len(scores) != L:
         raise ValueError("need the same, non-zero number of K pools, V pools and scores")
-    nb, hkv, bs, d = k_caches[0].shape
-    dt = k_caches[0].dtype
-    pool = k_caches[0].shape
-    for c in (*k_caches, *v_caches):
-        if c.shape != pool or c.dtype != dt:
-            raise ValueError("all pools must have one shape and dtype")
-    for t, n in ((block_tables, "block_tables"), (context_lens, "context_lens"),
-                 (keep_lens, "keep_lens")):
-        if t.dtype != torch.int32:
-            raise TypeError(f"{n} must be int32")
+    pool, dt = k_caches[0].shape, k_caches[0].dtype
+    nb, hkv, bs, d = pool
+    i32 = torch.int32
+    if block_tables.dtype != i32 or context_lens.dtype != i32 or keep_lens.dtype != i32:
+        raise TypeError("block_tables, context_lens and keep_lens must be int32")
     S = context_lens.shape[0]
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,) or \
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,) or \
             keep_lens.shape != (S,):
         raise ValueError("block_tables must be [S][max_blocks], context_lens and keep_lens [S]")
-    if dst_block_tables is not None and (
-            dst_block_tables.dtype != torch.int32 or dst_block_tables.dim() != 2 or
-            dst_block_tables.shape[0] != S):
+    dst = (S, 0) if dst_block_tables is None else dst_block_tables.shape
+    if len(dst) != 2 or dst[0] != S or (
+            dst_block_tables is not None and dst_block_tables.dtype != i32):
         raise ValueError("dst_block_tables must be int32 [S][blocks]")
 
-    def rows(xs, name, dtype):  # one shape and type for all layers
-        if len(xs) != L:
-            raise ValueError(f"need one {name} per layer")
-        first = xs[0].shape
-        ok = len(first) == 3 and first[0] == S and first[1] == hkv
-        for x in xs:
-            if not ok or x.dtype != dtype or x.shape != first:
-                raise ValueError(f"{name} must be {dtype} [S][Hkv][positions] in every layer")
-        return _layer_ptrs(xs, name), first[2]
+    # the layers' pointers, one array after the other
+    ptrs = _layer_ptrs(k_caches, "k_caches", L, pool, dt)
+    ptrs += _layer_ptrs(v_caches, "v_caches", L, pool, dt)
+
+    def rows(xs, name, dtype):  # [S][Hkv][positions]: where its array is, positions
+        first = xs[0].shape if len(xs) else ()
+        if len(first) != 3 or first[0] != S or first[1] != hkv:
+            raise ValueError(f"{name} must be {dtype} [S][Hkv][positions] in every layer")
+        ptrs.extend(_layer_ptrs(xs, name, L, first, dtype))
+        return len(ptrs) - L, first[2]
 
     sc = rows(scores, "scores", torch.float32)
-    out = (None, 0) if scores_out is None else rows(scores_out, "scores_out", torch.float32)
-    kp = (None, 0) if kept is None else rows(kept, "kept", torch.int32)
+    out = None if scores_out is None else rows(scores_out, "scores_out", torch.float32)
+    kp = None if kept is None else rows(kept, "kept", i32)
+    arrays = array.array("Q", ptrs)
+    base = arrays.buffer_info()[0]
+    none = (None, 0)
     if new_lens is None:
         new_lens = torch.empty(S, dtype=torch.int32, device=context_lens.device)
     elif new_lens.dtype != torch.int32 or new_lens.shape != (S,):
@@ -691,10 +703,11 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
         nbytes = evict_workspace_size(L, S, hkv, int(max_context_len), int(max_keep_len))
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=context_lens.device)
     st = load_library().pa_evict_tokens(
-        _layer_ptrs(k_caches, "k_caches"), _layer_ptrs(v_caches, "v_caches"), L, *sc, *out, *kp,
-        _dev(block_tables, "block_tables"), block_tables.shape[1],
-        _opt_ptr(dst_block_tables, "dst_block_tables"),
-        0 if dst_block_tables is None else dst_block_tables.shape[1],
+        base, base + 8 * L, L, base + 8 * sc[0], sc[1],
+        *(none if out is None else (base + 8 * out[0], out[1])),
+        *(none if kp is None else (base + 8 * kp[0], kp[1])),
+        _dev(block_tables, "block_tables"), tables[1],
+        _opt_ptr(dst_block_tables, "dst_block_tables"), dst[1],
         _dev(context_lens, "context_lens"), _dev(keep_lens, "keep_lens"),
         _dev(new_lens, "new_lens"), int(max_context_len), int(max_keep_len), int(num_sink),
         int(num_recent), S, nb, bs, hkv, d, _dtype_code(dt), _dev(workspace, "workspace"),
