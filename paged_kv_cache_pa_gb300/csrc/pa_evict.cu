@@ -205,6 +205,7 @@ __global__ void __launch_bounds__(THREADS)
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0);
             const int bins = pass == 2 ? 1024 : 2048;
+#pragma unroll 2
             for (int j = tid; 4 * j < i1; j += THREADS) {
                 const uint4 k4 = s_key4[j];
                 const uint32_t key[4] = {k4.x, k4.y, k4.z, k4.w};
@@ -245,10 +246,11 @@ __global__ void __launch_bounds__(THREADS)
                 }
                 if (lane == 31) s_warp[wid] = incl;
                 __syncthreads();
-                unsigned before = incl - sum;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) before += w < wid ? s_warp[w] : 0u;
-                if (before < left && before + sum >= left) {  // one thread
+                const unsigned before =
+                    incl - sum + __reduce_add_sync(0xffffffffu, lane < wid ? s_warp[lane] : 0u);
+                const unsigned hit =
+                    __ballot_sync(0xffffffffu, before < left && before + sum >= left);
+                if (hit) {  // one warp, and in it one lane
                     int k = 0;
                     unsigned b4 = before;
 #pragma unroll
@@ -257,15 +259,18 @@ __global__ void __launch_bounds__(THREADS)
                             b4 += c[e];
                             k = e + 1;
                         }
-                    const unsigned digit = (unsigned)(bins - 1 - (BPT * tid + k));
-                    if constexpr (CS > 1) {
-                        for (uint32_t r = 0; r < CS; ++r) {
-                            st_cluster(&s_digit, r, digit);
-                            st_cluster(&s_need, r, left - b4);
+                    const int src = __ffs((int)hit) - 1;
+                    const unsigned digit =
+                        __shfl_sync(0xffffffffu, (unsigned)(bins - 1 - (BPT * tid + k)), src);
+                    const unsigned rest = __shfl_sync(0xffffffffu, left - b4, src);
+                    if (lane < CS) {  // a lane for each CTA
+                        if constexpr (CS > 1) {
+                            st_cluster(&s_digit, (uint32_t)lane, digit);
+                            st_cluster(&s_need, (uint32_t)lane, rest);
+                        } else {
+                            s_digit = digit;
+                            s_need = rest;
                         }
-                    } else {
-                        s_digit = digit;
-                        s_need = left - b4;
                     }
                 }
             }
@@ -315,33 +320,22 @@ __global__ void __launch_bounds__(THREADS)
         return (unsigned)__popc(c & 0xffffu) | ((unsigned)__popc(c >> 16) << 16);
     };
     unsigned mine = 0u;
+#pragma unroll 2
     for (int i = w0 + 4 * lane; i < w1; i += 128) mine += counts(classify(i));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+    mine = __reduce_add_sync(0xffffffffu, mine);  // (both halves stay below 2^16)
     if (lane == 0) s_warp[wid] = mine;
     __syncthreads();
     // the parts before this one: in the CTA, then in the cluster
     unsigned prior = lane < kWarps ? s_warp[lane] : 0u;
-    unsigned total = prior;
-    if (lane >= wid) prior = 0u;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        prior += __shfl_xor_sync(0xffffffffu, prior, o);
-        total += __shfl_xor_sync(0xffffffffu, total, o);
-    }
+    const unsigned total = __reduce_add_sync(0xffffffffu, prior);
+    prior = __reduce_add_sync(0xffffffffu, lane < wid ? prior : 0u);
     unsigned b_gt = prior & 0xffffu, b_eq = prior >> 16;
     if constexpr (CS > 1) {
         if (tid == 0) s_total = total;
         cluster_sync();
         unsigned other = lane < rank ? ld_cluster(&s_total, (uint32_t)lane) : 0u;
-        unsigned o_gt = other & 0xffffu, o_eq = other >> 16;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-            o_gt += __shfl_xor_sync(0xffffffffu, o_gt, o);
-            o_eq += __shfl_xor_sync(0xffffffffu, o_eq, o);
-        }
-        b_gt += o_gt;
-        b_eq += o_eq;
+        b_gt += __reduce_add_sync(0xffffffffu, other & 0xffffu);
+        b_eq += __reduce_add_sync(0xffffffffu, other >> 16);
     }
     // A step's kept tokens have consecutive places: gathered in shared memory,
     // then written out with neighbouring lanes on neighbouring places.
