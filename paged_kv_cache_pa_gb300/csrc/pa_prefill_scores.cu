@@ -379,20 +379,21 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items<S
     bool ok = true;
     SItem it, nx;
     int e = -1, en = -1;
-    if (items.has(0)) {
-        nx = items.get(0);
+    auto ahead = [&](unsigned r) {
+        if (!items.has(r)) return;
+        nx = items.get(r);
         en = entry(nx);
-    }
+    };
+    ahead(0);
     for (unsigned r = 0; ok && items.has(r); ++r) {
         it = nx;
         e = en;
-        if (items.has(r + 1)) {  // its table entries arrive meanwhile
-            nx = items.get(r + 1);
-            en = entry(nx);
-        }
         if (!it.ok && it.k0 == 0 && it.hk == 0 && lane == 0 && P.err)
             atomicOr(P.err, PA_ERRBIT_CONTEXT_LEN);
-        if (!it.run) continue;
+        if (!it.run) {
+            ahead(r + 1);
+            continue;
+        }
         const int tok = it.k0 + (lane << lg_tbr);
         const int row = lane << lg_tbr;  // of the item's 256
         const bool use = lane < units && tok < it.L;
@@ -420,6 +421,7 @@ __device__ __forceinline__ void run_score_producer(const ScoreParams &P, Items<S
             ++kn;
         };
         load_k(0);
+        ahead(r + 1);  // its table entries arrive during the second tile's copies
         if (ok && first_tile<SPLIT>(P, it, 1) < it.tt1) load_k(1);
     }
     if (lane == 0) {
