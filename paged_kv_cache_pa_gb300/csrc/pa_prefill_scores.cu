@@ -691,11 +691,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
 // One product of this thread's key: the weights of `cols` columns of tensor
 // memory (a multiple of CH) in four chains of pairs.  CH columns at a time are
 // loaded into registers, and the buffer is given back through `bar` with the
-// last load, so the next product runs while their weights are worked out.  (32
-// columns measured 135 us on 2 prompts of 4096 tokens with 32 heads on 8; 64,
-// with more registers, 139; 16 in two sets of registers 143.)  ALL: every
-// column is visible; else those in [lo, hi) whose row has a weight at all (a
-// row without has nl = -inf).  nl: the rows' negated lse.
+// last load, so the next product runs while their weights are worked out.  (2
+// prompts of 4096 tokens with 32 heads on 8, 64 windows of 16 queries on 2048
+// tokens: 120 and 52 us with 32 columns, 130 and 52 with 16; with the last 48
+// at once, so that the buffer is free earlier, 121 and 97: more code.)  ALL:
+// every column is visible; else those in [lo, hi) whose row has a weight at all
+// (a row without has nl = -inf).  nl: the rows' negated lse.
 template <bool ALL, int CH>
 __device__ __forceinline__ float sum_product(uint32_t taddr, int cols, const float *nl, int lo,
                                              int hi, uint64_t sc2, uint64_t *bar) {
