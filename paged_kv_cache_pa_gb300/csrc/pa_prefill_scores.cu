@@ -137,7 +137,7 @@ struct STable {
 
 // Shared memory: lse [slot][128], its flags [slot], the sums handed over
 // [tile][128], barriers, the items' table; then, 1024-byte aligned, the K ring
-// of rk tiles [slice][128 keys][64] and the query ring of rq tiles
+// of rk tiles [16][slice][8 keys][64] and the query ring of rq tiles
 // [slice][rows][64].
 struct SLayout {
     static constexpr size_t dead_off = kMaxRing * kMaxCols * 4;
