@@ -13,7 +13,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import paged_kv_cache_pa_gb300 as pa
-from cachelib import logits64, weights64
+from cachelib import Cache, logits64, weights64
 from paged_kv_cache_pa_gb300.manager import BlockManager
 
 pytestmark = pytest.mark.gpu
@@ -395,3 +395,52 @@ def test_the_first_calls_of_a_process_may_be_captured():
     r = subprocess.run([sys.executable, "-c", FIRST_CALLS.format(root=os.path.dirname(tests), tests=tests)],
                        capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip().endswith("the same"), r.stdout[-2000:] + r.stderr[-4000:]
+
+
+def test_two_streams_at_once():
+    """Prompts scored and evicted in place on two streams at the same time, each
+    with its own workspaces, give what they give one after the other."""
+    jobs = []
+    for seed, lens, dtype in ((1, [1500, 700], torch.bfloat16), (2, [900, 333, 2000], torch.float16)):
+        c = Cache(lens, 2, 128, dtype, 16, seed=seed)
+        g = torch.Generator(device=DEV).manual_seed(seed)
+        q = torch.randn(sum(lens), 8, 128, generator=g, device=DEV).to(dtype)
+        qsl = torch.tensor([0] + list(np.cumsum(lens)), dtype=torch.int32, device=DEV)
+        keep = torch.tensor([n // 2 for n in lens], dtype=torch.int32, device=DEV)
+        jobs.append((c, q, qsl, keep))
+
+    def bufs(job):
+        c, q = job[:2]
+        S, L = len(c.lens_host), c.max_len
+        return (c.k[0].clone(), c.v[0].clone(), torch.empty_like(q), torch.empty(q.shape[:2], device=DEV),
+                torch.zeros(S, 2, L, device=DEV), torch.empty(S, dtype=torch.int32, device=DEV),
+                [torch.empty(64 << 20, dtype=torch.uint8, device=DEV) for _ in range(3)])
+
+    def run(job, b):
+        c, q, qsl, keep = job
+        k, v, out, lse, sc, new, ws = b
+        L = c.max_len
+        pa.prefill_attention(q, k, v, c.tables, qsl, c.lens, L, L, 0.09, out=out, workspace=ws[0], lse=lse)
+        pa.prefill_scores(q, lse, k, c.tables, qsl, c.lens, L, L, 0.09, sc, workspace=ws[1])
+        pa.evict_tokens([k], [v], [sc], c.tables, c.lens, keep, L, L // 2, num_sink=3, num_recent=10, new_lens=new,
+                        workspace=ws[2])
+
+    want = []
+    for job in jobs:
+        b = bufs(job)
+        run(job, b)
+        torch.cuda.synchronize()
+        want.append(b)
+    streams = [torch.cuda.Stream() for _ in jobs]
+    rounds = [[bufs(job) for job in jobs] for _ in range(6)]
+    torch.cuda.synchronize()
+    for r in rounds:
+        for s, job, b in zip(streams, jobs, r):
+            with torch.cuda.stream(s):
+                run(job, b)
+    torch.cuda.synchronize()
+    for r in rounds:
+        for w, b in zip(want, r):
+            for x, y in zip(w[:6], b[:6]):
+                assert torch.equal(x.view(torch.int16) if x.dtype in (torch.bfloat16, torch.float16) else x,
+                                   y.view(torch.int16) if y.dtype in (torch.bfloat16, torch.float16) else y)
