@@ -419,28 +419,30 @@ def decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
     here when not given.  Returns ``out``."""
     torch = _torch()
     S, H, D = query.shape
-    nb, hkv, bs, d2 = k_cache.shape
-    if d2 != D or v_cache.shape != k_cache.shape:
+    pool, dt = k_cache.shape, query.dtype
+    nb, hkv, bs, d2 = pool
+    if d2 != D or v_cache.shape != pool:
         raise ValueError("pool shape mismatch")
-    if k_cache.dtype != query.dtype or v_cache.dtype != query.dtype:
+    if k_cache.dtype != dt or v_cache.dtype != dt:
         raise ValueError("pools must match the query dtype")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise TypeError("block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [S][max_blocks], context_lens [S]")
     sc, stride = _score_rows(scores, (S, hkv))
     if out is None:
         out = torch.empty(S, H, D, dtype=out_dtype or torch.float32, device=query.device)
-    elif out.shape != query.shape:
+    elif out.shape != (S, H, D):
         raise ValueError("out must match the query")
     if workspace is None:
         nbytes = decode_scored_workspace_size(S, H, hkv, D, int(max_context_len))
         workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=query.device)
     st = load_library().pa_decode_attention_scored(
         _dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"), _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"), block_tables.shape[1],
+        _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"), tables[1],
         _dev(context_lens, "context_lens"), int(max_context_len), S, H, hkv, D, nb, bs,
-        float(scale), _dtype_code(query.dtype), sc, stride, _dev(workspace, "workspace"),
+        float(scale), _dtype_code(dt), sc, stride, _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
         _stream_ptr(stream, query.device))
     _check(st, "pa_decode_attention_scored")
