@@ -471,6 +471,17 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
         ok = __all_sync(0xffffffffu, mbar_wait(bar, phase, abort_flag));
         return ok;
     };
+    // Both issuers pass through every K tile and every query tile in order, and
+    // give back at once what is the other's alone: a wait by parity must never
+    // be a whole ring ahead or behind.  (Copies land in any order, so that an
+    // issuer's own tile is there says nothing about the one before it.)
+    auto pass_k = [&]() {  // the other issuer's key tile
+        if (!wait(&B.k_full[kr.slot], kr.phase)) return false;
+        if (elect_one()) mbar_arrive(&B.k_free[kr.slot]);
+        __syncwarp();
+        kr.next(P.rk);
+        return true;
+    };
     unsigned r = 0;
     auto next_item = [&]() {  // the next item with work, from round r on; not run: none left
         SItem it;
@@ -485,15 +496,9 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
     while (ok && nx.run) {
         const SItem it = nx;
         const bool two = first_tile<SPLIT>(P, it, 1) < it.tt1;
-        Ring ks = kr;  // this key tile's slot
-        kr.next(P.rk);
-        if (t == 1) ks = kr;
-        if (two) kr.next(P.rk);
+        if (t == 1 && !pass_k()) break;
         const int first = first_tile<SPLIT>(P, it, t);
-        // Both issuers pass through every query tile (a wait by parity must
-        // never be a whole ring ahead or behind), and give back their share of
-        // those that are the other key tile's alone.
-        int n = (first - it.tt0) * P.head_groups;
+        int n = (first - it.tt0) * P.head_groups;  // query tiles without a product here
         for (; n > 0; --n) {
             if (!wait(&B.q_full[qr.slot], qr.phase) || !wait(&B.l_full[qr.slot], qr.phase)) break;
             if (elect_one()) {
@@ -508,8 +513,8 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
             nx = next_item();
             continue;
         }
-        if (!wait(&B.k_full[ks.slot], ks.phase)) break;
-        const uint32_t dk = uniform((uint32_t)dk0 + (uint32_t)ks.slot * (ktile / 16u));
+        if (!wait(&B.k_full[kr.slot], kr.phase)) break;
+        const uint32_t dk = uniform((uint32_t)dk0 + (uint32_t)kr.slot * (ktile / 16u));
         for (; n > 0; --n) {
             if (!wait(&B.q_full[qr.slot], qr.phase)) break;
             if (!wait(&B.s_free[2 * t + sr.slot], sr.phase ^ 1u)) break;
@@ -529,13 +534,16 @@ __device__ __forceinline__ void run_score_mma(const ScoreParams &P, Items<SPLIT>
                              idesc, kk > 0 ? 1u : 0u);
                 umma_commit(&B.s_full[2 * t + sr.slot]);
                 umma_commit(&B.q_free[qr.slot]);
-                if (n == 1) umma_commit(&B.k_free[ks.slot]);
+                if (n == 1) umma_commit(&B.k_free[kr.slot]);
             }
             __syncwarp();
             if (n == 1) nx = next_item();  // while the products run
             sr.next(2);
             qr.next(P.rq);
         }
+        if (!ok) break;
+        kr.next(P.rk);
+        if (t == 0 && two && !pass_k()) break;
     }
     if (!ok) {
         *abort_flag = 1;
@@ -954,9 +962,10 @@ __global__ void __launch_bounds__(kThreadsS, 1)
         prefetch_tmap(&P.tmap_k);
         for (int b = 0; b < L::kBars; ++b) mbar_init(&bars[b], 1);
         for (int b = 0; b < 4; ++b) mbar_init(&B.s_free[b], kKeys);
-        // a query slot is given back for each key tile: the query rows by the
-        // product's completion, the lse by the four warps of the group
+        // a slot is given back by both issuers (or by the completion of their
+        // products), the lse by the four warps of each key tile's group
         for (int b = 0; b < kMaxRing; ++b) {
+            mbar_init(&B.k_free[b], 2);
             mbar_init(&B.q_free[b], 2);
             mbar_init(&B.l_free[b], 8);
         }

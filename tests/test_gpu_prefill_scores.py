@@ -290,3 +290,35 @@ def test_many_items_for_each_block_of_threads(S):
     per_row = scores.sum((1, 2), dtype=torch.float64).cpu()
     want = torch.tensor(new, dtype=torch.float64) * 64  # every row's weights sum to one
     assert float((per_row - want).abs().max()) < 1e-3
+
+
+def _mixed():
+    lens = [2500] + [40 + 97 * (i % 11) for i in range(40)]
+    return [500] + [min(n, 1 + 13 * (i % 9)) for i, n in enumerate(lens[1:])], lens
+
+
+@pytest.mark.parametrize("B", [8, 16, 128])
+@pytest.mark.parametrize("H,Hkv,D,new,lens", [
+    (32, 8, 128, [17] * 8, [1500 + 211 * i for i in range(8)]), (32, 8, 128, [32] * 8, [3000 + 130 * i for i in range(8)]),
+    (32, 8, 128, [64] * 8, [2900 - 129 * i for i in range(8)]), (32, 8, 128, [96] * 6, [2900 - 129 * i for i in range(6)]),
+    (16, 2, 128, [16] * 24, [900 + 257 * i for i in range(24)]), (8, 8, 128, [128] * 8, [2000 + 129 * i for i in range(8)]),
+    (32, 8, 64, [32] * 8, [3000 + 130 * i for i in range(8)]), (12, 2, 128, [32] * 16, [3000 + 300 * i for i in range(16)]),
+    (32, 8, 128, *_mixed()), (12, 2, 64, *_mixed())])
+def test_many_items_of_few_query_tiles(H, Hkv, D, new, lens, B):
+    """Several items a CTA with one to a few query tiles each: the two key tiles of an item,
+    and the items after it, share rings of a few slots, whose copies land in any order (part
+    of the keys in L2, part not)."""
+    c = Cache(lens, Hkv, D, torch.bfloat16, B, seed=B + H)
+    q, qsl, starts = _batch(c, new, H, D)
+    _, lse = _attend(c, q, qsl, new, D ** -0.5)
+    _check_scores(c, q, starts, qsl, new, lse, D ** -0.5)
+    want, flush = None, torch.empty(1 << 28, dtype=torch.uint8, device=DEV)
+    for i in range(12):
+        if i % 3 == 0:
+            flush.fill_(i)
+        if i % 3 == 1:
+            torch.nan_to_num(c.k[0][::2]).sum()  # every other block into L2
+        got = pa.prefill_scores(q, lse, c.k[0], c.tables, qsl, c.lens, max(new), c.max_len, D ** -0.5,
+                                torch.zeros(len(lens), Hkv, c.max_len, device=DEV))
+        want = got if want is None else want
+        assert torch.equal(got, want)
