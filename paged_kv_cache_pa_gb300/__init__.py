@@ -30,6 +30,12 @@ Pools are [num_blocks][num_kv_heads][block_size][head_dim]; the block size
 is read from their third dimension: 16 goes to the plain entry points, other
 supported sizes (powers of two from 8 to 256) to the ``*_ex`` ones.
 
+A call runs on ``stream`` (default: the current stream).  Tensors that it makes
+belong to that stream, as if made under ``torch.cuda.stream(stream)``: before
+another stream uses one that the call returns, it has to wait for the call, as
+for any tensor.  Tensors that the caller passes are the caller's to keep alive
+and to order.
+
 Build the library with ``python -m paged_kv_cache_pa_gb300.build``.
 """
 from __future__ import annotations
@@ -187,6 +193,27 @@ def _stream_ptr(stream, device) -> int:
     return int(stream.cuda_stream)
 
 
+def _empty(stream, shape, dtype, device, returned=False):
+    """A new tensor for a call that runs on ``stream``.  Its memory comes from
+    that stream's share of the allocator, so that neither what other streams
+    still do with memory they have given back, nor what they are given once
+    this tensor is dropped, meets the call's kernels.  returned: the caller
+    gets it, and may drop it while the current stream still uses it."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _workspace(stream, nbytes, device):
+    torch = _torch()
+    return _empty(stream, max(nbytes, 256), torch.uint8, device)
+
+
 def _opt_ptr(t, name):
     return None if t is None else _dev(t, name)
 
@@ -295,7 +322,7 @@ def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_
             (positions.shape[0] if positions.dim() == 2 else 1) < rotary.num_axes:
         raise ValueError("positions must be [axes][T] with an axis for each the frequencies name")
     if query_out is None:
-        query_out = torch.empty(T, H, D, dtype=dt, device=query.device)
+        query_out = _empty(stream, (T, H, D), dt, query.device, returned=True)
     elif query_out is not query and (query_out.shape != (T, H, D) or query_out.dtype != dt):
         raise ValueError("query_out must match the query")
     st = load_library().pa_rotary_cache_write(
@@ -345,10 +372,10 @@ def decode_attention(query, k_cache, v_cache, block_tables, context_lens,
     if block_tables.dim() != 2 or block_tables.shape[0] != S or context_lens.shape != (S,):
         raise ValueError("block_tables must be [S][max_blocks], context_lens [S]")
     if out is None:
-        out = torch.empty(S, H, D, dtype=out_dtype or torch.float32, device=query.device)
+        out = _empty(stream, (S, H, D), out_dtype or torch.float32, query.device, returned=True)
     if workspace is None:
         nbytes = decode_workspace_size(S, H, hkv, D, int(max_context_len))
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=query.device)
+        workspace = _workspace(stream, nbytes, query.device)
     head = (_dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"),
             _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
             _dev(block_tables, "block_tables"), block_tables.shape[1],
@@ -378,10 +405,10 @@ def decode_attention_contiguous(query, k_cache, v_cache, context_lens, max_conte
     if context_lens.dtype != torch.int32 or context_lens.shape != (S,):
         raise TypeError("context_lens must be int32 [S]")
     if out is None:
-        out = torch.empty(S, H, D, dtype=out_dtype or torch.float32, device=query.device)
+        out = _empty(stream, (S, H, D), out_dtype or torch.float32, query.device, returned=True)
     if workspace is None:
         nbytes = decode_workspace_size(S, H, hkv, D, int(max_context_len))
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=query.device)
+        workspace = _workspace(stream, nbytes, query.device)
     st = load_library().pa_decode_attention_contiguous(
         _dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"), _dev(k_cache, "k_cache"),
         _dev(v_cache, "v_cache"), rows, _dev(context_lens, "context_lens"), int(max_context_len),
@@ -432,12 +459,12 @@ def decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
         raise ValueError("block_tables must be [S][max_blocks], context_lens [S]")
     sc, stride = _score_rows(scores, (S, hkv))
     if out is None:
-        out = torch.empty(S, H, D, dtype=out_dtype or torch.float32, device=query.device)
+        out = _empty(stream, (S, H, D), out_dtype or torch.float32, query.device, returned=True)
     elif out.shape != (S, H, D):
         raise ValueError("out must match the query")
     if workspace is None:
         nbytes = decode_scored_workspace_size(S, H, hkv, D, int(max_context_len))
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=query.device)
+        workspace = _workspace(stream, nbytes, query.device)
     st = load_library().pa_decode_attention_scored(
         _dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"), _dev(k_cache, "k_cache"),
         _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"), tables[1],
@@ -550,10 +577,10 @@ def prefill_attention(query, k_cache, v_cache, block_tables, query_start_loc, co
             block_tables.shape[0] != S:
         raise ValueError("query_start_loc must be [S+1], block_tables [S][max_blocks]")
     if out is None:
-        out = torch.empty(T, H, D, dtype=out_dtype or torch.float32, device=query.device)
+        out = _empty(stream, (T, H, D), out_dtype or torch.float32, query.device, returned=True)
     if workspace is None:
         nbytes = prefill_workspace_size(S, H, hkv, D, int(max_query_len))
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=query.device)
+        workspace = _workspace(stream, nbytes, query.device)
     head = (_dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"),
             _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
             _dev(block_tables, "block_tables"), block_tables.shape[1],
@@ -612,7 +639,7 @@ def prefill_scores(query, lse, k_cache, block_tables, query_start_loc, context_l
     if workspace is None:
         nbytes = prefill_scores_workspace_size(S, H, hkv, D, int(max_query_len),
                                                int(max_context_len))
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=query.device)
+        workspace = _workspace(stream, nbytes, query.device)
     st = load_library().pa_prefill_scores(
         _dev(query, "query"), _lse_ptr(lse, T, H), _dev(k_cache, "k_cache"),
         _dev(block_tables, "block_tables"), block_tables.shape[1],
@@ -698,12 +725,12 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
     base = arrays.buffer_info()[0]
     none = (None, 0)
     if new_lens is None:
-        new_lens = torch.empty(S, dtype=torch.int32, device=context_lens.device)
+        new_lens = _empty(stream, S, torch.int32, context_lens.device, returned=True)
     elif new_lens.dtype != torch.int32 or new_lens.shape != (S,):
         raise ValueError("new_lens must be int32 [S]")
     if workspace is None:
         nbytes = evict_workspace_size(L, S, hkv, int(max_context_len), int(max_keep_len))
-        workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=context_lens.device)
+        workspace = _workspace(stream, nbytes, context_lens.device)
     st = load_library().pa_evict_tokens(
         base, base + 8 * L, L, base + 8 * sc[0], sc[1],
         *(none if out is None else (base + 8 * out[0], out[1])),

@@ -1,0 +1,127 @@
+"""What the Python binding hands to the library, seen through stand-ins for
+torch's CUDA part and for the library (no GPU needed)."""
+import contextlib
+import types
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import paged_kv_cache_pa_gb300 as pa
+
+
+class Tensor:
+    """A CUDA tensor as far as the binding looks; `home`: the stream whose memory it is."""
+
+    def __init__(self, shape, dtype, home="caller", device=0):
+        self.shape = torch.Size((shape,) if isinstance(shape, int) else shape)
+        self.dtype, self.home = dtype, home
+        self.device = types.SimpleNamespace(type="cuda", index=device)
+        self.is_cuda, self.used_by = True, []
+
+    def is_contiguous(self):
+        return True
+
+    def dim(self):
+        return len(self.shape)
+
+    def data_ptr(self):
+        return id(self)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return torch.empty((), dtype=self.dtype).element_size()
+
+    def record_stream(self, stream):
+        self.used_by.append(stream)
+
+
+class Torch:
+    """torch, its tensors and streams stood in for."""
+
+    def __init__(self, device=0):
+        self.stream, self.made, self.device = "current", [], device
+        outer = self
+
+        class Cuda:
+            @staticmethod
+            @contextlib.contextmanager
+            def stream(s):
+                before, outer.stream = outer.stream, s
+                yield
+                outer.stream = before
+
+            @staticmethod
+            def current_stream(device=None):
+                return outer.stream
+
+        self.cuda = Cuda
+        self._C = types.SimpleNamespace(_cuda_getCurrentRawStream=lambda i: 1000 + i,
+                                        _cuda_getDevice=lambda: outer.device)
+
+    def __getattr__(self, name):
+        return getattr(torch, name)
+
+    def empty(self, *shape, dtype=None, device=None):
+        shape = shape[0] if len(shape) == 1 else shape
+        self.made.append(Tensor(shape, dtype, self.stream))
+        return self.made[-1]
+
+
+class Library:
+    """Accepts every call."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.calls.append((name, args))
+            return 4096 if name.endswith("_size") else 0
+        return call
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    t, lib = Torch(), Library()
+    monkeypatch.setattr(pa, "_torch_module", t)
+    monkeypatch.setattr(pa, "_lib", lib)
+    monkeypatch.setattr(pa, "_DTYPE_CODES", {})
+    return types.SimpleNamespace(torch=t, lib=lib)
+
+
+def _calls():
+    h, i32, i64, f32 = torch.float16, torch.int32, torch.int64, torch.float32
+    q, new = Tensor((2, 8, 64), h), Tensor((2, 4, 64), h)
+    pool = Tensor((9, 4, 16, 64), h)
+    tab, lens, qsl = Tensor((2, 4), i32), Tensor(2, i32), Tensor(3, i32)
+    sc, lse = Tensor((2, 4, 64), f32), Tensor((2, 8), f32)
+    rot = types.SimpleNamespace(num_axes=1, _ptr=1, _struct=pa._RotaryStruct())
+    return {
+        "rotary": lambda **kw: pa.rotary_cache_write(q, new, new, Tensor(2, i64), rot, pool, pool, Tensor(2, i64), **kw),
+        "decode": lambda **kw: pa.decode_attention(q, pool, pool, tab, lens, 64, 0.1, **kw),
+        "contiguous": lambda **kw: pa.decode_attention_contiguous(q, Tensor((2, 4, 64, 64), h), Tensor((2, 4, 64, 64), h),
+                                                                  lens, 64, 0.1, **kw),
+        "scored": lambda **kw: pa.decode_attention_scored(q, pool, pool, tab, lens, 64, 0.1, sc, **kw),
+        "prefill": lambda **kw: pa.prefill_attention(q, pool, pool, tab, qsl, lens, 2, 64, 0.1, **kw),
+        "prompt scores": lambda **kw: pa.prefill_scores(q, lse, pool, tab, qsl, lens, 2, 64, 0.1, sc, **kw),
+        "evict": lambda **kw: pa.evict_tokens([pool], [pool], [sc], tab, lens, lens, 64, 32, **kw),
+    }
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_what_a_call_allocates_belongs_to_its_stream(fake, name):
+    """Memory of the current stream may still be in use there, and goes back to it when the
+    call returns: the call's kernels, on another stream, must not get it."""
+    side = types.SimpleNamespace(cuda_stream=7)
+    got = _calls()[name](stream=side)
+    assert all(t.home is side for t in fake.torch.made)
+    assert fake.lib.calls[-1][1][-1] == 7
+    if got in fake.torch.made:  # the current stream will use it
+        assert got.used_by == ["current"]
+    del fake.torch.made[:]
+    _calls()[name]()
+    assert all(t.home == "current" for t in fake.torch.made)
+    assert fake.lib.calls[-1][1][-1] == 1000
