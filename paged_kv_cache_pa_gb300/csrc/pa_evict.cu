@@ -436,7 +436,7 @@ __global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 5 : 4)
         __syncthreads();
         chunk = s_chunk;
     }
-    if (chunk >= chunks) return;
+    if ((unsigned)chunk >= (unsigned)chunks) return;
     unsigned *flags = P.flags + (size_t)unit * P.max_chunks;
     const int32_t *idx = P.index + (size_t)unit * P.max_keep_len;
     const int32_t *src = P.block_tables + (size_t)s * P.max_blocks_per_seq;
@@ -459,7 +459,10 @@ __global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 5 : 4)
         to[u] = -1;
         if (i >= q.n) continue;
         const int t = all ? i : idx[i];
-        const int b0 = src[t >> P.block_shift], b1 = dst[i >> P.block_shift];
+        // (list and counter come through the caller's workspace: checked before
+        // they become an address)
+        const bool in = t >= 0 && t < q.L;
+        const int b0 = in ? src[t >> P.block_shift] : -1, b1 = dst[i >> P.block_shift];
         const bool ok = b0 >= 0 && b0 < P.num_blocks && b1 >= 0 && b1 < P.num_blocks;
         oob |= !ok;
         if (!ok || (IN_PLACE && t == i)) continue;  // a row that stays needs no move
