@@ -863,7 +863,7 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
             ok = ok && mbar_wait(&B.s_full[2 * t + b], (uint32_t)taken & 1u, abort_flag);
             if (late) ok = ok && mbar_wait(&B.l_full[slot], phase, abort_flag);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) {  // at once: no sum that lacks this product is written
+            if (!ok) {  // at once: no sum that lacks this product is written or sent
                 *abort_flag = 1;
                 break;
             }
@@ -889,6 +889,9 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
             bar_sync(bar_full, 256);
             acc += part[rk];
             bar_arrive(bar_free, 256);
+            // (group (t, 1) sets the flag before it hands over a sum that lacks a
+            // product: such a sum is neither written nor sent on)
+            ok = __all_sync(0xffffffffu, ok && !*abort_flag);
             if (SPLIT && part_id) {  // to the cluster's first CTA
                 if (shared) ok = ok && wait_cluster(&B.c_free[t], (shared - 1u) & 1u, abort_flag);
                 ok = __all_sync(0xffffffffu, ok);
@@ -909,7 +912,7 @@ __device__ __forceinline__ void run_score_sums(const ScoreParams &P, Items<SPLIT
                 }
                 ++shared;
             }
-            if (part_id == 0u && ok && !*abort_flag && key < it.L && blk_now >= 0 &&
+            if (part_id == 0u && ok && key < it.L && blk_now >= 0 &&
                 blk_now < P.num_blocks)
                 P.scores[((long long)it.s * P.num_kv_heads + it.hk) * P.score_stride + key] =
                     old_now + acc;
