@@ -359,7 +359,10 @@ size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int num_kv_h
  * score_stride  >= max_context_len
  * workspace     >= pa_decode_scored_workspace_size(...) bytes, 256-byte aligned
  * Every other argument, the checks and the error bits are those of
- * pa_decode_attention_ex.  Sequences that share a prefix are read one by one
+ * pa_decode_attention_ex.  While PA_ERRBIT_TIMEOUT is set in *dev_error_word,
+ * by this call or before it, nothing is added to the scores (out is then not
+ * to be used); without an error word, scores are undefined after a wait that
+ * gave up.  Sequences that share a prefix are read one by one
  * here: their weights differ.  Enqueues the kernels of pa_decode_attention and
  * one that turns logits into weights; results do not depend on the order in
  * which work finishes.
@@ -501,7 +504,7 @@ size_t pa_prefill_scores_workspace_size(int num_seqs, int num_heads, int num_kv_
  * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence
  *               whose lengths break the rules (its scores are left as they
  *               were), PA_ERRBIT_BLOCK_OOB (the block's keys are skipped),
- *               PA_ERRBIT_TIMEOUT
+ *               PA_ERRBIT_TIMEOUT (a score has the whole sum added or nothing)
  */
 pa_status_t pa_prefill_scores(const void *query, const float *lse, const void *k_cache,
                               const int32_t *block_tables, int max_blocks_per_seq,

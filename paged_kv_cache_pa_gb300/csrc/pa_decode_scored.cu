@@ -9,6 +9,10 @@
 // A row without weight (no readable block, every logit -inf: L = 0) adds
 // nothing.  One thread owns a token's score, so the sum's order is fixed.
 //
+// Scores add up over calls, so weights made from what an attention kernel that
+// gave up has left in the workspace would stay: once PA_ERRBIT_TIMEOUT is in
+// the error word, nothing is added.
+//
 // A warp takes 256 tokens of one (sequence, KV head): it works out M and 1 / L
 // of each head itself (a lane a piece), so the CTA has no barrier, and its
 // loads of the logits, 16 bytes a lane, are all in flight together.  The
@@ -42,6 +46,8 @@ __device__ __forceinline__ void add_weights(const DecodeParams &P, float *__rest
     const int L = P.context_lens[s], G = P.G;
     if (L <= 0 || L > P.max_context_len || t0 >= L) return;  // empty or invalid: nothing to add
     const size_t row0 = (size_t)s * P.num_heads + (size_t)hk * G;
+    // (used only before the stores: on its way beside everything else)
+    const unsigned status = P.err ? __ldcg(P.err) : 0u;
     const int np = (L + P.part_tokens - 1) / P.part_tokens;
     const int n = min(kWarpTokens, L - t0);
     // every load of the first 32 pieces and of the old scores in flight at once
@@ -111,6 +117,7 @@ __device__ __forceinline__ void add_weights(const DecodeParams &P, float *__rest
             w[i].w = fmaf(ex2(x[i].w - M[g]), inv[g], w[i].w);
         }
     }
+    if (status & PA_ERRBIT_TIMEOUT) return;
 #pragma unroll
     for (int i = 0; i < kSteps; ++i) {
         const int t = i * 128 + 4 * lane;

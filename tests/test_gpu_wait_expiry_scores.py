@@ -57,10 +57,39 @@ def _prompts(pa, D, times, calls, err):
     return count, int((want > 0).sum())
 
 
+def _decode(pa, H, Hkv, S, err):
+    """(scores left, others) of 20 steps, each with the error word zeroed before and set after."""
+    from cachelib import Cache
+    lens = ([700, 1500, 33, 4000, 2] * S)[:S] if S > 2 else [200, 33]
+    c = Cache(lens, Hkv, 128, torch.bfloat16, seed=1)
+    g = torch.Generator(device=DEV).manual_seed(2)
+    q = torch.randn(S, H, 128, generator=g, device=DEV).to(torch.bfloat16)
+    base = torch.rand(S, Hkv, c.max_len, generator=g, device=DEV)
+    live = torch.arange(c.max_len, device=DEV)[None, None] < c.lens[:, None, None]
+    live = live.expand_as(base)
+    left = other = 0
+    for i in range(20):
+        err.zero_()
+        sc = base.clone()
+        # a workspace with something in it that could pass for logits and states
+        ws = torch.full((pa.decode_scored_workspace_size(S, H, Hkv, 128, c.max_len) // 4,), 0.5, device=DEV)
+        pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, c.max_len, 0.09, sc, workspace=ws, error_word=err)
+        torch.cuda.synchronize()
+        if not int(err.item()) & 8:
+            continue  # every wait was short enough this time
+        left += int((sc == base)[live].sum())
+        other += int((sc != base)[live].sum())
+    return left, other
+
+
 def _child(case, lib_path):
     import paged_kv_cache_pa_gb300 as pa
     pa._LIB_PATH = lib_path                 # this process loads only the test copy
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    if case.startswith("decode"):
+        left, other = _decode(pa, *(int(x) for x in case.split("_")[1:]), err)
+        print(json.dumps({"left": left, "other": other}), flush=True)
+        return
     _, D, times = case.split("_")
     (left, whole, other), _ = _prompts(pa, int(D), int(times), 40 if times == "1" else 4, err)
     print(json.dumps({"err": int(err.item()), "left": left, "whole": whole, "other": other}), flush=True)
@@ -85,6 +114,30 @@ def test_prompt_scores_are_left_or_whole(case, variant):
     err = torch.zeros(1, dtype=torch.int32, device=DEV)
     (_, whole, other), tokens = _prompts(pa, int(case.split("_")[1]), int(case.split("_")[2]), 1, err)
     assert int(err.item()) == 0 and other == 0 and whole == tokens
+
+
+@pytest.mark.parametrize("variant", ["shortwait", "midwait"])
+@pytest.mark.parametrize("case", ["decode_4_4_5", "decode_12_2_5", "decode_12_2_2"])
+def test_decode_scores_are_left(case, variant):
+    """(H, Hkv, sequences): both attention kernels, with and without partitions and plan."""
+    res = _run(case, variant)
+    assert res["other"] == 0 and (res["left"] or variant == "midwait"), res
+
+
+def test_scores_are_added_again_once_the_error_word_is_zeroed():
+    import paged_kv_cache_pa_gb300 as pa
+    from cachelib import Cache
+    c = Cache([300, 40], 2, 64, torch.float16, seed=1)
+    q = torch.randn(2, 4, 64, device=DEV).to(torch.float16)
+    sc = torch.zeros(2, 2, 300, device=DEV)
+    err = torch.full((1,), pa.ERRBIT_TIMEOUT, dtype=torch.int32, device=DEV)
+    pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, 300, 0.1, sc, error_word=err)
+    assert not sc.any()
+    for word in (0, pa.ERRBIT_BLOCK_OOB):  # another bit does not hold the scores back
+        err.fill_(word)
+        sc.zero_()
+        pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, 300, 0.1, sc, error_word=err)
+        assert torch.allclose(sc.sum(-1), torch.full((2, 2), 2.0, device=DEV), rtol=1e-4)
 
 
 if __name__ == "__main__":
