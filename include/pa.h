@@ -350,8 +350,9 @@ size_t pa_decode_scored_workspace_size(int num_seqs, int num_heads, int num_kv_h
  * head hk * G + g,
  *     scores[s][hk][t] += sum_{g < G} p_gt .
  * Weights and sums are fp32.  Scores of positions from context_lens[s] on, of
- * an empty or invalid sequence, and of tokens in a skipped block are left as
- * they were.  A new position's score has to be zero before its first call
+ * an empty or invalid sequence, and of tokens in a skipped block (of 8-token
+ * blocks: in a skipped pair of blocks 2 i and 2 i + 1) are left as they were.
+ * A new position's score has to be zero before its first call
  * (pa_evict_tokens leaves it so).
  *
  * scores        device fp32 [num_seqs][num_kv_heads][score_stride]; row s

@@ -179,3 +179,24 @@ def test_nan_stays_with_its_sequence_and_head(H, Hkv):
     pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, 600, 0.125, got)
     assert bool(torch.isnan(got[0, 1, :600]).all())
     assert torch.equal(got[0, 0], clean[0, 0]) and torch.equal(got[1], clean[1])
+
+
+@pytest.mark.parametrize("B", [8, 16, 64])
+@pytest.mark.parametrize("H,Hkv,D", [(2, 2, 64), (12, 2, 64), (6, 2, 256)])
+def test_a_nan_row_leaves_the_skipped_blocks_alone(H, Hkv, D, B):
+    c = Cache([600, 90], Hkv, D, torch.bfloat16, B, seed=11)
+    q = _q(2, H, D, torch.bfloat16)
+    c.k[0][int(c.tables_host[0, 53 // B]), 1, 53 % B] = float("nan")  # token 53 of sequence 0, head 1
+    first, last = (128 // B, 143 // B) if B < 64 else (2, 2)
+    c.tables[0, first] = 10 ** 7
+    c.tables[0, 599 // B] = -1  # the last, short block
+    skipped = torch.zeros(600, dtype=torch.bool, device=DEV)
+    skipped[first * B:(last + 1) * B] = True
+    skipped[599 // B * B // 16 * 16:] = True
+    base = torch.rand(2, Hkv, 603, device=DEV)
+    for sc in (base.clone(), base.clone()[:, :, :600].contiguous()):  # any row stride
+        pa.decode_attention_scored(q, c.k[0], c.v[0], c.tables, c.lens, 600, 0.1, sc)
+        assert torch.equal(sc[:, :, :600][0][:, skipped], base[:, :, :600][0][:, skipped])
+        assert bool(torch.isnan(sc[0, 1, :600][~skipped]).all())
+        assert bool(torch.isfinite(sc[0, 0]).all()) and bool(torch.isfinite(sc[1]).all())
+        assert bool((sc[0, 0, :600][~skipped] > base[0, 0, :600][~skipped]).any())
