@@ -157,7 +157,7 @@ typedef struct {
  * pa_rotary_init -- frequencies for pa_rotary_cache_write.  Host only.
  *
  * inv_freq      HOST, [num_pairs] angular frequencies (radians per position),
- *               finite; scaled variants pass their scaled values
+ *               below 2^64 in magnitude; scaled variants pass their scaled values
  * axes          HOST, [num_pairs] position axis of each pair, in
  *               [0, PA_MAX_ROTARY_AXES); NULL: axis 0 for all
  * num_pairs     a multiple of 8, at most PA_MAX_ROTARY_PAIRS
@@ -178,9 +178,9 @@ pa_status_t pa_rotary_init(pa_rotary_t *rotary, const double *inv_freq, const in
  *     (x, y) -> scale * (x cos - y sin, y cos + x sin)
  * for every query head (to query_out) and KV head of the key; elements from
  * rotary_dim on and the value are unchanged.  The key and the value go to the
- * slot as pa_cache_write puts them there.  The angle is exact modulo a turn
- * for any 64-bit position before it is rounded to fp32; rotations are fp32,
- * rounded once (to nearest even).
+ * slot as pa_cache_write puts them there.  The angle modulo a turn is off by
+ * |position| * 2^-65 turns before it is rounded to fp32 (below that rounding up
+ * to positions of 2^40); rotations are fp32, rounded once (to nearest even).
  *
  * query_out     device, token t's heads at t * query_out_stride; may be
  *               `query` itself with the same stride (in place), and must not

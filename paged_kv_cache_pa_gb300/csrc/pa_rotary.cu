@@ -12,10 +12,12 @@
 // Angles.  Only the angle's fraction of a turn matters, and positions are
 // whole numbers, so the frequency is kept as a 64-bit binary fraction of a
 // turn, F = frac(w / 2 pi) 2^64: the product position * F modulo 2^64 (one
-// wrapping integer multiply) is the fraction of a turn exactly, however far
-// the position, where a 32-bit product w * position is off by 0.03 rad at
-// position 10^6.  The fraction, read as a signed number, goes to sincospi,
-// one rounding to 32 bits before it.
+// wrapping integer multiply) is the fraction of a turn, where a 32-bit product
+// w * position is off by 0.03 rad at position 10^6.  F is w / 2 pi rounded to 64
+// bits once (turn_fraction: a double holds the quotient to 2^-53 of itself only,
+// 2^-25 of a turn at position 2^30 already), so the fraction is off by
+// |position| 2^-65 turns, less than the one rounding to 32 bits that follows up
+// to positions of 2^40.  Read as a signed number, it goes to sincospi.
 //
 // Bound: HBM.  Every row is read once and written once.  A row of head_dim
 // elements belongs to head_dim / 16 threads of two 16-byte chunks each, the
@@ -242,6 +244,31 @@ __global__ void __launch_bounds__(kRotThreads)
     }
 }
 
+// frac(|w| / 2 pi) 2^64, rounded to nearest, for |w| < 2^64: with |w| = m 2^e, m
+// of 53 bits, and C = floor(2^256 / 2 pi), it is m C 2^(e - 192) modulo 2^64, off
+// by |w| 2^-192 before the rounding.
+uint64_t turn_fraction(double w) {
+    static const uint64_t kC[4] = {0x7f9458eaf7aef158ull, 0x36d8a5664f10e410ull,  // least first
+                                   0x7f09d5f47d4d3770ull, 0x28be60db9391054aull};
+    int e;
+    const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(w), &e), 53);
+    const int shift = 192 - (e - 53);  // bits of m C behind the point; 181 or more
+    uint64_t p[6] = {};                // m C, one word to spare
+    unsigned __int128 carry = 0;
+    for (int i = 0; i < 4; ++i) {
+        carry += (unsigned __int128)m * kC[i];
+        p[i] = (uint64_t)carry;
+        carry >>= 64;
+    }
+    p[4] = (uint64_t)carry;
+    auto word = [&](int bit) -> uint64_t {  // 64 bits from `bit` on
+        const int i = bit >> 6, r = bit & 63;
+        if (i > 4) return 0u;
+        return r ? (p[i] >> r) | (p[i + 1] << (64 - r)) : p[i];
+    };
+    return word(shift) + (word(shift - 1) & 1u);
+}
+
 int log2_of(int x) {
     int l = 0;
     while ((1 << l) < x) ++l;
@@ -264,18 +291,14 @@ extern "C" pa_status_t pa_rotary_init(pa_rotary_t *rotary, const double *inv_fre
     r.num_axes = 1;
     r.interleaved = interleaved ? 1 : 0;
     r.scale = scale;
-    constexpr double kTwoPi = 6.283185307179586476925286766559;
     for (int i = 0; i < num_pairs; ++i) {
-        if (!std::isfinite(inv_freq[i])) return PA_ERR_INVALID_ARG;
+        if (!(std::fabs(inv_freq[i]) < 0x1p64)) return PA_ERR_INVALID_ARG;
         const int a = axes ? axes[i] : 0;
         if (a < 0 || a >= PA_MAX_ROTARY_AXES) return PA_ERR_INVALID_ARG;
         if (a + 1 > r.num_axes) r.num_axes = a + 1;
         r.axis[i] = (uint8_t)a;
-        double f = std::fmod(inv_freq[i] / kTwoPi, 1.0);
-        const bool neg = f < 0.0;
-        if (neg) f = -f;
-        const uint64_t u = (uint64_t)std::ldexp(f, 64);  // f < 1: below 2^64
-        r.turns[i] = neg ? 0u - u : u;
+        const uint64_t u = pa::turn_fraction(inv_freq[i]);
+        r.turns[i] = inv_freq[i] < 0.0 ? 0u - u : u;
     }
     *rotary = r;
     return PA_OK;

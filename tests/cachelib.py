@@ -1,6 +1,7 @@
 """Paged caches with shuffled blocks for the bounded-cache tests, and the
 operators' definitions in 64 bits (plain torch, one head at a time)."""
 import math
+from fractions import Fraction
 
 import numpy as np
 import torch
@@ -65,3 +66,20 @@ def weights64(x, err):
     p = torch.softmax(x, -1)
     rel = 2 * err.amax(-1, keepdim=True) + 2.0 ** -21 + min(x.shape[-1] * 2.0 ** -24, 2.0 ** -12)
     return p, p * rel
+
+
+def turn_fraction(w):
+    """The fraction of a turn of `w` radians (a double), times 2^64, to 2^-100."""
+    def arctan_inverse(x, one):
+        term = total = one // x
+        n, sign = 3, -1
+        while term:
+            term //= x * x
+            total += sign * (term // n)
+            n, sign = n + 2, -sign
+        return total
+
+    one = 1 << 1600
+    two_pi = 8 * (4 * arctan_inverse(5, one) - arctan_inverse(239, one))  # Machin
+    num, den = float(w).as_integer_ratio()
+    return (num * one * one // (den * two_pi) % one) / Fraction(one) * 2 ** 64

@@ -234,3 +234,22 @@ def test_manager_swapped_out_sequences_are_refused():
         with pytest.raises(pa.PaError):
             f(a, 1)
     bm.close()
+
+
+def test_rotary_frequencies_are_right_to_64_bits(lib):
+    """A position far out multiplies what the frequency is off by: rounded once, to 2^-65 turns."""
+    import random
+    from cachelib import turn_fraction
+    rng = random.Random(3)
+    freqs = [10000.0 ** (-i / 64) for i in range(64)] + [1e6 ** (-i / 32) for i in range(32)]
+    freqs += [math.ldexp(rng.uniform(0.5, 1), e) for e in range(64, -80, -7)]
+    freqs += [math.pi, 2 * math.pi, 0.0, -0.0, 5e-324, 1e-300, 2.0 ** 64 * (1 - 2.0 ** -53), -1.0, -10000.0]
+    freqs += [1.0] * (-len(freqs) % 8)
+    for i in range(0, len(freqs), 8):
+        st, r = _init(lib, 8, freqs=freqs[i:i + 8])
+        assert st == OK
+        for w, got in zip(freqs[i:i + 8], r.turns):
+            d = abs(got - turn_fraction(w))
+            assert min(d, 2 ** 64 - d) <= 0.5 + 2.0 ** -40, (w, float(d))
+    for w in (2.0 ** 64, -2.0 ** 64, 1e300):
+        assert _init(lib, 8, freqs=[w] * 8)[0] == INVALID

@@ -13,6 +13,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import paged_kv_cache_pa_gb300 as pa
+from cachelib import turn_fraction
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -186,3 +187,22 @@ def test_captured_and_replayed_on_another_stream():
         g.replay()
     st.synchronize()
     assert torch.equal(out, want) and kc[slots // 16, :, slots % 16].any()
+
+
+@pytest.mark.parametrize("far", [1 << 20, 1 << 31, 1 << 40])
+def test_far_positions_of_ordinary_frequencies(far):
+    """Slack: the frequency is right to 2^-65 turns, 2 pi far 2^-65 of an angle."""
+    q, k, v, kc, vc, slots, pos = _case(40, 4, 2, 64, torch.float16, seed=6, far=far)
+    pos = far - 1 - pos % 1000
+    pos[0, ::2] *= -1
+    freqs = _freqs(32)
+    out = pa.rotary_cache_write(q, k, v, pos, pa.Rotary(freqs), kc, vc, slots)
+    turns = [turn_fraction(f) for f in freqs]
+    ang = np.array([[float(int(p) * t % 2 ** 64) / 2 ** 64 for t in turns] for p in pos[0].cpu().numpy()])
+    z = np.exp(2j * np.pi * ang)[:, None]
+    x = q.double().cpu().numpy()
+    w = (x[..., :32] + 1j * x[..., 32:]) * z
+    mag = np.abs(x[..., :32]) + np.abs(x[..., 32:])
+    slack = 2 * math.pi * far * 2.0 ** -65 * mag
+    _close_far(out, np.concatenate([w.real, w.imag], -1), np.concatenate([mag, mag], -1),
+               np.concatenate([slack, slack], -1))
