@@ -267,9 +267,8 @@ class Rotary:
             raise ValueError("axes must name one axis per frequency")
         ax = None if axes is None else (ctypes.c_int32 * n)(*[int(a) for a in axes])
         self._struct = _RotaryStruct()
-        self._ptr = ctypes.addressof(self._struct)
         _check(load_library().pa_rotary_init(
-            self._ptr, ctypes.cast((ctypes.c_double * n)(*freqs), _P),
+            ctypes.addressof(self._struct), ctypes.cast((ctypes.c_double * n)(*freqs), _P),
             None if ax is None else ctypes.cast(ax, _P), n, int(bool(interleaved)),
             float(scale)), "pa_rotary_init")
 
@@ -327,7 +326,8 @@ def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_
         raise ValueError("query_out must match the query")
     st = load_library().pa_rotary_cache_write(
         *_rows(query_out, "query_out", H * D), *_rows(query, "query", H * D),
-        *_rows(key, "key", hkv * D), *_rows(value, "value", hkv * D), _dev(positions, "positions"), rotary._ptr,
+        *_rows(key, "key", hkv * D), *_rows(value, "value", hkv * D),
+        _dev(positions, "positions"), ctypes.addressof(rotary._struct),
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"),
         T, nb, bs, H, hkv, d, _dtype_code(dt), _opt_ptr(error_word, "error_word"),
         _stream_ptr(stream, query.device))

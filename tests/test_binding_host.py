@@ -98,7 +98,7 @@ def _calls():
     pool = Tensor((9, 4, 16, 64), h)
     tab, lens, qsl = Tensor((2, 4), i32), Tensor(2, i32), Tensor(3, i32)
     sc, lse = Tensor((2, 4, 64), f32), Tensor((2, 8), f32)
-    rot = types.SimpleNamespace(num_axes=1, _ptr=1, _struct=pa._RotaryStruct())
+    rot = types.SimpleNamespace(num_axes=1, _struct=pa._RotaryStruct())
     return {
         "rotary": lambda **kw: pa.rotary_cache_write(q, new, new, Tensor(2, i64), rot, pool, pool, Tensor(2, i64), **kw),
         "decode": lambda **kw: pa.decode_attention(q, pool, pool, tab, lens, 64, 0.1, **kw),
@@ -125,3 +125,21 @@ def test_what_a_call_allocates_belongs_to_its_stream(fake, name):
     _calls()[name]()
     assert all(t.home == "current" for t in fake.torch.made)
     assert fake.lib.calls[-1][1][-1] == 1000
+
+
+@pytest.mark.parametrize("how", ["copy", "deepcopy", "pickle"])
+def test_a_copied_rotary_has_frequencies_of_its_own(fake, how):
+    """A module that holds one may be copied, and outlive the original."""
+    import copy
+    import ctypes
+    import pickle
+    rot = pa.Rotary([0.5] * 8)
+    rot._struct.turns[3] = 77
+    again = {"copy": copy.copy, "deepcopy": copy.deepcopy,
+             "pickle": lambda r: pickle.loads(pickle.dumps(r))}[how](rot)
+    h, i64 = torch.float16, torch.int64
+    q, new, pool = Tensor((2, 8, 64), h), Tensor((2, 4, 64), h), Tensor((9, 4, 16, 64), h)
+    pa.rotary_cache_write(q, new, new, Tensor(2, i64), again, pool, pool, Tensor(2, i64))
+    name, args = fake.lib.calls[-1]
+    assert name == "pa_rotary_cache_write" and args[9] == ctypes.addressof(again._struct)
+    assert again._struct.turns[3] == 77 and again.rotary_dim == rot.rotary_dim
