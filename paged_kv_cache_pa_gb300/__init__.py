@@ -5,7 +5,7 @@ with the same operation names.  This module only marshals arguments (device
 pointers of torch tensors, sizes, the current CUDA stream); every step of the
 path runs in the library's CUDA kernels.  There is no CPU fallback: calling an
 operation without the built library, or with tensors that are not on a CUDA
-device, raises.
+device, or not on the current one, raises.
 
     cache_write(key, value, k_cache, v_cache, slot_mapping)
     decode_attention(query, k_cache, v_cache, block_tables, context_lens,
@@ -187,6 +187,9 @@ def _dev(t, name):
 
 def _stream_ptr(stream, device) -> int:
     torch = _torch()
+    if device.index != torch._C._cuda_getDevice():
+        # (a launch goes to the current device, whatever its pointers say)
+        raise ValueError(f"the tensors are on cuda:{device.index}, which is not the current device")
     if stream is None:
         # the current stream's handle, without making a Stream object
         return torch._C._cuda_getCurrentRawStream(device.index)

@@ -143,3 +143,13 @@ def test_a_copied_rotary_has_frequencies_of_its_own(fake, how):
     name, args = fake.lib.calls[-1]
     assert name == "pa_rotary_cache_write" and args[9] == ctypes.addressof(again._struct)
     assert again._struct.turns[3] == 77 and again.rotary_dim == rot.rotary_dim
+
+
+@pytest.mark.parametrize("name", list(_calls()))
+def test_tensors_on_another_device_than_the_current_one_are_refused(fake, name):
+    """The library launches on the current device; the default stream has the same handle on all."""
+    fake.torch.device = 1
+    for kw in ({}, {"stream": types.SimpleNamespace(cuda_stream=7)}):
+        with pytest.raises(ValueError, match="current device"):
+            _calls()[name](**kw)
+    assert all(n.endswith("_size") for n, _ in fake.lib.calls)
