@@ -93,7 +93,10 @@ pa_status_t pa_bm_build_batch(const pa_block_manager_t *bm, const int64_t *seqs,
 /* Make the blocks that hold the first num_tokens tokens of a GPU-resident
  * sequence its own, before pa_evict_tokens compacts into them: every one that
  * is shared is replaced by a fresh block, and the (old, new) pair is queued
- * for pa_bm_take_copies.  PA_ERR_NO_BLOCKS if the pool is short. */
+ * for pa_bm_take_copies.  PA_ERR_NO_BLOCKS if the pool is short;
+ * PA_ERR_INVALID_ARG if a queued pair writes a block that would now be copied
+ * from, or names a block that would now be handed out again (pa_copy_blocks
+ * takes the pairs of a call in any order): take the queued pairs first. */
 pa_status_t pa_bm_seq_make_private(pa_block_manager_t *bm, int64_t seq, int num_tokens);
 /* Set a GPU-resident sequence's length to num_tokens (at most its length) and
  * release the blocks behind, after pa_evict_tokens.  A released block may be

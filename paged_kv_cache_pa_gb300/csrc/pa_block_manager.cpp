@@ -66,6 +66,13 @@ class Pool {
         refs_[b] = 1;
         return b;
     }
+    // The ids the next n calls of alloc() hand out (n <= num_free()).
+    std::vector<int> next(int n) const {
+        std::vector<int> ids;
+        for (size_t i = 0; i < given_.size() && (int)ids.size() < n; ++i) ids.push_back(given_[i]);
+        for (auto rest = heap_; (int)ids.size() < n; rest.pop()) ids.push_back(rest.top());
+        return ids;
+    }
     void retain(int b) { ++refs_[b]; }
     void set_refs(int b, int r) { refs_[b] = r; }
     void release(int b) {
@@ -269,6 +276,20 @@ pa_status_t pa_bm_seq_make_private(pa_block_manager_t *bm, int64_t seq, int num_
     // room for the pairs first, so that nothing has changed if there is none
     const size_t queued = bm->copies.size();
     try {
+        // pairs are copied in any order: no block may be one's destination and
+        // another's source or destination
+        if (queued && shared) {
+            const std::vector<int> fresh = bm->gpu.next(shared);
+            auto in = [](const std::vector<int> &v, int64_t b) {
+                return std::find(v.begin(), v.end(), (int)b) != v.end();
+            };
+            std::vector<int> old;
+            for (size_t i = 0; i < nb; ++i)
+                if (bm->gpu.refs(s->table[i]) > 1) old.push_back(s->table[i]);
+            for (const auto &c : bm->copies)
+                if (in(old, c.second) || in(fresh, c.first) || in(fresh, c.second))
+                    return PA_ERR_INVALID_ARG;
+        }
         bm->copies.resize(queued + shared);
     } catch (const std::bad_alloc &) {
         return PA_ERR_NO_BLOCKS;

@@ -144,7 +144,8 @@ class BlockManager:
 
     def make_private(self, seq: int, num_tokens: int) -> None:
         """Before an eviction in place: the blocks of the first num_tokens
-        tokens become the sequence's own (copies queued); raises NoFreeBlocks."""
+        tokens become the sequence's own (copies queued); raises NoFreeBlocks,
+        and PaError where the copies queued so far have to be taken first."""
         _check(self._lib.pa_bm_seq_make_private(self._h, seq, num_tokens),
                "pa_bm_seq_make_private")
 

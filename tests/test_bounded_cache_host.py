@@ -253,3 +253,48 @@ def test_rotary_frequencies_are_right_to_64_bits(lib):
             assert min(d, 2 ** 64 - d) <= 0.5 + 2.0 ** -40, (w, float(d))
     for w in (2.0 ** 64, -2.0 ** 64, 1e300):
         assert _init(lib, 8, freqs=[w] * 8)[0] == INVALID
+
+
+def test_make_private_queues_no_chains():
+    """The pairs of one copy call are independent: no destination is another's source or destination."""
+    from paged_kv_cache_pa_gb300.manager import BlockManager
+
+    def independent(pairs):
+        src, dst = set(pairs[:, 0].tolist()), pairs[:, 1].tolist()
+        return len(set(dst)) == len(dst) and not src & set(dst)
+
+    bm = BlockManager(8, 0, 16)
+    a = bm.new_sequence()
+    bm.append(a, 20)
+    b = bm.fork(a)
+    bm.append(b, 1)                        # queues a copy of block 1 to a block of b's
+    c = bm.fork(b)
+    with pytest.raises(pa.PaError):
+        bm.make_private(c, 21)             # would copy from that block
+    assert bm.table(c) == bm.table(b) and bm.num_free_gpu == 5
+    pairs = bm.take_copies()
+    assert pairs.tolist() == [[1, 2]]
+    bm.make_private(c, 21)
+    pairs = bm.take_copies()
+    assert len(pairs) == 2 and independent(pairs)
+    bm.close()
+
+    bm = BlockManager(8, 0, 16)
+    a, d = bm.new_sequence(), bm.new_sequence()
+    bm.append(a, 20)
+    bm.append(d, 30)
+    b, e = bm.fork(a), bm.fork(d)
+    bm.append(b, 1)                        # copies block 1
+    bm.free(a)                             # and block 1 is free again
+    with pytest.raises(pa.PaError):
+        bm.make_private(e, 30)             # would copy to block 1
+    assert bm.table(e) == bm.table(d) and bm.num_free_gpu == 4
+    bm.take_copies()
+    bm.make_private(e, 30)
+    assert bm.table(e) == [1, 5]
+    # two copies of one block are independent
+    f = bm.fork(d)
+    bm.make_private(f, 16)
+    pairs = bm.take_copies()
+    assert len(pairs) == 3 and independent(pairs)
+    bm.close()
