@@ -468,8 +468,8 @@ pa_status_t pa_prefill_attention_lse(void *out, pa_dtype_t out_dtype, const void
                                      pa_stream_t stream);
 
 /*
- * pa_prefill_scores_workspace_size -- bytes of device workspace
- * pa_prefill_scores needs for these sizes; 0 for invalid ones.  Host only.
+ * pa_prefill_scores_workspace_size -- bytes of a device workspace for
+ * pa_prefill_scores at these sizes; 0 for invalid ones.  Host only.
  */
 size_t pa_prefill_scores_workspace_size(int num_seqs, int num_heads, int num_kv_heads,
                                         int head_dim, int max_query_len, int max_context_len);
@@ -500,8 +500,9 @@ size_t pa_prefill_scores_workspace_size(int num_seqs, int num_heads, int num_kv_
  * num_kv_heads at most 65535.  Lengths, tables and limits are those of
  * pa_prefill_attention; query_start_loc and context_lens are read as soon as
  * the kernel starts (as pa_decode_attention reads its lengths).
- * workspace     device, >= pa_prefill_scores_workspace_size(...) bytes,
- *               256-byte aligned; calls in flight at once must not share one
+ * workspace     nothing is kept in it: NULL with workspace_bytes 0, or as for
+ *               the other calls >= pa_prefill_scores_workspace_size(...) bytes,
+ *               256-byte aligned, neither read nor written
  * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence
  *               whose lengths break the rules (its scores are left as they
  *               were), PA_ERRBIT_BLOCK_OOB (the block's keys are skipped),

@@ -622,9 +622,8 @@ def prefill_scores(query, lse, k_cache, block_tables, query_start_loc, context_l
     query_start_loc[s] .. query_start_loc[s+1]-1 of query [T][H][D], its last
     positions: a prompt, a chunk or a window) give to its cached tokens to
     ``scores`` (fp32 [S][Hkv][>= max_context_len]).  ``lse`` [T][H] is the rows'
-    log-sum-exp (prefill_attention's).  ``workspace`` (uint8, >=
-    prefill_scores_workspace_size bytes) is allocated here when not given.
-    Returns ``scores``."""
+    log-sum-exp (prefill_attention's).  No ``workspace`` is needed (one of
+    prefill_scores_workspace_size bytes is accepted).  Returns ``scores``."""
     torch = _torch()
     T, H, D = query.shape
     nb, hkv, bs, d2 = k_cache.shape
@@ -639,17 +638,14 @@ def prefill_scores(query, lse, k_cache, block_tables, query_start_loc, context_l
             block_tables.shape[0] != S:
         raise ValueError("query_start_loc must be [S+1], block_tables [S][max_blocks]")
     sc, stride = _score_rows(scores, (S, hkv))
-    if workspace is None:
-        nbytes = prefill_scores_workspace_size(S, H, hkv, D, int(max_query_len),
-                                               int(max_context_len))
-        workspace = _workspace(stream, nbytes, query.device)
+    ws = (None, 0) if workspace is None else (
+        _dev(workspace, "workspace"), workspace.numel() * workspace.element_size())
     st = load_library().pa_prefill_scores(
         _dev(query, "query"), _lse_ptr(lse, T, H), _dev(k_cache, "k_cache"),
         _dev(block_tables, "block_tables"), block_tables.shape[1],
         _dev(query_start_loc, "query_start_loc"), _dev(context_lens, "context_lens"),
         int(max_query_len), int(max_context_len), S, T, H, hkv, D, nb, bs, float(scale),
-        _dtype_code(query.dtype), sc, stride, _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
+        _dtype_code(query.dtype), sc, stride, *ws, _opt_ptr(error_word, "error_word"),
         _stream_ptr(stream, query.device))
     _check(st, "pa_prefill_scores")
     return scores

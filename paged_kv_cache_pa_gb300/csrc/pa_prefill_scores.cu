@@ -1130,15 +1130,17 @@ extern "C" pa_status_t pa_prefill_scores(
         num_kv_heads > 65535 || num_seqs > 65535)
         return PA_ERR_UNSUPPORTED;
     if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0 || max_context_len == 0) return PA_OK;
+    const bool no_workspace = !workspace && workspace_bytes == 0;  // (the kernel needs none)
     if (!query || !lse || !k_cache || !block_tables || !query_start_loc || !context_lens || !scores ||
-        !workspace)
+        (!workspace && !no_workspace))
         return PA_ERR_INVALID_ARG;
     if (!is_aligned(query, 16) || !is_aligned(k_cache, 16) || !is_aligned(lse, 4) ||
         !is_aligned(scores, 4))
         return PA_ERR_INVALID_ARG;
-    if (!is_aligned(workspace, 256) ||
-        workspace_bytes < pa_prefill_scores_workspace_size(num_seqs, num_heads, num_kv_heads,
-                                                           head_dim, max_query_len, max_context_len))
+    if (!no_workspace &&
+        (!is_aligned(workspace, 256) ||
+         workspace_bytes < pa_prefill_scores_workspace_size(num_seqs, num_heads, num_kv_heads,
+                                                            head_dim, max_query_len, max_context_len)))
         return PA_ERR_WORKSPACE;
     const int sms = device_sms();
     if (sms <= 0) return PA_ERR_CUDA;

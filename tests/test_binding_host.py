@@ -153,3 +153,12 @@ def test_tensors_on_another_device_than_the_current_one_are_refused(fake, name):
         with pytest.raises(ValueError, match="current device"):
             _calls()[name](**kw)
     assert all(n.endswith("_size") for n, _ in fake.lib.calls)
+
+
+def test_prompt_scores_take_no_memory(fake):
+    _calls()["prompt scores"]()
+    assert not fake.torch.made
+    assert fake.lib.calls[-1][1][-4:-2] == (None, 0)
+    ws = Tensor(256, torch.uint8)
+    _calls()["prompt scores"](workspace=ws)
+    assert fake.lib.calls[-1][1][-4:-2] == (ws.data_ptr(), 256)

@@ -298,3 +298,10 @@ def test_make_private_queues_no_chains():
     pairs = bm.take_copies()
     assert len(pairs) == 3 and independent(pairs)
     bm.close()
+
+
+def test_prefill_scores_without_a_workspace(lib):
+    """Without one: what is refused is what else is wrong."""
+    for kw, want in (({"S": 0}, OK), ({"L": 128, "stride": 99}, INVALID), ({"sc": P + 2}, INVALID),
+                     ({"D": 256}, UNSUPPORTED), ({"wb": 256}, INVALID)):
+        assert _pscores(lib, **{"ws": None, "wb": 0, **kw}) == want
