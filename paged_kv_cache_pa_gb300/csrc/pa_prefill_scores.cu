@@ -1166,10 +1166,16 @@ extern "C" pa_status_t pa_prefill_scores(
         }
     }
     P.head_groups = G / P.nh;
-    // the rings: three K tiles and three full query tiles at head_dim 128; with
-    // query tiles of at most 64 rows (windows) more of both
+    // The rings (counted at head_dim 128; 64 has twice the slots): three K tiles and
+    // what is left in query tiles, three of 128 rows, four of 96; four K tiles where
+    // a query tile has at most 64 rows, which leaves four of those and more.  (96
+    // rows with four K tiles and two query tiles: 14.6 us for 8 windows of 32
+    // queries, 12 heads on 2, and 20.4 for 8 of 40, 24 heads on 2; 14.4 and 19.2
+    // so.)  The waits for a tile's lse need two query slots at least.
+    static_assert((kTileBytes - 3 * 32768) / 32768 >= 2 && (kTileBytes - 4 * 32768) / 16384 >= 2,
+                  "query slots");
     const uint32_t kbytes = (uint32_t)head_dim * 256u, qbytes = (uint32_t)head_dim * 2u * P.nh << P.lg_nq;
-    P.rk = qbytes < kbytes ? 4 : 3;
+    P.rk = 2 * qbytes <= kbytes ? 4 : 3;
     if (head_dim == 64) P.rk *= 2;
     P.rq = (int)((kTileBytes - (uint32_t)P.rk * kbytes) / qbytes);
     if (P.rq > kMaxRing) P.rq = kMaxRing;
