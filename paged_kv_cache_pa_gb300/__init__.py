@@ -185,14 +185,17 @@ def _dev(t, name):
                      else f"{name} must be contiguous")
 
 
-def _stream_ptr(stream, device) -> int:
-    torch = _torch()
-    if device.index != torch._C._cuda_getDevice():
+def _stream_ptr(stream, t) -> int:
+    """Handle of ``stream``, or of the current stream; t: a CUDA tensor of the
+    call, or None if it has none."""
+    cuda = _torch()._C
+    index = cuda._cuda_getDevice()
+    if t is not None and t.get_device() != index:
         # (a launch goes to the current device, whatever its pointers say)
-        raise ValueError(f"the tensors are on cuda:{device.index}, which is not the current device")
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
     if stream is None:
-        # the current stream's handle, without making a Stream object
-        return torch._C._cuda_getCurrentRawStream(device.index)
+        # without making a Stream object
+        return cuda._cuda_getCurrentRawStream(index)
     return int(stream.cuda_stream)
 
 
@@ -203,7 +206,7 @@ def _empty(stream, shape, dtype, device, returned=False):
     this tensor is dropped, meets the call's kernels.  returned: the caller
     gets it, and may drop it while the current stream still uses it."""
     torch = _torch()
-    if stream is None:
+    if stream is None or int(stream.cuda_stream) == torch._C._cuda_getCurrentRawStream(device.index):
         return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
         t = torch.empty(shape, dtype=dtype, device=device)
@@ -236,7 +239,7 @@ def cache_write(key, value, k_cache, v_cache, slot_mapping, error_word=None,
     args = (_dev(key, "key"), _dev(value, "value"), _dev(k_cache, "k_cache"),
             _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"), key.shape[0], nb)
     tail = (hkv, d, _dtype_code(key.dtype), _opt_ptr(error_word, "error_word"),
-            _stream_ptr(stream, key.device))
+            _stream_ptr(stream, key))
     lib = load_library()
     if bs == BLOCK_SIZE:
         _check(lib.pa_cache_write(*args, *tail), "pa_cache_write")
@@ -270,10 +273,19 @@ class Rotary:
             raise ValueError("axes must name one axis per frequency")
         ax = None if axes is None else (ctypes.c_int32 * n)(*[int(a) for a in axes])
         self._struct = _RotaryStruct()
+        self._ptr = ctypes.addressof(self._struct)
         _check(load_library().pa_rotary_init(
-            ctypes.addressof(self._struct), ctypes.cast((ctypes.c_double * n)(*freqs), _P),
+            self._ptr, ctypes.cast((ctypes.c_double * n)(*freqs), _P),
             None if ax is None else ctypes.cast(ax, _P), n, int(bool(interleaved)),
             float(scale)), "pa_rotary_init")
+
+    # a copy has frequencies, and their address, of its own
+    def __getstate__(self):
+        return bytes(self._struct)
+
+    def __setstate__(self, state):
+        self._struct = _RotaryStruct.from_buffer_copy(state)
+        self._ptr = ctypes.addressof(self._struct)
 
     @property
     def rotary_dim(self) -> int:
@@ -330,10 +342,10 @@ def rotary_cache_write(query, key, value, positions, rotary: Rotary, k_cache, v_
     st = load_library().pa_rotary_cache_write(
         *_rows(query_out, "query_out", H * D), *_rows(query, "query", H * D),
         *_rows(key, "key", hkv * D), *_rows(value, "value", hkv * D),
-        _dev(positions, "positions"), ctypes.addressof(rotary._struct),
+        _dev(positions, "positions"), rotary._ptr,
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"),
         T, nb, bs, H, hkv, d, _dtype_code(dt), _opt_ptr(error_word, "error_word"),
-        _stream_ptr(stream, query.device))
+        _stream_ptr(stream, query))
     _check(st, "pa_rotary_cache_write")
     return query_out
 
@@ -385,7 +397,7 @@ def decode_attention(query, k_cache, v_cache, block_tables, context_lens,
             _dev(context_lens, "context_lens"), int(max_context_len), S, H, hkv, D, nb)
     tail = (float(scale), _dtype_code(query.dtype), _dev(workspace, "workspace"),
             workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
-            _stream_ptr(stream, query.device))
+            _stream_ptr(stream, query))
     lib = load_library()
     if bs == BLOCK_SIZE:
         _check(lib.pa_decode_attention(*head, *tail), "pa_decode_attention")
@@ -417,7 +429,7 @@ def decode_attention_contiguous(query, k_cache, v_cache, context_lens, max_conte
         _dev(v_cache, "v_cache"), rows, _dev(context_lens, "context_lens"), int(max_context_len),
         S, H, hkv, D, float(scale), _dtype_code(query.dtype), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
-        _stream_ptr(stream, query.device))
+        _stream_ptr(stream, query))
     _check(st, "pa_decode_attention_contiguous")
     return out
 
@@ -474,7 +486,7 @@ def decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
         _dev(context_lens, "context_lens"), int(max_context_len), S, H, hkv, D, nb, bs,
         float(scale), _dtype_code(dt), sc, stride, _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
-        _stream_ptr(stream, query.device))
+        _stream_ptr(stream, query))
     _check(st, "pa_decode_attention_scored")
     return out
 
@@ -499,7 +511,7 @@ def copy_blocks(k_caches: Sequence, v_caches: Sequence, block_pairs, error_word=
     head = (ctypes.cast(kp, ctypes.c_void_p), ctypes.cast(vp, ctypes.c_void_p), L,
             _dev(block_pairs, "block_pairs") if npairs else None, npairs, nb)
     tail = (hkv, d, _dtype_code(k_caches[0].dtype), _opt_ptr(error_word, "error_word"),
-            _stream_ptr(stream, k_caches[0].device))
+            _stream_ptr(stream, k_caches[0]))
     lib = load_library()
     if bs == BLOCK_SIZE:
         _check(lib.pa_copy_blocks(*head, *tail), "pa_copy_blocks")
@@ -540,13 +552,13 @@ def swap_blocks(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_caches: Se
     arr = lambda xs, n: ctypes.cast((ctypes.c_void_p * L)(*[_pool_ptr(x, n) for x in xs]),
                                     ctypes.c_void_p)
     npairs = block_pairs.shape[0] if block_pairs.numel() else 0
-    dev = next((c.device for c in [block_pairs] + list(dst_k_caches) + list(src_k_caches)
-                if c.is_cuda), None)
+    on_gpu = next((c for c in [block_pairs] + list(dst_k_caches) + list(src_k_caches)
+                   if c.is_cuda), None)
     st = load_library().pa_swap_blocks(
         arr(dst_k_caches, "dst_k_caches"), arr(dst_v_caches, "dst_v_caches"),
         arr(src_k_caches, "src_k_caches"), arr(src_v_caches, "src_v_caches"), L,
         block_pairs.data_ptr() if npairs else None, npairs, nd, ns, bs, hkv, d, _dtype_code(dt),
-        _opt_ptr(error_word, "error_word"), _stream_ptr(stream, dev))
+        _opt_ptr(error_word, "error_word"), _stream_ptr(stream, on_gpu))
     _check(st, "pa_swap_blocks")
 
 
@@ -591,7 +603,7 @@ def prefill_attention(query, k_cache, v_cache, block_tables, query_start_loc, co
             int(max_query_len), int(max_context_len), S, T, H, hkv, D, nb, bs, float(scale),
             _dtype_code(query.dtype))
     tail = (_dev(workspace, "workspace"), workspace.numel() * workspace.element_size(),
-            _opt_ptr(error_word, "error_word"), _stream_ptr(stream, query.device))
+            _opt_ptr(error_word, "error_word"), _stream_ptr(stream, query))
     lib = load_library()
     if lse is None:
         _check(lib.pa_prefill_attention(*head, *tail), "pa_prefill_attention")
@@ -646,7 +658,7 @@ def prefill_scores(query, lse, k_cache, block_tables, query_start_loc, context_l
         _dev(query_start_loc, "query_start_loc"), _dev(context_lens, "context_lens"),
         int(max_query_len), int(max_context_len), S, T, H, hkv, D, nb, bs, float(scale),
         _dtype_code(query.dtype), sc, stride, *ws, _opt_ptr(error_word, "error_word"),
-        _stream_ptr(stream, query.device))
+        _stream_ptr(stream, query))
     _check(st, "pa_prefill_scores")
     return scores
 
@@ -740,6 +752,6 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
         _dev(new_lens, "new_lens"), int(max_context_len), int(max_keep_len), int(num_sink),
         int(num_recent), S, nb, bs, hkv, d, _dtype_code(dt), _dev(workspace, "workspace"),
         workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
-        _stream_ptr(stream, k_caches[0].device))
+        _stream_ptr(stream, k_caches[0]))
     _check(st, "pa_evict_tokens")
     return new_lens

@@ -25,6 +25,9 @@ class Tensor:
     def dim(self):
         return len(self.shape)
 
+    def get_device(self):
+        return self.device.index
+
     def data_ptr(self):
         return id(self)
 
@@ -98,7 +101,7 @@ def _calls():
     pool = Tensor((9, 4, 16, 64), h)
     tab, lens, qsl = Tensor((2, 4), i32), Tensor(2, i32), Tensor(3, i32)
     sc, lse = Tensor((2, 4, 64), f32), Tensor((2, 8), f32)
-    rot = types.SimpleNamespace(num_axes=1, _struct=pa._RotaryStruct())
+    rot = types.SimpleNamespace(num_axes=1, _ptr=1)
     return {
         "rotary": lambda **kw: pa.rotary_cache_write(q, new, new, Tensor(2, i64), rot, pool, pool, Tensor(2, i64), **kw),
         "decode": lambda **kw: pa.decode_attention(q, pool, pool, tab, lens, 64, 0.1, **kw),
@@ -162,3 +165,22 @@ def test_prompt_scores_take_no_memory(fake):
     ws = Tensor(256, torch.uint8)
     _calls()["prompt scores"](workspace=ws)
     assert fake.lib.calls[-1][1][-4:-2] == (ws.data_ptr(), 256)
+
+
+def test_the_current_stream_given_by_name_is_the_current_stream(fake):
+    side = types.SimpleNamespace(cuda_stream=1000)  # the current stream's handle
+    for call in _calls().values():
+        call(stream=side)
+        assert fake.lib.calls[-1][1][-1] == 1000
+    assert all(t.home == "current" and not t.used_by for t in fake.torch.made)
+
+
+def test_a_swap_between_pinned_pools_needs_no_device(fake):
+    """Nothing to move, and no tensor of the call on a GPU."""
+    def host(shape, dtype):
+        t = Tensor(shape, dtype)
+        t.is_cuda, t.is_pinned = False, lambda: True
+        return t
+    pool = host((9, 4, 16, 64), torch.float16)
+    pa.swap_blocks([pool], [pool], [pool], [pool], host((0, 2), torch.int64), stream=types.SimpleNamespace(cuda_stream=7))
+    assert fake.lib.calls[-1][0] == "pa_swap_blocks" and fake.lib.calls[-1][1][-1] == 7
