@@ -185,17 +185,23 @@ def _dev(t, name):
                      else f"{name} must be contiguous")
 
 
+_several_devices = None
+
+
 def _stream_ptr(stream, t) -> int:
     """Handle of ``stream``, or of the current stream; t: a CUDA tensor of the
     call, or None if it has none."""
-    cuda = _torch()._C
-    index = cuda._cuda_getDevice()
-    if t is not None and t.get_device() != index:
+    global _several_devices
+    torch = _torch()
+    if _several_devices is None:
+        _several_devices = torch.cuda.device_count() > 1
+    if _several_devices and t is not None and t.get_device() != torch._C._cuda_getDevice():
         # (a launch goes to the current device, whatever its pointers say)
         raise ValueError(f"the tensors are on {t.device}, which is not the current device")
     if stream is None:
         # without making a Stream object
-        return cuda._cuda_getCurrentRawStream(index)
+        return torch._C._cuda_getCurrentRawStream(
+            torch._C._cuda_getDevice() if t is None else t.get_device())
     return int(stream.cuda_stream)
 
 

@@ -57,6 +57,10 @@ class Torch:
                 outer.stream = before
 
             @staticmethod
+            def device_count():
+                return 2
+
+            @staticmethod
             def current_stream(device=None):
                 return outer.stream
 
@@ -92,6 +96,7 @@ def fake(monkeypatch):
     monkeypatch.setattr(pa, "_torch_module", t)
     monkeypatch.setattr(pa, "_lib", lib)
     monkeypatch.setattr(pa, "_DTYPE_CODES", {})
+    monkeypatch.setattr(pa, "_several_devices", None)
     return types.SimpleNamespace(torch=t, lib=lib)
 
 
