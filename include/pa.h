@@ -729,7 +729,8 @@ size_t pa_evict_workspace_size(int num_layers, int num_seqs, int num_kv_heads,
  *               with L outside [0, max_context_len], a negative keep_lens or
  *               n > max_keep_len (it is left as it was, new_lens[s] = L);
  *               PA_ERRBIT_BLOCK_OOB (a row from or to a block outside the pool
- *               is not moved); PA_ERRBIT_TIMEOUT
+ *               is not moved); PA_ERRBIT_TIMEOUT (in place: some kept rows were
+ *               not moved, and the sequences are not to be used)
  */
 pa_status_t pa_evict_tokens(void *const *k_caches, void *const *v_caches, int num_layers,
                             const float *const *scores, int64_t score_stride,

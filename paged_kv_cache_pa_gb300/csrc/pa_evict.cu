@@ -410,9 +410,9 @@ __device__ __forceinline__ bool wait_chunk(const unsigned *flag) {
 // moves towards the front), so a CTA reads its chunk into registers, sets the
 // chunk's flag, and writes once the chunks on whose old rows it writes have
 // been read.  Chunks are taken in order by a counter, so those it waits for
-// have been started, and a chunk's reads wait for nothing.  Four layers of 16
-// prompts of up to 8000 tokens cut to 1200, in place: 127 us for both kernels,
-// 124 into other blocks (a unit's chunks side by side and four CTAs an SM: 184).
+// have been started, and a chunk's reads wait for nothing.  16 layers of 4
+// prompts of up to 8000 tokens cut to 1200, in place: 128 us for both kernels,
+// 125 into other blocks (a unit's chunks side by side and four CTAs an SM: 184).
 template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 5 : 4)
     evict_move_kernel(const __grid_constant__ EvictParams P) {

@@ -31,7 +31,8 @@
 //     items;
 //   * warps 1 and 2: S_t = K_t Q^T (M = 128 keys, N = the tile's rows,
 //     K = head_dim) for key tile 0 and 1 into one of two tensor-memory buffers
-//     each (two issuers: the waits of one fall into the other's products);
+//     each (two issuers: the waits of one fall into the other's products; both
+//     pass through every tile of both rings, their own or not);
 //     causal: a key tile starts with the query tile that holds the first token
 //     to see its first key, so the second tile's copy has time while the first
 //     one works alone.  Warp 1 allocates tensor memory;
@@ -50,7 +51,7 @@
 // cluster of 2, 4 or 8 CTAs shares each: the query tiles in equal parts one
 // after the other, and the first CTA's group (t, 0) adds the others' sums, in
 // their order, through distributed shared memory.  One prompt, 32 heads on 8 of
-// 128, with clusters and without: 4096 tokens 68 and 119 us, 1024 tokens 21 and
+// 128, with clusters and without: 4096 tokens 70 and 119 us, 1024 tokens 21 and
 // 39 us.
 //
 // Bound: 2 prompts of 4096 tokens, 32 heads on 8 of 128, bf16, take 120 us; the
@@ -62,7 +63,7 @@
 // memory is full with two buffers a key tile.  (Query tiles of 256 rows with
 // one buffer: 134 to 151 us.)  Windows of few queries are bound by the steps of
 // an item one after the other: 8 of 32 queries on 3000 to 16384 tokens, 12
-// heads on 2, take 18.6 us for 39 MB.
+// heads on 2, take 18.5 us for 39 MB.
 //
 // A wait that gives up sets the abort flag; the groups then go through the
 // rest of their items without waiting or writing, so that their named barriers

@@ -2,11 +2,12 @@
 added a token's whole weight or nothing.  The child process runs the test copy
 of the library whose waits give up after a few polls (test_gpu_wait_expiry).
 
-Tolerance of a whole weight: that of test_gpu_prefill_scores for fp16 inputs of
-this size is below 1e-4 of it (|lse| = 7, |x| below 8: 2^-20 from lse, 66 2^-24
-8 from x, 2^-21 and 2^-12 from exponential and sum); the score itself, below
-2^5, adds 2^-18.  A key's weight on 200 and more rows is above 1e-2 and lacks at
-least a tenth where a product is missing."""
+Tolerance of a whole weight, relative: 130 2^-24 sum |q k| scale = 7e-5 from x
+(128 products of standard normal numbers, scaled, sum to 9 at most), 2^-20 from
+lse and its product, 2^-21 from the exponential, and 2^-12 from a sum of 3600
+terms in any order: together below 4e-4.  The score itself, below 2^5, adds
+2^-18.  A sum that lacks a product lacks one of at most 38, some hundredths of
+it."""
 import json
 import os
 import subprocess
@@ -51,7 +52,7 @@ def _prompts(pa, D, times, calls, err):
         pa.prefill_scores(q, lse, c.k[0], c.tables, qsl, c.lens, 1200, 1500, D ** -0.5, sc, error_word=err)
         torch.cuda.synchronize()
         left = sc == base
-        whole = ~left & ((sc.double() - base.double() - want).abs() <= 1e-4 * want + 2.0 ** -18)
+        whole = ~left & ((sc.double() - base.double() - want).abs() <= 4e-4 * want + 2.0 ** -18)
         for k, x in enumerate((left, whole, ~left & ~whole)):
             count[k] += int(x.sum())
     return count, int((want > 0).sum())
