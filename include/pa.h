@@ -26,6 +26,11 @@
  *                        cached token received, added up per KV head
  *   pa_evict_tokens      keeps the tokens that matter, compacts the rest away
  *
+ * A cache held in 4 bits (no counterpart in the pages):
+ *   pa_cache_write_q4, pa_rotary_cache_write_q4  quantise and write new tokens
+ *   pa_decode_attention_q4  attention of the newest tokens over such a cache
+ *   pa_unpack_blocks_q4  its blocks in 16 bits, for the other kernels
+ *
  * Conventions for every entry point:
  *   - Every pointer named "device" is device memory owned by the caller; the
  *     library allocates nothing, keeps no state between calls and never
@@ -65,7 +70,8 @@ extern "C" {
 /* Same type as cudaStream_t (struct CUstream_st *), declared without CUDA headers. */
 typedef struct CUstream_st *pa_stream_t;
 
-typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2 } pa_dtype_t;
+/* PA_Q4: a 4-bit cache's blocks, for the calls that move whole blocks. */
+typedef enum { PA_F16 = 0, PA_BF16 = 1, PA_F32 = 2, PA_Q4 = 3 } pa_dtype_t;
 
 typedef enum {
     PA_OK = 0,
@@ -621,7 +627,8 @@ pa_status_t pa_copy_blocks(void *const *k_caches, void *const *v_caches, int num
  * block (whole blocks of num_kv_heads * block_size * head_dim elements).
  * block_size: a power of two in [PA_MIN_BLOCK_SIZE, PA_MAX_BLOCK_SIZE]
  * (others: PA_ERR_UNSUPPORTED).  pa_copy_blocks(...) is
- * pa_copy_blocks_ex(..., num_blocks, PA_BLOCK_SIZE, ...).
+ * pa_copy_blocks_ex(..., num_blocks, PA_BLOCK_SIZE, ...).  dtype PA_Q4: 4-bit
+ * pools (block_size 16 or more), whole blocks of their bytes.
  */
 pa_status_t pa_copy_blocks_ex(void *const *k_caches, void *const *v_caches, int num_layers,
                               const int64_t *block_pairs, int num_pairs, int num_blocks,
@@ -657,6 +664,7 @@ pa_status_t pa_copy_blocks_ex(void *const *k_caches, void *const *v_caches, int 
  * block_pairs   int64 [num_pairs][2] (src, dst), device or pinned host memory
  * block_size    a power of two in [PA_MIN_BLOCK_SIZE, PA_MAX_BLOCK_SIZE]
  * num_layers    1 .. PA_MAX_LAYERS
+ * dtype         PA_F16, PA_BF16, or PA_Q4 for 4-bit pools (block_size 16 or more)
  * Each dst must be distinct; src == dst is a real copy (two pools).  The
  * host memory must stay pinned until the work on `stream` has finished.
  * dev_error_word  device, may be NULL: PA_ERRBIT_BLOCK_OOB (pair skipped)
@@ -744,6 +752,150 @@ pa_status_t pa_evict_tokens(void *const *k_caches, void *const *v_caches, int nu
                             int block_size, int num_kv_heads, int head_dim, pa_dtype_t dtype,
                             void *workspace, size_t workspace_bytes,
                             unsigned int *dev_error_word, pa_stream_t stream);
+
+/*
+ * ---- A cache held in 4 bits -------------------------------------------------
+ *
+ * The K and V pools of a 4-bit cache are [num_blocks][num_kv_heads][block_size]
+ * [PA_Q4_ROW_BYTES(head_dim)] bytes, 16-byte aligned: 3.6 times the tokens of a
+ * 16-bit pool in the same memory.  A token's head is held in groups of 64
+ * channels.  With T the 16-bit type `dtype` of the keys and values, a group
+ * x_0 .. x_63 is held as
+ *     z = min x,   s = T((max x - z) / 15),   n_i = (x_i - z) / s,
+ * the difference and its fifteenth in fp32, s rounded to T, n_i rounded to the
+ * nearest whole number (ties to even) and cut to 0 .. 15 (0 where s is 0), and
+ * stands for s n_i + z.  z is exact, and an element is off by s / 2 and the
+ * rounding of s.  A group with an infinity or a NaN, or whose range does not
+ * fit fp32, stands for NaN in all its channels.
+ * Block tables, slots and lengths are those of 16-bit pools.  The layout inside a
+ * block is the library's own (its calls write and read it); a block is
+ * contiguous, and pa_copy_blocks_ex and pa_swap_blocks move blocks with dtype
+ * PA_Q4.  T is the caller's to keep: every call on a pool names the same dtype.
+ * block_size: a power of two from 16 to PA_MAX_BLOCK_SIZE.  No counterpart in the
+ * pages, whose caches are 16-bit.
+ */
+#define PA_Q4_GROUP 64
+#define PA_Q4_ROW_BYTES(head_dim) ((head_dim) / PA_Q4_GROUP * 36)
+
+/*
+ * pa_cache_write_q4 -- pa_cache_write_ex into a 4-bit cache: quantises each new
+ * token's key and value rows, group by group, and writes them into the slot
+ * named by slot_mapping.
+ *
+ * key, value    device; token t's [num_kv_heads][head_dim] at t * stride
+ *               (elements, a multiple of 8, at least a token's row), 16-byte
+ *               aligned bases
+ * k_cache, v_cache  device 4-bit pools, written in place
+ * slot_mapping  device int64 [num_tokens]; < 0 skips the token
+ * head_dim      64, 128 or 256; dtype PA_F16 or PA_BF16
+ * dev_error_word  device, may be NULL: PA_ERRBIT_SLOT_OOB (the token is skipped)
+ * Distinct tokens must name distinct slots.  Other slots' bytes are left as they
+ * were.
+ */
+pa_status_t pa_cache_write_q4(const void *key, int64_t key_stride, const void *value,
+                              int64_t value_stride, void *k_cache, void *v_cache,
+                              const int64_t *slot_mapping, int num_tokens, int num_blocks,
+                              int block_size, int num_kv_heads, int head_dim, pa_dtype_t dtype,
+                              unsigned int *dev_error_word, pa_stream_t stream);
+
+/*
+ * pa_rotary_cache_write_q4 -- pa_rotary_cache_write into a 4-bit cache: turns
+ * query and key as that call does, and quantises the turned key, rounded to
+ * dtype, and the value into the slot.  Arguments, limits and errors are those of
+ * pa_rotary_cache_write, with 4-bit pools.
+ */
+pa_status_t pa_rotary_cache_write_q4(
+    void *query_out, int64_t query_out_stride, const void *query, int64_t query_stride,
+    const void *key, int64_t key_stride, const void *value, int64_t value_stride,
+    const int64_t *positions, const pa_rotary_t *rotary, void *k_cache, void *v_cache,
+    const int64_t *slot_mapping, int num_tokens, int num_blocks, int block_size, int num_heads,
+    int num_kv_heads, int head_dim, pa_dtype_t dtype, unsigned int *dev_error_word,
+    pa_stream_t stream);
+
+/* Most query tokens of a sequence that pa_decode_attention_q4 takes. */
+#define PA_MAX_Q4_QUERY 16
+
+/*
+ * pa_decode_q4_workspace_size -- bytes of device workspace pa_decode_attention_q4
+ * needs for these sizes; 0 for invalid ones.  Host only.
+ */
+size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
+                                   int max_query_len, int max_context_len);
+
+/*
+ * pa_decode_attention_q4 -- attention of each sequence's newest token, or of its
+ * newest few, over a 4-bit cache.
+ *
+ * Defines: sequence s has n_s = query_start_loc[s+1] - query_start_loc[s] query
+ * tokens, rows query_start_loc[s] .. of `query`, those of its last n_s
+ * positions (a decode step's token; the tokens of a draft that is verified in
+ * one step), whose keys and values are in the cache.  Query token i is at position
+ * p = context_lens[s] - n_s + i, and for query head h, KV head h / G,
+ *     out[t][h] = sum_{j <= p} exp(x_j - max x) v_j / sum_{j <= p} exp(x_j - max x),
+ *     x_j = scale * <query[t][h], k_j>,
+ * with k_j and v_j what the cache's codes stand for, s n + z, unrounded.  fp32
+ * sums; the products' operands are exact, but for the weights, which are rounded
+ * in two parts to 2^-22.  A sequence without tokens (context_lens[s] = 0) gives
+ * zero rows.  Longer chunks go through pa_unpack_blocks_q4 and
+ * pa_prefill_attention.
+ *
+ * out           device [num_tokens][num_heads][head_dim], out_dtype = PA_F32 or
+ *               dtype (round to nearest even)
+ * query         device [num_tokens][num_heads][head_dim], dtype
+ * k_cache, v_cache  device 4-bit pools
+ * block_tables  device int32 [num_seqs][max_blocks_per_seq]; entries past a
+ *               sequence's blocks are never read
+ * query_start_loc  device int32 [num_seqs + 1], non-decreasing from 0 to
+ *               num_tokens; or NULL: one token a sequence (num_tokens =
+ *               num_seqs, max_query_len = 1)
+ * context_lens  device int32 [num_seqs], 0 or n_s <= context_lens[s] <=
+ *               max_context_len
+ * max_query_len host-known bound on n_s, 1 .. PA_MAX_Q4_QUERY (PA_ERR_UNSUPPORTED
+ *               beyond); max_context_len host-known bound on context_lens,
+ *               <= block_size * max_blocks_per_seq
+ * num_heads % num_kv_heads == 0; head_dim 64, 128 or 256; dtype PA_F16 or PA_BF16
+ * workspace     device, >= pa_decode_q4_workspace_size(...) bytes, 256-byte
+ *               aligned; needs no initialisation; calls in flight at once must
+ *               not share one, calls on one stream may, whatever their sizes
+ * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence
+ *               whose lengths break the rules (its rows are zeroed),
+ *               PA_ERRBIT_BLOCK_OOB (the block's tokens are skipped)
+ * Results do not depend on the block size or on the order in which work
+ * finishes.  Enqueues one kernel, and a merge kernel where max_context_len is
+ * above 256.
+ */
+pa_status_t pa_decode_attention_q4(
+    void *out, pa_dtype_t out_dtype, const void *query, const void *k_cache, const void *v_cache,
+    const int32_t *block_tables, int max_blocks_per_seq, const int32_t *query_start_loc,
+    const int32_t *context_lens, int max_query_len, int max_context_len, int num_seqs,
+    int num_tokens, int num_heads, int num_kv_heads, int head_dim, int num_blocks, int block_size,
+    float scale, pa_dtype_t dtype, void *workspace, size_t workspace_bytes,
+    unsigned int *dev_error_word, pa_stream_t stream);
+
+/*
+ * pa_unpack_blocks_q4 -- blocks of a 4-bit cache as blocks of a 16-bit one, every
+ * pair and every layer in one launch: a sequence's cached tokens for the kernels
+ * that read 16-bit pools (pa_prefill_attention of its next chunk).
+ *
+ * Defines: for every layer and pair i with (src, dst) = (block_pairs[2i],
+ * block_pairs[2i+1]): every element of 16-bit block dst is s n + z of 4-bit block
+ * src's (one fp32 rounding, then one to dtype), K and V.  Slots that were never
+ * written give whatever their bytes stand for.
+ *
+ * dst_k_caches, dst_v_caches  HOST arrays of num_layers device pools
+ *               [num_dst_blocks][num_kv_heads][block_size][head_dim], dtype
+ * src_k_caches, src_v_caches  HOST arrays of num_layers device 4-bit pools of
+ *               num_src_blocks blocks
+ * block_pairs   device int64 [num_pairs][2]; each dst distinct
+ * num_layers    1 .. PA_MAX_LAYERS
+ * dev_error_word  device, may be NULL: PA_ERRBIT_BLOCK_OOB (pair skipped)
+ */
+pa_status_t pa_unpack_blocks_q4(void *const *dst_k_caches, void *const *dst_v_caches,
+                                const void *const *src_k_caches, const void *const *src_v_caches,
+                                int num_layers, const int64_t *block_pairs, int num_pairs,
+                                int num_dst_blocks, int num_src_blocks, int block_size,
+                                int num_kv_heads, int head_dim, pa_dtype_t dtype,
+                                unsigned int *dev_error_word, pa_stream_t stream);
 
 /* Static, human-readable name of a status. */
 const char *pa_status_string(pa_status_t status);

@@ -26,6 +26,16 @@ A cache that stays within a budget:
     evict_tokens(k_caches, v_caches, scores, block_tables, context_lens, keep_lens,
                  max_context_len, max_keep_len, num_sink, num_recent, ...)
 
+A cache held in 4 bits, in uint8 pools of the shape q4_pool_shape gives (which
+copy_blocks and swap_blocks take too):
+
+    cache_write_q4(key, value, k_cache, v_cache, slot_mapping)
+    rotary_cache_write_q4(query, key, value, positions, rotary, k_cache, v_cache,
+                          slot_mapping, ...)
+    decode_attention_q4(query, k_cache, v_cache, block_tables, context_lens,
+                        max_context_len, scale, query_start_loc=None, ...)
+    unpack_blocks_q4(dst_k_caches, dst_v_caches, src_k_caches, src_v_caches, block_pairs)
+
 Pools are [num_blocks][num_kv_heads][block_size][head_dim]; the block size
 is read from their third dimension: 16 goes to the plain entry points, other
 supported sizes (powers of two from 8 to 256) to the ``*_ex`` ones.
@@ -55,13 +65,17 @@ __all__ = ["cache_write", "decode_attention", "decode_attention_contiguous",
            "MAX_LAYERS", "BLOCK_SIZES", "swap_blocks", "prefill_attention",
            "Rotary", "rotary_cache_write", "decode_attention_scored",
            "decode_scored_workspace_size", "prefill_scores", "prefill_scores_workspace_size",
-           "evict_tokens", "evict_workspace_size", "MAX_ROTARY_PAIRS"]
+           "evict_tokens", "evict_workspace_size", "MAX_ROTARY_PAIRS",
+           "cache_write_q4", "rotary_cache_write_q4", "decode_attention_q4",
+           "decode_q4_workspace_size", "unpack_blocks_q4", "q4_pool_shape", "MAX_Q4_QUERY"]
 
 BLOCK_SIZE = 16
 BLOCK_SIZES = (8, 16, 32, 64, 128, 256)
 MAX_LAYERS = 128
 MAX_ROTARY_PAIRS = 128
-PA_F16, PA_BF16, PA_F32 = 0, 1, 2
+MAX_Q4_QUERY = 16
+PA_F16, PA_BF16, PA_F32, PA_Q4 = 0, 1, 2, 3
+_Q4_GROUP, _Q4_GROUP_BYTES = 64, 36  # channels that share a scale; their bytes in a token
 ERRBIT_BLOCK_OOB, ERRBIT_SLOT_OOB, ERRBIT_CONTEXT_LEN, ERRBIT_TIMEOUT = 1, 2, 4, 8
 ERRBIT_INTERNAL = 16  # PA_DEBUG builds only
 
@@ -79,6 +93,13 @@ _SIGNATURES = {
     "pa_rotary_init": (_I, [_P, _P, _P, _I, _I, ctypes.c_float]),
     "pa_rotary_cache_write": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
                                    _I, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "pa_cache_write_q4": (_I, [_P, _I64, _P, _I64, _P, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "pa_rotary_cache_write_q4": (_I, [_P, _I64, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _P,
+                                      _I, _I, _I, _I, _I, _I, _I, _P, _P]),
+    "pa_decode_q4_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
+    "pa_decode_attention_q4": (_I, [_P, _I, _P, _P, _P, _P, _I, _P, _P, _I, _I, _I, _I, _I, _I,
+                                    _I, _I, _I, ctypes.c_float, _I, _P, ctypes.c_size_t, _P, _P]),
+    "pa_unpack_blocks_q4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _P, _P]),
     "pa_decode_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "pa_decode_partition_tokens": (_I, [_I, _I, _I]),
     "pa_decode_kernel_launches": (_I, [_I, _I, _I, _I, _I]),
@@ -497,10 +518,17 @@ def decode_attention_scored(query, k_cache, v_cache, block_tables, context_lens,
     return out
 
 
+def _move_dims(row, dtype):
+    """(head_dim, dtype code) of pools whose rows have `row` elements (4-bit ones: bytes)."""
+    if dtype == _torch().uint8:
+        return _q4_head_dim(row), PA_Q4
+    return row, _dtype_code(dtype)
+
+
 def copy_blocks(k_caches: Sequence, v_caches: Sequence, block_pairs, error_word=None,
                 stream=None) -> None:
     """For every layer: pools[dst] = pools[src] for each (src, dst) row of
-    block_pairs (int64 [P][2], on the device)."""
+    block_pairs (int64 [P][2], on the device).  16-bit pools or 4-bit ones."""
     torch = _torch()
     if len(k_caches) != len(v_caches) or not k_caches:
         raise ValueError("need the same, non-zero number of K and V pools")
@@ -510,14 +538,14 @@ def copy_blocks(k_caches: Sequence, v_caches: Sequence, block_pairs, error_word=
     for c in list(k_caches) + list(v_caches):
         if c.shape != k_caches[0].shape or c.dtype != k_caches[0].dtype:
             raise ValueError("all pools must have one shape and dtype")
+    d, code = _move_dims(d, k_caches[0].dtype)
     L = len(k_caches)
     kp = (ctypes.c_void_p * L)(*[_dev(c, "k_caches") for c in k_caches])
     vp = (ctypes.c_void_p * L)(*[_dev(c, "v_caches") for c in v_caches])
     npairs = block_pairs.shape[0] if block_pairs.numel() else 0
     head = (ctypes.cast(kp, ctypes.c_void_p), ctypes.cast(vp, ctypes.c_void_p), L,
             _dev(block_pairs, "block_pairs") if npairs else None, npairs, nb)
-    tail = (hkv, d, _dtype_code(k_caches[0].dtype), _opt_ptr(error_word, "error_word"),
-            _stream_ptr(stream, k_caches[0]))
+    tail = (hkv, d, code, _opt_ptr(error_word, "error_word"), _stream_ptr(stream, k_caches[0]))
     lib = load_library()
     if bs == BLOCK_SIZE:
         _check(lib.pa_copy_blocks(*head, *tail), "pa_copy_blocks")
@@ -538,8 +566,8 @@ def swap_blocks(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_caches: Se
                 src_v_caches: Sequence, block_pairs, error_word=None, stream=None) -> None:
     """For every layer: dst[pair dst] = src[pair src] for each (src, dst) row
     of block_pairs (int64 [P][2], on the device).  Pools are
-    [num_blocks][Hkv][block_size][D]; either side may be device memory or
-    pinned host memory (the CPU swap space)."""
+    [num_blocks][Hkv][block_size][D], or 4-bit ones; either side may be device
+    memory or pinned host memory (the CPU swap space)."""
     torch = _torch()
     L = len(dst_k_caches)
     if not (L == len(dst_v_caches) == len(src_k_caches) == len(src_v_caches)) or not L:
@@ -555,6 +583,7 @@ def swap_blocks(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_caches: Se
     for c in list(src_k_caches) + list(src_v_caches):
         if tuple(c.shape) != (ns, hkv, bs, d) or c.dtype != dt:
             raise ValueError("source pools must match the destination's block shape and dtype")
+    d, code = _move_dims(d, dt)
     arr = lambda xs, n: ctypes.cast((ctypes.c_void_p * L)(*[_pool_ptr(x, n) for x in xs]),
                                     ctypes.c_void_p)
     npairs = block_pairs.shape[0] if block_pairs.numel() else 0
@@ -563,7 +592,7 @@ def swap_blocks(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_caches: Se
     st = load_library().pa_swap_blocks(
         arr(dst_k_caches, "dst_k_caches"), arr(dst_v_caches, "dst_v_caches"),
         arr(src_k_caches, "src_k_caches"), arr(src_v_caches, "src_v_caches"), L,
-        block_pairs.data_ptr() if npairs else None, npairs, nd, ns, bs, hkv, d, _dtype_code(dt),
+        block_pairs.data_ptr() if npairs else None, npairs, nd, ns, bs, hkv, d, code,
         _opt_ptr(error_word, "error_word"), _stream_ptr(stream, on_gpu))
     _check(st, "pa_swap_blocks")
 
@@ -761,3 +790,172 @@ def evict_tokens(k_caches: Sequence, v_caches: Sequence, scores: Sequence, block
         _stream_ptr(stream, k_caches[0]))
     _check(st, "pa_evict_tokens")
     return new_lens
+
+
+def q4_pool_shape(num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int) -> tuple:
+    """Shape of a 4-bit pool (torch.uint8): a scale, a least value and 64 halves of a byte for
+    every 64 channels of a token.  Its bytes are written by cache_write_q4 and
+    rotary_cache_write_q4 and read by decode_attention_q4 and unpack_blocks_q4; the layout
+    inside a block is the library's own."""
+    if head_dim not in (64, 128, 256):
+        raise ValueError("head_dim must be 64, 128 or 256")
+    return (num_blocks, num_kv_heads, block_size, head_dim // _Q4_GROUP * _Q4_GROUP_BYTES)
+
+
+def _q4_head_dim(row_bytes) -> int:
+    if row_bytes % _Q4_GROUP_BYTES:
+        raise ValueError("a 4-bit pool is uint8 of q4_pool_shape's shape")
+    return row_bytes // _Q4_GROUP_BYTES * _Q4_GROUP
+
+
+def _q4_pools(k_cache, v_cache, heads, dim):
+    """(num_blocks, block_size) of a 4-bit pool pair for `heads` KV heads of `dim`."""
+    u8 = _torch().uint8
+    if k_cache.dtype != u8 or v_cache.dtype != u8:
+        raise TypeError("4-bit pools must be uint8")
+    nb, hkv, bs, row = k_cache.shape
+    if v_cache.shape != k_cache.shape or hkv != heads or row * _Q4_GROUP != dim * _Q4_GROUP_BYTES:
+        raise ValueError("shape mismatch between the rows and the 4-bit pools")
+    return nb, bs
+
+
+def cache_write_q4(key, value, k_cache, v_cache, slot_mapping, error_word=None,
+                   stream=None) -> None:
+    """Quantise key[t] / value[t] ([T][Hkv][D], token strides free) to 4 bits and write them into
+    slot slot_mapping[t] (int64; < 0 skips) of 4-bit pools (q4_pool_shape)."""
+    torch = _torch()
+    T, hkv, d = key.shape
+    dt = key.dtype
+    if value.shape != (T, hkv, d) or value.dtype != dt:
+        raise ValueError("key and value must have one shape and dtype")
+    nb, bs = _q4_pools(k_cache, v_cache, hkv, d)
+    if slot_mapping.dtype != torch.int64:
+        raise TypeError("slot_mapping must be int64")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    st = load_library().pa_cache_write_q4(
+        *_rows(key, "key", hkv * d), *_rows(value, "value", hkv * d), _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"), T, nb, bs, hkv, d,
+        _dtype_code(dt), _opt_ptr(error_word, "error_word"), _stream_ptr(stream, key))
+    _check(st, "pa_cache_write_q4")
+
+
+def rotary_cache_write_q4(query, key, value, positions, rotary: Rotary, k_cache, v_cache,
+                          slot_mapping, query_out=None, error_word=None, stream=None):
+    """rotary_cache_write into 4-bit pools (q4_pool_shape): the turned key, rounded to its
+    dtype, and the value are quantised.  Returns the turned query: ``query_out``,
+    ``query`` itself for an update in place, or a new dense tensor."""
+    torch = _torch()
+    T, H, d = query.shape
+    hkv, dt = key.shape[1], query.dtype
+    new = (T, hkv, d)
+    if key.shape != new or value.shape != new:
+        raise ValueError("shape mismatch between query, key and value")
+    if not dt == key.dtype == value.dtype:
+        raise ValueError("query, key and value must have one dtype")
+    nb, bs = _q4_pools(k_cache, v_cache, hkv, d)
+    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
+        raise TypeError("slot_mapping and positions must be int64")
+    if slot_mapping.shape != (T,):
+        raise ValueError("slot_mapping must be [T]")
+    if positions.shape[-1:] != (T,) or positions.dim() > 2 or \
+            (positions.shape[0] if positions.dim() == 2 else 1) < rotary.num_axes:
+        raise ValueError("positions must be [axes][T] with an axis for each the frequencies name")
+    if query_out is None:
+        query_out = _empty(stream, (T, H, d), dt, query.device, returned=True)
+    elif query_out is not query and (query_out.shape != (T, H, d) or query_out.dtype != dt):
+        raise ValueError("query_out must match the query")
+    st = load_library().pa_rotary_cache_write_q4(
+        *_rows(query_out, "query_out", H * d), *_rows(query, "query", H * d),
+        *_rows(key, "key", hkv * d), *_rows(value, "value", hkv * d),
+        _dev(positions, "positions"), rotary._ptr,
+        _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"),
+        T, nb, bs, H, hkv, d, _dtype_code(dt), _opt_ptr(error_word, "error_word"),
+        _stream_ptr(stream, query))
+    _check(st, "pa_rotary_cache_write_q4")
+    return query_out
+
+
+def decode_q4_workspace_size(num_seqs: int, num_heads: int, num_kv_heads: int, head_dim: int,
+                             max_query_len: int, max_context_len: int) -> int:
+    return int(load_library().pa_decode_q4_workspace_size(
+        num_seqs, num_heads, num_kv_heads, head_dim, max_query_len, max_context_len))
+
+
+def decode_attention_q4(query, k_cache, v_cache, block_tables, context_lens,
+                        max_context_len: int, scale: float, query_start_loc=None,
+                        max_query_len: int = 1, out=None, out_dtype=None, workspace=None,
+                        error_word=None, stream=None):
+    """Attention over 4-bit pools (q4_pool_shape): of each sequence's newest token
+    (query [S][H][D]), or with query_start_loc (int32 [S+1]) of its newest few
+    (query [T][H][D], at most max_query_len <= MAX_Q4_QUERY a sequence, each seeing the
+    tokens up to its own).  Returns ``out`` like the query's shape (fp32 unless
+    ``out_dtype`` / ``out`` says the input dtype).  ``workspace`` (uint8, >=
+    decode_q4_workspace_size bytes) is allocated here when not given."""
+    torch = _torch()
+    T, H, D = query.shape
+    hkv = k_cache.shape[1]
+    nb, bs = _q4_pools(k_cache, v_cache, hkv, D)
+    i32 = torch.int32
+    if block_tables.dtype != i32 or context_lens.dtype != i32 or (
+            query_start_loc is not None and query_start_loc.dtype != i32):
+        raise TypeError("block_tables, context_lens and query_start_loc must be int32")
+    S = context_lens.shape[0]
+    tables = block_tables.shape
+    if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,):
+        raise ValueError("block_tables must be [S][max_blocks], context_lens [S]")
+    if query_start_loc is None:
+        if T != S or max_query_len != 1:
+            raise ValueError("without query_start_loc there is one query token a sequence")
+    elif query_start_loc.shape != (S + 1,):
+        raise ValueError("query_start_loc must be [S+1]")
+    if out is None:
+        out = _empty(stream, (T, H, D), out_dtype or torch.float32, query.device, returned=True)
+    elif out.shape != (T, H, D):
+        raise ValueError("out must match the query")
+    if workspace is None:
+        nbytes = decode_q4_workspace_size(S, H, hkv, D, int(max_query_len), int(max_context_len))
+        workspace = _workspace(stream, nbytes, query.device)
+    st = load_library().pa_decode_attention_q4(
+        _dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"), _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"), tables[1],
+        _opt_ptr(query_start_loc, "query_start_loc"), _dev(context_lens, "context_lens"),
+        int(max_query_len), int(max_context_len), S, T, H, hkv, D, nb, bs, float(scale),
+        _dtype_code(query.dtype), _dev(workspace, "workspace"),
+        workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
+        _stream_ptr(stream, query))
+    _check(st, "pa_decode_attention_q4")
+    return out
+
+
+def unpack_blocks_q4(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_caches: Sequence,
+                     src_v_caches: Sequence, block_pairs, error_word=None, stream=None) -> None:
+    """For every layer: 16-bit pool block dst = what 4-bit pool block src stands for, for each
+    (src, dst) row of block_pairs (int64 [P][2], on the device).  16-bit pools are
+    [num_blocks][Hkv][block_size][D] of the dtype the tokens were written with, 4-bit ones of
+    q4_pool_shape's shape."""
+    torch = _torch()
+    L = len(dst_k_caches)
+    if not (L == len(dst_v_caches) == len(src_k_caches) == len(src_v_caches)) or not L:
+        raise ValueError("need the same, non-zero number of pools on each side")
+    if block_pairs.dtype != torch.int64:
+        raise TypeError("block_pairs must be int64")
+    dst, dt = dst_k_caches[0].shape, dst_k_caches[0].dtype
+    nd, hkv, bs, d = dst
+    src = src_k_caches[0].shape
+    ns, sbs = _q4_pools(src_k_caches[0], src_v_caches[0], hkv, d)
+    if sbs != bs:
+        raise ValueError("pools must have one block size")
+    npairs = block_pairs.shape[0] if block_pairs.numel() else 0
+    # the layers' pointers, one array after the other
+    ptrs = _layer_ptrs(dst_k_caches, "dst_k_caches", L, dst, dt)
+    ptrs += _layer_ptrs(dst_v_caches, "dst_v_caches", L, dst, dt)
+    ptrs += _layer_ptrs(src_k_caches, "src_k_caches", L, src, torch.uint8)
+    ptrs += _layer_ptrs(src_v_caches, "src_v_caches", L, src, torch.uint8)
+    arrays = array.array("Q", ptrs)
+    base = arrays.buffer_info()[0]
+    st = load_library().pa_unpack_blocks_q4(
+        base, base + 8 * L, base + 16 * L, base + 24 * L, L,
+        _dev(block_pairs, "block_pairs") if npairs else None, npairs, nd, ns, bs, hkv, d,
+        _dtype_code(dt), _opt_ptr(error_word, "error_word"), _stream_ptr(stream, dst_k_caches[0]))
+    _check(st, "pa_unpack_blocks_q4")

@@ -111,9 +111,10 @@ bool head_dim_ok(int d) { return d == 64 || d == 128 || d == 256; }
 // One launch of copy_blocks_kernel over every pair and layer.
 pa_status_t launch_move(const LayerPools &pools, int num_layers, const int64_t *block_pairs,
                         int num_pairs, int num_src_blocks, int num_dst_blocks, int same_pool,
-                        int block_size, int num_kv_heads, int head_dim,
+                        int block_size, int num_kv_heads, int head_dim, pa_dtype_t dtype,
                         unsigned int *dev_error_word, pa_stream_t stream) {
-    const long long chunks_per_block = (long long)num_kv_heads * block_size * head_dim * 2 / 16;
+    const int row_bytes = dtype == PA_Q4 ? PA_Q4_ROW_BYTES(head_dim) : head_dim * 2;
+    const long long chunks_per_block = (long long)num_kv_heads * block_size * row_bytes / 16;
     // about 32 KiB per CTA: enough bytes in flight per CTA, enough CTAs per copy
     const long long chunks_per_cta = 2048;
     const long long splits = (chunks_per_block + chunks_per_cta - 1) / chunks_per_cta;
@@ -139,6 +140,14 @@ const void *device_view(const void *p, int dev) {
     if (a.type == cudaMemoryTypeManaged) return p;
     if (a.type == cudaMemoryTypeHost) return a.devicePointer;
     return nullptr;
+}
+
+// Whether blocks of this dtype and size can be moved: 16-bit ones, and 4-bit ones
+// in whole tiles of 16 tokens.
+pa_status_t movable(pa_dtype_t dtype, int block_size) {
+    if (dtype == PA_F16 || dtype == PA_BF16) return PA_OK;
+    if (dtype != PA_Q4) return PA_ERR_INVALID_ARG;
+    return block_size >= 16 ? PA_OK : PA_ERR_UNSUPPORTED;
 }
 
 // log2 of a supported block size, or -1
@@ -197,7 +206,7 @@ extern "C" pa_status_t pa_copy_blocks_ex(void *const *k_caches, void *const *v_c
         return PA_ERR_INVALID_ARG;
     if (block_shift_of(block_size) < 0) return PA_ERR_UNSUPPORTED;
     if (num_layers > PA_MAX_LAYERS) return PA_ERR_UNSUPPORTED;
-    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+    if (const pa_status_t st = movable(dtype, block_size)) return st;
     if (!head_dim_ok(head_dim)) return PA_ERR_UNSUPPORTED;
     if (num_pairs == 0) return PA_OK;
     if (!k_caches || !v_caches || !block_pairs) return PA_ERR_INVALID_ARG;
@@ -209,7 +218,7 @@ extern "C" pa_status_t pa_copy_blocks_ex(void *const *k_caches, void *const *v_c
         pools.src_v[l] = pools.dst_v[l] = (uint4 *)v_caches[l];
     }
     return launch_move(pools, num_layers, block_pairs, num_pairs, num_blocks, num_blocks, 1,
-                       block_size, num_kv_heads, head_dim, dev_error_word, stream);
+                       block_size, num_kv_heads, head_dim, dtype, dev_error_word, stream);
 }
 
 extern "C" pa_status_t pa_copy_blocks(void *const *k_caches, void *const *v_caches,
@@ -236,7 +245,7 @@ extern "C" pa_status_t pa_swap_blocks(void *const *dst_k_caches, void *const *ds
         return PA_ERR_INVALID_ARG;
     if (num_layers > PA_MAX_LAYERS) return PA_ERR_UNSUPPORTED;
     if (block_shift_of(block_size) < 0) return PA_ERR_UNSUPPORTED;
-    if (dtype != PA_F16 && dtype != PA_BF16) return PA_ERR_INVALID_ARG;
+    if (const pa_status_t st = movable(dtype, block_size)) return st;
     if (!head_dim_ok(head_dim)) return PA_ERR_UNSUPPORTED;
     if (num_pairs == 0) return PA_OK;
     if (!dst_k_caches || !dst_v_caches || !src_k_caches || !src_v_caches || !block_pairs)
@@ -262,8 +271,8 @@ extern "C" pa_status_t pa_swap_blocks(void *const *dst_k_caches, void *const *ds
         pools.dst_k[l] = (uint4 *)dk;
         pools.dst_v[l] = (uint4 *)dv;
     }
-    return launch_move(pools, num_layers, pairs, num_pairs, num_src_blocks, num_dst_blocks, 0, block_size, num_kv_heads, head_dim, dev_error_word,
-                       stream);
+    return launch_move(pools, num_layers, pairs, num_pairs, num_src_blocks, num_dst_blocks, 0,
+                       block_size, num_kv_heads, head_dim, dtype, dev_error_word, stream);
 }
 
 extern "C" const char *pa_status_string(pa_status_t s) {
