@@ -54,7 +54,9 @@ constexpr int kQ4Warps = 4;  // of a CTA
 constexpr int kQ4Threads = 32 * kQ4Warps;
 constexpr int kQ4Sms = 152;  // that the workers are sized for (right for any number)
 constexpr float kQ4NoMax = -1e30f;   // m before any token: below every logit that counts
-constexpr float kQ4TopWeight = 32768.0f;
+// A weight (2^6 where the maximum was last taken) and a scale (below 2^5 then) beyond
+// which both are taken anew: their product stays below fp16's 2^16.
+constexpr float kQ4TopP = 1024.f, kQ4TopS = 32.f;
 
 struct Q4DecodeParams {
     void *out;
@@ -119,6 +121,16 @@ __device__ __forceinline__ uint32_t q4_transpose(uint32_t a) {
     return d;
 }
 
+__device__ __forceinline__ uint32_t q4_mul2(uint32_t a, uint32_t b) {
+    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+__device__ __forceinline__ uint32_t q4_fma2(uint32_t a, uint32_t b, uint32_t c) {
+    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
+                              *reinterpret_cast<const __half2 *>(&c));
+    return *reinterpret_cast<const uint32_t *>(&r);
+}
+
 __device__ __forceinline__ void q4_copy16(uint32_t dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -141,22 +153,32 @@ struct Q4Shape {
     static constexpr size_t kSmem = (size_t)kQ4Warps * kStages * kStageBytes;
 };
 
-// Where a warp is in the batch's chunks.
+// Where a warp is in the batch's chunks: sequence, KV head, tile of its query rows,
+// chunk, from the slowest to the fastest (a head's tiles read the same chunks: the
+// later ones find them in L2).
 struct Q4Cursor {
-    int s, unit, chunk;  // sequence, (KV head, tile of rows), chunk
-    int chunks, units;   // of the sequence
+    int s, head, tile, chunk;
+    Q4Seq q;
 };
 
-// Moves to the next chunk; past the last sequence s = num_seqs.
+// The next sequence with work; past the last one s = num_seqs.
 template <int RT>
-__device__ __forceinline__ bool q4_next_seq(const Q4DecodeParams &P, Q4Cursor &c) {
-    do {
-        if (++c.s >= P.num_seqs) return false;
-        const Q4Seq q = q4_seq<RT>(P, c.s);
-        c.chunks = q.chunks;
-        c.units = q.tiles * P.num_kv_heads;
-    } while (c.chunks == 0);
-    c.unit = c.chunk = 0;
+__device__ __forceinline__ void q4_next_seq(const Q4DecodeParams &P, Q4Cursor &c) {
+    c.head = c.tile = c.chunk = 0;
+    while (++c.s < P.num_seqs) {
+        c.q = q4_seq<RT>(P, c.s);
+        if (c.q.chunks) break;
+    }
+}
+
+// The next (sequence, head, tile); true where that is another sequence's.
+template <int RT>
+__device__ __forceinline__ bool q4_next_unit(const Q4DecodeParams &P, Q4Cursor &c) {
+    c.chunk = 0;
+    if (++c.tile < c.q.tiles) return false;
+    c.tile = 0;
+    if (++c.head < P.num_kv_heads) return false;
+    q4_next_seq<RT>(P, c);
     return true;
 }
 
@@ -168,7 +190,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
     extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ long long s_base[kQ4Threads];  // chunks of the batch before a thread's sequences
     __shared__ long long s_warp[kQ4Warps];
-    __shared__ int4 s_meta[kQ4Warps][S::kStages];  // sequence, unit, chunk, block outside the pool
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
@@ -205,8 +226,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
 
     if (start < end) {
         // the sequence that holds `start`
-        Q4Cursor at;
-        long long pos = start;  // of `at` in the batch's chunks
         int lo = 0;
 #pragma unroll
         for (int i = 0; i < kQ4Threads; i += 32)
@@ -214,66 +233,84 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
         lo -= 1;  // the last thread whose sequences begin at or before it; where they are
                   // empty, those behind them have it
         long long off = start - s_base[lo];
+        Q4Cursor at;  // the next chunk to ask for
         at.s = lo * each - 1;
-        while (q4_next_seq<RT>(P, at)) {
-            const long long n = (long long)at.chunks * at.units;
+        for (;;) {
+            q4_next_seq<RT>(P, at);
+            if (at.s >= P.num_seqs) break;
+            const long long n = (long long)at.q.chunks * at.q.tiles * P.num_kv_heads;
             if (off < n) break;
             off -= n;
         }
-        at.unit = (int)off / at.chunks;
-        at.chunk = (int)off - at.unit * at.chunks;
-        if (P.whole && at.chunk > 0) {  // that unit is the worker's in whose range it begins
-            pos += at.chunks - at.chunk;
-            at.chunk = 0;
-            if (++at.unit == at.units) q4_next_seq<RT>(P, at);
+        const int count = (int)(end - start);  // chunks of the range
+        int pos = 0;                           // of `at` in it
+        if (at.s < P.num_seqs) {
+            const int unit = (int)off / at.q.chunks;
+            at.chunk = (int)off - unit * at.q.chunks;
+            at.head = unit / at.q.tiles;
+            at.tile = unit - at.head * at.q.tiles;
+            if (P.whole && at.chunk > 0) {  // that unit is the worker's in whose range it begins
+                pos = at.q.chunks - at.chunk;
+                q4_next_unit<RT>(P, at);
+            }
         }
+        Q4Cursor cu = at;  // the chunk at hand
         uint8_t *ring = s_ring + (size_t)warp * S::kStages * S::kStageBytes;
         const uint32_t ring_u32 = smem_u32(ring);
 
         // ---- asking for chunks ----
-        int ids = 0, ids_s = -1, ids_c = 0;  // lane's block id of chunk ids_c + lane of sequence ids_s
-        auto ask = [&](int slot) {
-            if (at.s < P.num_seqs && (P.whole ? pos - at.chunk : pos) < end) {
-                if (at.s != ids_s || (at.chunk & ~31) != ids_c) {
-                    ids_s = at.s;
-                    ids_c = at.chunk & ~31;
-                    ids = ids_c + lane < at.chunks
-                              ? P.block_tables[(size_t)at.s * P.max_blocks_per_seq +
-                                               ((ids_c + lane) >> P.sub_shift)]
-                              : 0;
+        // A stage is the K tile and the V tile, 16 bytes a lane and step; one step has the end
+        // of the one and the beginning of the other.
+        constexpr int kPieces = S::kTileBytes / 16, kMixed = kPieces / 32 * 32;
+        const uint8_t *k_lane = P.k_cache + lane * 16;
+        const uint8_t *v_lane = P.v_cache + lane * 16 - S::kTileBytes;
+        const uint8_t *m_lane = kMixed + lane < kPieces ? k_lane : v_lane;
+        const uint32_t dst_lane = ring_u32 + lane * 16;
+        const uint32_t block_bytes = (uint32_t)(P.num_kv_heads << P.sub_shift) * S::kTileBytes;
+        const int sub_mask = (1 << P.sub_shift) - 1;
+        int asked = 0, used = 0;
+        uint32_t bad = 0;       // bit i & 31: the i-th chunk's block is outside the pool
+        int ids = 0;            // the lane's block id, of chunk (at.chunk & ~31) + lane
+        bool load_ids = true;
+        uint32_t head_off = (uint32_t)(at.head << P.sub_shift) * S::kTileBytes;
+        auto ask = [&](uint32_t slot) {
+            if (at.s < P.num_seqs && (pos < count || (P.whole && at.chunk > 0))) {
+                if (load_ids) {
+                    const int c = (at.chunk & ~31) + lane;
+                    ids = c < at.q.chunks ? P.block_tables[(size_t)at.s * P.max_blocks_per_seq +
+                                                           (c >> P.sub_shift)]
+                                          : 0;
+                    load_ids = false;
                 }
                 const int id = __shfl_sync(0xffffffffu, ids, at.chunk & 31);
-                const bool bad = id < 0 || id >= P.num_blocks;
-                if (bad) {
-                    if (lane == 0 && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
-                } else {
-                    const int head = at.unit % P.num_kv_heads;
-                    const size_t tile = (((size_t)id * P.num_kv_heads + head) << P.sub_shift) +
-                                        (at.chunk & ((1 << P.sub_shift) - 1));
-                    const uint8_t *k = P.k_cache + tile * S::kTileBytes;
-                    const uint8_t *v = P.v_cache + tile * S::kTileBytes;
-                    const uint32_t dst = ring_u32 + slot * S::kStageBytes;
-                    constexpr int kPieces = S::kTileBytes / 16;
+                if ((unsigned)id < (unsigned)P.num_blocks) {
+                    const size_t o = (size_t)(uint32_t)id * block_bytes +
+                                     (head_off + (uint32_t)(at.chunk & sub_mask) * S::kTileBytes);
 #pragma unroll
                     for (int i = 0; i < 2 * kPieces; i += 32) {
-                        const int p = i + lane;
-                        if (i + 32 <= 2 * kPieces || p < 2 * kPieces)
-                            q4_copy16(dst + p * 16, p < kPieces ? k + p * 16 : v + (p - kPieces) * 16);
+                        const uint8_t *src = i < kMixed ? k_lane : i == kMixed ? m_lane : v_lane;
+                        if (i + 32 <= 2 * kPieces || i + lane < 2 * kPieces)
+                            q4_copy16(dst_lane + slot + i * 16, src + o + i * 16);
                     }
+                } else {
+                    bad |= 1u << (asked & 31);
+                    if (lane == 0 && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
                 }
-                if (lane == 0) s_meta[warp][slot] = make_int4(at.s, at.unit, at.chunk, bad);
                 ++pos;
-                if (++at.chunk == at.chunks) {
-                    at.chunk = 0;
-                    if (++at.unit == at.units) q4_next_seq<RT>(P, at);
+                ++asked;
+                if (++at.chunk == at.q.chunks) {
+                    // (a table of at most 32 chunks is all in the lanes, for every head)
+                    load_ids = at.q.chunks > 32;
+                    if (q4_next_unit<RT>(P, at)) load_ids = true;
+                    head_off = (uint32_t)(at.head << P.sub_shift) * S::kTileBytes;
+                } else if ((at.chunk & 31) == 0) {
+                    load_ids = true;
                 }
-            } else if (lane == 0) {
-                s_meta[warp][slot] = make_int4(-1, 0, 0, 0);
             }
             q4_copy_commit();
         };
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) ask(i);
+        for (int i = 0; i < S::kStages - 1; ++i) ask(i * S::kStageBytes);
 
         // ---- the unit at hand ----
         float O[NT][C][4][4];           // [rows of 16 channels: cell, nibble j][fragment]
@@ -282,21 +319,14 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
         float c1[NT][2], qz[NT][C][2];
         int lim[NT][2], lim_min = 0;    // tokens a column sees; the fewest of any
         float vs = 0.f;                 // power of two on the weights times scales
-        int unit_s = -1, unit_u = -1, first_chunk = 0, len = 0, unit_chunks = 0, q0 = 0, rows = 0,
-            row0 = 0, head = 0, last_chunk = 0;
+        int first_chunk = 0, rows = 0, row0 = 0;
+        bool fresh = true;              // the chunk at hand begins a unit, or the range
 
-        auto begin_unit = [&](const int4 &mt) {
-            unit_s = mt.x;
-            unit_u = mt.y;
-            first_chunk = mt.z;
-            const Q4Seq q = q4_seq<RT>(P, unit_s);
-            len = q.len;
-            unit_chunks = q.chunks;
-            q0 = q.q0;
-            head = unit_u % P.num_kv_heads;
-            row0 = unit_u / P.num_kv_heads * RT;
-            rows = min(RT, q.n * P.G - row0);
-            lim_min = len - q.n + 1 + row0 / P.G;
+        auto begin_unit = [&]() {
+            first_chunk = cu.chunk;
+            row0 = cu.tile * RT;
+            rows = min(RT, cu.q.n * P.G - row0);
+            lim_min = cu.q.len - cu.q.n + 1 + row0 / P.G;
             vs = 0x1p60f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -310,8 +340,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                     for (int h = 0; h < 2; ++h) {
                         uint4 w = make_uint4(0, 0, 0, 0);
                         if (col < rows) {
-                            const size_t row = (size_t)(q0 + r / P.G) * P.num_heads +
-                                               (size_t)head * P.G + r % P.G;
+                            const size_t row = (size_t)(cu.q.q0 + r / P.G) * P.num_heads +
+                                               (size_t)cu.head * P.G + r % P.G;
                             w = *reinterpret_cast<const uint4 *>(
                                 static_cast<const T *>(P.query) + row * D + c * 64 + h * 32 + 8 * t);
                         }
@@ -363,7 +393,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                         za[nt][c][e] = 0.f;
                     }
                     const int cc = S::kDouble ? ((2 * t + e) & 3) : nt * 8 + 2 * t + e;
-                    lim[nt][e] = len - q.n + 1 + (row0 + cc) / P.G;
+                    lim[nt][e] = cu.q.len - cu.q.n + 1 + (row0 + cc) / P.G;
                     m[nt][e] = kQ4NoMax;
                     l[nt][e] = 0.f;
                 }
@@ -380,11 +410,11 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
         // the workspace: slot 0 of a worker is its first unit's if that began
         // before, slot 1 its last one's.
         auto end_unit = [&]() {
-            const bool all = first_chunk == 0 && last_chunk + 1 == unit_chunks;
+            const bool all = first_chunk == 0 && cu.chunk + 1 == cu.q.chunks;
             const int slot = 2 * worker + (first_chunk == 0 ? 1 : 0);
             if (!all && first_chunk == 0) {
-                const int rest = unit_chunks - last_chunk - 1;
-                tail = make_int4(unit_s, unit_u, (int)((rest + per - 1) / per), rows);
+                const int rest = cu.q.chunks - cu.chunk - 1;
+                tail = make_int4(cu.s, cu.head, cu.tile, (int)((rest + per - 1) / per));
             }
             const float unscale = 0x1p24f / vs;
 #pragma unroll
@@ -397,8 +427,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                     const int col = nt * 8 + 2 * t + e;
                     const bool in = col < rows && (!S::kDouble || col < 4);
                     const int r = row0 + col;
-                    const size_t out_row = (size_t)(q0 + r / P.G) * P.num_heads +
-                                           (size_t)head * P.G + r % P.G;
+                    const size_t out_row = (size_t)(cu.q.q0 + r / P.G) * P.num_heads +
+                                           (size_t)cu.head * P.G + r % P.G;
                     const float inv = !all ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
                     if (!all && in && g == 0)
                         P.part_ml[(size_t)slot * RT + col] = make_float2(m[nt][e], ls);
@@ -437,9 +467,9 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
         const int lm_token = (lane & 7) + ((lane >> 3) & 1) * 8;
         const uint32_t lm_off = q4_word(lm_token, (lane >> 4) * 4);
 
-        auto chunk_step = [&](int slot, const int4 &mt) {
-            const uint32_t kb = ring_u32 + slot * S::kStageBytes, vb = kb + S::kTileBytes;
-            const uint8_t *kp = ring + slot * S::kStageBytes, *vp = kp + S::kTileBytes;
+        auto chunk_step = [&](uint32_t slot) {
+            const uint32_t kb = ring_u32 + slot, vb = kb + S::kTileBytes;
+            const uint8_t *kp = ring + slot, *vp = kp + S::kTileBytes;
             // x = scale <q, k> in units of log2: rows g, g + 8 (tokens) of columns 2t, 2t + 1
             float x[NT][4];
             {
@@ -500,22 +530,31 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                     zv[c][i] = p.y;
                 }
             }
-            const bool masked = mt.w || mt.z * kQ4Tokens + kQ4Tokens > lim_min;
-            if (masked) {
+            const bool skip = (bad >> (used & 31)) & 1u;
+            if (skip || (cu.chunk + 1) * kQ4Tokens > lim_min) {
                 // past the context, past a column's own token, or a block that was skipped:
                 // whatever lies there must not meet a weight, not even one of zero
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int p = mt.w ? 0x7fffffff : mt.z * kQ4Tokens + g + 8 * i;
+                    const int p = skip ? 0x7fffffff : cu.chunk * kQ4Tokens + g + 8 * i;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int e = 0; e < 2; ++e)
                             if (p >= lim[nt][e]) x[nt][2 * i + e] = -INFINITY;
-                    if (p >= len)
 #pragma unroll
-                        for (int c = 0; c < C; ++c) sv[c][i] = zv[c][i] = 0.f;
+                    for (int c = 0; c < C; ++c) {
+                        const bool nan = !(sv[c][i] + zv[c][i] == sv[c][i] + zv[c][i]);
+                        if (p < cu.q.len && nan)  // of the columns that see it alone
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                                for (int e = 0; e < 2; ++e)
+                                    if (p < lim[nt][e]) za[nt][c][e] = NAN;
+                        if (p >= cu.q.len || nan) sv[c][i] = zv[c][i] = 0.f;
+                    }
                 }
+                bad &= ~(1u << (used & 31));
             }
             float p[NT][4], top;
             auto weights = [&]() {
@@ -529,11 +568,11 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                     }
             };
             weights();
-            float s_top = 128.f / vs;  // (p alone stays below 2^8)
+            float s_top = 0.f;
 #pragma unroll
             for (int c = 0; c < C; ++c) s_top = fmaxf(s_top, fmaxf(sv[c][0], sv[c][1]));
-            if (__any_sync(0xffffffffu, top * s_top * vs > kQ4TopWeight)) {
-                // new maxima, and a new power of two that brings the largest scale to 2^7
+            if (__any_sync(0xffffffffu, fmaxf(top, s_top * vs * (kQ4TopP / kQ4TopS)) > kQ4TopP)) {
+                // new maxima, and a new power of two on the scales
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -542,7 +581,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1)
                             a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                        a = fmaxf(a, m[nt][e]);
+                        a = fmaxf(a - 6.f, m[nt][e]);
                         const float f = ex2(m[nt][e] - a);
                         m[nt][e] = a;
                         l[nt][e] *= f;
@@ -556,13 +595,11 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                             }
                         }
                     }
-                float st = 0.f;
 #pragma unroll
-                for (int c = 0; c < C; ++c) st = fmaxf(st, fmaxf(sv[c][0], sv[c][1]));
-#pragma unroll
-                for (int o = 1; o < 32; o <<= 1) st = fmaxf(st, __shfl_xor_sync(0xffffffffu, st, o));
-                const int sb = (__float_as_int(st) >> 23) & 255;
-                const float nv = fminf(vs, __int_as_float(max(1, min(187, 261 - sb)) << 23));
+                for (int o = 1; o < 32; o <<= 1)
+                    s_top = fmaxf(s_top, __shfl_xor_sync(0xffffffffu, s_top, o));
+                const int sb = (__float_as_int(s_top) >> 23) & 255;
+                const float nv = fminf(vs, __int_as_float(max(1, min(187, 258 - sb)) << 23));
                 if (nv != vs) {
                     const float f = nv / vs;
                     vs = nv;
@@ -577,37 +614,42 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                 }
                 weights();
             }
+            // the weights in two parts of fp16, tokens g and g + 8
+            uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) l[nt][i & 1] += p[nt][i];
+                for (int i = 0; i < 2; ++i) {
+                    const float p0 = p[nt][2 * i], p1 = p[nt][2 * i + 1];
+                    l[nt][0] += p0;
+                    l[nt][1] += p1;
+                    ph[nt][i] = Pack<__half>::down(p0, p1);
+                    const float2 h = Pack<__half>::up(ph[nt][i]);
+                    pl[nt][i] = Pack<__half>::down(p0 - h.x, p1 - h.y);
+                }
 #pragma unroll
             for (int c = 0; c < C; ++c) {
                 uint32_t r[4];
                 ldsm_x4_trans(r[0], r[1], r[2], r[3], vb + c * kQ4CellBytes + lm_off);
+                uint32_t s2[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float v = sv[c][i] * vs;
+                    s2[i] = Pack<__half>::down(v, v);
+                }
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
                     uint32_t b[2], bl[2];
 #pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        const float s = sv[c][i] * vs;
-                        float w0 = p[nt][2 * i] * s, w1 = p[nt][2 * i + 1] * s;
-                        float z0 = p[nt][2 * i] * zv[c][i], z1 = p[nt][2 * i + 1] * zv[c][i];
-                        if (masked) {  // (a NaN among the values is the seeing columns' alone)
-                            if (x[nt][2 * i] == -INFINITY) w0 = z0 = 0.f;
-                            if (x[nt][2 * i + 1] == -INFINITY) w1 = z1 = 0.f;
-                        }
-                        za[nt][c][0] += z0;
-                        za[nt][c][1] += z1;
-                        uint32_t hi = Pack<__half>::down(w0, w1);
-                        const float2 h = Pack<__half>::up(hi);
-                        const uint32_t lo = Pack<__half>::down(w0 - h.x, w1 - h.y);
-                        if (S::kDouble) {
-                            if (t >= 2) hi = lo;
-                        } else {
-                            bl[i] = q4_transpose(lo);
-                        }
-                        b[i] = q4_transpose(hi);
+                        za[nt][c][0] = fmaf(p[nt][2 * i], zv[c][i], za[nt][c][0]);
+                        za[nt][c][1] = fmaf(p[nt][2 * i + 1], zv[c][i], za[nt][c][1]);
+                        // times the scale: rounded, and what that and the weight left
+                        const uint32_t hi = q4_mul2(ph[nt][i], s2[i]);
+                        const uint32_t lo =
+                            q4_fma2(pl[nt][i], s2[i], q4_fma2(ph[nt][i], s2[i], hi ^ 0x80008000u));
+                        b[i] = q4_transpose(S::kDouble && t >= 2 ? lo : hi);
+                        if (!S::kDouble) bl[i] = q4_transpose(lo);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -622,19 +664,22 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
             }
         };
 
-        for (int i = 0;; ++i) {
-            const int slot = i % S::kStages;
+        uint32_t slot = 0, prev = (S::kStages - 1) * S::kStageBytes;
+        while (used < asked) {
             q4_copy_wait<S::kStages - 2>();
-            __syncwarp();
-            const int4 mt = s_meta[warp][slot];
-            ask((i + S::kStages - 1) % S::kStages);
-            if (mt.x != unit_s || mt.y != unit_u) {
-                if (unit_s >= 0) end_unit();
-                if (mt.x < 0) break;
-                begin_unit(mt);
+            __syncwarp();  // the stage is whole, and nothing reads the one before any more
+            ask(prev);
+            if (fresh) begin_unit();
+            chunk_step(slot);
+            prev = slot;
+            slot = slot == (S::kStages - 1) * S::kStageBytes ? 0 : slot + S::kStageBytes;
+            fresh = ++used == asked || cu.chunk + 1 == cu.q.chunks;
+            if (fresh) {
+                end_unit();
+                q4_next_unit<RT>(P, cu);
+            } else {
+                ++cu.chunk;
             }
-            chunk_step(slot, mt);
-            last_chunk = mt.z;
         }
         q4_copy_wait<0>();
     }
@@ -668,8 +713,8 @@ __global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q
     const int4 tail = P.tails[worker];
     if (tail.x < 0) return;
     const Q4Seq q = q4_seq<RT>(P, tail.x);
-    const int head = tail.y % P.num_kv_heads, row0 = tail.y / P.num_kv_heads * RT;
-    const int parts = 1 + tail.z, rows = tail.w;
+    const int head = tail.y, row0 = tail.z * RT;
+    const int parts = 1 + tail.w, rows = min(RT, q.n * P.G - row0);
     const int d0 = (threadIdx.x % kLanes) * 4;
     for (int col = threadIdx.x / kLanes; col < rows; col += kRowsAtOnce) {
         float M = kQ4NoMax, L = 0.f;
