@@ -32,16 +32,18 @@ struct Plan {
 
 template <int D>
 int max_workers(int rows) {
-    if (rows == 4) return Q4Shape<D, 4>::kWorkers;
-    if (rows == 8) return Q4Shape<D, 8>::kWorkers;
-    return Q4Shape<D, 16>::kWorkers;
+    return rows <= 8 ? Q4Shape<D, 8>::kWorkers : Q4Shape<D, 16>::kWorkers;
 }
 
 // False: sizes past what the kernels count in 32 bits.
 bool make_plan(Plan *p, int num_seqs, int num_heads, int num_kv_heads, int head_dim,
                int max_query_len, int max_context_len) {
     const long long G = num_heads / num_kv_heads, most = G * max_query_len;
-    p->rows = most <= 4 ? 4 : most <= 8 || head_dim == 256 ? 8 : 16;
+    p->rows = most <= (head_dim == 256 ? 2 : 1) ? (head_dim == 256 ? 2 : 1)
+              : most <= 2                       ? 2
+              : most <= 4                       ? 4
+              : most <= 8 || head_dim == 256    ? 8
+                                                : 16;
     const long long chunks = ((long long)max_context_len + kQ4Tokens - 1) / kQ4Tokens;
     const long long units = num_kv_heads * ((most + p->rows - 1) / p->rows);
     if (most > INT_MAX || units > INT_MAX || units * (chunks + 1) > INT_MAX) return false;

@@ -20,23 +20,33 @@
 // that brings its largest element to 2^13: exact, but for elements 2^-28 of the
 // largest, where fp16 itself ends.
 //
+// The values' products take a byte's two nibbles as they lie, n_0 and n_0 + 16 n_1
+// (two ANDs, a byte permute and an AND for eight), and leave the subtraction to
+// the end.
+//
 // The weights p s go to fp16 in two parts (their rounding, and its remainder), so
 // their error is 2^-22 of them; a running power of two keeps them in range
-// (below).  With at most four rows the two parts are two columns of one product,
-// which has eight, at no cost.
+// (below).
+//
+// Few rows.  The products have eight columns.  With at most four rows a column is
+// (chunk of 16 tokens, row, part of the weight): a step of 4 / rows chunks fills
+// them, and each lane has two logits of one row, all different ones, instead of
+// repeating a row's softmax in idle columns.  With more rows a column is a row, and
+// the second parts have a product of their own.
 //
 // Softmax in one pass.  Each warp keeps a maximum m per row which it moves only
-// when a weight has outgrown 2^8 (the first chunk, then rarely): the check is
-// one comparison and a vote instead of three exchanges between the lanes, and
-// any m gives the same quotient.
+// when a weight has outgrown 2^4 (the first chunk, then rarely): the check is
+// one comparison and a vote instead of exchanges between the lanes, and any m
+// gives the same quotient.
 //
 // Work.  A warp works on its own, without barriers: it has a range of chunks (16
 // tokens of a sequence's KV head) of the batch's, all laid end to end and cut
-// into equal parts, and a ring of kStages chunks that it fills itself by
-// asynchronous copies.  A (sequence, head, rows) that is cut leaves partial
-// results, which the merge kernel puts together.
+// into equal parts, and a ring of kStages stages of kStep chunks that it fills
+// itself by bulk copies, one a lane for every K and V tile.  A (sequence, head,
+// rows) that is cut leaves partial results, which the merge kernel puts together.
 //
-// Bound: HBM, 72 bytes a group and token of K and V.
+// Bound: HBM, 72 bytes a group and token of K and V; next, the integer pipe (the
+// nibbles' ANDs).
 #pragma once
 
 #include <cuda_runtime.h>
@@ -114,6 +124,16 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same on a zeroed accumulator.
+__device__ __forceinline__ void q4_mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                             uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+
 // An 8 x 8 matrix of 16-bit units, spread as ldmatrix gives it, transposed.
 __device__ __forceinline__ uint32_t q4_transpose(uint32_t a) {
     uint32_t d;
@@ -131,24 +151,20 @@ __device__ __forceinline__ uint32_t q4_fma2(uint32_t a, uint32_t b, uint32_t c) 
     return *reinterpret_cast<const uint32_t *>(&r);
 }
 
-__device__ __forceinline__ void q4_copy16(uint32_t dst, const void *src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void q4_copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void q4_copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-template <int D, int RT>
+template <int D, int R>
 struct Q4Shape {
     static constexpr int kCells = D / kQ4Group;
     static constexpr int kTileBytes = kCells * kQ4CellBytes;
-    static constexpr int kStageBytes = 2 * kTileBytes;
-    static constexpr int kStages = D == 64 ? 6 : 4;
-    static constexpr int kTiles8 = RT <= 8 ? 1 : RT / 8;  // groups of eight columns
-    static constexpr bool kDouble = RT == 4;  // columns 4-7: the weights' remainders
-    static constexpr int kCtas = D <= 128 && RT <= 8 ? 4 : 3;  // an SM
+    static constexpr int kChunkBytes = 2 * kTileBytes;
+    static constexpr int kStep = D == 256 ? 2 : 4;           // chunks of a stage
+    static constexpr int kStages = D == 64 ? 3 : 2;
+    static constexpr bool kPacked = R <= 4;
+    static constexpr int kPack = kPacked ? 4 / R : 1;        // chunks at once
+    static_assert(kPack <= kStep, "a pack is of one stage");
+    static constexpr int kTiles8 = kPacked ? 1 : R / 8;      // groups of eight columns
+    static constexpr int kRows = kPacked ? 1 : 2 * kTiles8;  // rows of a lane
+    static constexpr int kStageBytes = kStep * kChunkBytes;
+    static constexpr int kCtas = D == 64 && R <= 8 ? 4 : 3;  // an SM
     static constexpr int kWorkers = kQ4Sms * kCtas * kQ4Warps;
     static constexpr size_t kSmem = (size_t)kQ4Warps * kStages * kStageBytes;
 };
@@ -182,24 +198,31 @@ __device__ __forceinline__ bool q4_next_unit(const Q4DecodeParams &P, Q4Cursor &
     return true;
 }
 
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
     q4_decode_kernel(const __grid_constant__ Q4DecodeParams P) {
-    using S = Q4Shape<D, RT>;
-    constexpr int NT = S::kTiles8, C = S::kCells;
+    using S = Q4Shape<D, R>;
+    constexpr int NT = S::kTiles8, C = S::kCells, NR = S::kRows, kPack = S::kPack;
     extern __shared__ __align__(128) uint8_t s_ring[];
     __shared__ long long s_base[kQ4Threads];  // chunks of the batch before a thread's sequences
     __shared__ long long s_warp[kQ4Warps];
+    __shared__ uint64_t s_full[kQ4Warps][S::kStages];
+    __shared__ int s_never;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
+    if (tid == 0) s_never = 0;
+    if (lane == 0) {
+        for (int i = 0; i < S::kStages; ++i) mbar_init(&s_full[warp][i], 1);
+        fence_mbar_init();
+    }
     pdl_wait();  // earlier kernels on the stream may still write what this reads
 
     // The batch's chunks, laid end to end: thread i's sequences are i * each ..
     const int each = (P.num_seqs + kQ4Threads - 1) / kQ4Threads;
     long long mine = 0;
     for (int s = tid * each; s < min(P.num_seqs, (tid + 1) * each); ++s) {
-        const Q4Seq q = q4_seq<RT>(P, s);
+        const Q4Seq q = q4_seq<R>(P, s);
         mine += (long long)q.chunks * q.tiles * P.num_kv_heads;
     }
     long long incl = mine;
@@ -236,7 +259,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
         Q4Cursor at;  // the next chunk to ask for
         at.s = lo * each - 1;
         for (;;) {
-            q4_next_seq<RT>(P, at);
+            q4_next_seq<R>(P, at);
             if (at.s >= P.num_seqs) break;
             const long long n = (long long)at.q.chunks * at.q.tiles * P.num_kv_heads;
             if (off < n) break;
@@ -251,86 +274,91 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
             at.tile = unit - at.head * at.q.tiles;
             if (P.whole && at.chunk > 0) {  // that unit is the worker's in whose range it begins
                 pos = at.q.chunks - at.chunk;
-                q4_next_unit<RT>(P, at);
+                q4_next_unit<R>(P, at);
             }
         }
         Q4Cursor cu = at;  // the chunk at hand
+        const int pos0 = pos;
         uint8_t *ring = s_ring + (size_t)warp * S::kStages * S::kStageBytes;
         const uint32_t ring_u32 = smem_u32(ring);
 
         // ---- asking for chunks ----
-        // A stage is the K tile and the V tile, 16 bytes a lane and step; one step has the end
-        // of the one and the beginning of the other.
-        constexpr int kPieces = S::kTileBytes / 16, kMixed = kPieces / 32 * 32;
-        const uint8_t *k_lane = P.k_cache + lane * 16;
-        const uint8_t *v_lane = P.v_cache + lane * 16 - S::kTileBytes;
-        const uint8_t *m_lane = kMixed + lane < kPieces ? k_lane : v_lane;
-        const uint32_t dst_lane = ring_u32 + lane * 16;
         const uint32_t block_bytes = (uint32_t)(P.num_kv_heads << P.sub_shift) * S::kTileBytes;
         const int sub_mask = (1 << P.sub_shift) - 1;
-        int asked = 0, used = 0;
-        uint32_t bad = 0;       // bit i & 31: the i-th chunk's block is outside the pool
-        int ids = 0;            // the lane's block id, of chunk (at.chunk & ~31) + lane
-        bool load_ids = true;
-        uint32_t head_off = (uint32_t)(at.head << P.sub_shift) * S::kTileBytes;
-        auto ask = [&](uint32_t slot) {
-            if (at.s < P.num_seqs && (pos < count || (P.whole && at.chunk > 0))) {
-                if (load_ids) {
-                    const int c = (at.chunk & ~31) + lane;
-                    ids = c < at.q.chunks ? P.block_tables[(size_t)at.s * P.max_blocks_per_seq +
-                                                           (c >> P.sub_shift)]
-                                          : 0;
-                    load_ids = false;
-                }
-                const int id = __shfl_sync(0xffffffffu, ids, at.chunk & 31);
-                if ((unsigned)id < (unsigned)P.num_blocks) {
-                    const size_t o = (size_t)(uint32_t)id * block_bytes +
-                                     (head_off + (uint32_t)(at.chunk & sub_mask) * S::kTileBytes);
-#pragma unroll
-                    for (int i = 0; i < 2 * kPieces; i += 32) {
-                        const uint8_t *src = i < kMixed ? k_lane : i == kMixed ? m_lane : v_lane;
-                        if (i + 32 <= 2 * kPieces || i + lane < 2 * kPieces)
-                            q4_copy16(dst_lane + slot + i * 16, src + o + i * 16);
-                    }
-                } else {
-                    bad |= 1u << (asked & 31);
-                    if (lane == 0 && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
-                }
-                ++pos;
-                ++asked;
-                if (++at.chunk == at.q.chunks) {
-                    // (a table of at most 32 chunks is all in the lanes, for every head)
-                    load_ids = at.q.chunks > 32;
-                    if (q4_next_unit<RT>(P, at)) load_ids = true;
-                    head_off = (uint32_t)(at.head << P.sub_shift) * S::kTileBytes;
-                } else if ((at.chunk & 31) == 0) {
-                    load_ids = true;
-                }
+        const uint8_t *lane_pool = lane & 1 ? P.v_cache : P.k_cache;
+        const uint64_t policy = l2_evict_first_policy();
+        int asked = 0, used = 0;  // steps
+        uint32_t bad = 0;         // of a step a byte: chunks whose block is outside the pool
+        int ids = 0;              // the lane's block id, of chunk ids_c + lane
+        int ids_c = 1 << 30;
+        // chunks of the step at a cursor that has `left` chunks of the range before it
+        auto step_chunks = [&](const Q4Cursor &c, int left) {
+            const int n = min(S::kStep, c.q.chunks - c.chunk);
+            return P.whole ? n : min(n, left);
+        };
+        auto ask = [&]() {
+            if (at.s >= P.num_seqs || !(pos < count || (P.whole && at.chunk > 0))) return;
+            const int n = step_chunks(at, count - pos);
+            if (at.chunk < ids_c || at.chunk + n > ids_c + 32) {
+                ids_c = at.chunk;
+                const int c = ids_c + lane;
+                ids = c < at.q.chunks ? P.block_tables[(size_t)at.s * P.max_blocks_per_seq +
+                                                       (c >> P.sub_shift)]
+                                      : 0;
             }
-            q4_copy_commit();
+            const int stage = asked % S::kStages;
+            // lane 2j: K tile of chunk j, lane 2j + 1: its V tile
+            const int c = at.chunk + (lane >> 1);
+            const int id = __shfl_sync(0xffffffffu, ids, (c - ids_c) & 31);
+            const bool mine = lane < 2 * n, good = (unsigned)id < (unsigned)P.num_blocks;
+            const uint32_t copies = __ballot_sync(0xffffffffu, mine && good);
+            const uint32_t lost = ~copies & ((1u << (2 * n)) - 1u);
+            bad = (bad & ~(255u << (8 * (asked & 3)))) | lost << (8 * (asked & 3));
+            if (lane == 0) {
+                mbar_arrive_expect_tx(&s_full[warp][stage], __popc(copies) * S::kTileBytes);
+                if (lost && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
+            }
+            __syncwarp();
+            if (mine && good) {
+                const size_t o = (size_t)(uint32_t)id * block_bytes +
+                                 (size_t)((uint32_t)(at.head << P.sub_shift) + (uint32_t)(c & sub_mask)) *
+                                     S::kTileBytes;
+                bulk_g2s(ring + stage * S::kStageBytes + lane * S::kTileBytes, lane_pool + o,
+                         S::kTileBytes, &s_full[warp][stage], policy);
+            }
+            ++asked;
+            pos += n;
+            at.chunk += n;
+            if (at.chunk == at.q.chunks) {
+                if (q4_next_unit<R>(P, at)) ids_c = 1 << 30;
+            }
         };
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) ask(i * S::kStageBytes);
+        for (int i = 0; i < S::kStages - 1; ++i) ask();
 
         // ---- the unit at hand ----
-        float O[NT][C][4][4];           // [rows of 16 channels: cell, nibble j][fragment]
-        float m[NT][2], l[NT][2], za[NT][C][2];  // columns 2t, 2t + 1
-        uint32_t qf[NT][C][2][2][2];    // the query's fragments: cell, half, nibble pair
-        float c1[NT][2], qz[NT][C][2];
-        int lim[NT][2], lim_min = 0;    // tokens a column sees; the fewest of any
-        float vs = 0.f;                 // power of two on the weights times scales
-        int first_chunk = 0, rows = 0, row0 = 0;
-        bool fresh = true;              // the chunk at hand begins a unit, or the range
+        // A lane's rows: packed, row t % R of chunk t / R of a pack; else 2t and 2t + 1 of
+        // every eight.
+        float O[NT][C][4][4];     // [rows of 16 channels: cell, nibble][fragment]
+        float m[NR], l[NR], za[NR][C];
+        uint32_t qf[NT][C][2][2][2];  // the query's fragments: cell, half, nibble pair
+        float c1[NR], qz[NR][C];
+        int lim[NR], lim_min = 0;     // tokens a row sees; the fewest of any
+        float vs = 0.f;               // power of two on the values' scales
+        int first_chunk = 0, rows = 0, row0 = 0, upos = pos0;
+        bool fresh = true;            // the step at hand begins a unit, or the range
+        const int jl = S::kPacked ? t / R : 0;  // the lane's chunk of a pack
 
         auto begin_unit = [&]() {
             first_chunk = cu.chunk;
-            row0 = cu.tile * RT;
-            rows = min(RT, cu.q.n * P.G - row0);
-            lim_min = cu.q.len - cu.q.n + 1 + row0 / P.G;
+            row0 = cu.tile * R;
+            rows = min(R, cu.q.n * P.G - row0);
+            const int seen0 = cu.q.len - cu.q.n + 1;
+            lim_min = seen0 + row0 / P.G;
             vs = 0x1p60f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const int col = S::kDouble ? (g & 3) : nt * 8 + g;
+                const int col = S::kPacked ? (g >> 1) % R : nt * 8 + g;
                 const int r = row0 + col;
                 float f[C][2][8];
                 float top = 0.f;
@@ -383,19 +411,19 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                     sum[c] *= P.scale_log2;
                 }
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    // column 2t + e of this group: its row is that of lanes 4 (2t + e) ..
-                    const int src = 4 * (2 * t + e);
-                    c1[nt][e] = __shfl_sync(0xffffffffu, back, src);
+                for (int e = 0; e < (S::kPacked ? 1 : 2); ++e) {
+                    const int i = 2 * nt + e;
+                    const int mine = S::kPacked ? t % R : 2 * t + e;  // row of the eight
+                    const int src = S::kPacked ? 8 * mine : 4 * mine;  // a lane that has its sums
+                    c1[i] = __shfl_sync(0xffffffffu, back, src);
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        qz[nt][c][e] = __shfl_sync(0xffffffffu, sum[c], src);
-                        za[nt][c][e] = 0.f;
+                        qz[i][c] = __shfl_sync(0xffffffffu, sum[c], src);
+                        za[i][c] = 0.f;
                     }
-                    const int cc = S::kDouble ? ((2 * t + e) & 3) : nt * 8 + 2 * t + e;
-                    lim[nt][e] = cu.q.len - cu.q.n + 1 + (row0 + cc) / P.G;
-                    m[nt][e] = kQ4NoMax;
-                    l[nt][e] = 0.f;
+                    lim[i] = seen0 + (row0 + nt * 8 + mine) / P.G;
+                    m[i] = kQ4NoMax;
+                    l[i] = 0.f;
                 }
 #pragma unroll
                 for (int c = 0; c < C; ++c)
@@ -406,165 +434,199 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
             }
         };
 
-        // What the unit's chunks so far give, to the output or, where it is cut, to
-        // the workspace: slot 0 of a worker is its first unit's if that began
+        // Sum over the lanes that have a row's other tokens.
+        auto row_sum = [&](float v) {
+#pragma unroll
+            for (int o = S::kPacked ? R : 4; o < 32; o <<= 1)
+                v += __shfl_xor_sync(0xffffffffu, v, o);
+            return v;
+        };
+
+        // What the unit's chunks so far give, up to chunk `stop`, to the output or, where it
+        // is cut, to the workspace: slot 0 of a worker is its first unit's if that began
         // before, slot 1 its last one's.
-        auto end_unit = [&]() {
-            const bool all = first_chunk == 0 && cu.chunk + 1 == cu.q.chunks;
+        auto end_unit = [&](int stop) {
+            const bool all = first_chunk == 0 && stop == cu.q.chunks;
             const int slot = 2 * worker + (first_chunk == 0 ? 1 : 0);
-            if (!all && first_chunk == 0) {
-                const int rest = cu.q.chunks - cu.chunk - 1;
-                tail = make_int4(cu.s, cu.head, cu.tile, (int)((rest + per - 1) / per));
-            }
+            if (!all && first_chunk == 0)
+                tail = make_int4(cu.s, cu.head, cu.tile,
+                                 (int)((cu.q.chunks - stop + per - 1) / per));
             const float unscale = 0x1p24f / vs;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < NR; ++i) {
+                const int nt = i / 2, e = i % 2;
+                const int row = S::kPacked ? t % R : nt * 8 + 2 * t + e;  // of the tile
+                const bool in = row < rows && (!S::kPacked || t < R);
+                const int r = row0 + row;
+                const size_t out_row = (size_t)(cu.q.q0 + r / P.G) * P.num_heads +
+                                       (size_t)cu.head * P.G + r % P.G;
+                const float ls = row_sum(l[i]);
+                const float inv = !all ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
+                if (!all && in && g == 0) P.part_ml[(size_t)slot * R + row] = make_float2(m[i], ls);
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float ls = l[nt][e];
+                for (int c = 0; c < C; ++c) {
+                    const float z = row_sum(za[i][c]);
 #pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
-                    const int col = nt * 8 + 2 * t + e;
-                    const bool in = col < rows && (!S::kDouble || col < 4);
-                    const int r = row0 + col;
-                    const size_t out_row = (size_t)(cu.q.q0 + r / P.G) * P.num_heads +
-                                           (size_t)cu.head * P.G + r % P.G;
-                    const float inv = !all ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
-                    if (!all && in && g == 0)
-                        P.part_ml[(size_t)slot * RT + col] = make_float2(m[nt][e], ls);
+                    for (int h = 0; h < 2; ++h) {
+                        float v[4];
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        float z = za[nt][c][e];
+                        for (int j = 0; j < 4; ++j) {
+                            if (S::kPacked) {  // both parts, and the pack's chunks
+                                v[j] = O[nt][c][j][2 * h] + O[nt][c][j][2 * h + 1];
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1) z += __shfl_xor_sync(0xffffffffu, z, o);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float v[4];
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float x = O[nt][c][j][2 * h + e];
-                                if (S::kDouble) x += __shfl_xor_sync(0xffffffffu, x, 2);
-                                v[j] = fmaf(x, j & 1 ? unscale * 0.0625f : unscale, z) * inv;
-                            }
-                            const int d0 = c * 64 + h * 32 + 4 * g;
-                            if (!in) continue;
-                            if (!all) {
-                                *reinterpret_cast<float4 *>(P.part + ((size_t)slot * RT + col) * D + d0) =
-                                    make_float4(v[0], v[1], v[2], v[3]);
-                            } else if (P.out_f32) {
-                                *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + out_row * D + d0) =
-                                    make_float4(v[0], v[1], v[2], v[3]);
+                                for (int o = R; o < 4; o <<= 1)
+                                    v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
                             } else {
-                                *reinterpret_cast<uint2 *>(static_cast<T *>(P.out) + out_row * D + d0) =
-                                    make_uint2(Pack<T>::down(v[0], v[1]), Pack<T>::down(v[2], v[3]));
+                                v[j] = O[nt][c][j][2 * h + e];
                             }
+                        }
+                        v[1] = (v[1] - v[0]) * 0.0625f;  // n_0 + 16 n_1 -> n_1
+                        v[3] = (v[3] - v[2]) * 0.0625f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], unscale, z) * inv;
+                        const int d0 = c * 64 + h * 32 + 4 * g;
+                        if (!in) continue;
+                        if (!all) {
+                            *reinterpret_cast<float4 *>(P.part + ((size_t)slot * R + row) * D + d0) =
+                                make_float4(v[0], v[1], v[2], v[3]);
+                        } else if (P.out_f32) {
+                            *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + out_row * D + d0) =
+                                make_float4(v[0], v[1], v[2], v[3]);
+                        } else {
+                            *reinterpret_cast<uint2 *>(static_cast<T *>(P.out) + out_row * D + d0) =
+                                make_uint2(Pack<T>::down(v[0], v[1]), Pack<T>::down(v[2], v[3]));
                         }
                     }
                 }
+            }
         };
 
         // lane's row of the 8 x 8 matrices that ldmatrix takes from a cell
         const int lm_token = (lane & 7) + ((lane >> 3) & 1) * 8;
         const uint32_t lm_off = q4_word(lm_token, (lane >> 4) * 4);
 
-        auto chunk_step = [&](uint32_t slot) {
-            const uint32_t kb = ring_u32 + slot, vb = kb + S::kTileBytes;
-            const uint8_t *kp = ring + slot, *vp = kp + S::kTileBytes;
-            // x = scale <q, k> in units of log2: rows g, g + 8 (tokens) of columns 2t, 2t + 1
-            float x[NT][4];
+        // The products of a K tile's cell with the query.
+        auto keys = [&](uint32_t cell, int c, float (&acc)[NT][4]) {
+            uint32_t r[4];
+            ldsm_x4(r[0], r[1], r[2], r[3], cell + lm_off);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint32_t lo = r[2 * h] >> (8 * i), hi = r[2 * h + 1] >> (8 * i);
+                    const uint32_t a0 = lo & 0x000f000fu, a1 = hi & 0x000f000fu;
+                    const uint32_t a2 = lo & 0x00f000f0u, a3 = hi & 0x00f000f0u;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const uint32_t(&q)[2] = qf[nt][c][h][i];
+                        if (h == 0 && i == 0) q4_mma_first(acc[nt], a0, a1, a2, a3, q[0], q[1]);
+                        else q4_mma(acc[nt], a0, a1, a2, a3, q[0], q[1]);
+                    }
+                }
+        };
+        // The products of a V tile's cell (its words in r) with weights.
+        auto values = [&](const uint32_t (&r)[4], float (&o)[4][4], uint32_t b0, uint32_t b1) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    w[i] = j ? __byte_perm(r[i], 0, 0x4341) : r[i] & 0x00ff00ffu;
+                q4_mma(o[2 * j], w[0] & 0x000f000fu, w[2] & 0x000f000fu, w[1] & 0x000f000fu,
+                       w[3] & 0x000f000fu, b0, b1);
+                q4_mma(o[2 * j + 1], w[0], w[2], w[1], w[3], b0, b1);
+            }
+        };
+
+        // A pack of chunks from chunk `chunk` on, `n` of them there, in the stage at `at_pack`;
+        // lost: bits of the tiles that were not copied.
+        auto pack_step = [&](uint32_t at_pack, int chunk, int n, uint32_t lost) {
+            const uint32_t base = ring_u32 + at_pack;
+            const uint8_t *pk = ring + at_pack + jl * (S::kPacked ? S::kChunkBytes : 0) +
+                                kQ4CellParams + 4 * g;  // the lane's chunk's scales
+            // x = scale <q, k> in units of log2, tokens g and g + 8 of the lane's rows
+            float x[NR][2];
             {
-                float acc[NT][C][4];
+                float a[C][NR][2];
+#pragma unroll
+                for (int j = 0; j < kPack; ++j)
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        float acc[NT][4];
+                        keys(base + j * S::kChunkBytes + c * kQ4CellBytes, c, acc);
+                        if constexpr (S::kPacked) {
+                            if (kPack == 1 || j == 0 || jl == j) {
+                                a[c][0][0] = acc[0][0];
+                                a[c][0][1] = acc[0][2];
+                            }
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < NR; ++i) {
+                                a[c][i][0] = acc[i / 2][i % 2];
+                                a[c][i][1] = acc[i / 2][2 + i % 2];
+                            }
+                        }
+                    }
+                float y[NR][2];
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
+                    const float2 p0 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pk + c * kQ4CellBytes));
+                    const float2 p1 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pk + c * kQ4CellBytes + 32));
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[nt][c][i] = 0.f;
-                    uint32_t r[4];
-                    ldsm_x4(r[0], r[1], r[2], r[3], kb + c * kQ4CellBytes + lm_off);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const uint32_t lo = r[2 * h] >> (8 * i), hi = r[2 * h + 1] >> (8 * i);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-                                q4_mma(acc[nt][c], lo & 0x000f000fu, hi & 0x000f000fu,
-                                       lo & 0x00f000f0u, hi & 0x00f000f0u, qf[nt][c][h][i][0],
-                                       qf[nt][c][h][i][1]);
-                        }
+                    for (int i = 0; i < NR; ++i) {
+                        y[i][0] = c == 0 ? p0.x * a[c][i][0] : fmaf(p0.x, a[c][i][0], y[i][0]);
+                        y[i][1] = c == 0 ? p1.x * a[c][i][1] : fmaf(p1.x, a[c][i][1], y[i][1]);
+                        x[i][0] = c == 0 ? p0.y * qz[i][c] : fmaf(p0.y, qz[i][c], x[i][0]);
+                        x[i][1] = c == 0 ? p1.y * qz[i][c] : fmaf(p1.y, qz[i][c], x[i][1]);
+                    }
                 }
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < NR; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) x[nt][i] = 0.f;
-                float y[NT][4];
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    const uint8_t *pp = kp + c * kQ4CellBytes + kQ4CellParams;
-                    const float2 p0 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pp + 4 * g));
-                    const float2 p1 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pp + 4 * g + 32));
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float2 p = i < 2 ? p0 : p1;
-                            y[nt][i] = c == 0 ? p.x * acc[nt][c][i] : fmaf(p.x, acc[nt][c][i], y[nt][i]);
-                            x[nt][i] = fmaf(p.y, qz[nt][c][i & 1], x[nt][i]);
-                        }
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) x[nt][i] = fmaf(y[nt][i], c1[nt][i & 1], x[nt][i]);
+                    for (int k = 0; k < 2; ++k) x[i][k] = fmaf(y[i][k], c1[i], x[i][k]);
             }
             // the values' scales and least values
             float sv[C][2], zv[C][2];
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                const uint8_t *pp = vp + c * kQ4CellBytes + kQ4CellParams;
+            for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float2 p = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pp + 4 * g + 32 * i));
-                    sv[c][i] = p.x;
-                    zv[c][i] = p.y;
+                for (int k = 0; k < 2; ++k) {
+                    const float2 p = Pack<T>::up(*reinterpret_cast<const uint32_t *>(
+                        pk + S::kTileBytes + c * kQ4CellBytes + 32 * k));
+                    sv[c][k] = p.x;
+                    zv[c][k] = p.y;
                 }
-            }
-            const bool skip = (bad >> (used & 31)) & 1u;
-            if (skip || (cu.chunk + 1) * kQ4Tokens > lim_min) {
-                // past the context, past a column's own token, or a block that was skipped:
-                // whatever lies there must not meet a weight, not even one of zero
+            if (n < kPack || lost || (chunk + kPack) * kQ4Tokens > lim_min) {
+                // past the context or the range, past a row's own token, or a block that was
+                // skipped: whatever lies there must not meet a weight, not even one of zero
+                const bool there = jl < n && !((lost >> (2 * jl)) & 3u);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int p = skip ? 0x7fffffff : cu.chunk * kQ4Tokens + g + 8 * i;
+                for (int k = 0; k < 2; ++k) {
+                    const int tok = (chunk + jl) * kQ4Tokens + g + 8 * k;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            if (p >= lim[nt][e]) x[nt][2 * i + e] = -INFINITY;
+                    for (int i = 0; i < NR; ++i)
+                        if (!there || tok >= lim[i]) x[i][k] = -INFINITY;
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        const bool nan = !(sv[c][i] + zv[c][i] == sv[c][i] + zv[c][i]);
-                        if (p < cu.q.len && nan)  // of the columns that see it alone
+                        const bool in = there && tok < cu.q.len;
+                        const bool nan = !(sv[c][k] + zv[c][k] == sv[c][k] + zv[c][k]);
+                        if (in && nan)  // of the rows that see it alone
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                                for (int e = 0; e < 2; ++e)
-                                    if (p < lim[nt][e]) za[nt][c][e] = NAN;
-                        if (p >= cu.q.len || nan) sv[c][i] = zv[c][i] = 0.f;
+                            for (int i = 0; i < NR; ++i)
+                                if (tok < lim[i]) za[i][c] = NAN;
+                        if (!in || nan) sv[c][k] = zv[c][k] = 0.f;
                     }
                 }
-                bad &= ~(1u << (used & 31));
             }
-            float p[NT][4], top;
+            float p[NR][2], top;
             auto weights = [&]() {
                 top = 0.f;
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < NR; ++i)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        p[nt][i] = ex2(x[nt][i] - m[nt][i & 1]);
-                        top = fmaxf(top, p[nt][i]);
+                    for (int k = 0; k < 2; ++k) {
+                        p[i][k] = ex2(x[i][k] - m[i]);
+                        top = fmaxf(top, p[i][k]);
                     }
             };
             weights();
@@ -574,27 +636,30 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
             if (__any_sync(0xffffffffu, fmaxf(top, s_top * vs * (kQ4TopP / kQ4TopS)) > kQ4TopP)) {
                 // new maxima, and a new power of two on the scales
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int i = 0; i < NR; ++i) {
+                    float a = fmaxf(x[i][0], x[i][1]);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float a = fmaxf(x[nt][e], x[nt][2 + e]);
+                    for (int o = S::kPacked ? R : 4; o < 32; o <<= 1)
+                        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+                    a = fmaxf(a - 6.f, m[i]);
+                    const float f = ex2(m[i] - a);
+                    m[i] = a;
+                    l[i] *= f;
 #pragma unroll
-                        for (int o = 4; o < 32; o <<= 1)
-                            a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                        a = fmaxf(a - 6.f, m[nt][e]);
-                        const float f = ex2(m[nt][e] - a);
-                        m[nt][e] = a;
-                        l[nt][e] *= f;
+                    for (int c = 0; c < C; ++c) {
+                        za[i][c] *= f;
 #pragma unroll
-                        for (int c = 0; c < C; ++c) {
-                            za[nt][c][e] *= f;
+                        for (int j = 0; j < 4; ++j) {
+                            if (S::kPacked) {
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                O[nt][c][j][e] *= f;
-                                O[nt][c][j][2 + e] *= f;
+                                for (int k = 0; k < 4; ++k) O[0][c][j][k] *= f;
+                            } else {
+                                O[i / 2][c][j][i % 2] *= f;
+                                O[i / 2][c][j][2 + i % 2] *= f;
                             }
                         }
                     }
+                }
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1)
                     s_top = fmaxf(s_top, __shfl_xor_sync(0xffffffffu, s_top, o));
@@ -614,74 +679,102 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
                 }
                 weights();
             }
-            // the weights in two parts of fp16, tokens g and g + 8
-            uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int i = 0; i < NR; ++i) {
+                l[i] += p[i][0] + p[i][1];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float p0 = p[nt][2 * i], p1 = p[nt][2 * i + 1];
-                    l[nt][0] += p0;
-                    l[nt][1] += p1;
-                    ph[nt][i] = Pack<__half>::down(p0, p1);
-                    const float2 h = Pack<__half>::up(ph[nt][i]);
-                    pl[nt][i] = Pack<__half>::down(p0 - h.x, p1 - h.y);
-                }
+                for (int c = 0; c < C; ++c)
+                    za[i][c] = fmaf(p[i][0], zv[c][0], fmaf(p[i][1], zv[c][1], za[i][c]));
+            }
+            if constexpr (S::kPacked) {
 #pragma unroll
-            for (int c = 0; c < C; ++c) {
-                uint32_t r[4];
-                ldsm_x4_trans(r[0], r[1], r[2], r[3], vb + c * kQ4CellBytes + lm_off);
-                uint32_t s2[2];
+                for (int c = 0; c < C; ++c) {
+                    // both parts of a weight side by side: columns 2t and 2t + 1
+                    uint32_t b[2];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float v = sv[c][i] * vs;
-                    s2[i] = Pack<__half>::down(v, v);
-                }
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    uint32_t b[2], bl[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        za[nt][c][0] = fmaf(p[nt][2 * i], zv[c][i], za[nt][c][0]);
-                        za[nt][c][1] = fmaf(p[nt][2 * i + 1], zv[c][i], za[nt][c][1]);
-                        // times the scale: rounded, and what that and the weight left
-                        const uint32_t hi = q4_mul2(ph[nt][i], s2[i]);
-                        const uint32_t lo =
-                            q4_fma2(pl[nt][i], s2[i], q4_fma2(ph[nt][i], s2[i], hi ^ 0x80008000u));
-                        b[i] = q4_transpose(S::kDouble && t >= 2 ? lo : hi);
-                        if (!S::kDouble) bl[i] = q4_transpose(lo);
+                    for (int k = 0; k < 2; ++k) {
+                        const float w = p[0][k] * (sv[c][k] * vs);
+                        const float2 hi = Pack<__half>::up(Pack<__half>::down(w, w));
+                        b[k] = q4_transpose(Pack<__half>::down(w, w - hi.x));
                     }
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t mask = j & 1 ? 0x00f000f0u : 0x000f000fu;
-                        const int sh = j >> 1 ? 8 : 0;
-                        const uint32_t a0 = (r[0] >> sh) & mask, a1 = (r[2] >> sh) & mask;
-                        const uint32_t a2 = (r[1] >> sh) & mask, a3 = (r[3] >> sh) & mask;
-                        q4_mma(O[nt][c][j], a0, a1, a2, a3, b[0], b[1]);
-                        if (!S::kDouble) q4_mma(O[nt][c][j], a0, a1, a2, a3, bl[0], bl[1]);
+                    for (int j = 0; j < kPack; ++j) {
+                        uint32_t r[4];
+                        ldsm_x4_trans(r[0], r[1], r[2], r[3],
+                                      base + j * S::kChunkBytes + S::kTileBytes + c * kQ4CellBytes + lm_off);
+                        // a chunk's weights are in its own columns
+                        const bool own = 4 / R == 1 || (g >> 1) / R == j;
+                        values(r, O[0][c], own ? b[0] : 0u, own ? b[1] : 0u);
+                    }
+                }
+            } else {
+                // the weights' parts, tokens g and g + 8, of two columns
+                uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float p0 = p[2 * nt % NR][k], p1 = p[(2 * nt + 1) % NR][k];
+                        ph[nt][k] = Pack<__half>::down(p0, p1);
+                        const float2 h = Pack<__half>::up(ph[nt][k]);
+                        pl[nt][k] = Pack<__half>::down(p0 - h.x, p1 - h.y);
+                    }
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    uint32_t r[4], s2[2];
+                    ldsm_x4_trans(r[0], r[1], r[2], r[3], base + S::kTileBytes + c * kQ4CellBytes + lm_off);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float v = sv[c][k] * vs;
+                        s2[k] = Pack<__half>::down(v, v);
+                    }
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        uint32_t b[2], bl[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            // times the scale: rounded, and what that and the weight left
+                            const uint32_t hi = q4_mul2(ph[nt][k], s2[k]);
+                            const uint32_t lo = q4_fma2(
+                                pl[nt][k], s2[k], q4_fma2(ph[nt][k], s2[k], hi ^ 0x80008000u));
+                            b[k] = q4_transpose(hi);
+                            bl[k] = q4_transpose(lo);
+                        }
+                        values(r, O[nt][c], b[0], b[1]);
+                        values(r, O[nt][c], bl[0], bl[1]);
                     }
                 }
             }
         };
 
-        uint32_t slot = 0, prev = (S::kStages - 1) * S::kStageBytes;
+        bool gone = false;  // a wait gave up
         while (used < asked) {
-            q4_copy_wait<S::kStages - 2>();
-            __syncwarp();  // the stage is whole, and nothing reads the one before any more
-            ask(prev);
+            const int stage = used % S::kStages;
+            if (!mbar_wait(&s_full[warp][stage], (used / S::kStages) & 1u, &s_never)) {
+                gone = true;
+                break;
+            }
+            __syncwarp();  // nothing reads the stage before this one any more
+            ask();
             if (fresh) begin_unit();
-            chunk_step(slot);
-            prev = slot;
-            slot = slot == (S::kStages - 1) * S::kStageBytes ? 0 : slot + S::kStageBytes;
-            fresh = ++used == asked || cu.chunk + 1 == cu.q.chunks;
+            const int n = step_chunks(cu, count - upos);
+            const uint32_t lost = (bad >> (8 * (used & 3))) & 255u;
+            for (int j = 0; j < n; j += kPack)
+                pack_step(stage * S::kStageBytes + j * S::kChunkBytes, cu.chunk + j, n - j, lost >> (2 * j));
+            ++used;
+            upos += n;
+            cu.chunk += n;
+            fresh = used == asked || cu.chunk == cu.q.chunks;
             if (fresh) {
-                end_unit();
-                q4_next_unit<RT>(P, cu);
-            } else {
-                ++cu.chunk;
+                end_unit(cu.chunk);
+                if (cu.chunk == cu.q.chunks) q4_next_unit<R>(P, cu);
             }
         }
-        q4_copy_wait<0>();
+        if (gone) {
+            if (lane == 0 && P.err) atomicOr(P.err, PA_ERRBIT_TIMEOUT);
+            for (; used < asked; ++used)  // the warp's copies in flight
+                mbar_drain_wait(&s_full[warp][used % S::kStages], (used / S::kStages) & 1u, &s_never);
+        }
     }
     if (!P.whole) {
         if (lane == 0) P.tails[worker] = tail;
@@ -690,7 +783,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, RT>::kCtas))
 
     // rows without anything to attend over
     for (int s = blockIdx.x; s < P.num_seqs; s += gridDim.x) {
-        const Q4Seq q = q4_seq<RT>(P, s);
+        const Q4Seq q = q4_seq<R>(P, s);
         if (q.bad && tid == 0 && P.err) atomicOr(P.err, PA_ERRBIT_CONTEXT_LEN);
         if (q.chunks) continue;
         const int r0 = max(0, min(q.q0, P.num_tokens));

@@ -24,6 +24,9 @@ cudaError_t launch_q4_decode(const Q4DecodeParams &P, int rows, pa_dtype_t dtype
                              bool merge, cudaStream_t stream) {
     auto go = [&](auto t) -> cudaError_t {
         using T = decltype(t);
+        if constexpr (D <= 128)
+            if (rows == 1) return launch_q4_decode_rows<T, D, 1>(P, ctas, merge, stream);
+        if (rows == 2) return launch_q4_decode_rows<T, D, 2>(P, ctas, merge, stream);
         if (rows == 4) return launch_q4_decode_rows<T, D, 4>(P, ctas, merge, stream);
         if (rows == 8) return launch_q4_decode_rows<T, D, 8>(P, ctas, merge, stream);
         if constexpr (D <= 128) return launch_q4_decode_rows<T, D, 16>(P, ctas, merge, stream);
