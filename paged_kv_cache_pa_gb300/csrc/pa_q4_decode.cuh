@@ -62,6 +62,9 @@ namespace pa {
 
 constexpr int kQ4Warps = 4;  // of a CTA
 constexpr int kQ4Threads = 32 * kQ4Warps;
+// What a unit costs beside its chunks, in chunks: its query, the first maxima, its
+// output.  The warps' shares count it.
+constexpr int kQ4UnitCost = 2;
 constexpr int kQ4Sms = 152;  // that the workers are sized for (right for any number)
 constexpr float kQ4NoMax = -1e30f;   // m before any token: below every logit that counts
 // A weight (2^6 where the maximum was last taken) and a scale (below 2^5 then) beyond
@@ -218,12 +221,13 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
     }
     pdl_wait();  // earlier kernels on the stream may still write what this reads
 
-    // The batch's chunks, laid end to end: thread i's sequences are i * each ..
+    // The batch's units, laid end to end, each its chunks' number and kQ4UnitCost
+    // long; thread i's sequences are i * each ..
     const int each = (P.num_seqs + kQ4Threads - 1) / kQ4Threads;
     long long mine = 0;
     for (int s = tid * each; s < min(P.num_seqs, (tid + 1) * each); ++s) {
         const Q4Seq q = q4_seq<R>(P, s);
-        mine += (long long)q.chunks * q.tiles * P.num_kv_heads;
+        if (q.chunks) mine += (long long)(q.chunks + kQ4UnitCost) * q.tiles * P.num_kv_heads;
     }
     long long incl = mine;
 #pragma unroll
@@ -261,19 +265,23 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         for (;;) {
             q4_next_seq<R>(P, at);
             if (at.s >= P.num_seqs) break;
-            const long long n = (long long)at.q.chunks * at.q.tiles * P.num_kv_heads;
+            const long long n =
+                (long long)(at.q.chunks + kQ4UnitCost) * at.q.tiles * P.num_kv_heads;
             if (off < n) break;
             off -= n;
         }
-        const int count = (int)(end - start);  // chunks of the range
+        // A range that begins in what a unit costs beside its chunks has its first chunk.
+        const int count = (int)(end - start);  // length of the range
         int pos = 0;                           // of `at` in it
         if (at.s < P.num_seqs) {
-            const int unit = (int)off / at.q.chunks;
-            at.chunk = (int)off - unit * at.q.chunks;
+            const int length = at.q.chunks + kQ4UnitCost;
+            const int unit = (int)off / length, o = (int)off - unit * length;
+            at.chunk = max(0, o - kQ4UnitCost);
+            pos = max(0, kQ4UnitCost - o);
             at.head = unit / at.q.tiles;
             at.tile = unit - at.head * at.q.tiles;
             if (P.whole && at.chunk > 0) {  // that unit is the worker's in whose range it begins
-                pos = at.q.chunks - at.chunk;
+                pos = length - o + kQ4UnitCost;
                 q4_next_unit<R>(P, at);
             }
         }
@@ -296,16 +304,27 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             const int n = min(S::kStep, c.q.chunks - c.chunk);
             return P.whole ? n : min(n, left);
         };
-        auto ask = [&]() {
-            if (at.s >= P.num_seqs || !(pos < count || (P.whole && at.chunk > 0))) return;
-            const int n = step_chunks(at, count - pos);
-            if (at.chunk < ids_c || at.chunk + n > ids_c + 32) {
+        // What the next step needs, on its way while the one before is worked on: the block
+        // ids, and for a unit's first step its query rows (128 bytes a lane).
+        auto look_ahead = [&]() {
+            if (at.s >= P.num_seqs) return;
+            if (at.chunk < ids_c || at.chunk + S::kStep > ids_c + 32) {
                 ids_c = at.chunk;
                 const int c = ids_c + lane;
                 ids = c < at.q.chunks ? P.block_tables[(size_t)at.s * P.max_blocks_per_seq +
                                                        (c >> P.sub_shift)]
                                       : 0;
             }
+            const int r = at.tile * R + lane / C;
+            if (at.chunk == 0 && lane < R * C && r < at.q.n * P.G) {
+                const size_t row = (size_t)(at.q.q0 + r / P.G) * P.num_heads +
+                                   (size_t)at.head * P.G + r % P.G;
+                prefetch_l1(static_cast<const T *>(P.query) + row * D + lane % C * kQ4Group);
+            }
+        };
+        auto ask = [&]() {
+            if (at.s >= P.num_seqs || !(pos < count || (P.whole && at.chunk > 0))) return;
+            const int n = step_chunks(at, count - pos);
             const int stage = asked % S::kStages;
             // lane 2j: K tile of chunk j, lane 2j + 1: its V tile
             const int c = at.chunk + (lane >> 1);
@@ -330,9 +349,12 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             pos += n;
             at.chunk += n;
             if (at.chunk == at.q.chunks) {
+                pos += kQ4UnitCost;
                 if (q4_next_unit<R>(P, at)) ids_c = 1 << 30;
             }
+            look_ahead();
         };
+        look_ahead();
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) ask();
 
@@ -767,7 +789,10 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             fresh = used == asked || cu.chunk == cu.q.chunks;
             if (fresh) {
                 end_unit(cu.chunk);
-                if (cu.chunk == cu.q.chunks) q4_next_unit<R>(P, cu);
+                if (cu.chunk == cu.q.chunks) {
+                    upos += kQ4UnitCost;
+                    q4_next_unit<R>(P, cu);
+                }
             }
         }
         if (gone) {
