@@ -23,6 +23,9 @@ constexpr int kWholeChunks = 16;
 // A warp's least share of a batch whose contexts may be cut.
 constexpr int kMinShare = 4;
 
+constexpr int kMostUnitCost = 5;
+static_assert(Q4Shape<128, 1>::kUnitCost <= kMostUnitCost, "what a unit costs");
+
 struct Plan {
     int rows;     // query rows of a tile
     int ctas;
@@ -46,10 +49,10 @@ bool make_plan(Plan *p, int num_seqs, int num_heads, int num_kv_heads, int head_
                                                 : 16;
     const long long chunks = ((long long)max_context_len + kQ4Tokens - 1) / kQ4Tokens;
     const long long units = num_kv_heads * ((most + p->rows - 1) / p->rows);
-    if (most > INT_MAX || units > INT_MAX || units * (chunks + kQ4UnitCost) > INT_MAX) return false;
+    if (most > INT_MAX || units > INT_MAX || units * (chunks + kMostUnitCost) > INT_MAX) return false;
     // (bytes of a block; below, a warp's share of the chunks)
     if ((long long)num_kv_heads * PA_MAX_BLOCK_SIZE * PA_Q4_ROW_BYTES(head_dim) > INT_MAX ||
-        num_seqs * (units * (chunks + kQ4UnitCost) / 1024) > INT_MAX)
+        num_seqs * (units * (chunks + kMostUnitCost) / 1024) > INT_MAX)
         return false;
     p->whole = chunks <= kWholeChunks;
     const int top = head_dim == 64    ? max_workers<64>(p->rows)

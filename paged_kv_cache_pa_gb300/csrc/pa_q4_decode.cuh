@@ -62,9 +62,6 @@ namespace pa {
 
 constexpr int kQ4Warps = 4;  // of a CTA
 constexpr int kQ4Threads = 32 * kQ4Warps;
-// What a unit costs beside its chunks, in chunks: its query, the first maxima, its
-// output.  The warps' shares count it.
-constexpr int kQ4UnitCost = 2;
 constexpr int kQ4Sms = 152;  // that the workers are sized for (right for any number)
 constexpr float kQ4NoMax = -1e30f;   // m before any token: below every logit that counts
 // A weight (2^6 where the maximum was last taken) and a scale (below 2^5 then) beyond
@@ -166,6 +163,9 @@ struct Q4Shape {
     static_assert(kPack <= kStep, "a pack is of one stage");
     static constexpr int kTiles8 = kPacked ? 1 : R / 8;      // groups of eight columns
     static constexpr int kRows = kPacked ? 1 : 2 * kTiles8;  // rows of a lane
+    // What a unit costs beside its chunks, in chunks: its query, the first maxima, its
+    // output, half a pack that is not full.  The warps' shares count it.
+    static constexpr int kUnitCost = 3 + kPack / 2;
     static constexpr int kStageBytes = kStep * kChunkBytes;
     static constexpr int kCtas = D == 64 && R <= 8 ? 4 : 3;  // an SM
     static constexpr int kWorkers = kQ4Sms * kCtas * kQ4Warps;
@@ -221,13 +221,16 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
     }
     pdl_wait();  // earlier kernels on the stream may still write what this reads
 
-    // The batch's units, laid end to end, each its chunks' number and kQ4UnitCost
+    // (the merge kernel, which waits for this one's end)
+    if (!P.whole) pdl_trigger();
+
+    // The batch's units, laid end to end, each its chunks' number and S::kUnitCost
     // long; thread i's sequences are i * each ..
     const int each = (P.num_seqs + kQ4Threads - 1) / kQ4Threads;
     long long mine = 0;
     for (int s = tid * each; s < min(P.num_seqs, (tid + 1) * each); ++s) {
         const Q4Seq q = q4_seq<R>(P, s);
-        if (q.chunks) mine += (long long)(q.chunks + kQ4UnitCost) * q.tiles * P.num_kv_heads;
+        if (q.chunks) mine += (long long)(q.chunks + S::kUnitCost) * q.tiles * P.num_kv_heads;
     }
     long long incl = mine;
 #pragma unroll
@@ -266,7 +269,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             q4_next_seq<R>(P, at);
             if (at.s >= P.num_seqs) break;
             const long long n =
-                (long long)(at.q.chunks + kQ4UnitCost) * at.q.tiles * P.num_kv_heads;
+                (long long)(at.q.chunks + S::kUnitCost) * at.q.tiles * P.num_kv_heads;
             if (off < n) break;
             off -= n;
         }
@@ -274,14 +277,14 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         const int count = (int)(end - start);  // length of the range
         int pos = 0;                           // of `at` in it
         if (at.s < P.num_seqs) {
-            const int length = at.q.chunks + kQ4UnitCost;
+            const int length = at.q.chunks + S::kUnitCost;
             const int unit = (int)off / length, o = (int)off - unit * length;
-            at.chunk = max(0, o - kQ4UnitCost);
-            pos = max(0, kQ4UnitCost - o);
+            at.chunk = max(0, o - S::kUnitCost);
+            pos = max(0, S::kUnitCost - o);
             at.head = unit / at.q.tiles;
             at.tile = unit - at.head * at.q.tiles;
             if (P.whole && at.chunk > 0) {  // that unit is the worker's in whose range it begins
-                pos = length - o + kQ4UnitCost;
+                pos = length - o + S::kUnitCost;
                 q4_next_unit<R>(P, at);
             }
         }
@@ -349,7 +352,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             pos += n;
             at.chunk += n;
             if (at.chunk == at.q.chunks) {
-                pos += kQ4UnitCost;
+                pos += S::kUnitCost;
                 if (q4_next_unit<R>(P, at)) ids_c = 1 << 30;
             }
             look_ahead();
@@ -370,6 +373,16 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         int first_chunk = 0, rows = 0, row0 = 0, upos = pos0;
         bool fresh = true;            // the step at hand begins a unit, or the range
         const int jl = S::kPacked ? t / R : 0;  // the lane's chunk of a pack
+
+        // 1 where chunk j of a pack is the lane's: its logits, its columns of the weights.
+        float own_f[kPack];
+        uint32_t own_c[kPack];
+#pragma unroll
+        for (int j = 0; j < kPack; ++j) {
+            own_f[j] = S::kPacked && t / R == j ? 1.f : 0.f;
+            own_c[j] = S::kPacked && (g >> 1) / R == j ? 1u : 0u;
+            asm volatile("" : "+f"(own_f[j]), "+r"(own_c[j]));
+        }
 
         auto begin_unit = [&]() {
             first_chunk = cu.chunk;
@@ -422,10 +435,25 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         for (int i = 0; i < 8; ++i) sum[c] += f[c][h][i];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
-                            const float *x = f[c][h] + 2 * i;
-                            qf[nt][c][h][i][0] = Pack<__half>::down(x[0] * norm, x[4] * norm);
-                            qf[nt][c][h][i][1] =
-                                Pack<__half>::down(x[1] * norm * 0.0625f, x[5] * norm * 0.0625f);
+                            // elements 2i (+ 4) and 2i + 1 (+ 4) of the word's eight
+                            const float e0 = f[c][h][2 * i] * norm, e4 = f[c][h][2 * i + 4] * norm;
+                            const float o0 = f[c][h][2 * i + 1] * (norm * 0.0625f);
+                            const float o4 = f[c][h][2 * i + 5] * (norm * 0.0625f);
+                            uint32_t(&q)[2] = qf[nt][c][h][i];
+                            if (!S::kPacked) {
+                                q[0] = Pack<__half>::down(e0, e4);
+                                q[1] = Pack<__half>::down(o0, o4);
+                            } else {
+                                // for n_0 and n_0 + 16 n_1: even columns the factors, odd ones
+                                // what their rounding left
+                                q[0] = Pack<__half>::down(e0 - o0, e4 - o4);
+                                q[1] = Pack<__half>::down(o0, o4);
+                                const float2 h0 = Pack<__half>::up(q[0]), h1 = Pack<__half>::up(q[1]);
+                                if (g & 1) {
+                                    q[0] = Pack<__half>::down(e0 - o0 - h0.x, e4 - o4 - h0.y);
+                                    q[1] = Pack<__half>::down(o0 - h1.x, o4 - h1.y);
+                                }
+                            }
                         }
                     }
                     sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 1);
@@ -535,9 +563,17 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const uint32_t lo = r[2 * h] >> (8 * i), hi = r[2 * h + 1] >> (8 * i);
-                    const uint32_t a0 = lo & 0x000f000fu, a1 = hi & 0x000f000fu;
-                    const uint32_t a2 = lo & 0x00f000f0u, a3 = hi & 0x00f000f0u;
+                    uint32_t a0, a1, a2, a3;
+                    if (S::kPacked) {
+                        a2 = i ? __byte_perm(r[2 * h], 0, 0x4341) : r[2 * h] & 0x00ff00ffu;
+                        a3 = i ? __byte_perm(r[2 * h + 1], 0, 0x4341) : r[2 * h + 1] & 0x00ff00ffu;
+                        a0 = a2 & 0x000f000fu;
+                        a1 = a3 & 0x000f000fu;
+                    } else {
+                        const uint32_t lo = r[2 * h] >> (8 * i), hi = r[2 * h + 1] >> (8 * i);
+                        a0 = lo & 0x000f000fu, a1 = hi & 0x000f000fu;
+                        a2 = lo & 0x00f000f0u, a3 = hi & 0x00f000f0u;
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
                         const uint32_t(&q)[2] = qf[nt][c][h][i];
@@ -577,9 +613,13 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         float acc[NT][4];
                         keys(base + j * S::kChunkBytes + c * kQ4CellBytes, c, acc);
                         if constexpr (S::kPacked) {
-                            if (kPack == 1 || j == 0 || jl == j) {
-                                a[c][0][0] = acc[0][0];
-                                a[c][0][1] = acc[0][2];
+                            // the lane's chunk, by a factor of 0 or 1: not another
+                            // instruction for the integer pipe
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const float u = acc[0][2 * k], v = acc[0][2 * k + 1];
+                                if (kPack == 1) a[c][0][k] = u + v;
+                                else a[c][0][k] = fmaf(v, own_f[j], j == 0 ? u * own_f[j] : fmaf(u, own_f[j], a[c][0][k]));
                             }
                         } else {
 #pragma unroll
@@ -725,8 +765,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         ldsm_x4_trans(r[0], r[1], r[2], r[3],
                                       base + j * S::kChunkBytes + S::kTileBytes + c * kQ4CellBytes + lm_off);
                         // a chunk's weights are in its own columns
-                        const bool own = 4 / R == 1 || (g >> 1) / R == j;
-                        values(r, O[0][c], own ? b[0] : 0u, own ? b[1] : 0u);
+                        if (kPack == 1) values(r, O[0][c], b[0], b[1]);
+                        else values(r, O[0][c], b[0] * own_c[j], b[1] * own_c[j]);
                     }
                 }
             } else {
@@ -790,7 +830,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             if (fresh) {
                 end_unit(cu.chunk);
                 if (cu.chunk == cu.q.chunks) {
-                    upos += kQ4UnitCost;
+                    upos += S::kUnitCost;
                     q4_next_unit<R>(P, cu);
                 }
             }
@@ -801,10 +841,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 mbar_drain_wait(&s_full[warp][used % S::kStages], (used / S::kStages) & 1u, &s_never);
         }
     }
-    if (!P.whole) {
-        if (lane == 0) P.tails[worker] = tail;
-        pdl_trigger();
-    }
+    if (!P.whole && lane == 0) P.tails[worker] = tail;
 
     // rows without anything to attend over
     for (int s = blockIdx.x; s < P.num_seqs; s += gridDim.x) {
@@ -819,47 +856,112 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
     }
 }
 
-// Puts together the units that the main kernel's ranges cut.  CTA = the worker
-// in whose range a unit begins; its parts are slot 1 of that worker and slot 0
-// of the ones behind it.
-template <typename T, int D, int RT>
-__global__ void __launch_bounds__(256) q4_merge_kernel(const __grid_constant__ Q4DecodeParams P) {
-    constexpr int kLanes = D / 4;               // threads of a row, four channels each
-    constexpr int kRowsAtOnce = 256 / kLanes;
+// Puts together the units that the main kernel's ranges cut: the unit that
+// begins in a worker's range and goes on has its parts in slot 1 of that worker
+// and slot 0 of the ones behind it.  A CTA takes kQ4MergeTails neighbouring workers,
+// a quarter of its warps each; where one of their units has many parts, all warps
+// take one after the other.  A warp sums some of the parts of a row, with 8
+// loads in flight; shared memory joins the warps of a row.
+constexpr int kQ4MergeThreads = 512;
+constexpr int kQ4MergeTails = 4;
+constexpr int kQ4MergeMany = 12;  // parts
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kQ4MergeThreads)
+    q4_merge_kernel(const __grid_constant__ Q4DecodeParams P) {
+    constexpr int kWarps = kQ4MergeThreads / 32, kVec = D / 32;  // channels of a lane
+    __shared__ float s_acc[kWarps][D];
+    __shared__ float s_l[kWarps];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
-    const int worker = blockIdx.x;
-    const int4 tail = P.tails[worker];
-    if (tail.x < 0) return;
-    const Q4Seq q = q4_seq<RT>(P, tail.x);
-    const int head = tail.y, row0 = tail.z * RT;
-    const int parts = 1 + tail.w, rows = min(RT, q.n * P.G - row0);
-    const int d0 = (threadIdx.x % kLanes) * 4;
-    for (int col = threadIdx.x / kLanes; col < rows; col += kRowsAtOnce) {
-        float M = kQ4NoMax, L = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < parts; ++i) {
-            const size_t slot = i == 0 ? 2 * (size_t)worker + 1 : 2 * (size_t)(worker + i);
-            const float2 ml = __ldcg(P.part_ml + slot * RT + col);
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(P.part + (slot * RT + col) * D + d0));
-            const float mn = fmaxf(M, ml.x);
-            const float fa = ex2(M - mn), fb = ex2(ml.x - mn);
-            M = mn;
-            L = L * fa + ml.y * fb;
-            acc.x = acc.x * fa + v.x * fb;
-            acc.y = acc.y * fa + v.y * fb;
-            acc.z = acc.z * fa + v.z * fb;
-            acc.w = acc.w * fa + v.w * fb;
+    int most = 0;
+    int4 tails[kQ4MergeTails];
+#pragma unroll
+    for (int i = 0; i < kQ4MergeTails; ++i) {
+        const int w = blockIdx.x * kQ4MergeTails + i;
+        tails[i] = w < P.workers ? __ldcg(P.tails + w) : make_int4(-1, 0, 0, 0);
+        if (tails[i].x >= 0) most = max(most, tails[i].w + 1);
+    }
+    if (most == 0) return;
+    const bool together = most > kQ4MergeMany;
+    const int group = together ? kWarps : kWarps / kQ4MergeTails;  // warps of a unit
+    const int in_group = warp % group;
+    for (int turn = 0; turn < (together ? kQ4MergeTails : 1); ++turn) {
+        const int which = together ? turn : warp / group;
+        int4 tail = tails[0];
+#pragma unroll
+        for (int i = 1; i < kQ4MergeTails; ++i)
+            if (which == i) tail = tails[i];
+        const bool any = tail.x >= 0;
+        Q4Seq q = {};
+        if (any) q = q4_seq<R>(P, tail.x);
+        const int row0 = tail.z * R, rows = any ? min(R, q.n * P.G - row0) : 0;
+        const int parts = 1 + tail.w;
+        const size_t worker = (size_t)blockIdx.x * kQ4MergeTails + which;
+        auto slot = [&](int i) { return i == 0 ? 2 * worker + 1 : 2 * (worker + i); };
+        // rows at once, and the warps of each (the same in every group of the CTA, whatever
+        // rows its unit has: the barriers below are the CTA's)
+        const int at_once = min(R, group), share = group / at_once;
+        for (int first = 0; first < R; first += at_once) {
+            const int row = first + in_group / share, mine = in_group % share;
+            const bool in = row < rows;
+            float M = kQ4NoMax, L = 0.f, acc[kVec] = {};
+            if (in) {
+                for (int i = lane; i < parts; i += 32)
+                    M = fmaxf(M, __ldcg(P.part_ml + slot(i) * R + row).x);
+#pragma unroll
+                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+#pragma unroll 8
+                for (int i = mine; i < parts; i += share) {
+                    const float2 ml = __ldcg(P.part_ml + slot(i) * R + row);
+                    const float *v = P.part + (slot(i) * R + row) * D + lane * kVec;
+                    const float f = ex2(ml.x - M);
+                    L = fmaf(ml.y, f, L);
+                    if constexpr (kVec == 2) {
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
+                        acc[0] = fmaf(x.x, f, acc[0]);
+                        acc[1] = fmaf(x.y, f, acc[1]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < kVec; k += 4) {
+                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(v + k));
+                            acc[k] = fmaf(x.x, f, acc[k]);
+                            acc[k + 1] = fmaf(x.y, f, acc[k + 1]);
+                            acc[k + 2] = fmaf(x.z, f, acc[k + 2]);
+                            acc[k + 3] = fmaf(x.w, f, acc[k + 3]);
+                        }
+                    }
+                }
+            }
+            if (mine > 0) {
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) s_acc[warp][lane * kVec + k] = acc[k];
+                if (lane == 0) s_l[warp] = L;
+            }
+            __syncthreads();
+            if (mine == 0 && in) {
+                for (int i = 1; i < share; ++i) {
+                    L += s_l[warp + i];
+#pragma unroll
+                    for (int k = 0; k < kVec; ++k) acc[k] += s_acc[warp + i][lane * kVec + k];
+                }
+                const float inv = L == 0.f ? 0.f : 1.f / L;
+                const int r = row0 + row;
+                const size_t o = ((size_t)(q.q0 + r / P.G) * P.num_heads + (size_t)tail.y * P.G + r % P.G) * D +
+                                 lane * kVec;
+                if (P.out_f32) {
+#pragma unroll
+                    for (int k = 0; k < kVec; k += 2)
+                        *reinterpret_cast<float2 *>(static_cast<float *>(P.out) + o + k) =
+                            make_float2(acc[k] * inv, acc[k + 1] * inv);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < kVec; k += 2)
+                        *reinterpret_cast<uint32_t *>(static_cast<T *>(P.out) + o + k) =
+                            Pack<T>::down(acc[k] * inv, acc[k + 1] * inv);
+                }
+            }
+            __syncthreads();
         }
-        const float inv = L == 0.f ? 0.f : 1.f / L;
-        const int r = row0 + col;
-        const size_t out_row =
-            (size_t)(q.q0 + r / P.G) * P.num_heads + (size_t)head * P.G + r % P.G;
-        if (P.out_f32)
-            *reinterpret_cast<float4 *>(static_cast<float *>(P.out) + out_row * D + d0) =
-                make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        else
-            *reinterpret_cast<uint2 *>(static_cast<T *>(P.out) + out_row * D + d0) =
-                make_uint2(Pack<T>::down(acc.x * inv, acc.y * inv), Pack<T>::down(acc.z * inv, acc.w * inv));
     }
 }
 

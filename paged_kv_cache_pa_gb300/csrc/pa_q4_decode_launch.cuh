@@ -14,7 +14,8 @@ cudaError_t launch_q4_decode_rows(const Q4DecodeParams &P, int ctas, bool merge,
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kQ4Threads), smem, stream, P);
     if (e == cudaSuccess && merge)
-        e = launch_pdl(q4_merge_kernel<T, D, RT>, dim3((unsigned)(ctas * kQ4Warps)), dim3(256), 0,
+        e = launch_pdl(q4_merge_kernel<T, D, RT>, dim3((unsigned)ctas * kQ4Warps / kQ4MergeTails),
+                       dim3(kQ4MergeThreads), 0,
                        stream, P);
     return e;
 }
