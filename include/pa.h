@@ -849,7 +849,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads
  *               num_tokens; or NULL: one token a sequence (num_tokens =
  *               num_seqs, max_query_len = 1)
  * context_lens  device int32 [num_seqs], 0 or n_s <= context_lens[s] <=
- *               max_context_len
+ *               max_context_len; lengths, tables and query_start_loc are read as
+ *               soon as the kernel starts (as pa_decode_attention reads them)
  * max_query_len host-known bound on n_s, 1 .. PA_MAX_Q4_QUERY (PA_ERR_UNSUPPORTED
  *               beyond); max_context_len host-known bound on context_lens,
  *               <= block_size * max_blocks_per_seq

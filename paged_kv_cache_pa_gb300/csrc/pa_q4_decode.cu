@@ -23,7 +23,7 @@ constexpr int kWholeChunks = 16;
 // A warp's least share of a batch whose contexts may be cut.
 constexpr int kMinShare = 4;
 
-constexpr int kMostUnitCost = 5;
+constexpr int kMostUnitCost = 8;
 static_assert(Q4Shape<128, 1>::kUnitCost <= kMostUnitCost, "what a unit costs");
 
 struct Plan {

@@ -165,7 +165,7 @@ struct Q4Shape {
     static constexpr int kRows = kPacked ? 1 : 2 * kTiles8;  // rows of a lane
     // What a unit costs beside its chunks, in chunks: its query, the first maxima, its
     // output, half a pack that is not full.  The warps' shares count it.
-    static constexpr int kUnitCost = 3 + kPack / 2;
+    static constexpr int kUnitCost = 4 + kPack;
     static constexpr int kStageBytes = kStep * kChunkBytes;
     static constexpr int kCtas = D == 64 && R <= 8 ? 4 : 3;  // an SM
     static constexpr int kWorkers = kQ4Sms * kCtas * kQ4Warps;
@@ -219,10 +219,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         for (int i = 0; i < S::kStages; ++i) mbar_init(&s_full[warp][i], 1);
         fence_mbar_init();
     }
-    pdl_wait();  // earlier kernels on the stream may still write what this reads
-
-    // (the merge kernel, which waits for this one's end)
-    if (!P.whole) pdl_trigger();
+    // (Lengths and tables are read before the wait, as the other decode calls read
+    // them: the search below and the first block ids overlap the kernel ahead.)
 
     // The batch's units, laid end to end, each its chunks' number and S::kUnitCost
     // long; thread i's sequences are i * each ..
@@ -358,6 +356,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             look_ahead();
         };
         look_ahead();
+        pdl_wait();  // earlier kernels on the stream may still write the query and the cache
+        if (!P.whole) pdl_trigger();  // (the merge kernel, which waits for this one's end)
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) ask();
 
@@ -371,6 +371,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         int lim[NR], lim_min = 0;     // tokens a row sees; the fewest of any
         float vs = 0.f;               // power of two on the values' scales
         int first_chunk = 0, rows = 0, row0 = 0, upos = pos0;
+        // (a tile of at most eight rows leaves the second eight columns out)
+        auto empty = [&](int nt) { return nt > 0 && rows <= 8 * nt; };
         bool fresh = true;            // the step at hand begins a unit, or the range
         const int jl = S::kPacked ? t / R : 0;  // the lane's chunk of a pack
 
@@ -499,8 +501,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             const bool all = first_chunk == 0 && stop == cu.q.chunks;
             const int slot = 2 * worker + (first_chunk == 0 ? 1 : 0);
             if (!all && first_chunk == 0)
-                tail = make_int4(cu.s, cu.head, cu.tile,
-                                 (int)((cu.q.chunks - stop + per - 1) / per));
+                tail = make_int4(cu.q.q0, cu.head, row0,
+                                 (int)((cu.q.chunks - stop + per - 1) / per) << 5 | rows);
             const float unscale = 0x1p24f / vs;
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
@@ -560,6 +562,10 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             uint32_t r[4];
             ldsm_x4(r[0], r[1], r[2], r[3], cell + lm_off);
 #pragma unroll
+            for (int nt = 1; nt < NT; ++nt)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[nt][i] = 0.f;
+#pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
@@ -576,8 +582,9 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
+                        if (empty(nt)) break;
                         const uint32_t(&q)[2] = qf[nt][c][h][i];
-                        if (h == 0 && i == 0) q4_mma_first(acc[nt], a0, a1, a2, a3, q[0], q[1]);
+                        if (nt == 0 && h == 0 && i == 0) q4_mma_first(acc[nt], a0, a1, a2, a3, q[0], q[1]);
                         else q4_mma(acc[nt], a0, a1, a2, a3, q[0], q[1]);
                     }
                 }
@@ -792,6 +799,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     }
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt) {
+                        if (empty(nt)) break;
                         uint32_t b[2], bl[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
@@ -841,7 +849,11 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 mbar_drain_wait(&s_full[warp][used % S::kStages], (used / S::kStages) & 1u, &s_never);
         }
     }
-    if (!P.whole && lane == 0) P.tails[worker] = tail;
+    pdl_wait();  // (the warps without work)
+    if (!P.whole) {
+        pdl_trigger();
+        if (lane == 0) P.tails[worker] = tail;
+    }
 
     // rows without anything to attend over
     for (int s = blockIdx.x; s < P.num_seqs; s += gridDim.x) {
@@ -860,8 +872,9 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 // begins in a worker's range and goes on has its parts in slot 1 of that worker
 // and slot 0 of the ones behind it.  A CTA takes kQ4MergeTails neighbouring workers,
 // a quarter of its warps each; where one of their units has many parts, all warps
-// take one after the other.  A warp sums some of the parts of a row, with 8
-// loads in flight; shared memory joins the warps of a row.
+// take one after the other.  A warp sums some of the parts of a row with many
+// loads in flight (what takes time here is the chain of loads); shared memory joins
+// the warps of a row.
 constexpr int kQ4MergeThreads = 512;
 constexpr int kQ4MergeTails = 4;
 constexpr int kQ4MergeMany = 12;  // parts
@@ -870,83 +883,89 @@ __global__ void __launch_bounds__(kQ4MergeThreads)
     q4_merge_kernel(const __grid_constant__ Q4DecodeParams P) {
     constexpr int kWarps = kQ4MergeThreads / 32, kVec = D / 32;  // channels of a lane
     __shared__ float s_acc[kWarps][D];
-    __shared__ float s_l[kWarps];
+    __shared__ float2 s_ml[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     int most = 0;
     int4 tails[kQ4MergeTails];
 #pragma unroll
     for (int i = 0; i < kQ4MergeTails; ++i) {
-        const int w = blockIdx.x * kQ4MergeTails + i;
-        tails[i] = w < P.workers ? __ldcg(P.tails + w) : make_int4(-1, 0, 0, 0);
-        if (tails[i].x >= 0) most = max(most, tails[i].w + 1);
+        tails[i] = __ldcg(P.tails + blockIdx.x * kQ4MergeTails + i);
+        if (tails[i].x >= 0) most = max(most, (tails[i].w >> 5) + 1);
     }
     if (most == 0) return;
     const bool together = most > kQ4MergeMany;
     const int group = together ? kWarps : kWarps / kQ4MergeTails;  // warps of a unit
     const int in_group = warp % group;
+    // rows at once, and the warps of each (the same in every group of the CTA, whatever
+    // rows its unit has: the barriers below are the CTA's)
+    const int at_once = min(R, group), share = group / at_once;
+    const int mine = in_group % share;
     for (int turn = 0; turn < (together ? kQ4MergeTails : 1); ++turn) {
         const int which = together ? turn : warp / group;
         int4 tail = tails[0];
 #pragma unroll
         for (int i = 1; i < kQ4MergeTails; ++i)
             if (which == i) tail = tails[i];
-        const bool any = tail.x >= 0;
-        Q4Seq q = {};
-        if (any) q = q4_seq<R>(P, tail.x);
-        const int row0 = tail.z * R, rows = any ? min(R, q.n * P.G - row0) : 0;
-        const int parts = 1 + tail.w;
+        const int rows = tail.x >= 0 ? tail.w & 31 : 0, row0 = tail.z;
+        const int parts = 1 + (tail.w >> 5);
         const size_t worker = (size_t)blockIdx.x * kQ4MergeTails + which;
         auto slot = [&](int i) { return i == 0 ? 2 * worker + 1 : 2 * (worker + i); };
-        // rows at once, and the warps of each (the same in every group of the CTA, whatever
-        // rows its unit has: the barriers below are the CTA's)
-        const int at_once = min(R, group), share = group / at_once;
         for (int first = 0; first < R; first += at_once) {
-            const int row = first + in_group / share, mine = in_group % share;
+            const int row = first + in_group / share;
             const bool in = row < rows;
             float M = kQ4NoMax, L = 0.f, acc[kVec] = {};
+            auto add = [&](float m, float l, const float (&x)[kVec]) {
+                const float mn = fmaxf(M, m);
+                const float fa = ex2(M - mn), fb = ex2(m - mn);
+                M = mn;
+                L = L * fa + l * fb;
+#pragma unroll
+                for (int k = 0; k < kVec; ++k) acc[k] = acc[k] * fa + x[k] * fb;
+            };
             if (in) {
-                for (int i = lane; i < parts; i += 32)
-                    M = fmaxf(M, __ldcg(P.part_ml + slot(i) * R + row).x);
+                constexpr int kBatch = D == 256 ? 6 : D == 128 ? 10 : 16;
+                for (int i0 = mine; i0 < parts; i0 += kBatch * share) {
+                    float2 ml[kBatch];
+                    float x[kBatch][kVec];
 #pragma unroll
-                for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-#pragma unroll 8
-                for (int i = mine; i < parts; i += share) {
-                    const float2 ml = __ldcg(P.part_ml + slot(i) * R + row);
-                    const float *v = P.part + (slot(i) * R + row) * D + lane * kVec;
-                    const float f = ex2(ml.x - M);
-                    L = fmaf(ml.y, f, L);
-                    if constexpr (kVec == 2) {
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
-                        acc[0] = fmaf(x.x, f, acc[0]);
-                        acc[1] = fmaf(x.y, f, acc[1]);
-                    } else {
+                    for (int j = 0; j < kBatch; ++j) {
+                        const int i = i0 + j * share;
+                        if (i >= parts) break;
+                        ml[j] = __ldcg(P.part_ml + slot(i) * R + row);
+                        const float *v = P.part + (slot(i) * R + row) * D + lane * kVec;
+                        if constexpr (kVec == 2) {
+                            *reinterpret_cast<float2 *>(x[j]) = __ldcg(reinterpret_cast<const float2 *>(v));
+                        } else {
 #pragma unroll
-                        for (int k = 0; k < kVec; k += 4) {
-                            const float4 x = __ldcg(reinterpret_cast<const float4 *>(v + k));
-                            acc[k] = fmaf(x.x, f, acc[k]);
-                            acc[k + 1] = fmaf(x.y, f, acc[k + 1]);
-                            acc[k + 2] = fmaf(x.z, f, acc[k + 2]);
-                            acc[k + 3] = fmaf(x.w, f, acc[k + 3]);
+                            for (int k = 0; k < kVec; k += 4)
+                                *reinterpret_cast<float4 *>(x[j] + k) =
+                                    __ldcg(reinterpret_cast<const float4 *>(v + k));
                         }
+                    }
+#pragma unroll
+                    for (int j = 0; j < kBatch; ++j) {
+                        if (i0 + j * share >= parts) break;
+                        add(ml[j].x, ml[j].y, x[j]);
                     }
                 }
             }
             if (mine > 0) {
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) s_acc[warp][lane * kVec + k] = acc[k];
-                if (lane == 0) s_l[warp] = L;
+                if (lane == 0) s_ml[warp] = make_float2(M, L);
             }
             __syncthreads();
             if (mine == 0 && in) {
                 for (int i = 1; i < share; ++i) {
-                    L += s_l[warp + i];
+                    float x[kVec];
 #pragma unroll
-                    for (int k = 0; k < kVec; ++k) acc[k] += s_acc[warp + i][lane * kVec + k];
+                    for (int k = 0; k < kVec; ++k) x[k] = s_acc[warp + i][lane * kVec + k];
+                    add(s_ml[warp + i].x, s_ml[warp + i].y, x);
                 }
                 const float inv = L == 0.f ? 0.f : 1.f / L;
                 const int r = row0 + row;
-                const size_t o = ((size_t)(q.q0 + r / P.G) * P.num_heads + (size_t)tail.y * P.G + r % P.G) * D +
+                const size_t o = ((size_t)(tail.x + r / P.G) * P.num_heads + (size_t)tail.y * P.G + r % P.G) * D +
                                  lane * kVec;
                 if (P.out_f32) {
 #pragma unroll
