@@ -64,6 +64,7 @@ struct Pack<__half> {
                                       *reinterpret_cast<const __half2 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+    static constexpr float kLeastScale = 0x1p-14f;  // the least that is not subnormal
     static constexpr uint32_t kInf2 = 0x7c007c00u;
     static constexpr uint32_t kNan2 = 0x7fff7fffu;
 };
@@ -81,6 +82,7 @@ struct Pack<__nv_bfloat16> {
                                              *reinterpret_cast<const __nv_bfloat162 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+    static constexpr float kLeastScale = 0x1p-100f;
     static constexpr uint32_t kInf2 = 0x7f807f80u;
     static constexpr uint32_t kNan2 = 0x7fff7fffu;
 };
@@ -99,45 +101,64 @@ __device__ __forceinline__ uint32_t q4_range8(const uint4 &v) {
 // A group's scale and least value from its (least, -greatest).
 struct Q4Scale {
     uint32_t params;  // s, z in T
-    float s, z, inv;  // inv: 1 / s, or 0 (see q4_codes8)
+    float s, z, inv;  // inv: 1 / s to 2^-22, or 0 (see q4_codes8)
 };
 template <typename T>
 __device__ __forceinline__ Q4Scale q4_scale(uint32_t range) {
     const float2 r = Pack<T>::up(range);
     const float width = -r.y - r.x;
     Q4Scale q;
-    if (width < INFINITY) {
-        const uint32_t s16 = Pack<T>::down(__fdiv_rn(width, 15.0f), 0.0f);
-        q.params = (s16 & 0xffffu) | (range << 16);
-        q.s = Pack<T>::up(s16).x;
-    } else {  // an infinity or a NaN among them, or a range past fp32
+    // width / 15, rounded once: a product with the reciprocal and its exact
+    // remainder's (right for every fp32 width above 2^-100; the type's rounding takes
+    // what is below)
+    float f = width * (1.0f / 15.0f);
+    f = fmaf(fmaf(-15.0f, f, width), 1.0f / 15.0f, f);
+    const uint32_t s16 = Pack<T>::down(width < 0x1p-100f ? __fdiv_rn(width, 15.0f) : f, 0.0f);
+    q.z = r.x;
+    q.s = Pack<T>::up(s16).x;
+    q.params = (s16 & 0xffffu) | (range << 16);
+    if (!(width < INFINITY)) {  // an infinity or a NaN among them, or a range past fp32
         q.params = Pack<T>::kNan2;
         q.s = 0.0f;
     }
-    q.z = r.x;
-    q.inv = q.s >= 0x1p-100f ? __frcp_rn(q.s) : 0.0f;
+    q.inv = q.s >= Pack<T>::kLeastScale ? __frcp_rn(q.s) : 0.0f;
     return q;
 }
 
-// n of eight elements.  The quotient is rounded to fp32 once (a product with
-// the reciprocal, corrected by its exact remainder), then to a whole number by
-// adding 1.5 2^23, whose low bits then hold it; the words' constant parts are
-// taken off together.  Scales whose reciprocal or remainders leave fp32's normal
-// range (bf16 groups a hair wide) are divided by.
+// The same by division, for scales that are subnormal in T (then 15 s may be
+// well below the range) or whose reciprocal or remainders leave fp32's normal range.
+template <typename T>
+__device__ __noinline__ uint32_t q4_codes8_small(uint4 v, float s, float z) {
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t w = 0;
+    if (!(s > 0.0f)) return 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 x = Pack<T>::up(u[i / 2]);
+        const float t = __fdiv_rn((i & 1 ? x.y : x.x) - z, s);
+        w |= (uint32_t)__float2int_rn(fminf(t, 15.0f)) << (4 * i);
+    }
+    return w;
+}
+
+// n of eight elements.  The quotient is a product with the reciprocal, corrected by
+// its exact remainder, which leaves ties where they are; adding 1.5 2^23 rounds it to
+// a whole number, in the low bits; the words' constant parts are taken off
+// together.  (s is at least range / 15 less half a step of T, so n stays below 15.5.)
 template <typename T>
 __device__ __forceinline__ uint32_t q4_codes8(const uint4 &v, const Q4Scale &q) {
+    if (q.inv == 0.0f) return q4_codes8_small<T>(v, q.s, q.z);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t acc = 0;
+    uint32_t acc = 0u - 0x4b400000u * 0x11111111u;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float2 x = Pack<T>::up(u[i / 2]);
         const float d = (i & 1 ? x.y : x.x) - q.z;
         float t = d * q.inv;
         t = fmaf(fmaf(-t, q.s, d), q.inv, t);
-        if (q.inv == 0.0f) t = __fdiv_rn(d, q.s);
-        acc += __float_as_uint(fminf(t, 15.0f) + 12582912.0f) << (4 * i);
+        acc += __float_as_uint(t + 12582912.0f) << (4 * i);
     }
-    return q.s > 0.0f ? acc - 0x4b400000u * 0x11111111u : 0u;
+    return acc;
 }
 
 // Eight elements from their word, as T.

@@ -37,6 +37,7 @@
 
 #include <cstdint>
 #include <cstring>
+#include <type_traits>
 
 #include "pa.h"
 #include "pa_host.cuh"
@@ -92,33 +93,54 @@ __device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 *cs) {
 }
 
 // A row's two chunks of every thread, quantised, to token `token` of tile `tile`
-// of a 4-bit pool.  Called by the `lpr` lanes of a row together (j: the lane's
+// of a 4-bit pool.  Called by the D / 16 lanes of a row together (j: the lane's
 // place among them).  A group's range is reduced over all of the row's lanes,
 // whichever of its chunks they hold: with a rotation of less than the head the
 // two halves' chunks are spread unevenly.
-template <typename T>
-__device__ __forceinline__ void store_q4(uint8_t *pool, size_t tile, int token, int cells, int lpr,
-                                         int j, int ca, int cb, const uint4 &a, const uint4 &b) {
-    const unsigned lane = threadIdx.x & 31;
-    const unsigned row = ((1u << lpr) - 1u) << (lane & ~(unsigned)(lpr - 1));
+template <typename T, int D>
+__device__ __forceinline__ void store_q4(uint8_t *pool, size_t tile, int token, int j, int ca,
+                                         int cb, const uint4 &a, const uint4 &b) {
+    constexpr int kLanes = D / 16, kCells = D / kQ4Group;
+    const unsigned row = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(unsigned)(kLanes - 1));
     const uint32_t ra = q4_range8<T>(a), rb = q4_range8<T>(b);
-    uint8_t *cell = pool + tile * (size_t)(cells * kQ4CellBytes);
-    for (int g = 0; g < cells; ++g, cell += kQ4CellBytes) {
-        const bool ina = ca >> 3 == g, inb = cb >> 3 == g;
-        uint32_t x = Pack<T>::min2(ina ? ra : Pack<T>::kInf2, inb ? rb : Pack<T>::kInf2);
-        for (int o = 1; o < lpr; o <<= 1) x = Pack<T>::min2(x, __shfl_xor_sync(row, x, o));
-        const Q4Scale q = q4_scale<T>(x);
-        if (ina) *reinterpret_cast<uint32_t *>(cell + q4_word(token, ca & 7)) = q4_codes8<T>(a, q);
-        if (inb) *reinterpret_cast<uint32_t *>(cell + q4_word(token, cb & 7)) = q4_codes8<T>(b, q);
-        if (j == g) *reinterpret_cast<uint32_t *>(cell + kQ4CellParams + 4 * token) = q.params;
+    uint8_t *cells = pool + tile * (size_t)(kCells * kQ4CellBytes);
+    uint32_t range[kCells];
+#pragma unroll
+    for (int g = 0; g < kCells; ++g)
+        range[g] = kCells == 1 ? Pack<T>::min2(ra, rb)
+                               : Pack<T>::min2(ca >> 3 == g ? ra : Pack<T>::kInf2,
+                                               cb >> 3 == g ? rb : Pack<T>::kInf2);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+        for (int g = 0; g < kCells; ++g)
+            range[g] = Pack<T>::min2(range[g], __shfl_xor_sync(row, range[g], o));
+    uint32_t of_a = range[0], of_b = range[0], mine = range[0];
+#pragma unroll
+    for (int g = 1; g < kCells; ++g) {
+        if (ca >> 3 == g) of_a = range[g];
+        if (cb >> 3 == g) of_b = range[g];
+        if (j == g) mine = range[g];
     }
+    // (a lane of the first kCells writes a group's scale: it has that of its own
+    // chunks at hand, or makes it)
+    const Q4Scale qa = q4_scale<T>(of_a);
+    *reinterpret_cast<uint32_t *>(cells + (ca >> 3) * kQ4CellBytes + q4_word(token, ca & 7)) =
+        q4_codes8<T>(a, qa);
+    const Q4Scale qb = ca >> 3 == cb >> 3 ? qa : q4_scale<T>(of_b);
+    *reinterpret_cast<uint32_t *>(cells + (cb >> 3) * kQ4CellBytes + q4_word(token, cb & 7)) =
+        q4_codes8<T>(b, qb);
+    if (j < kCells)
+        *reinterpret_cast<uint32_t *>(cells + j * kQ4CellBytes + kQ4CellParams + 4 * token) =
+            j == ca >> 3 ? qa.params : j == cb >> 3 ? qb.params : q4_scale<T>(mine).params;
 }
 
 // A CTA takes `rounds` times 256 / (threads a row * rows at once) tokens; thread
 // = (token, row, unit j of the row).  A token's rows are its query heads, its
 // key heads and its value heads; a thread goes through its rows of all its
-// tokens as one list, four at a time.  Q4: the pools hold 4 bits an element.
-template <typename T, bool IL, bool Q4>
+// tokens as one list, four at a time.  QD: 0 for 16-bit pools, else 4-bit pools of
+// that head_dim.
+template <typename T, bool IL, int QD>
 __global__ void __launch_bounds__(kRotThreads)
     rotary_cache_write_kernel(const __grid_constant__ RotaryParams P) {
     extern __shared__ __align__(16) float2 s_cs[];  // [token][pair]
@@ -240,9 +262,9 @@ __global__ void __launch_bounds__(kRotThreads)
             // the head's rows of the slot's block
             const size_t tile = ((size_t)(slot[u] >> P.block_shift) * Hkv + h) << P.block_shift;
             const int off = (int)(slot[u] & ((1 << P.block_shift) - 1));
-            if constexpr (Q4) {
-                store_q4<T>(static_cast<uint8_t *>(pool), (tile + off) / kQ4Tokens, off % kQ4Tokens,
-                            1 << (lg_cpr - 3), lpr, j, ca, cb, a[u], b[u]);
+            if constexpr (QD > 0) {
+                store_q4<T, QD>(static_cast<uint8_t *>(pool), (tile + off) / kQ4Tokens,
+                                off % kQ4Tokens, j, ca, cb, a[u], b[u]);
             } else {
                 uint4 *dst = static_cast<uint4 *>(pool) + ((tile + off) << lg_cpr);
                 dst[ca] = a[u];
@@ -345,12 +367,22 @@ inline pa_status_t rotary_write(void *query_out, int64_t query_out_stride, const
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaErrorInvalidValue;
     auto go = [&](auto kern) { e = launch_pdl(kern, grid, dim3(kRotThreads), smem, st, P); };
-    if (dtype == PA_F16) {
-        if (P.rot.interleaved) go(rotary_cache_write_kernel<__half, true, Q4>);
-        else go(rotary_cache_write_kernel<__half, false, Q4>);
+    auto dim = [&](auto d) {
+        constexpr int QD = decltype(d)::value;
+        if (dtype == PA_F16) {
+            if (P.rot.interleaved) go(rotary_cache_write_kernel<__half, true, QD>);
+            else go(rotary_cache_write_kernel<__half, false, QD>);
+        } else {
+            if (P.rot.interleaved) go(rotary_cache_write_kernel<__nv_bfloat16, true, QD>);
+            else go(rotary_cache_write_kernel<__nv_bfloat16, false, QD>);
+        }
+    };
+    if constexpr (!Q4) {
+        dim(std::integral_constant<int, 0>());
     } else {
-        if (P.rot.interleaved) go(rotary_cache_write_kernel<__nv_bfloat16, true, Q4>);
-        else go(rotary_cache_write_kernel<__nv_bfloat16, false, Q4>);
+        if (head_dim == 64) dim(std::integral_constant<int, 64>());
+        else if (head_dim == 128) dim(std::integral_constant<int, 128>());
+        else dim(std::integral_constant<int, 256>());
     }
     return e == cudaSuccess ? PA_OK : PA_ERR_CUDA;
 }
