@@ -98,6 +98,16 @@ __device__ __forceinline__ uint32_t q4_range8(const uint4 &v) {
     return Pack<T>::min2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
 }
 
+// Out of line: few groups are this narrow.
+static __device__ __noinline__ float q4_fifteenth(float width) { return __fdiv_rn(width, 15.0f); }
+
+// Reciprocal to one step (MUFU).
+__device__ __forceinline__ float q4_rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // A group's scale and least value from its (least, -greatest).
 struct Q4Scale {
     uint32_t params;  // s, z in T
@@ -113,7 +123,8 @@ __device__ __forceinline__ Q4Scale q4_scale(uint32_t range) {
     // what is below)
     float f = width * (1.0f / 15.0f);
     f = fmaf(fmaf(-15.0f, f, width), 1.0f / 15.0f, f);
-    const uint32_t s16 = Pack<T>::down(width < 0x1p-100f ? __fdiv_rn(width, 15.0f) : f, 0.0f);
+    if (width < 0x1p-100f) f = q4_fifteenth(width);
+    const uint32_t s16 = Pack<T>::down(f, 0.0f);
     q.z = r.x;
     q.s = Pack<T>::up(s16).x;
     q.params = (s16 & 0xffffu) | (range << 16);
@@ -121,7 +132,7 @@ __device__ __forceinline__ Q4Scale q4_scale(uint32_t range) {
         q.params = Pack<T>::kNan2;
         q.s = 0.0f;
     }
-    q.inv = q.s >= Pack<T>::kLeastScale ? __frcp_rn(q.s) : 0.0f;
+    q.inv = q.s >= Pack<T>::kLeastScale ? q4_rcp(q.s) : 0.0f;
     return q;
 }
 
@@ -149,14 +160,16 @@ template <typename T>
 __device__ __forceinline__ uint32_t q4_codes8(const uint4 &v, const Q4Scale &q) {
     if (q.inv == 0.0f) return q4_codes8_small<T>(v, q.s, q.z);
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    const float2 nz = make_float2(-q.z, -q.z), ns = make_float2(-q.s, -q.s);
+    const float2 inv = make_float2(q.inv, q.inv), whole = make_float2(12582912.0f, 12582912.0f);
     uint32_t acc = 0u - 0x4b400000u * 0x11111111u;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 x = Pack<T>::up(u[i / 2]);
-        const float d = (i & 1 ? x.y : x.x) - q.z;
-        float t = d * q.inv;
-        t = fmaf(fmaf(-t, q.s, d), q.inv, t);
-        acc += __float_as_uint(t + 12582912.0f) << (4 * i);
+    for (int i = 0; i < 4; ++i) {  // two at once
+        const float2 d = __fadd2_rn(Pack<T>::up(u[i]), nz);
+        float2 t = __fmul2_rn(d, inv);
+        t = __ffma2_rn(__ffma2_rn(t, ns, d), inv, t);
+        t = __fadd2_rn(t, whole);
+        acc += (__float_as_uint(t.x) << (8 * i)) + (__float_as_uint(t.y) << (8 * i + 4));
     }
     return acc;
 }

@@ -96,8 +96,8 @@ __device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 *cs) {
 // of a 4-bit pool.  Called by the D / 16 lanes of a row together (j: the lane's
 // place among them).  A group's range is reduced over all of the row's lanes,
 // whichever of its chunks they hold: with a rotation of less than the head the
-// two halves' chunks are spread unevenly.
-template <typename T, int D>
+// two halves' chunks are spread unevenly.  IL: both chunks are of one group.
+template <typename T, bool IL, int D>
 __device__ __forceinline__ void store_q4(uint8_t *pool, size_t tile, int token, int j, int ca,
                                          int cb, const uint4 &a, const uint4 &b) {
     constexpr int kLanes = D / 16, kCells = D / kQ4Group;
@@ -127,7 +127,8 @@ __device__ __forceinline__ void store_q4(uint8_t *pool, size_t tile, int token, 
     const Q4Scale qa = q4_scale<T>(of_a);
     *reinterpret_cast<uint32_t *>(cells + (ca >> 3) * kQ4CellBytes + q4_word(token, ca & 7)) =
         q4_codes8<T>(a, qa);
-    const Q4Scale qb = ca >> 3 == cb >> 3 ? qa : q4_scale<T>(of_b);
+    Q4Scale qb = qa;
+    if (!IL && ca >> 3 != cb >> 3) qb = q4_scale<T>(of_b);
     *reinterpret_cast<uint32_t *>(cells + (cb >> 3) * kQ4CellBytes + q4_word(token, cb & 7)) =
         q4_codes8<T>(b, qb);
     if (j < kCells)
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kRotThreads)
             const size_t tile = ((size_t)(slot[u] >> P.block_shift) * Hkv + h) << P.block_shift;
             const int off = (int)(slot[u] & ((1 << P.block_shift) - 1));
             if constexpr (QD > 0) {
-                store_q4<T, QD>(static_cast<uint8_t *>(pool), (tile + off) / kQ4Tokens,
+                store_q4<T, IL, QD>(static_cast<uint8_t *>(pool), (tile + off) / kQ4Tokens,
                                 off % kQ4Tokens, j, ca, cb, a[u], b[u]);
             } else {
                 uint4 *dst = static_cast<uint4 *>(pool) + ((tile + off) << lg_cpr);
