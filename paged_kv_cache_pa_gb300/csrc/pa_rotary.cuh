@@ -50,12 +50,17 @@ namespace {
 
 
 constexpr int kRotThreads = 256;
-constexpr int kRotBatch = 4;  // rows a thread has in flight
+// Rows a thread has in flight.  Quantising takes registers and instructions: two rows
+// and four CTAs an SM there (16384 tokens of 40 heads of 128: 176 us; four rows and
+// three CTAs 195, one row and six 180).
+template <bool Q4>
+constexpr int kRotBatch = Q4 ? 2 : 4;
+template <bool Q4>
+constexpr int kRotCtas = Q4 ? 4 : 0;  // 0: not stated
 
 struct RotaryParams {
     const uint4 *q, *k, *v;
-    uint4 *q_out;
-    void *k_cache, *v_cache;
+    uint4 *q_out, *k_cache, *v_cache;
     long long q_stride, k_stride, v_stride, q_out_stride;  // 16-byte chunks between tokens
     const int64_t *positions;                              // [num_axes][num_tokens]
     const int64_t *slot_mapping;
@@ -142,7 +147,7 @@ __device__ __forceinline__ void store_q4(uint8_t *pool, size_t tile, int token, 
 // tokens as one list, four at a time.  QD: 0 for 16-bit pools, else 4-bit pools of
 // that head_dim.
 template <typename T, bool IL, int QD>
-__global__ void __launch_bounds__(kRotThreads)
+__global__ void __launch_bounds__(kRotThreads, kRotCtas<(QD > 0)>)
     rotary_cache_write_kernel(const __grid_constant__ RotaryParams P) {
     extern __shared__ __align__(16) float2 s_cs[];  // [token][pair]
     const int lpr = 1 << P.lg_lpr, rows_at_once = 1 << P.lg_rows;
@@ -190,11 +195,12 @@ __global__ void __launch_bounds__(kRotThreads)
         }
     };
     auto in_list = [&](const At &p) { return p.tok < tokens && t0 + p.tok < P.num_tokens; };
-    uint4 a[kRotBatch], b[kRotBatch];
-    int64_t slot[kRotBatch];
+    constexpr int kBatch = kRotBatch<(QD > 0)>;
+    uint4 a[kBatch], b[kBatch];
+    int64_t slot[kBatch];
     auto load = [&](At p) {
 #pragma unroll
-        for (int u = 0; u < kRotBatch; ++u, next(p)) {
+        for (int u = 0; u < kBatch; ++u, next(p)) {
             if (!in_list(p)) break;
             const long long t = t0 + p.tok;
             const int r = p.r;
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kRotThreads)
     while (in_list(at)) {
         At p = at;
 #pragma unroll
-        for (int u = 0; u < kRotBatch; ++u, next(p)) {
+        for (int u = 0; u < kBatch; ++u, next(p)) {
             if (!in_list(p)) break;
             const long long t = t0 + p.tok;
             const int r = p.r;
@@ -247,30 +253,30 @@ __global__ void __launch_bounds__(kRotThreads)
                     turn_halves<T>(a[u], b[u], cs);
                 }
             }
+            uint4 *dst;
             if (r < H) {
-                uint4 *dst = P.q_out + t * P.q_out_stride + ((size_t)r << lg_cpr);
-                dst[ca] = a[u];
-                dst[cb] = b[u];
-                continue;
-            }
-            if (slot[u] < 0) continue;  // padding
-            if (slot[u] >= P.num_slots) {
-                if (r == H && j == 0 && P.err) atomicOr(P.err, PA_ERRBIT_SLOT_OOB);
-                continue;
-            }
-            const int h = r < H + Hkv ? r - H : r - H - Hkv;
-            void *pool = r < H + Hkv ? P.k_cache : P.v_cache;
-            // the head's rows of the slot's block
-            const size_t tile = ((size_t)(slot[u] >> P.block_shift) * Hkv + h) << P.block_shift;
-            const int off = (int)(slot[u] & ((1 << P.block_shift) - 1));
-            if constexpr (QD > 0) {
-                store_q4<T, IL, QD>(static_cast<uint8_t *>(pool), (tile + off) / kQ4Tokens,
-                                off % kQ4Tokens, j, ca, cb, a[u], b[u]);
+                dst = P.q_out + t * P.q_out_stride + ((size_t)r << lg_cpr);
             } else {
-                uint4 *dst = static_cast<uint4 *>(pool) + ((tile + off) << lg_cpr);
-                dst[ca] = a[u];
-                dst[cb] = b[u];
+                if (slot[u] < 0) continue;  // padding
+                if (slot[u] >= P.num_slots) {
+                    if (r == H && j == 0 && P.err) atomicOr(P.err, PA_ERRBIT_SLOT_OOB);
+                    continue;
+                }
+                const int h = r < H + Hkv ? r - H : r - H - Hkv;
+                // the slot's row of its head in the pool
+                const size_t at_row =
+                    ((((size_t)(slot[u] >> P.block_shift) * Hkv) + h) << P.block_shift) +
+                    (size_t)(slot[u] & ((1 << P.block_shift) - 1));
+                if constexpr (QD > 0) {
+                    store_q4<T, IL, QD>(reinterpret_cast<uint8_t *>(r < H + Hkv ? P.k_cache : P.v_cache),
+                                        at_row / kQ4Tokens, (int)(at_row % kQ4Tokens), j, ca, cb,
+                                        a[u], b[u]);
+                    continue;
+                }
+                dst = (r < H + Hkv ? P.k_cache : P.v_cache) + (at_row << lg_cpr);
             }
+            dst[ca] = a[u];
+            dst[cb] = b[u];
         }
         at = p;
         load(at);
@@ -330,8 +336,8 @@ inline pa_status_t rotary_write(void *query_out, int64_t query_out_stride, const
     P.k = (const uint4 *)key;
     P.v = (const uint4 *)value;
     P.q_out = (uint4 *)query_out;
-    P.k_cache = k_cache;
-    P.v_cache = v_cache;
+    P.k_cache = (uint4 *)k_cache;
+    P.v_cache = (uint4 *)v_cache;
     P.q_stride = query_stride / 8;
     P.k_stride = key_stride / 8;
     P.v_stride = value_stride / 8;
@@ -357,7 +363,7 @@ inline pa_status_t rotary_write(void *query_out, int64_t query_out_stride, const
     const int sms = device_sms();
     if (sms <= 0) return PA_ERR_CUDA;
     P.rounds = 1;
-    while (P.rounds * groups < kRotBatch &&
+    while (P.rounds * groups < kRotBatch<Q4> &&
            (long long)num_tokens >= 2ll * sms * lanes * (2 * P.rounds))
         P.rounds *= 2;
     const int tokens = lanes * P.rounds;
