@@ -64,6 +64,11 @@ struct Pack<__half> {
                                       *reinterpret_cast<const __half2 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        const __half2 h = __hmax2_nan(*reinterpret_cast<const __half2 *>(&a),
+                                      *reinterpret_cast<const __half2 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
     static constexpr float kLeastScale = 0x1p-14f;  // the least that is not subnormal
     static constexpr uint32_t kInf2 = 0x7c007c00u;
     static constexpr uint32_t kNan2 = 0x7fff7fffu;
@@ -82,6 +87,11 @@ struct Pack<__nv_bfloat16> {
                                              *reinterpret_cast<const __nv_bfloat162 *>(&b));
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+    static __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+        const __nv_bfloat162 h = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&b));
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
     static constexpr float kLeastScale = 0x1p-100f;
     static constexpr uint32_t kInf2 = 0x7f807f80u;
     static constexpr uint32_t kNan2 = 0x7fff7fffu;
@@ -91,11 +101,10 @@ struct Pack<__nv_bfloat16> {
 template <typename T>
 __device__ __forceinline__ uint32_t q4_range8(const uint4 &v) {
     const uint32_t lo = Pack<T>::min2(Pack<T>::min2(v.x, v.y), Pack<T>::min2(v.z, v.w));
-    const uint32_t hi = Pack<T>::min2(
-        Pack<T>::min2(v.x ^ 0x80008000u, v.y ^ 0x80008000u),
-        Pack<T>::min2(v.z ^ 0x80008000u, v.w ^ 0x80008000u));
-    // halves of lo, and of hi, against each other
-    return Pack<T>::min2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));
+    const uint32_t hi = Pack<T>::max2(Pack<T>::max2(v.x, v.y), Pack<T>::max2(v.z, v.w));
+    // halves of lo, and of -hi, against each other
+    return Pack<T>::min2(__byte_perm(lo, hi, 0x5410) ^ 0x80000000u,
+                         __byte_perm(lo, hi, 0x7632) ^ 0x80000000u);
 }
 
 // Out of line: few groups are this narrow.

@@ -99,46 +99,60 @@ __device__ __forceinline__ void turn_neighbours(uint4 &a, const float2 *cs) {
 
 // A row's two chunks of every thread, quantised, to token `token` of tile `tile`
 // of a 4-bit pool.  Called by the D / 16 lanes of a row together (j: the lane's
-// place among them).  A group's range is reduced over all of the row's lanes,
-// whichever of its chunks they hold: with a rotation of less than the head the
-// two halves' chunks are spread unevenly.  IL: both chunks are of one group.
+// place among them).  How the chunks lie decides which lanes have a group:
+//   IL: neighbouring chunks (interleaved pairs, or no rotation): four lanes;
+//   halves of the whole head: eight lanes have a group of the one half and a group
+//       of the other (D = 64: four lanes, both chunks);
+//   halves of a part of it: spread unevenly, so every group is reduced over all lanes.
 template <typename T, bool IL, int D>
 __device__ __forceinline__ void store_q4(uint8_t *pool, size_t tile, int token, int j, int ca,
-                                         int cb, const uint4 &a, const uint4 &b) {
+                                         int cb, bool whole, const uint4 &a, const uint4 &b) {
     constexpr int kLanes = D / 16, kCells = D / kQ4Group;
     const unsigned row = ((1u << kLanes) - 1u) << (threadIdx.x & 31 & ~(unsigned)(kLanes - 1));
-    const uint32_t ra = q4_range8<T>(a), rb = q4_range8<T>(b);
+    uint32_t ra = q4_range8<T>(a), rb = q4_range8<T>(b);
     uint8_t *cells = pool + tile * (size_t)(kCells * kQ4CellBytes);
-    uint32_t range[kCells];
+    uint8_t *cell_a = cells + (ca >> 3) * kQ4CellBytes, *cell_b = cells + (cb >> 3) * kQ4CellBytes;
+    auto reduce = [&](uint32_t x, int lanes) {
 #pragma unroll
-    for (int g = 0; g < kCells; ++g)
-        range[g] = kCells == 1 ? Pack<T>::min2(ra, rb)
-                               : Pack<T>::min2(ca >> 3 == g ? ra : Pack<T>::kInf2,
-                                               cb >> 3 == g ? rb : Pack<T>::kInf2);
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1)
-#pragma unroll
-        for (int g = 0; g < kCells; ++g)
-            range[g] = Pack<T>::min2(range[g], __shfl_xor_sync(row, range[g], o));
-    uint32_t of_a = range[0], of_b = range[0], mine = range[0];
-#pragma unroll
-    for (int g = 1; g < kCells; ++g) {
-        if (ca >> 3 == g) of_a = range[g];
-        if (cb >> 3 == g) of_b = range[g];
-        if (j == g) mine = range[g];
+        for (int o = 1; o < kLanes; o <<= 1)
+            if (o < lanes) x = Pack<T>::min2(x, __shfl_xor_sync(row, x, o));
+        return x;
+    };
+    if (IL || kCells == 1) {
+        const Q4Scale q = q4_scale<T>(reduce(Pack<T>::min2(ra, rb), 4));
+        *reinterpret_cast<uint32_t *>(cell_a + q4_word(token, ca & 7)) = q4_codes8<T>(a, q);
+        *reinterpret_cast<uint32_t *>(cell_b + q4_word(token, cb & 7)) = q4_codes8<T>(b, q);
+        if ((j & 3) == 0)
+            *reinterpret_cast<uint32_t *>(cell_a + kQ4CellParams + 4 * token) = q.params;
+        return;
     }
-    // (a lane of the first kCells writes a group's scale: it has that of its own
-    // chunks at hand, or makes it)
-    const Q4Scale qa = q4_scale<T>(of_a);
-    *reinterpret_cast<uint32_t *>(cells + (ca >> 3) * kQ4CellBytes + q4_word(token, ca & 7)) =
-        q4_codes8<T>(a, qa);
-    Q4Scale qb = qa;
-    if (!IL && ca >> 3 != cb >> 3) qb = q4_scale<T>(of_b);
-    *reinterpret_cast<uint32_t *>(cells + (cb >> 3) * kQ4CellBytes + q4_word(token, cb & 7)) =
-        q4_codes8<T>(b, qb);
-    if (j < kCells)
-        *reinterpret_cast<uint32_t *>(cells + j * kQ4CellBytes + kQ4CellParams + 4 * token) =
-            j == ca >> 3 ? qa.params : j == cb >> 3 ? qb.params : q4_scale<T>(mine).params;
+    bool first_a, first_b;  // the lane writes its chunks' scales
+    if (whole) {
+        ra = reduce(ra, 8);
+        rb = reduce(rb, 8);
+        first_a = first_b = (j & 7) == 0;
+    } else {
+        uint32_t of_a = 0, of_b = 0;
+        first_a = first_b = false;
+#pragma unroll
+        for (int g = 0; g < kCells; ++g) {
+            const bool in_a = ca >> 3 == g, in_b = cb >> 3 == g;
+            const uint32_t x = reduce(Pack<T>::min2(in_a ? ra : Pack<T>::kInf2, in_b ? rb : Pack<T>::kInf2), kLanes);
+            if (in_a) of_a = x;
+            if (in_b) of_b = x;
+            // (the lane that has the group's first chunk)
+            first_a |= ca == 8 * g;
+            first_b |= cb == 8 * g;
+        }
+        ra = of_a;
+        rb = of_b;
+    }
+    const Q4Scale qa = q4_scale<T>(ra);
+    *reinterpret_cast<uint32_t *>(cell_a + q4_word(token, ca & 7)) = q4_codes8<T>(a, qa);
+    if (first_a) *reinterpret_cast<uint32_t *>(cell_a + kQ4CellParams + 4 * token) = qa.params;
+    const Q4Scale qb = q4_scale<T>(rb);
+    *reinterpret_cast<uint32_t *>(cell_b + q4_word(token, cb & 7)) = q4_codes8<T>(b, qb);
+    if (first_b) *reinterpret_cast<uint32_t *>(cell_b + kQ4CellParams + 4 * token) = qb.params;
 }
 
 // A CTA takes `rounds` times 256 / (threads a row * rows at once) tokens; thread
@@ -270,7 +284,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas<(QD > 0)>)
                 if constexpr (QD > 0) {
                     store_q4<T, IL, QD>(reinterpret_cast<uint8_t *>(r < H + Hkv ? P.k_cache : P.v_cache),
                                         at_row / kQ4Tokens, (int)(at_row % kQ4Tokens), j, ca, cb,
-                                        a[u], b[u]);
+                                        rot_units == lpr, a[u], b[u]);
                     continue;
                 }
                 dst = (r < H + Hkv ? P.k_cache : P.v_cache) + (at_row << lg_cpr);
@@ -374,13 +388,14 @@ inline pa_status_t rotary_write(void *query_out, int64_t query_out_stride, const
     const cudaStream_t st = (cudaStream_t)stream;
     cudaError_t e = cudaErrorInvalidValue;
     auto go = [&](auto kern) { e = launch_pdl(kern, grid, dim3(kRotThreads), smem, st, P); };
+    const bool neighbours = P.rot.interleaved || plain;
     auto dim = [&](auto d) {
         constexpr int QD = decltype(d)::value;
         if (dtype == PA_F16) {
-            if (P.rot.interleaved) go(rotary_cache_write_kernel<__half, true, QD>);
+            if (neighbours) go(rotary_cache_write_kernel<__half, true, QD>);
             else go(rotary_cache_write_kernel<__half, false, QD>);
         } else {
-            if (P.rot.interleaved) go(rotary_cache_write_kernel<__nv_bfloat16, true, QD>);
+            if (neighbours) go(rotary_cache_write_kernel<__nv_bfloat16, true, QD>);
             else go(rotary_cache_write_kernel<__nv_bfloat16, false, QD>);
         }
     };
