@@ -167,7 +167,9 @@ struct Q4Shape {
     // output, half a pack that is not full.  The warps' shares count it.
     static constexpr int kUnitCost = 4 + kPack;
     static constexpr int kStageBytes = kStep * kChunkBytes;
-    static constexpr int kCtas = D == 64 && R <= 8 ? 4 : 3;  // an SM
+    // CTAs an SM: what the registers allow without spills (five tokens of 32 heads on 8 of
+    // 128: 87 us with two, 105 with three; 12 heads on 2 of 256: 35 and 45)
+    static constexpr int kCtas = D == 256 || (D == 128 && R == 16) ? 2 : D == 64 && R <= 8 ? 4 : 3;
     static constexpr int kWorkers = kQ4Sms * kCtas * kQ4Warps;
     static constexpr size_t kSmem = (size_t)kQ4Warps * kStages * kStageBytes;
 };
