@@ -860,7 +860,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads
  *               not share one, calls on one stream may, whatever their sizes
  * dev_error_word  device, may be NULL: PA_ERRBIT_CONTEXT_LEN for a sequence
  *               whose lengths break the rules (its rows are zeroed),
- *               PA_ERRBIT_BLOCK_OOB (the block's tokens are skipped)
+ *               PA_ERRBIT_BLOCK_OOB (the block's tokens are skipped),
+ *               PA_ERRBIT_TIMEOUT (out is not to be used)
  * Results do not depend on the block size or on the order in which work
  * finishes.  Enqueues one kernel, and a merge kernel where max_context_len is
  * above 256.

@@ -170,8 +170,8 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *tmap, int x, 
         : "memory");
 }
 
-__device__ __forceinline__ void prefetch_l1(const void *p) {
-    asm volatile("prefetch.global.L1 [%0];" ::"l"(p) : "memory");
+__device__ __forceinline__ void prefetch_l2(const void *p) {
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
 }
 
 __device__ __forceinline__ void prefetch_tmap(const void *tmap) {

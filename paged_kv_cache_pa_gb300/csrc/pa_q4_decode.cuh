@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             if (at.chunk == 0 && lane < R * C && r < at.q.n * P.G) {
                 const size_t row = (size_t)(at.q.q0 + r / P.G) * P.num_heads +
                                    (size_t)at.head * P.G + r % P.G;
-                prefetch_l1(static_cast<const T *>(P.query) + row * D + lane % C * kQ4Group);
+                prefetch_l2(static_cast<const T *>(P.query) + row * D + lane % C * kQ4Group);
             }
         };
         auto ask = [&]() {
@@ -409,8 +409,10 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         if (col < rows) {
                             const size_t row = (size_t)(cu.q.q0 + r / P.G) * P.num_heads +
                                                (size_t)cu.head * P.G + r % P.G;
-                            w = *reinterpret_cast<const uint4 *>(
-                                static_cast<const T *>(P.query) + row * D + c * 64 + h * 32 + 8 * t);
+                            // (from L2: what this SM has read of its line before the wait for
+                            // the kernel ahead may be older than what that has written)
+                            w = __ldcg(reinterpret_cast<const uint4 *>(
+                                static_cast<const T *>(P.query) + row * D + c * 64 + h * 32 + 8 * t));
                         }
                         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll

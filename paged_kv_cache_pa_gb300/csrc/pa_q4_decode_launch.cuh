@@ -1,17 +1,29 @@
 // pa_q4_decode_launch.cuh -- launches of the 4-bit decode kernels, per head_dim.
 #pragma once
 
+#include <atomic>
+
 #include "pa_q4_decode.cuh"
 
 namespace pa {
+
+constexpr int kMaxDevices = 64;
 
 template <typename T, int D, int RT>
 cudaError_t launch_q4_decode_rows(const Q4DecodeParams &P, int ctas, bool merge,
                                   cudaStream_t stream) {
     constexpr size_t smem = Q4Shape<D, RT>::kSmem;
     auto kern = q4_decode_kernel<T, D, RT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    static std::atomic<bool> set[kMaxDevices];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!set[dev].load(std::memory_order_relaxed)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return e;
+        set[dev].store(true, std::memory_order_relaxed);
+    }
     e = launch_pdl(kern, dim3((unsigned)ctas), dim3(kQ4Threads), smem, stream, P);
     if (e == cudaSuccess && merge)
         e = launch_pdl(q4_merge_kernel<T, D, RT>, dim3((unsigned)ctas * kQ4Warps / kQ4MergeTails),

@@ -290,3 +290,34 @@ def test_two_streams_at_once():
                 got[i].append(pa.decode_attention_q4(*args[i]))
     torch.cuda.synchronize()
     assert all(torch.equal(x, want[i]) for i in range(2) for x in got[i])
+
+
+@pytest.mark.parametrize("H,Hkv,D", [(8, 8, 128), (12, 2, 128), (16, 1, 64), (4, 2, 256)])
+def test_a_query_written_by_the_kernel_ahead(H, Hkv, D):
+    """The attention starts while the write ahead of it, a long one whose last tokens are the
+    queries, still runs: it must see what that writes."""
+    S, T, dt = 32, 6000, torch.bfloat16
+    g = torch.Generator(device=DEV).manual_seed(9)
+    c = Q4Cache([int(n) for n in torch.randint(20, 900, (S,), generator=torch.Generator().manual_seed(3))], Hkv, D, dt,
+                seed=2)
+    qkv = torch.randn(T, (H + 2 * Hkv) * D, generator=g, device=DEV).to(dt)
+    q, k, v = (t.view(T, -1, D) for t in qkv.split([H * D, Hkv * D, Hkv * D], 1))
+    spare = [torch.zeros(pa.q4_pool_shape(T // 16 + 1, Hkv, 16, D), dtype=torch.uint8, device=DEV) for _ in range(2)]
+    pos, slots = torch.arange(T, device=DEV), torch.arange(T, device=DEV)
+    rot = pa.Rotary([0.01 * (i + 1) for i in range(D // 2)])
+    out = torch.empty(T, H, D, dtype=dt, device=DEV)
+    ws = torch.empty(pa.decode_q4_workspace_size(S, H, Hkv, D, 1, c.max_len), dtype=torch.uint8, device=DEV)
+
+    def attend():
+        return pa.decode_attention_q4(out[-S:], c.k4[0], c.v4[0], c.tables, c.lens, c.max_len, 0.1, workspace=ws)
+
+    pa.rotary_cache_write_q4(q, k, v, pos, rot, *spare, slots, query_out=out)
+    torch.cuda.synchronize()
+    want = attend()
+    for _ in range(20):
+        out.fill_(float("nan"))
+        attend()                                      # (lines of the old query in the caches)
+        torch.cuda.synchronize()
+        pa.rotary_cache_write_q4(q, k, v, pos, rot, *spare, slots, query_out=out)
+        got = attend()
+        assert torch.equal(got, want)
