@@ -35,7 +35,9 @@ struct Plan {
 
 template <int D>
 int max_workers(int rows) {
-    return rows <= 8 ? Q4Shape<D, 8>::kWorkers : Q4Shape<D, 16>::kWorkers;
+    return rows <= 4   ? Q4Shape<D, 4>::kWorkers
+           : rows <= 8 ? Q4Shape<D, 8>::kWorkers
+                       : Q4Shape<D, 16>::kWorkers;
 }
 
 // False: sizes past what the kernels count in 32 bits.
@@ -49,7 +51,8 @@ bool make_plan(Plan *p, int num_seqs, int num_heads, int num_kv_heads, int head_
                                                 : 16;
     const long long chunks = ((long long)max_context_len + kQ4Tokens - 1) / kQ4Tokens;
     const long long units = num_kv_heads * ((most + p->rows - 1) / p->rows);
-    if (most > INT_MAX || units > INT_MAX || units * (chunks + kMostUnitCost) > INT_MAX) return false;
+    // (rows of a sequence: q4_token_of)
+    if (most >= 65536 || units > INT_MAX || units * (chunks + kMostUnitCost) > INT_MAX) return false;
     // (bytes of a block; below, a warp's share of the chunks)
     if ((long long)num_kv_heads * PA_MAX_BLOCK_SIZE * PA_Q4_ROW_BYTES(head_dim) > INT_MAX ||
         num_seqs * (units * (chunks + kMostUnitCost) / 1024) > INT_MAX)
@@ -149,6 +152,7 @@ extern "C" pa_status_t pa_decode_attention_q4(
     P.whole = plan.whole;
     P.workers = plan.ctas * kQ4Warps;
     P.scale_log2 = scale * 1.4426950408889634f;
+    P.inv_G = 1.0f / (float)P.G;
     const cudaStream_t st = (cudaStream_t)stream;
     const cudaError_t e =
         head_dim == 64    ? launch_q4_decode_d64(P, plan.rows, dtype, plan.ctas, !plan.whole, st)

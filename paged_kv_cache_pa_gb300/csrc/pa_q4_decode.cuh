@@ -83,8 +83,19 @@ struct Q4DecodeParams {
     int sub_shift;      // log2 of a block's tiles
     int whole;          // no unit is cut
     int workers;
-    float scale_log2;
+    float scale_log2, inv_G;
 };
+
+// Query token and head of row r of a sequence's rows, [token][G]: r / G of a number
+// below 2^16 by a product in fp32 (a half is far more than its rounding).
+__device__ __forceinline__ int q4_token_of(const Q4DecodeParams &P, int r) {
+    return __float2int_rz(((float)r + 0.5f) * P.inv_G);
+}
+// The row of [num_tokens][num_heads] that has row r of the sequence from token q0 on.
+__device__ __forceinline__ size_t q4_out_row(const Q4DecodeParams &P, int q0, int head, int r) {
+    const int i = q4_token_of(P, r);
+    return (size_t)(q0 + i) * P.num_heads + (size_t)(head * P.G + r - i * P.G);
+}
 
 // A sequence's share of the work.
 struct Q4Seq {
@@ -117,7 +128,7 @@ __device__ __forceinline__ Q4Seq q4_seq(const Q4DecodeParams &P, int s) {
 
 __device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                        uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
@@ -127,7 +138,7 @@ __device__ __forceinline__ void q4_mma(float (&d)[4], uint32_t a0, uint32_t a1, 
 // The same on a zeroed accumulator.
 __device__ __forceinline__ void q4_mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                              uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
         "{%8, %9}, {%10, %10, %10, %10};"
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
@@ -137,7 +148,7 @@ __device__ __forceinline__ void q4_mma_first(float (&d)[4], uint32_t a0, uint32_
 // An 8 x 8 matrix of 16-bit units, spread as ldmatrix gives it, transposed.
 __device__ __forceinline__ uint32_t q4_transpose(uint32_t a) {
     uint32_t d;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
 }
 
@@ -156,20 +167,24 @@ struct Q4Shape {
     static constexpr int kCells = D / kQ4Group;
     static constexpr int kTileBytes = kCells * kQ4CellBytes;
     static constexpr int kChunkBytes = 2 * kTileBytes;
-    static constexpr int kStep = D == 256 ? 2 : 4;           // chunks of a stage
-    static constexpr int kStages = D == 64 ? 3 : 2;
+    // Chunks of a stage: what asking for them costs is shared by more where shared memory
+    // has room.
+    static constexpr int kStep = D == 256 ? 2 : R < 8 ? 4 : D == 64 ? 8 : 6;
+    static constexpr int kStages = D == 64 && R < 8 ? 3 : 2;
     static constexpr bool kPacked = R <= 4;
     static constexpr int kPack = kPacked ? 4 / R : 1;        // chunks at once
-    static_assert(kPack <= kStep, "a pack is of one stage");
+    static constexpr int kUnroll = R >= 4 ? 2 : 1;           // packs at once
+    static_assert(kStep % (kPack * kUnroll) == 0, "packs are of one stage");
     static constexpr int kTiles8 = kPacked ? 1 : R / 8;      // groups of eight columns
     static constexpr int kRows = kPacked ? 1 : 2 * kTiles8;  // rows of a lane
     // What a unit costs beside its chunks, in chunks: its query, the first maxima, its
     // output, half a pack that is not full.  The warps' shares count it.
     static constexpr int kUnitCost = 4 + kPack;
     static constexpr int kStageBytes = kStep * kChunkBytes;
-    // CTAs an SM: what the registers allow without spills (five tokens of 32 heads on 8 of
-    // 128: 87 us with two, 105 with three; 12 heads on 2 of 256: 35 and 45)
-    static constexpr int kCtas = D == 256 || (D == 128 && R == 16) ? 2 : D == 64 && R <= 8 ? 4 : 3;
+    // CTAs an SM: what the registers allow without spills, which cost more than warps bring
+    // (drafts of five tokens, 32 heads on 8 of 128: 87 us with two, 105 with three; 12 heads
+    // on 2 of 256: 35 and 45; but 40 heads of 128, one row each: 166 with two, 143 with three)
+    static constexpr int kCtas = D == 256 || (D == 128 && R >= 8) ? 2 : D == 64 && R < 8 ? 4 : 3;
     static constexpr int kWorkers = kQ4Sms * kCtas * kQ4Warps;
     static constexpr size_t kSmem = (size_t)kQ4Warps * kStages * kStageBytes;
 };
@@ -212,13 +227,17 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
     __shared__ long long s_base[kQ4Threads];  // chunks of the batch before a thread's sequences
     __shared__ long long s_warp[kQ4Warps];
     __shared__ uint64_t s_full[kQ4Warps][S::kStages];
+    __shared__ uint32_t s_lost[kQ4Warps][S::kStages];  // tiles of a stage that were not copied
     __shared__ int s_never;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, t = lane & 3;
 
     if (tid == 0) s_never = 0;
     if (lane == 0) {
-        for (int i = 0; i < S::kStages; ++i) mbar_init(&s_full[warp][i], 1);
+        for (int i = 0; i < S::kStages; ++i) {
+            mbar_init(&s_full[warp][i], 1);
+            s_lost[warp][i] = 0;
+        }
         fence_mbar_init();
     }
     // (Lengths and tables are read before the wait, as the other decode calls read
@@ -250,7 +269,11 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
     __syncthreads();
 
     const int worker = blockIdx.x * kQ4Warps + warp;
-    const long long per = max((total + P.workers - 1) / P.workers, 1ll);
+    // (a 64-bit division takes longer than the rest of the search)
+    const long long per =
+        total <= 0x7fffffffll - P.workers
+            ? max(((int)total + P.workers - 1) / P.workers, 1)
+            : (total + P.workers - 1) / P.workers;
     const long long start = min(worker * per, total), end = min(start + per, total);
     int4 tail = make_int4(-1, 0, 0, 0);
 
@@ -299,7 +322,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         const uint8_t *lane_pool = lane & 1 ? P.v_cache : P.k_cache;
         const uint64_t policy = l2_evict_first_policy();
         int asked = 0, used = 0;  // steps
-        uint32_t bad = 0;         // of a step a byte: chunks whose block is outside the pool
+        bool any_lost = false;    // a block was outside the pool: s_lost counts from then on
         int ids = 0;              // the lane's block id, of chunk ids_c + lane
         int ids_c = 1 << 30;
         // chunks of the step at a cursor that has `left` chunks of the range before it
@@ -320,8 +343,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             }
             const int r = at.tile * R + lane / C;
             if (at.chunk == 0 && lane < R * C && r < at.q.n * P.G) {
-                const size_t row = (size_t)(at.q.q0 + r / P.G) * P.num_heads +
-                                   (size_t)at.head * P.G + r % P.G;
+                const size_t row = q4_out_row(P, at.q.q0, at.head, r);
                 prefetch_l2(static_cast<const T *>(P.query) + row * D + lane % C * kQ4Group);
             }
         };
@@ -334,10 +356,11 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             const int id = __shfl_sync(0xffffffffu, ids, (c - ids_c) & 31);
             const bool mine = lane < 2 * n, good = (unsigned)id < (unsigned)P.num_blocks;
             const uint32_t copies = __ballot_sync(0xffffffffu, mine && good);
-            const uint32_t lost = ~copies & ((1u << (2 * n)) - 1u);
-            bad = (bad & ~(255u << (8 * (asked & 3)))) | lost << (8 * (asked & 3));
+            const uint32_t lost = ~copies & (uint32_t)((1ull << (2 * n)) - 1ull);
+            any_lost |= lost != 0;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&s_full[warp][stage], __popc(copies) * S::kTileBytes);
+                if (any_lost) s_lost[warp][stage] = lost;
                 if (lost && P.err) atomicOr(P.err, PA_ERRBIT_BLOCK_OOB);
             }
             __syncwarp();
@@ -359,7 +382,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         };
         look_ahead();
         pdl_wait();  // earlier kernels on the stream may still write the query and the cache
-        if (!P.whole) pdl_trigger();  // (the merge kernel, which waits for this one's end)
+        pdl_trigger();  // (what follows waits for this kernel's end before it touches its data)
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) ask();
 
@@ -393,12 +416,12 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             row0 = cu.tile * R;
             rows = min(R, cu.q.n * P.G - row0);
             const int seen0 = cu.q.len - cu.q.n + 1;
-            lim_min = seen0 + row0 / P.G;
+            lim_min = seen0 + q4_token_of(P, row0);
             vs = 0x1p60f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int col = S::kPacked ? (g >> 1) % R : nt * 8 + g;
-                const int r = row0 + col;
+                const size_t row = q4_out_row(P, cu.q.q0, cu.head, row0 + col);
                 float f[C][2][8];
                 float top = 0.f;
 #pragma unroll
@@ -407,8 +430,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     for (int h = 0; h < 2; ++h) {
                         uint4 w = make_uint4(0, 0, 0, 0);
                         if (col < rows) {
-                            const size_t row = (size_t)(cu.q.q0 + r / P.G) * P.num_heads +
-                                               (size_t)cu.head * P.G + r % P.G;
                             // (from L2: what this SM has read of its line before the wait for
                             // the kernel ahead may be older than what that has written)
                             w = __ldcg(reinterpret_cast<const uint4 *>(
@@ -477,7 +498,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         qz[i][c] = __shfl_sync(0xffffffffu, sum[c], src);
                         za[i][c] = 0.f;
                     }
-                    lim[i] = seen0 + (row0 + nt * 8 + mine) / P.G;
+                    lim[i] = seen0 + q4_token_of(P, row0 + nt * 8 + mine);
                     m[i] = kQ4NoMax;
                     l[i] = 0.f;
                 }
@@ -506,18 +527,16 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             const int slot = 2 * worker + (first_chunk == 0 ? 1 : 0);
             if (!all && first_chunk == 0)
                 tail = make_int4(cu.q.q0, cu.head, row0,
-                                 (int)((cu.q.chunks - stop + per - 1) / per) << 5 | rows);
-            const float unscale = 0x1p24f / vs;
+                                 (cu.q.chunks - stop + (int)per - 1) / (int)per << 5 | rows);
+            const float unscale = 0x1p24f * __int_as_float((254 << 23) - __float_as_int(vs));  // 2^24 / vs
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 const int nt = i / 2, e = i % 2;
                 const int row = S::kPacked ? t % R : nt * 8 + 2 * t + e;  // of the tile
                 const bool in = row < rows && (!S::kPacked || t < R);
-                const int r = row0 + row;
-                const size_t out_row = (size_t)(cu.q.q0 + r / P.G) * P.num_heads +
-                                       (size_t)cu.head * P.G + r % P.G;
+                const size_t out_row = q4_out_row(P, cu.q.q0, cu.head, row0 + row);
                 const float ls = row_sum(l[i]);
-                const float inv = !all ? 1.f : ls == 0.f ? 0.f : 1.f / ls;
+                const float inv = !all ? 1.f : ls == 0.f ? 0.f : __fdividef(1.f, ls);
                 if (!all && in && g == 0) P.part_ml[(size_t)slot * R + row] = make_float2(m[i], ls);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
@@ -607,110 +626,130 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             }
         };
 
-        // A pack of chunks from chunk `chunk` on, `n` of them there, in the stage at `at_pack`;
-        // lost: bits of the tiles that were not copied.
+        // U packs of chunks from chunk `chunk` on, `n` of them there, in the stage at `at_pack`;
+        // lost: bits of the tiles that were not copied.  (Two packs, where the registers
+        // allow: one's products run while the other's logits are worked on.)
+        constexpr int U = S::kUnroll;
         auto pack_step = [&](uint32_t at_pack, int chunk, int n, uint32_t lost) {
             const uint32_t base = ring_u32 + at_pack;
+            // the scales of the lane's chunk
             const uint8_t *pk = ring + at_pack + jl * (S::kPacked ? S::kChunkBytes : 0) +
-                                kQ4CellParams + 4 * g;  // the lane's chunk's scales
+                                kQ4CellParams + 4 * g;
+            constexpr int kPackBytes = kPack * S::kChunkBytes;
             // x = scale <q, k> in units of log2, tokens g and g + 8 of the lane's rows
-            float x[NR][2];
-            {
-                float a[C][NR][2];
+            float x[U][NR][2];
+            float a[U][C][NR][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
 #pragma unroll
                 for (int j = 0; j < kPack; ++j)
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         float acc[NT][4];
-                        keys(base + j * S::kChunkBytes + c * kQ4CellBytes, c, acc);
+                        keys(base + u * kPackBytes + j * S::kChunkBytes + c * kQ4CellBytes, c, acc);
                         if constexpr (S::kPacked) {
                             // the lane's chunk, by a factor of 0 or 1: not another
                             // instruction for the integer pipe
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                const float u = acc[0][2 * k], v = acc[0][2 * k + 1];
-                                if (kPack == 1) a[c][0][k] = u + v;
-                                else a[c][0][k] = fmaf(v, own_f[j], j == 0 ? u * own_f[j] : fmaf(u, own_f[j], a[c][0][k]));
+                                const float v = acc[0][2 * k], w = acc[0][2 * k + 1];
+                                float &o = a[u][c][0][k];
+                                if (kPack == 1) o = v + w;
+                                else o = fmaf(w, own_f[j], j == 0 ? v * own_f[j] : fmaf(v, own_f[j], o));
                             }
                         } else {
 #pragma unroll
                             for (int i = 0; i < NR; ++i) {
-                                a[c][i][0] = acc[i / 2][i % 2];
-                                a[c][i][1] = acc[i / 2][2 + i % 2];
+                                a[u][c][i][0] = acc[i / 2][i % 2];
+                                a[u][c][i][1] = acc[i / 2][2 + i % 2];
                             }
                         }
                     }
+            // the values' scales and least values
+            float sv[U][C][2], zv[U][C][2];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const uint8_t *pu = pk + u * kPackBytes;
                 float y[NR][2];
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
-                    const float2 p0 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pk + c * kQ4CellBytes));
-                    const float2 p1 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pk + c * kQ4CellBytes + 32));
+                    const float2 p0 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pu + c * kQ4CellBytes));
+                    const float2 p1 = Pack<T>::up(*reinterpret_cast<const uint32_t *>(pu + c * kQ4CellBytes + 32));
 #pragma unroll
                     for (int i = 0; i < NR; ++i) {
-                        y[i][0] = c == 0 ? p0.x * a[c][i][0] : fmaf(p0.x, a[c][i][0], y[i][0]);
-                        y[i][1] = c == 0 ? p1.x * a[c][i][1] : fmaf(p1.x, a[c][i][1], y[i][1]);
-                        x[i][0] = c == 0 ? p0.y * qz[i][c] : fmaf(p0.y, qz[i][c], x[i][0]);
-                        x[i][1] = c == 0 ? p1.y * qz[i][c] : fmaf(p1.y, qz[i][c], x[i][1]);
+                        y[i][0] = c == 0 ? p0.x * a[u][c][i][0] : fmaf(p0.x, a[u][c][i][0], y[i][0]);
+                        y[i][1] = c == 0 ? p1.x * a[u][c][i][1] : fmaf(p1.x, a[u][c][i][1], y[i][1]);
+                        x[u][i][0] = c == 0 ? p0.y * qz[i][c] : fmaf(p0.y, qz[i][c], x[u][i][0]);
+                        x[u][i][1] = c == 0 ? p1.y * qz[i][c] : fmaf(p1.y, qz[i][c], x[u][i][1]);
                     }
                 }
 #pragma unroll
                 for (int i = 0; i < NR; ++i)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) x[i][k] = fmaf(y[i][k], c1[i], x[i][k]);
+                    for (int k = 0; k < 2; ++k) x[u][i][k] = fmaf(y[i][k], c1[i], x[u][i][k]);
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const float2 p = Pack<T>::up(*reinterpret_cast<const uint32_t *>(
+                            pu + S::kTileBytes + c * kQ4CellBytes + 32 * k));
+                        sv[u][c][k] = p.x;
+                        zv[u][c][k] = p.y;
+                    }
             }
-            // the values' scales and least values
-            float sv[C][2], zv[C][2];
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const float2 p = Pack<T>::up(*reinterpret_cast<const uint32_t *>(
-                        pk + S::kTileBytes + c * kQ4CellBytes + 32 * k));
-                    sv[c][k] = p.x;
-                    zv[c][k] = p.y;
-                }
-            if (n < kPack || lost || (chunk + kPack) * kQ4Tokens > lim_min) {
+            if (n < U * kPack || lost || (chunk + U * kPack) * kQ4Tokens > lim_min) {
                 // past the context or the range, past a row's own token, or a block that was
                 // skipped: whatever lies there must not meet a weight, not even one of zero
-                const bool there = jl < n && !((lost >> (2 * jl)) & 3u);
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int tok = (chunk + jl) * kQ4Tokens + g + 8 * k;
+                for (int u = 0; u < U; ++u) {
+                    const int j = u * kPack + jl;
+                    const bool there = j < n && !((lost >> (2 * j)) & 3u);
 #pragma unroll
-                    for (int i = 0; i < NR; ++i)
-                        if (!there || tok >= lim[i]) x[i][k] = -INFINITY;
+                    for (int k = 0; k < 2; ++k) {
+                        const int tok = (chunk + j) * kQ4Tokens + g + 8 * k;
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        const bool in = there && tok < cu.q.len;
-                        const bool nan = !(sv[c][k] + zv[c][k] == sv[c][k] + zv[c][k]);
-                        if (in && nan)  // of the rows that see it alone
+                        for (int i = 0; i < NR; ++i)
+                            if (!there || tok >= lim[i]) x[u][i][k] = -INFINITY;
 #pragma unroll
-                            for (int i = 0; i < NR; ++i)
-                                if (tok < lim[i]) za[i][c] = NAN;
-                        if (!in || nan) sv[c][k] = zv[c][k] = 0.f;
+                        for (int c = 0; c < C; ++c) {
+                            float &s = sv[u][c][k], &z = zv[u][c][k];
+                            const bool in = there && tok < cu.q.len;
+                            const bool nan = !(s + z == s + z);
+                            if (in && nan)  // of the rows that see it alone
+#pragma unroll
+                                for (int i = 0; i < NR; ++i)
+                                    if (tok < lim[i]) za[i][c] = NAN;
+                            if (!in || nan) s = z = 0.f;
+                        }
                     }
                 }
             }
-            float p[NR][2], top;
+            float p[U][NR][2], top;
             auto weights = [&]() {
                 top = 0.f;
 #pragma unroll
-                for (int i = 0; i < NR; ++i)
+                for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        p[i][k] = ex2(x[i][k] - m[i]);
-                        top = fmaxf(top, p[i][k]);
-                    }
+                    for (int i = 0; i < NR; ++i)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            p[u][i][k] = ex2(x[u][i][k] - m[i]);
+                            top = fmaxf(top, p[u][i][k]);
+                        }
             };
             weights();
             float s_top = 0.f;
 #pragma unroll
-            for (int c = 0; c < C; ++c) s_top = fmaxf(s_top, fmaxf(sv[c][0], sv[c][1]));
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int c = 0; c < C; ++c) s_top = fmaxf(s_top, fmaxf(sv[u][c][0], sv[u][c][1]));
             if (__any_sync(0xffffffffu, fmaxf(top, s_top * vs * (kQ4TopP / kQ4TopS)) > kQ4TopP)) {
                 // new maxima, and a new power of two on the scales
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
-                    float a = fmaxf(x[i][0], x[i][1]);
+                    float a = fmaxf(x[0][i][0], x[0][i][1]);
+#pragma unroll
+                    for (int u = 1; u < U; ++u) a = fmaxf(a, fmaxf(x[u][i][0], x[u][i][1]));
 #pragma unroll
                     for (int o = S::kPacked ? R : 4; o < 32; o <<= 1)
                         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
@@ -753,69 +792,75 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 weights();
             }
 #pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                l[i] += p[i][0] + p[i][1];
+            for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int c = 0; c < C; ++c)
-                    za[i][c] = fmaf(p[i][0], zv[c][0], fmaf(p[i][1], zv[c][1], za[i][c]));
-            }
-            if constexpr (S::kPacked) {
+                for (int i = 0; i < NR; ++i) {
+                    l[i] += p[u][i][0] + p[u][i][1];
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    // both parts of a weight side by side: columns 2t and 2t + 1
-                    uint32_t b[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float w = p[0][k] * (sv[c][k] * vs);
-                        const float2 hi = Pack<__half>::up(Pack<__half>::down(w, w));
-                        b[k] = q4_transpose(Pack<__half>::down(w, w - hi.x));
-                    }
-#pragma unroll
-                    for (int j = 0; j < kPack; ++j) {
-                        uint32_t r[4];
-                        ldsm_x4_trans(r[0], r[1], r[2], r[3],
-                                      base + j * S::kChunkBytes + S::kTileBytes + c * kQ4CellBytes + lm_off);
-                        // a chunk's weights are in its own columns
-                        if (kPack == 1) values(r, O[0][c], b[0], b[1]);
-                        else values(r, O[0][c], b[0] * own_c[j], b[1] * own_c[j]);
-                    }
+                    for (int c = 0; c < C; ++c)
+                        za[i][c] = fmaf(p[u][i][0], zv[u][c][0], fmaf(p[u][i][1], zv[u][c][1], za[i][c]));
                 }
-            } else {
-                // the weights' parts, tokens g and g + 8, of two columns
-                uint32_t ph[NT][2], pl[NT][2];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int u = 0; u < U; ++u) {
+                const uint32_t v_base = base + u * kPackBytes + S::kTileBytes + lm_off;
+                if constexpr (S::kPacked) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float p0 = p[2 * nt % NR][k], p1 = p[(2 * nt + 1) % NR][k];
-                        ph[nt][k] = Pack<__half>::down(p0, p1);
-                        const float2 h = Pack<__half>::up(ph[nt][k]);
-                        pl[nt][k] = Pack<__half>::down(p0 - h.x, p1 - h.y);
-                    }
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    uint32_t r[4], s2[2];
-                    ldsm_x4_trans(r[0], r[1], r[2], r[3], base + S::kTileBytes + c * kQ4CellBytes + lm_off);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const float v = sv[c][k] * vs;
-                        s2[k] = Pack<__half>::down(v, v);
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt) {
-                        if (empty(nt)) break;
-                        uint32_t b[2], bl[2];
+                    for (int c = 0; c < C; ++c) {
+                        // both parts of a weight side by side: columns 2t and 2t + 1
+                        uint32_t b[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            // times the scale: rounded, and what that and the weight left
-                            const uint32_t hi = q4_mul2(ph[nt][k], s2[k]);
-                            const uint32_t lo = q4_fma2(
-                                pl[nt][k], s2[k], q4_fma2(ph[nt][k], s2[k], hi ^ 0x80008000u));
-                            b[k] = q4_transpose(hi);
-                            bl[k] = q4_transpose(lo);
+                            const float w = p[u][0][k] * (sv[u][c][k] * vs);
+                            const float2 hi = Pack<__half>::up(Pack<__half>::down(w, w));
+                            b[k] = q4_transpose(Pack<__half>::down(w, w - hi.x));
                         }
-                        values(r, O[nt][c], b[0], b[1]);
-                        values(r, O[nt][c], bl[0], bl[1]);
+#pragma unroll
+                        for (int j = 0; j < kPack; ++j) {
+                            uint32_t r[4];
+                            ldsm_x4_trans(r[0], r[1], r[2], r[3],
+                                          v_base + j * S::kChunkBytes + c * kQ4CellBytes);
+                            // a chunk's weights are in its own columns
+                            if (kPack == 1) values(r, O[0][c], b[0], b[1]);
+                            else values(r, O[0][c], b[0] * own_c[j], b[1] * own_c[j]);
+                        }
+                    }
+                } else {
+                    // the weights' parts, tokens g and g + 8, of two columns
+                    uint32_t ph[NT][2], pl[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float p0 = p[u][2 * nt % NR][k], p1 = p[u][(2 * nt + 1) % NR][k];
+                            ph[nt][k] = Pack<__half>::down(p0, p1);
+                            const float2 h = Pack<__half>::up(ph[nt][k]);
+                            pl[nt][k] = Pack<__half>::down(p0 - h.x, p1 - h.y);
+                        }
+#pragma unroll
+                    for (int c = 0; c < C; ++c) {
+                        uint32_t r[4], s2[2];
+                        ldsm_x4_trans(r[0], r[1], r[2], r[3], v_base + c * kQ4CellBytes);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float v = sv[u][c][k] * vs;
+                            s2[k] = Pack<__half>::down(v, v);
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (empty(nt)) break;
+                            uint32_t b[2], bl[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                // times the scale: rounded, and what that and the weight left
+                                const uint32_t hi = q4_mul2(ph[nt][k], s2[k]);
+                                const uint32_t lo = q4_fma2(
+                                    pl[nt][k], s2[k], q4_fma2(ph[nt][k], s2[k], hi ^ 0x80008000u));
+                                b[k] = q4_transpose(hi);
+                                bl[k] = q4_transpose(lo);
+                            }
+                            values(r, O[nt][c], b[0], b[1]);
+                            values(r, O[nt][c], bl[0], bl[1]);
+                        }
                     }
                 }
             }
@@ -832,8 +877,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             ask();
             if (fresh) begin_unit();
             const int n = step_chunks(cu, count - upos);
-            const uint32_t lost = (bad >> (8 * (used & 3))) & 255u;
-            for (int j = 0; j < n; j += kPack)
+            const uint32_t lost = any_lost ? s_lost[warp][stage] : 0u;
+            for (int j = 0; j < n; j += U * kPack)
                 pack_step(stage * S::kStageBytes + j * S::kChunkBytes, cu.chunk + j, n - j, lost >> (2 * j));
             ++used;
             upos += n;
@@ -854,10 +899,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         }
     }
     pdl_wait();  // (the warps without work)
-    if (!P.whole) {
-        pdl_trigger();
-        if (lane == 0) P.tails[worker] = tail;
-    }
+    pdl_trigger();
+    if (!P.whole && lane == 0) P.tails[worker] = tail;
 
     // rows without anything to attend over
     for (int s = blockIdx.x; s < P.num_seqs; s += gridDim.x) {
@@ -954,6 +997,8 @@ __global__ void __launch_bounds__(kQ4MergeThreads)
                     }
                 }
             }
+            // (nothing of the workspace is read any more: a later call may write to it)
+            if (first + at_once >= R && (!together || turn + 1 == kQ4MergeTails)) pdl_trigger();
             if (mine > 0) {
 #pragma unroll
                 for (int k = 0; k < kVec; ++k) s_acc[warp][lane * kVec + k] = acc[k];
@@ -968,9 +1013,7 @@ __global__ void __launch_bounds__(kQ4MergeThreads)
                     add(s_ml[warp + i].x, s_ml[warp + i].y, x);
                 }
                 const float inv = L == 0.f ? 0.f : 1.f / L;
-                const int r = row0 + row;
-                const size_t o = ((size_t)(tail.x + r / P.G) * P.num_heads + (size_t)tail.y * P.G + r % P.G) * D +
-                                 lane * kVec;
+                const size_t o = q4_out_row(P, tail.x, tail.y, row0 + row) * D + lane * kVec;
                 if (P.out_f32) {
 #pragma unroll
                     for (int k = 0; k < kVec; k += 2)
