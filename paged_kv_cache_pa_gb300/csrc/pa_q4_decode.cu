@@ -21,9 +21,9 @@ namespace {
 // rows) alone, and no merge kernel runs.
 constexpr int kWholeChunks = 16;
 // A warp's least share of a batch whose contexts may be cut.
-constexpr int kMinShare = 4;
+constexpr int kMinShare = 8;
 
-constexpr int kMostUnitCost = 8;
+constexpr int kMostUnitCost = 7;
 static_assert(Q4Shape<128, 1>::kUnitCost <= kMostUnitCost, "what a unit costs");
 
 struct Plan {

@@ -11,18 +11,16 @@
 // group.
 //
 // Operands without conversion.  Read as fp16, the bits 0x000n are n 2^-24 (a
-// subnormal, which the tensor cores multiply exactly) and 0x00n0 are 16 n 2^-24.
-// Two nibbles of a 32-bit word become a pair of fp16 factors by one AND, eight by
-// a shift and four: no subtraction, no conversion.  The other factor takes up
-// the powers of two: odd nibbles' queries are divided by 16 ahead, odd channels
-// of the output at the end.  It works in fp16 only (bf16 has no such
-// subnormals), so a bf16 query goes to fp16, each row scaled by the power of two
-// that brings its largest element to 2^13: exact, but for elements 2^-28 of the
-// largest, where fp16 itself ends.
-//
-// The values' products take a byte's two nibbles as they lie, n_0 and n_0 + 16 n_1
-// (two ANDs, a byte permute and an AND for eight), and leave the subtraction to
-// the end.
+// subnormal, which the tensor cores multiply exactly), 0x00n0 are 16 n 2^-24 and a
+// byte 0x00hl is (l + 16 h) 2^-24.  A 32-bit word's eight nibbles become the pairs
+// l and l + 16 h by two ANDs, a byte permute and an AND; no subtraction, no
+// conversion.  The other side of the product makes up for it: a value's two
+// sums are subtracted at the end; a key's factors are q_1 / 16 for l + 16 h and q_0 - q_1 / 16
+// for l, in two parts of fp16 in the two columns that a row has (with more than
+// four rows, one column each: l and 16 h, by another shift, for q_0 and q_1 / 16).  It
+// works in fp16 only (bf16 has no such subnormals), so a query row is scaled by
+// the power of two that brings its largest element to 2^13; what fp16 then
+// cannot hold of an element is below 2^-34 of the largest.
 //
 // The weights p s go to fp16 in two parts (their rounding, and its remainder), so
 // their error is 2^-22 of them; a running power of two keeps them in range
@@ -45,8 +43,12 @@
 // itself by bulk copies, one a lane for every K and V tile.  A (sequence, head,
 // rows) that is cut leaves partial results, which the merge kernel puts together.
 //
-// Bound: HBM, 72 bytes a group and token of K and V; next, the integer pipe (the
-// nibbles' ANDs).
+// Bound: HBM, 72 bytes a group and token of K and V.  256 sequences of 40 heads of
+// 128, one row each: 137 us, 6.0 TB/s, 0.89 of the measured copy; without the
+// copies the same work takes 123, without the products 131.  With more rows the
+// products and the softmax bound it (8 heads of 64 rows in all, 125000 tokens: 46 us;
+// 39 without the values' products, 27 without any and without copies): the warps that
+// the registers leave (8 an SM) do not hide each other's latencies.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -63,7 +65,7 @@ namespace pa {
 constexpr int kQ4Warps = 4;  // of a CTA
 constexpr int kQ4Threads = 32 * kQ4Warps;
 constexpr int kQ4Sms = 152;  // that the workers are sized for (right for any number)
-constexpr float kQ4NoMax = -1e30f;   // m before any token: below every logit that counts
+constexpr float kQ4NoMax = -3e38f;   // m before any token
 // A weight (2^6 where the maximum was last taken) and a scale (below 2^5 then) beyond
 // which both are taken anew: their product stays below fp16's 2^16.
 constexpr float kQ4TopP = 1024.f, kQ4TopS = 32.f;
@@ -179,7 +181,7 @@ struct Q4Shape {
     static constexpr int kRows = kPacked ? 1 : 2 * kTiles8;  // rows of a lane
     // What a unit costs beside its chunks, in chunks: its query, the first maxima, its
     // output, half a pack that is not full.  The warps' shares count it.
-    static constexpr int kUnitCost = 4 + kPack;
+    static constexpr int kUnitCost = 3 + kPack;
     static constexpr int kStageBytes = kStep * kChunkBytes;
     // CTAs an SM: what the registers allow without spills, which cost more than warps bring
     // (drafts of five tokens, 32 heads on 8 of 128: 87 us with two, 105 with three; 12 heads
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
     using S = Q4Shape<D, R>;
     constexpr int NT = S::kTiles8, C = S::kCells, NR = S::kRows, kPack = S::kPack;
     extern __shared__ __align__(128) uint8_t s_ring[];
-    __shared__ long long s_base[kQ4Threads];  // chunks of the batch before a thread's sequences
+    __shared__ long long s_base[kQ4Threads];  // length of the batch before a thread's sequences
     __shared__ long long s_warp[kQ4Warps];
     __shared__ uint64_t s_full[kQ4Warps][S::kStages];
     __shared__ uint32_t s_lost[kQ4Warps][S::kStages];  // tiles of a stage that were not copied
@@ -451,7 +453,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 // zeros or with an infinity
                 const int nb = eb == 0 || eb == 255 ? 127 : max(1, min(250, 267 - eb));
                 const float norm = __int_as_float(nb << 23);
-                const float back = __int_as_float((254 - nb) << 23) * (0x1p24f * P.scale_log2);
+                const float back = __int_as_float((254 - nb) << 23) * 0x1p24f * P.scale_log2;
                 float sum[C];
 #pragma unroll
                 for (int c = 0; c < C; ++c) {

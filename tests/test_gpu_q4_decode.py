@@ -6,7 +6,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import paged_kv_cache_pa_gb300 as pa
-from q4lib import Q4Cache, attention, rounded
+from q4lib import Q4Cache, attention, rounded, values
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda:0"
@@ -284,3 +284,27 @@ def test_pools_past_four_gigabytes():
     want, _ = _run(c, q)
     got = pa.decode_attention_q4(q, k4, v4, far, c.lens, L, D ** -0.5)
     assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("H", [2, 12, 24])
+@pytest.mark.parametrize("scale", [1e30, -1e32, 3e34])
+def test_logits_of_any_size(H, scale):
+    """All weight on the largest logit, however far from zero the logits are: the output is that
+    token's value, s n + z in fp32."""
+    c = Q4Cache([300, 40], 2, 128, torch.bfloat16, seed=30)
+    q = _query(2, H, 128, torch.bfloat16)
+    out, err = _run(c, q, scale=scale)
+    assert err == 0
+    checked = 0
+    for s in range(2):
+        for h in range(H):
+            k, v = values(c.rows(c.k[0], s, h // (H // 2)))[0], values(c.rows(c.v[0], s, h // (H // 2)))
+            x = (q[s, h].double() @ k.T) * (1 if scale > 0 else -1)
+            top = x.topk(2)
+            if top.values[0] - top.values[1] < 1e-2:    # (fp32's rounding of a logit is far less)
+                continue
+            j = top.indices[0]
+            # two parts of the weight, 2^-22, and a few roundings in 32 bits
+            assert bool(((out[s, h].double() - v[0][j]).abs() <= 2.0 ** -20 * v[1][j]).all())
+            checked += 1
+    assert checked >= H
