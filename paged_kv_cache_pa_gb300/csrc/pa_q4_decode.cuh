@@ -22,6 +22,15 @@
 // the power of two that brings its largest element to 2^13; what fp16 then
 // cannot hold of an element is below 2^-34 of the largest.
 //
+// Sums around the middle.  The tensor cores cut what does not fit a sum off, always
+// towards zero: a sum of many terms of one sign, as n >= 0 makes it, loses half a
+// step a product, the same way every time (two documents of 131072 tokens: 1.6 10^-3
+// of the output, whose terms cancel to 1 / 200 of their size).  So the kernel adds up
+//     sum_j (p_j s_j) (n_j - 7.5) + sum_j p_j (z_j + 7.5 s_j),
+// the middle of a group in the second sum, which is fp32 with ordinary rounding,
+// and takes 7.5 sum p s off the products' sums every few chunks: they stay near zero
+// (1.2 10^-4 then, for 2 to 5% more time).
+//
 // The weights p s go to fp16 in two parts (their rounding, and its remainder), so
 // their error is 2^-22 of them; a running power of two keeps them in range
 // (below).
@@ -44,11 +53,12 @@
 // rows) that is cut leaves partial results, which the merge kernel puts together.
 //
 // Bound: HBM, 72 bytes a group and token of K and V.  256 sequences of 40 heads of
-// 128, one row each: 137 us, 6.0 TB/s, 0.89 of the measured copy; without the
-// copies the same work takes 123, without the products 131.  With more rows the
-// products and the softmax bound it (8 heads of 64 rows in all, 125000 tokens: 46 us;
-// 39 without the values' products, 27 without any and without copies): the warps that
-// the registers leave (8 an SM) do not hide each other's latencies.
+// 128, one row each: 140 us, 5.9 TB/s, 0.87 of the measured copy; before the sums'
+// correction the same work without the copies took 123, without the products
+// 131, all of it 137.  With more rows the products and the softmax bound it (64 heads on 8, 125000
+// tokens: 48 us; 39 without the values' products, 27 without any and without
+// copies): the warps that the registers leave (8 an SM) do not hide each other's
+// latencies.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -182,6 +192,8 @@ struct Q4Shape {
     // What a unit costs beside its chunks, in chunks: its query, the first maxima, its
     // output, half a pack that is not full.  The warps' shares count it.
     static constexpr int kUnitCost = 3 + kPack;
+    // Steps between two corrections of the sums: about eight chunks.
+    static constexpr int kCentre = kStep >= 6 ? 1 : 8 / kStep;
     static constexpr int kStageBytes = kStep * kChunkBytes;
     // CTAs an SM: what the registers allow without spills, which cost more than warps bring
     // (drafts of five tokens, 32 heads on 8 of 128: 87 us with two, 105 with three; 12 heads
@@ -393,6 +405,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         // every eight.
         float O[NT][C][4][4];     // [rows of 16 channels: cell, nibble][fragment]
         float m[NR], l[NR], za[NR][C];
+        float ws[NR][C];              // sum p s (scaled) that O has not been rid of 7.5 times of
         uint32_t qf[NT][C][2][2][2];  // the query's fragments: cell, half, nibble pair
         float c1[NR], qz[NR][C];
         int lim[NR], lim_min = 0;     // tokens a row sees; the fewest of any
@@ -498,7 +511,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         qz[i][c] = __shfl_sync(0xffffffffu, sum[c], src);
-                        za[i][c] = 0.f;
+                        za[i][c] = ws[i][c] = 0.f;
                     }
                     lim[i] = seen0 + q4_token_of(P, row0 + nt * 8 + mine);
                     m[i] = kQ4NoMax;
@@ -510,6 +523,30 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) O[nt][c][j][i] = 0.f;
+            }
+        };
+
+        // Takes the middle of the values off the sums (see above): of a column's tokens, in
+        // the lanes of its t; packed, all from the first parts' column.
+        auto centre = [&]() {
+            constexpr float kMid0 = 7.5f * 0x1p-24f, kMid1 = 127.5f * 0x1p-24f;  // n_0, n_0 + 16 n_1
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                if (!S::kPacked && empty(i / 2)) break;
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    float w = ws[i][c];
+                    ws[i][c] = 0.f;
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float &o = O[i / 2][c][j][2 * h + i % 2];
+                            o = fmaf(w, j & 1 ? -kMid1 : -kMid0, o);
+                        }
+                }
             }
         };
 
@@ -762,6 +799,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         za[i][c] *= f;
+                        ws[i][c] *= f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (S::kPacked) {
@@ -783,6 +821,10 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     const float f = nv / vs;
                     vs = nv;
 #pragma unroll
+                    for (int i = 0; i < NR; ++i)
+#pragma unroll
+                        for (int c = 0; c < C; ++c) ws[i][c] *= f;
+#pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int c = 0; c < C; ++c)
@@ -796,11 +838,22 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        zv[u][c][k] = fmaf(7.5f, sv[u][c][k], zv[u][c][k]);
+                        sv[u][c][k] *= vs;
+                    }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
                 for (int i = 0; i < NR; ++i) {
                     l[i] += p[u][i][0] + p[u][i][1];
 #pragma unroll
-                    for (int c = 0; c < C; ++c)
+                    for (int c = 0; c < C; ++c) {
                         za[i][c] = fmaf(p[u][i][0], zv[u][c][0], fmaf(p[u][i][1], zv[u][c][1], za[i][c]));
+                        ws[i][c] = fmaf(p[u][i][0], sv[u][c][0], fmaf(p[u][i][1], sv[u][c][1], ws[i][c]));
+                    }
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -812,7 +865,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         uint32_t b[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float w = p[u][0][k] * (sv[u][c][k] * vs);
+                            const float w = p[u][0][k] * sv[u][c][k];
                             const float2 hi = Pack<__half>::up(Pack<__half>::down(w, w));
                             b[k] = q4_transpose(Pack<__half>::down(w, w - hi.x));
                         }
@@ -844,8 +897,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         ldsm_x4_trans(r[0], r[1], r[2], r[3], v_base + c * kQ4CellBytes);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float v = sv[u][c][k] * vs;
-                            s2[k] = Pack<__half>::down(v, v);
+                            s2[k] = Pack<__half>::down(sv[u][c][k], sv[u][c][k]);
                         }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
@@ -886,6 +938,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             upos += n;
             cu.chunk += n;
             fresh = used == asked || cu.chunk == cu.q.chunks;
+            // every kCentre steps of the sequence; a unit's rest at its end
+            if (fresh || (cu.chunk / S::kStep) % S::kCentre == 0) centre();
             if (fresh) {
                 end_unit(cu.chunk);
                 if (cu.chunk == cu.q.chunks) {
