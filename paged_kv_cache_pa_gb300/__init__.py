@@ -712,7 +712,7 @@ def _layer_ptrs(xs, name, num_layers, shape, dtype):
     for x in xs:
         if x.shape != shape or x.dtype != dtype:
             raise ValueError(f"{name} must be {dtype} {list(shape)} in every layer")
-        ptrs.append(_dev(x, name))
+        ptrs.append(x.data_ptr() if x.is_cuda and x.is_contiguous() else _dev(x, name))
     return ptrs
 
 
@@ -813,8 +813,9 @@ def _q4_pools(k_cache, v_cache, heads, dim):
     u8 = _torch().uint8
     if k_cache.dtype != u8 or v_cache.dtype != u8:
         raise TypeError("4-bit pools must be uint8")
-    nb, hkv, bs, row = k_cache.shape
-    if v_cache.shape != k_cache.shape or hkv != heads or row * _Q4_GROUP != dim * _Q4_GROUP_BYTES:
+    shape = k_cache.shape
+    nb, hkv, bs, row = shape
+    if v_cache.shape != shape or hkv != heads or row * _Q4_GROUP != dim * _Q4_GROUP_BYTES:
         raise ValueError("shape mismatch between the rows and the 4-bit pools")
     return nb, bs
 
@@ -823,21 +824,22 @@ def cache_write_q4(key, value, k_cache, v_cache, slot_mapping, error_word=None,
                    stream=None) -> None:
     """Quantise key[t] / value[t] ([T][Hkv][D], token strides free) to 4 bits and write them into
     slot slot_mapping[t] (int64; < 0 skips) of 4-bit pools (q4_pool_shape)."""
-    torch = _torch()
-    T, hkv, d = key.shape
-    dt = key.dtype
-    if value.shape != (T, hkv, d) or value.dtype != dt:
+    shape, dt = key.shape, key.dtype
+    if value.shape != shape or value.dtype != dt:
         raise ValueError("key and value must have one shape and dtype")
+    T, hkv, d = shape
     nb, bs = _q4_pools(k_cache, v_cache, hkv, d)
-    if slot_mapping.dtype != torch.int64:
+    if slot_mapping.dtype != _torch().int64:
         raise TypeError("slot_mapping must be int64")
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
+    row = hkv * d
     st = load_library().pa_cache_write_q4(
-        *_rows(key, "key", hkv * d), *_rows(value, "value", hkv * d), _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"), T, nb, bs, hkv, d,
-        _dtype_code(dt), _opt_ptr(error_word, "error_word"), _stream_ptr(stream, key))
-    _check(st, "pa_cache_write_q4")
+        *_rows(key, "key", row), *_rows(value, "value", row), _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"), T, nb, bs, hkv, d, _dtype_code(dt),
+        None if error_word is None else _dev(error_word, "error_word"), _stream_ptr(stream, key))
+    if st:
+        _check(st, "pa_cache_write_q4")
 
 
 def rotary_cache_write_q4(query, key, value, positions, rotary: Rotary, k_cache, v_cache,
@@ -845,34 +847,36 @@ def rotary_cache_write_q4(query, key, value, positions, rotary: Rotary, k_cache,
     """rotary_cache_write into 4-bit pools (q4_pool_shape): the turned key, rounded to its
     dtype, and the value are quantised.  Returns the turned query: ``query_out``,
     ``query`` itself for an update in place, or a new dense tensor."""
-    torch = _torch()
-    T, H, d = query.shape
-    hkv, dt = key.shape[1], query.dtype
-    new = (T, hkv, d)
-    if key.shape != new or value.shape != new:
+    shape, new, dt = query.shape, key.shape, query.dtype
+    T, H, d = shape
+    t, hkv, e = new
+    if value.shape != new or t != T or e != d:
         raise ValueError("shape mismatch between query, key and value")
     if not dt == key.dtype == value.dtype:
         raise ValueError("query, key and value must have one dtype")
     nb, bs = _q4_pools(k_cache, v_cache, hkv, d)
-    if slot_mapping.dtype != torch.int64 or positions.dtype != torch.int64:
+    i64 = _torch().int64
+    if slot_mapping.dtype != i64 or positions.dtype != i64:
         raise TypeError("slot_mapping and positions must be int64")
     if slot_mapping.shape != (T,):
         raise ValueError("slot_mapping must be [T]")
-    if positions.shape[-1:] != (T,) or positions.dim() > 2 or \
-            (positions.shape[0] if positions.dim() == 2 else 1) < rotary.num_axes:
+    at = positions.shape
+    if (1 if at == (T,) else at[0] if len(at) == 2 and at[1] == T else 0) < rotary.num_axes:
         raise ValueError("positions must be [axes][T] with an axis for each the frequencies name")
     if query_out is None:
         query_out = _empty(stream, (T, H, d), dt, query.device, returned=True)
-    elif query_out is not query and (query_out.shape != (T, H, d) or query_out.dtype != dt):
+    elif query_out is not query and (query_out.shape != shape or query_out.dtype != dt):
         raise ValueError("query_out must match the query")
+    q_row, row = H * d, hkv * d
     st = load_library().pa_rotary_cache_write_q4(
-        *_rows(query_out, "query_out", H * d), *_rows(query, "query", H * d),
-        *_rows(key, "key", hkv * d), *_rows(value, "value", hkv * d),
+        *_rows(query_out, "query_out", q_row), *_rows(query, "query", q_row),
+        *_rows(key, "key", row), *_rows(value, "value", row),
         _dev(positions, "positions"), rotary._ptr,
         _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _dev(slot_mapping, "slot_mapping"),
-        T, nb, bs, H, hkv, d, _dtype_code(dt), _opt_ptr(error_word, "error_word"),
-        _stream_ptr(stream, query))
-    _check(st, "pa_rotary_cache_write_q4")
+        T, nb, bs, H, hkv, d, _dtype_code(dt),
+        None if error_word is None else _dev(error_word, "error_word"), _stream_ptr(stream, query))
+    if st:
+        _check(st, "pa_rotary_cache_write_q4")
     return query_out
 
 
@@ -892,17 +896,17 @@ def decode_attention_q4(query, k_cache, v_cache, block_tables, context_lens,
     tokens up to its own).  Returns ``out`` like the query's shape (fp32 unless
     ``out_dtype`` / ``out`` says the input dtype).  ``workspace`` (uint8, >=
     decode_q4_workspace_size bytes) is allocated here when not given."""
-    torch = _torch()
-    T, H, D = query.shape
+    shape, dt = query.shape, query.dtype
+    T, H, D = shape
     hkv = k_cache.shape[1]
     nb, bs = _q4_pools(k_cache, v_cache, hkv, D)
-    i32 = torch.int32
+    i32 = _torch().int32
     if block_tables.dtype != i32 or context_lens.dtype != i32 or (
             query_start_loc is not None and query_start_loc.dtype != i32):
         raise TypeError("block_tables, context_lens and query_start_loc must be int32")
-    S = context_lens.shape[0]
     tables = block_tables.shape
-    if len(tables) != 2 or tables[0] != S or context_lens.shape != (S,):
+    S = tables[0] if len(tables) == 2 else -1
+    if context_lens.shape != (S,):
         raise ValueError("block_tables must be [S][max_blocks], context_lens [S]")
     if query_start_loc is None:
         if T != S or max_query_len != 1:
@@ -910,8 +914,8 @@ def decode_attention_q4(query, k_cache, v_cache, block_tables, context_lens,
     elif query_start_loc.shape != (S + 1,):
         raise ValueError("query_start_loc must be [S+1]")
     if out is None:
-        out = _empty(stream, (T, H, D), out_dtype or torch.float32, query.device, returned=True)
-    elif out.shape != (T, H, D):
+        out = _empty(stream, (T, H, D), out_dtype or _torch().float32, query.device, returned=True)
+    elif out.shape != shape:
         raise ValueError("out must match the query")
     if workspace is None:
         nbytes = decode_q4_workspace_size(S, H, hkv, D, int(max_query_len), int(max_context_len))
@@ -919,12 +923,13 @@ def decode_attention_q4(query, k_cache, v_cache, block_tables, context_lens,
     st = load_library().pa_decode_attention_q4(
         _dev(out, "out"), _dtype_code(out.dtype), _dev(query, "query"), _dev(k_cache, "k_cache"),
         _dev(v_cache, "v_cache"), _dev(block_tables, "block_tables"), tables[1],
-        _opt_ptr(query_start_loc, "query_start_loc"), _dev(context_lens, "context_lens"),
-        int(max_query_len), int(max_context_len), S, T, H, hkv, D, nb, bs, float(scale),
-        _dtype_code(query.dtype), _dev(workspace, "workspace"),
-        workspace.numel() * workspace.element_size(), _opt_ptr(error_word, "error_word"),
-        _stream_ptr(stream, query))
-    _check(st, "pa_decode_attention_q4")
+        None if query_start_loc is None else _dev(query_start_loc, "query_start_loc"),
+        _dev(context_lens, "context_lens"), int(max_query_len), int(max_context_len), S, T, H,
+        hkv, D, nb, bs, float(scale), _dtype_code(dt), _dev(workspace, "workspace"),
+        workspace.nbytes,
+        None if error_word is None else _dev(error_word, "error_word"), _stream_ptr(stream, query))
+    if st:
+        _check(st, "pa_decode_attention_q4")
     return out
 
 
@@ -940,9 +945,9 @@ def unpack_blocks_q4(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_cache
         raise ValueError("need the same, non-zero number of pools on each side")
     if block_pairs.dtype != torch.int64:
         raise TypeError("block_pairs must be int64")
-    dst, dt = dst_k_caches[0].shape, dst_k_caches[0].dtype
+    first, u8 = dst_k_caches[0], torch.uint8
+    dst, dt, src = first.shape, first.dtype, src_k_caches[0].shape
     nd, hkv, bs, d = dst
-    src = src_k_caches[0].shape
     ns, sbs = _q4_pools(src_k_caches[0], src_v_caches[0], hkv, d)
     if sbs != bs:
         raise ValueError("pools must have one block size")
@@ -950,12 +955,14 @@ def unpack_blocks_q4(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_cache
     # the layers' pointers, one array after the other
     ptrs = _layer_ptrs(dst_k_caches, "dst_k_caches", L, dst, dt)
     ptrs += _layer_ptrs(dst_v_caches, "dst_v_caches", L, dst, dt)
-    ptrs += _layer_ptrs(src_k_caches, "src_k_caches", L, src, torch.uint8)
-    ptrs += _layer_ptrs(src_v_caches, "src_v_caches", L, src, torch.uint8)
+    ptrs += _layer_ptrs(src_k_caches, "src_k_caches", L, src, u8)
+    ptrs += _layer_ptrs(src_v_caches, "src_v_caches", L, src, u8)
     arrays = array.array("Q", ptrs)
-    base = arrays.buffer_info()[0]
+    base, step = arrays.buffer_info()[0], 8 * L
     st = load_library().pa_unpack_blocks_q4(
-        base, base + 8 * L, base + 16 * L, base + 24 * L, L,
+        base, base + step, base + 2 * step, base + 3 * step, L,
         _dev(block_pairs, "block_pairs") if npairs else None, npairs, nd, ns, bs, hkv, d,
-        _dtype_code(dt), _opt_ptr(error_word, "error_word"), _stream_ptr(stream, dst_k_caches[0]))
-    _check(st, "pa_unpack_blocks_q4")
+        _dtype_code(dt), None if error_word is None else _dev(error_word, "error_word"),
+        _stream_ptr(stream, first))
+    if st:
+        _check(st, "pa_unpack_blocks_q4")
