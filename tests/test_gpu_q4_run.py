@@ -321,3 +321,63 @@ def test_a_query_written_by_the_kernel_ahead(H, Hkv, D):
         pa.rotary_cache_write_q4(q, k, v, pos, rot, *spare, slots, query_out=out)
         got = attend()
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("call", ["attend", "attend_cut", "write", "unpack"])
+def test_a_16_bit_decode_in_memory_that_the_inputs_had(call):
+    """A 16-bit decode step right behind a 4-bit call, whose workspace lies where that call's
+    inputs did: its plan writes there as soon as it starts, and the 4-bit call must have read
+    them by then."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    S, H, Hkv, D, dt = 256, 32, 8, 128, torch.bfloat16
+    c = Q4Cache([250 if call != "attend_cut" else 700] * S, Hkv, D, dt, 16, seed=8)
+    # the 16-bit step: 64 sequences of 40 pages
+    k16, v16 = (torch.randn(64 * 40, 8, 16, 128, generator=g, device=DEV).to(dt) for _ in range(2))
+    q16 = torch.randn(64, 8, 128, generator=g, device=DEV).to(dt)
+    t16, l16 = _i32(np.arange(64 * 40).reshape(64, 40)), _i32(np.arange(64) * 9 + 1)
+    out16 = torch.empty(64, 8, 128, device=DEV)
+    nbytes = pa.decode_workspace_size(64, 8, 8, 128, 640)
+    mem = torch.empty(max(nbytes, 1 << 24), dtype=torch.uint8, device=DEV)
+    want16 = pa.decode_attention(q16, k16, v16, t16, l16, 640, 0.1)
+
+    def step16():
+        pa.decode_attention(q16, k16, v16, t16, l16, 640, 0.1, out=out16, workspace=mem)
+
+    if call in ("attend", "attend_cut"):
+        data = torch.randn(S, H, D, generator=g, device=DEV).to(dt)
+        there = mem[:data.nbytes].view(dt).view(S, H, D)
+        out = torch.empty(S, H, D, device=DEV)
+        ws = torch.empty(pa.decode_q4_workspace_size(S, H, Hkv, D, 1, c.max_len), dtype=torch.uint8, device=DEV)
+
+        def run(x):
+            pa.decode_attention_q4(x, c.k4[0], c.v4[0], c.tables, c.lens, c.max_len, 0.1, out=out, workspace=ws)
+            return [out]
+    elif call == "write":
+        T = 4000
+        data = torch.randn(T, Hkv, D, generator=g, device=DEV).to(dt)
+        there = mem[:data.nbytes].view(dt).view(T, Hkv, D)
+        pools = [torch.zeros(pa.q4_pool_shape(T // 16, Hkv, 16, D), dtype=torch.uint8, device=DEV) for _ in range(2)]
+        slots = torch.randperm(T, device=DEV)
+
+        def run(x):
+            pa.cache_write_q4(x, x, *pools, slots)
+            return pools
+    else:
+        n = c.tables.numel()
+        data = torch.stack([c.tables.flatten().long(), torch.arange(n, device=DEV)], 1).contiguous()
+        there = mem[:data.nbytes].view(torch.int64).view(n, 2)
+        pools = [torch.zeros(n, Hkv, 16, D, dtype=dt, device=DEV) for _ in range(2)]
+
+        def run(x):
+            pa.unpack_blocks_q4(pools[:1], pools[1:], c.k4[:1], c.v4[:1], x)
+            return pools
+    want = [t.clone() for t in run(data)]
+    for _ in range(20):
+        there.copy_(data)
+        for t in run(data):
+            t.zero_()
+        got = run(there)
+        step16()
+        # (bytes: slots that were never written unpack to NaN)
+        assert all(torch.equal(a.view(torch.uint8), b.view(torch.uint8)) for a, b in zip(got, want))
+        assert torch.equal(out16, want16)
