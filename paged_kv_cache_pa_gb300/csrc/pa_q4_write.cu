@@ -2,6 +2,10 @@
 // (turned by their positions, or not) and values into a cache held in 4 bits.
 // The kernel is that of pa_rotary.cuh, whose threads quantise their row together
 // before they store it: no pass over the new rows of its own.
+//
+// Bound: instructions.  16384 tokens of 40 heads of 128, K and V turned and all in 4 bits:
+// 165 us where the bytes alone would take 113 and the 16-bit write, with a third more
+// bytes, takes 150.
 #include <cuda_runtime.h>
 
 #include "pa.h"

@@ -52,7 +52,8 @@ namespace {
 constexpr int kRotThreads = 256;
 // Rows a thread has in flight.  Quantising takes registers and instructions: two rows
 // and four CTAs an SM there (16384 tokens of 40 heads of 128: 176 us; four rows and
-// three CTAs 195, one row and six 180).
+// three CTAs 195, one row and six 180; it takes 165 since a group's range comes from its
+// own lanes).
 template <bool Q4>
 constexpr int kRotBatch = Q4 ? 2 : 4;
 template <bool Q4>

@@ -173,3 +173,13 @@ def test_error_values_match_the_header():
     text = open(os.path.join(ROOT, "include", "pa.h")).read()
     assert re.search(r"#define PA_MAX_Q4_QUERY (\d+)", text).group(1) == str(pa.MAX_Q4_QUERY)
     assert re.search(r"PA_Q4 = (\d+)", text).group(1) == str(pa.PA_Q4)
+
+
+@pytest.mark.parametrize("shape", [(2,), (6,), (2, 3), (1, 2, 2)])
+def test_unpack_wants_pairs(shape):
+    """Rows of two: anything else would be read past its end."""
+    torch = pytest.importorskip("torch")
+    pool = torch.zeros(pa.q4_pool_shape(4, 2, 16, 64), dtype=torch.uint8)
+    half = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
+    with pytest.raises(ValueError, match="block_pairs must be"):
+        pa.unpack_blocks_q4([half], [half], [pool], [pool], torch.zeros(shape, dtype=torch.int64))
