@@ -143,18 +143,15 @@ WsLayout ws_layout(int num_seqs, int num_heads, int num_kv_heads, int head_dim,
 //     in 16-token chunks): shared-prefix pieces in list 0, the others in
 //     list 0 or, when the call runs the CUDA-core kernel beside the
 //     tensor-core one, in list 1.
-//  4. After the programmatic-dependent-launch wait: the per-sequence counts
-//     of partitions, and zero output rows for empty sequences.
+//  4. After the programmatic-dependent-launch wait: the lists, the
+//     per-sequence counts of partitions, and zero output rows for empty
+//     sequences.
 //
-// Steps 1-3 run before the wait, so they overlap the kernel before this call
-// on the stream (the cache write of a decode step): context_lens and
-// block_tables are inputs, complete before the call (a kernel that wrote
-// them has finished, unless it let dependents launch before writing), and
-// the work lists are free -- the attention kernels of earlier calls that
-// share the workspace read them in their producers, which release the claim
-// counters with a fence before they allow dependents to launch.  The
-// partition counts are written after the wait because the epilogue and the
-// merge of an earlier call may still read them until that call completes.
+// Steps 1-3, up to the places of the first 1024 sequences' pieces, run before
+// the wait, so they overlap the kernel before this call on the stream (the
+// cache write of a decode step): context_lens and block_tables are inputs,
+// complete before the call (a kernel that wrote them has finished, unless it
+// let dependents launch before writing).
 // ---------------------------------------------------------------------------
 // The plan's block: one thread per sequence up to 1024 (at least 128), so a
 // small batch's barriers involve few warps; with shared prefixes each
@@ -354,100 +351,121 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const __grid_constan
         __syncthreads();
     }
 
-    // ---- 2, 3. pieces, counted then placed longest first ------------------
-    // One pass counts (place = false), the other writes (place = true).
+    // ---- 2. pieces, counted ------------------------------------------------
     // Thread-strided over sequences, 1024 at a time; each thread handles its
     // sequence's own range and, for a group's first sequence, the prefix.
     // A range of len tokens is len / PT full pieces and one of len % PT.
-    const int own_list = A.split ? 1 : 0;
+    struct Range {
+        int first, len, t0, pbase, cnt, list;
+        bool grp;
+    };
+    // range 0: the group's shared prefix (its first sequence only);
+    // range 1: the sequence's own tokens
+    auto range_of = [&](int s, int L, const Group &g, int seg) {
+        Range r;
+        r.grp = seg == 0;
+        r.first = r.grp ? g.first : s;
+        r.t0 = r.grp ? 0 : g.T;
+        r.len = r.grp ? ((L > 0 && g.n >= 2 && g.first == s) ? g.T : 0) : (L > 0 ? L - g.T : 0);
+        r.pbase = r.grp ? 0 : pieces_of(g.T, PT);
+        r.cnt = r.grp ? g.n : r.pbase + pieces_of(r.len, PT);
+        r.list = r.grp ? 0 : (A.split ? 1 : 0);
+        return r;
+    };
     const int L_first = tid < S ? valid_len(A, tid) : 0;  // this thread's first sequence
-    for (int pass = 0; pass < 2; ++pass) {
-        const bool place = pass == 1;
-        for (int s0 = 0; s0 < S; s0 += (int)blockDim.x) {
-            const int s = s0 + tid;
-            const int L = s0 == 0 ? L_first : (s < S ? valid_len(A, s) : 0);
-            Group g = {s, 1, 0};
-            if (grouped && L > 0) g = group_of(A, sh, s, grouped);
-            // segment 0: the group's shared prefix (its first sequence only);
-            // segment 1: the sequence's own range
-            for (int seg = grouped ? 0 : 1; seg < 2; ++seg) {
-                int len, t0, pbase, list, cnt;
-                bool grp;
-                if (seg == 0) {
-                    grp = true;
-                    len = (L > 0 && g.n >= 2 && g.first == s) ? g.T : 0;
-                    t0 = 0;
-                    pbase = 0;
-                    list = 0;
-                    cnt = g.n;
-                } else {
-                    grp = false;
-                    len = L > 0 ? L - g.T : 0;
-                    t0 = g.T;
-                    pbase = pieces_of(g.T, PT);
-                    list = own_list;
-                    cnt = pbase + pieces_of(len, PT);
-                }
-                const int nf = len / PT, rem = len - nf * PT;
-                const int key = (rem + kBlock - 1) / kBlock;  // 0: no short piece
-                if (!place) {
-                    // full pieces: one add per warp; the short piece: one add
-                    int full = nf;
+    Group g_first = {tid, 1, 0};
+    if (grouped && L_first > 0) g_first = group_of(A, sh, tid, grouped);
+    for (int s0 = 0; s0 < S; s0 += (int)blockDim.x) {
+        const int s = s0 + tid;
+        const int L = s0 == 0 ? L_first : (s < S ? valid_len(A, s) : 0);
+        Group g = {s, 1, 0};
+        if (s0 == 0) g = g_first;
+        else if (grouped && L > 0) g = group_of(A, sh, s, grouped);
+        for (int seg = grouped ? 0 : 1; seg < 2; ++seg) {
+            const Range r = range_of(s, L, g, seg);
+            const int key = (r.len % PT + kBlock - 1) / kBlock;  // 0: no short piece
+            // full pieces: one add per warp; the short piece: one add
+            int full = r.len / PT;
 #pragma unroll
-                    for (int off = 16; off > 0; off >>= 1)
-                        full += __shfl_xor_sync(0xffffffffu, full, off);
-                    if (lane == 0 && full) atomicAdd(&sh.hist[list][PB], full);
-                    if (key) atomicAdd(&sh.hist[list][key], 1);
-                } else {
-                    // full pieces of the warp: a contiguous range from one add
-                    int incl = nf;
+            for (int off = 16; off > 0; off >>= 1) full += __shfl_xor_sync(0xffffffffu, full, off);
+            if (lane == 0 && full) atomicAdd(&sh.hist[r.list][PB], full);
+            if (key) atomicAdd(&sh.hist[r.list][key], 1);
+        }
+    }
+    __syncthreads();
+    int n_items = 0;  // of list tid / 32, in its lane 31
+    if (tid < (A.split ? 64 : 32)) {  // exclusive scans over sizes, largest first
+        const int list = tid >> 5;
+        const int key = PB - lane;
+        const int v = (lane < PB) ? sh.hist[list][key] : 0;
+        n_items = v;
 #pragma unroll
-                    for (int off = 1; off < 32; off <<= 1) {
-                        const int u = __shfl_up_sync(0xffffffffu, incl, off);
-                        if (lane >= off) incl += u;
-                    }
-                    int base = 0;
-                    if (lane == 31 && incl) base = atomicAdd(&sh.offs[list][PB], incl);
-                    base = __shfl_sync(0xffffffffu, base, 31) + incl - nf;
-                    int4 *items = list ? A.items1 : A.items0;
-                    const int first = grp ? g.first : s;
-                    for (int k = 0; k < nf; ++k)
-                        items[base + k] = make_int4(first, t0 + k * PT, PT,
-                                                    make_item_w(pbase + k, cnt, grp));
-                    if (key) {
-                        const int slot = atomicAdd(&sh.offs[list][key], 1);
-                        items[slot] = make_int4(first, t0 + nf * PT, rem,
-                                                make_item_w(pbase + nf, cnt, grp));
-                    }
-                }
-            }
+        for (int off = 1; off < 32; off <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, n_items, off);
+            if (lane >= off) n_items += u;
         }
-        if (place) break;  // the placing pass is the last: nothing to order after it
-        __syncthreads();
-        if (tid < (A.split ? 64 : 32)) {  // exclusive scans over sizes, largest first
-            const int list = tid >> 5;
-            const int key = PB - lane;
-            const int v = (lane < PB) ? sh.hist[list][key] : 0;
-            int incl = v;
+        if (lane < PB) sh.offs[list][key] = n_items - v;
+    }
+    __syncthreads();
+
+    // ---- 3. and placed, longest first --------------------------------------
+    // Places of a range's full pieces (a contiguous range a warp, from one add) and of
+    // its short one.
+    auto place = [&](const Range &r) {
+        const int nf = r.len / PT, key = (r.len % PT + kBlock - 1) / kBlock;
+        int incl = nf;
 #pragma unroll
-            for (int off = 1; off < 32; off <<= 1) {
-                const int u = __shfl_up_sync(0xffffffffu, incl, off);
-                if (lane >= off) incl += u;
-            }
-            if (lane < PB) sh.offs[list][key] = incl - v;
-            if (lane == 31) {
-                A.hdr->counter[list] = 0u;
-                A.hdr->n_items[list] = (unsigned)incl * (unsigned)A.num_kv_heads;
-            }
+        for (int off = 1; off < 32; off <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += u;
         }
-        if (tid == 32 && !A.split) {
-            A.hdr->counter[1] = 0u;
-            A.hdr->n_items[1] = 0u;
+        int base = 0;
+        if (lane == 31 && incl) base = atomicAdd(&sh.offs[r.list][PB], incl);
+        base = __shfl_sync(0xffffffffu, base, 31) + incl - nf;
+        return make_int2(base, key ? atomicAdd(&sh.offs[r.list][key], 1) : 0);
+    };
+    auto write = [&](const Range &r, int2 at) {
+        const int nf = r.len / PT, rem = r.len - nf * PT;
+        int4 *items = r.list ? A.items1 : A.items0;
+        for (int k = 0; k < nf; ++k)
+            items[at.x + k] = make_int4(r.first, r.t0 + k * PT, PT, make_item_w(r.pbase + k, r.cnt, r.grp));
+        if (rem)
+            items[at.y] = make_int4(r.first, r.t0 + nf * PT, rem, make_item_w(r.pbase + nf, r.cnt, r.grp));
+    };
+    const Range own = range_of(tid, L_first, g_first, 1);
+    Range prefix = own;
+    prefix.len = 0;
+    if (grouped) prefix = range_of(tid, L_first, g_first, 0);
+    const int2 own_at = place(own);
+    const int2 prefix_at = grouped ? place(prefix) : make_int2(0, 0);
+
+    // Nothing is written before this wait.  The kernels ahead let this one start while they
+    // still read their inputs and use their workspaces, and the caller may have given that
+    // memory to this call: a query or positions that were dropped after the call that read
+    // them, the workspace of a prefill.  (Places are known by now: what the wait holds back
+    // is the stores.)
+    pdl_wait();
+    if (lane == 31 && tid < (A.split ? 64 : 32)) {
+        A.hdr->counter[tid >> 5] = 0u;
+        A.hdr->n_items[tid >> 5] = (unsigned)n_items * (unsigned)A.num_kv_heads;
+    }
+    if (tid == 32 && !A.split) {
+        A.hdr->counter[1] = 0u;
+        A.hdr->n_items[1] = 0u;
+    }
+    if (grouped) write(prefix, prefix_at);
+    write(own, own_at);
+    for (int s0 = (int)blockDim.x; s0 < S; s0 += (int)blockDim.x) {
+        const int s = s0 + tid;
+        const int L = s < S ? valid_len(A, s) : 0;
+        Group g = {s, 1, 0};
+        if (grouped && L > 0) g = group_of(A, sh, s, grouped);
+        for (int seg = grouped ? 0 : 1; seg < 2; ++seg) {
+            const Range r = range_of(s, L, g, seg);
+            write(r, place(r));
         }
-        __syncthreads();
     }
 
-    pdl_wait();  // earlier work on the stream may still read nparts and out
     for (int s0 = 0; s0 < S; s0 += (int)blockDim.x) {
         const int s = s0 + tid;
         const int L0 = s >= S ? 1 : (s0 == 0 ? (L_first > 0 ? L_first : A.lens[s]) : A.lens[s]);

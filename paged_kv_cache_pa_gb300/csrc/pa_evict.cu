@@ -417,8 +417,7 @@ template <bool IN_PLACE>
 __global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 5 : 4)
     evict_move_kernel(const __grid_constant__ EvictParams P) {
     __shared__ int s_chunk;
-    // (no dependent is let through early: the next call's plan may write to a
-    // workspace that it shares with this one as soon as it starts)
+    // (no dependent is let through early)
     pdl_wait();
     const unsigned units = gridDim.x / (unsigned)P.max_chunks;
     int chunk = (int)(blockIdx.x / units);

@@ -1,8 +1,12 @@
 // pa_launch.cuh -- host helper: launch a kernel on a stream with programmatic
 // dependent launch allowed, so its launch overlaps the tail of the previous
 // kernel on the stream.  Every kernel launched this way calls
-// griddepcontrol.wait (pa::pdl_wait) before it touches global memory that
-// earlier work may write or read.
+// griddepcontrol.wait (pa::pdl_wait) before it writes to global memory, and
+// before it reads what earlier work may write.  Lengths, tables and starts are
+// read before it: they are complete before a call (pa.h).  No write comes
+// before it, not even to a call's own workspace: the kernels ahead may let
+// this one start while they still read their inputs and use their
+// workspaces, and the caller may have given this call that memory.
 #pragma once
 
 #include <cuda_runtime.h>

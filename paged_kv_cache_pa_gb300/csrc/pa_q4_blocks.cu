@@ -41,6 +41,7 @@ template <typename T>
 __global__ void __launch_bounds__(kUnpackThreads)
     unpack_blocks_kernel(const __grid_constant__ UnpackParams P) {
     pdl_wait();  // earlier kernels on the stream may still read or write the pools
+    pdl_trigger();  // (what follows waits for this grid's end before it writes anything)
     const int64_t src = P.pairs[2 * blockIdx.x], dst = P.pairs[2 * blockIdx.x + 1];
     if (src < 0 || src >= P.num_src_blocks || dst < 0 || dst >= P.num_dst_blocks) {
         if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && P.err)
@@ -66,9 +67,6 @@ __global__ void __launch_bounds__(kUnpackThreads)
         w[u] = __ldcs(reinterpret_cast<const uint32_t *>(cell + q4_word(token, c & 7)));
         sz[u] = __ldcs(reinterpret_cast<const uint32_t *>(cell + kQ4CellParams + 4 * token));
     }
-    // (not before the pairs are read: a decode call's plan writes to its workspace before it
-    // waits, and that may be memory that they had)
-    pdl_trigger();
 #pragma unroll
     for (int u = 0; u < kUnpackBatch; ++u) {
         const unsigned i = i0 + u * kUnpackThreads;

@@ -186,8 +186,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas<(QD > 0)>)
         s_axis[threadIdx.x] = P.rot.axis[threadIdx.x];
     }
     pdl_wait();  // earlier kernels on the stream may still read or write what this touches
-    // (after the wait: what follows may start before this grid ends, not before those)
-    if constexpr (QD == 0) pdl_trigger();
+    pdl_trigger();  // (after the wait: what follows may start before this grid ends, not before those)
 
     // this thread's two chunks of a row
     int ca, cb;
@@ -228,20 +227,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas<(QD > 0)>)
             b[u] = __ldcs(src + cb);
         }
     };
-    // 4-bit pools: what follows may start once a thread's last rows are on their way.  A
-    // decode call's plan writes to its workspace before it waits, and that may be memory
-    // that these rows had.
-    auto let_follow = [&](At p) {
-        if constexpr (QD > 0) {
-#pragma unroll
-            for (int u = 0; u < kBatch; ++u) next(p);
-            if (!in_list(p)) pdl_trigger();
-        }
-    };
     At at = {tl, r0};
     if (r0 >= rows) at.tok = tokens;  // more threads than rows
     load(at);
-    let_follow(at);
 
     // sines and cosines of the CTA's tokens, once each
     if (staged) __syncthreads();
@@ -307,7 +295,6 @@ __global__ void __launch_bounds__(kRotThreads, kRotCtas<(QD > 0)>)
         }
         at = p;
         load(at);
-        let_follow(at);
     }
 }
 
