@@ -400,6 +400,17 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
         for (int i = 0; i < S::kStages - 1; ++i) ask();
 
+        // Whether the next step's chunks are here.  The warp goes on or gives up as a whole: one
+        // lane's wait may give up where another's just ends, and those that go on would
+        // exchange data with lanes that are gone, with copies in flight when the CTA has ended.
+        auto arrived = [&]() {
+            const bool mine = mbar_wait(&s_full[warp][used % S::kStages], (used / S::kStages) & 1u, &s_never);
+            return __all_sync(0xffffffffu, mine) != 0;
+        };
+        bool gone = false;  // a wait gave up
+        // (the test build's few polls: right behind the copies, before these can have come)
+        if constexpr (kShortWaits) gone = used < asked && !arrived();
+
         // ---- the unit at hand ----
         // A lane's rows: packed, row t % R of chunk t / R of a pack; else 2t and 2t + 1 of
         // every eight.
@@ -920,10 +931,9 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             }
         };
 
-        bool gone = false;  // a wait gave up
         while (used < asked) {
             const int stage = used % S::kStages;
-            if (!mbar_wait(&s_full[warp][stage], (used / S::kStages) & 1u, &s_never)) {
+            if (gone || !arrived()) {
                 gone = true;
                 break;
             }
