@@ -834,8 +834,11 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads
  *     out[t][h] = sum_{j <= p} exp(x_j - max x) v_j / sum_{j <= p} exp(x_j - max x),
  *     x_j = scale * <query[t][h], k_j>,
  * with k_j and v_j what the cache's codes stand for, s n + z, unrounded.  fp32
- * sums; the products' operands are exact, but for the weights, which are rounded
- * in two parts to 2^-22.  A sequence without tokens (context_lens[s] = 0) gives
+ * sums; the products' operands are exact, but for the weights times the values'
+ * scales, which are rounded in two parts: to 2^-22 of themselves, and no finer than
+ * 2^-35 of the largest of them that up to 16 query rows of a KV head have met in that
+ * group of 64 channels (scales alone, of tokens without weight, do not count).
+ * A sequence without tokens (context_lens[s] = 0) gives
  * zero rows.  Longer chunks go through pa_unpack_blocks_q4 and
  * pa_prefill_attention.
  *

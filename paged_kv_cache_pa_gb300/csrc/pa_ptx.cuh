@@ -212,4 +212,11 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// log2, -infinity of zero
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 }  // namespace pa

@@ -31,9 +31,11 @@
 // and takes 7.5 sum p s off the products' sums every few chunks: they stay near zero
 // (1.2 10^-4 then, for 2 to 5% more time).
 //
-// The weights p s go to fp16 in two parts (their rounding, and its remainder), so
-// their error is 2^-22 of them; a running power of two keeps them in range
-// (below).
+// The weights p s, in fp32, go to fp16 in two parts (their rounding, and its
+// remainder), so their error is 2^-22 of them.  A power of two for every group of
+// channels, moved now and then, keeps the largest of them between 2^10 and 2^15: what
+// is below 2^-35 of that is rounded off.  It follows the weights, not the scales: a
+// token of huge values without weight does not move it, and other groups' scales do not.
 //
 // Few rows.  The products have eight columns.  With at most four rows a column is
 // (chunk of 16 tokens, row, part of the weight): a step of 4 / rows chunks fills
@@ -76,9 +78,10 @@ constexpr int kQ4Warps = 4;  // of a CTA
 constexpr int kQ4Threads = 32 * kQ4Warps;
 constexpr int kQ4Sms = 152;  // that the workers are sized for (right for any number)
 constexpr float kQ4NoMax = -3e38f;   // m before any token
-// A weight (2^6 where the maximum was last taken) and a scale (below 2^5 then) beyond
-// which both are taken anew: their product stays below fp16's 2^16.
-constexpr float kQ4TopP = 1024.f, kQ4TopS = 32.f;
+constexpr float kQ4NoRow = 3e38f;    // m of a tile's idle rows, whose weights are zero
+// A weight, 2^6 where the maximum was last taken, is taken anew beyond 2^10; weight times
+// scale, 2^10 where the power of two was last taken, beyond 2^15 (fp16 ends at 2^16).
+constexpr float kQ4TopP = 0x1p10f, kQ4TopW = 0x1p15f;
 
 struct Q4DecodeParams {
     void *out;
@@ -162,16 +165,6 @@ __device__ __forceinline__ uint32_t q4_transpose(uint32_t a) {
     uint32_t d;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
     return d;
-}
-
-__device__ __forceinline__ uint32_t q4_mul2(uint32_t a, uint32_t b) {
-    const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b));
-    return *reinterpret_cast<const uint32_t *>(&r);
-}
-__device__ __forceinline__ uint32_t q4_fma2(uint32_t a, uint32_t b, uint32_t c) {
-    const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&a), *reinterpret_cast<const __half2 *>(&b),
-                              *reinterpret_cast<const __half2 *>(&c));
-    return *reinterpret_cast<const uint32_t *>(&r);
 }
 
 template <int D, int R>
@@ -420,7 +413,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         uint32_t qf[NT][C][2][2][2];  // the query's fragments: cell, half, nibble pair
         float c1[NR], qz[NR][C];
         int lim[NR], lim_min = 0;     // tokens a row sees; the fewest of any
-        float vs = 0.f;               // power of two on the values' scales
+        float vs[C];                  // power of two on the values' scales, by group of channels
         int first_chunk = 0, rows = 0, row0 = 0, upos = pos0;
         // (a tile of at most eight rows leaves the second eight columns out)
         auto empty = [&](int nt) { return nt > 0 && rows <= 8 * nt; };
@@ -443,7 +436,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             rows = min(R, cu.q.n * P.G - row0);
             const int seen0 = cu.q.len - cu.q.n + 1;
             lim_min = seen0 + q4_token_of(P, row0);
-            vs = 0x1p60f;
+#pragma unroll
+            for (int c = 0; c < C; ++c) vs[c] = 1.f;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int col = S::kPacked ? (g >> 1) % R : nt * 8 + g;
@@ -525,7 +519,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         za[i][c] = ws[i][c] = 0.f;
                     }
                     lim[i] = seen0 + q4_token_of(P, row0 + nt * 8 + mine);
-                    m[i] = kQ4NoMax;
+                    m[i] = nt * 8 + mine < rows ? kQ4NoMax : kQ4NoRow;
                     l[i] = 0.f;
                 }
 #pragma unroll
@@ -578,7 +572,10 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             if (!all && first_chunk == 0)
                 tail = make_int4(cu.q.q0, cu.head, row0,
                                  (cu.q.chunks - stop + (int)per - 1) / (int)per << 5 | rows);
-            const float unscale = 0x1p24f * __int_as_float((254 << 23) - __float_as_int(vs));  // 2^24 / vs
+            float unscale[C];  // 2^24 / vs
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                unscale[c] = 0x1p24f * __int_as_float((254 << 23) - __float_as_int(vs[c]));
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 const int nt = i / 2, e = i % 2;
@@ -608,7 +605,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         v[1] = (v[1] - v[0]) * 0.0625f;  // n_0 + 16 n_1 -> n_1
                         v[3] = (v[3] - v[2]) * 0.0625f;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], unscale, z) * inv;
+                        for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], unscale[c], z) * inv;
                         const int d0 = c * 64 + h * 32 + 4 * g;
                         if (!in) continue;
                         if (!all) {
@@ -774,27 +771,42 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     }
                 }
             }
-            float p[U][NR][2], top;
+            // Weights, and what is to be multiplied out: packed, weight times scale (the power of
+            // two first: finite whatever the scale, and zero where the weight is); else the
+            // scales times the power of two, below.  A token's largest weight and largest
+            // scale bound its products.
+            float p[U][NR][2], pm[U][2], w[U][C][2], top;
             auto weights = [&]() {
                 top = 0.f;
 #pragma unroll
                 for (int u = 0; u < U; ++u)
 #pragma unroll
-                    for (int i = 0; i < NR; ++i)
+                    for (int k = 0; k < 2; ++k) {
+                        pm[u][k] = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
+                        for (int i = 0; i < NR; ++i) {
                             p[u][i][k] = ex2(x[u][i][k] - m[i]);
-                            top = fmaxf(top, p[u][i][k]);
+                            pm[u][k] = fmaxf(pm[u][k], p[u][i][k]);
                         }
+                        if constexpr (S::kPacked) {
+                            top = fmaxf(top, p[u][0][k] * (kQ4TopW / kQ4TopP));
+#pragma unroll
+                            for (int c = 0; c < C; ++c) {
+                                w[u][c][k] = p[u][0][k] * vs[c] * sv[u][c][k];
+                                top = fmaxf(top, w[u][c][k]);
+                            }
+                        } else {
+                            float s = kQ4TopW / kQ4TopP;
+#pragma unroll
+                            for (int c = 0; c < C; ++c) s = fmaxf(s, sv[u][c][k] * vs[c]);
+                            top = fmaxf(top, pm[u][k] * s);
+                        }
+                    }
             };
             weights();
-            float s_top = 0.f;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int c = 0; c < C; ++c) s_top = fmaxf(s_top, fmaxf(sv[u][c][0], sv[u][c][1]));
-            if (__any_sync(0xffffffffu, fmaxf(top, s_top * vs * (kQ4TopP / kQ4TopS)) > kQ4TopP)) {
-                // new maxima, and a new power of two on the scales
+            if (__any_sync(0xffffffffu, top > kQ4TopW)) {
+                // new maxima, and new powers of two on the scales
+                float kept = 0.f;  // what stays of a row's sums, of the row with the most
 #pragma unroll
                 for (int i = 0; i < NR; ++i) {
                     float a = fmaxf(x[0][i][0], x[0][i][1]);
@@ -806,6 +818,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     a = fmaxf(a - 6.f, m[i]);
                     const float f = ex2(m[i] - a);
                     m[i] = a;
+                    if (l[i] > 0.f) kept = fmaxf(kept, f);
                     l[i] *= f;
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
@@ -825,24 +838,32 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 }
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1)
-                    s_top = fmaxf(s_top, __shfl_xor_sync(0xffffffffu, s_top, o));
-                const int sb = (__float_as_int(s_top) >> 23) & 255;
-                const float nv = fminf(vs, __int_as_float(max(1, min(187, 258 - sb)) << 23));
-                if (nv != vs) {
-                    const float f = nv / vs;
-                    vs = nv;
+                    kept = fmaxf(kept, __shfl_xor_sync(0xffffffffu, kept, o));
+                weights();  // (for the maxima alone)
 #pragma unroll
-                    for (int i = 0; i < NR; ++i)
+                for (int c = 0; c < C; ++c) {
+                    float e = -INFINITY;  // log2 of the largest weight times scale of the packs
 #pragma unroll
-                        for (int c = 0; c < C; ++c) ws[i][c] *= f;
+                    for (int u = 0; u < U; ++u)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) e = fmaxf(e, lg2(pm[u][k]) + lg2(sv[u][c][k]));
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1)
+                        e = fmaxf(e, __shfl_xor_sync(0xffffffffu, e, o));
+                    // up by no more than the sums have just come down, so that they stay in range
+                    const int was = (__float_as_int(vs[c]) >> 23) - 127;
+                    const int now = __float2int_rd(
+                        fmaxf(-126.f, fminf(116.f, fminf(10.f - e, (float)was - lg2(kept)))));
+                    const float f = __int_as_float((max(-126, min(127, now - was)) + 127) << 23);
+                    vs[c] = __int_as_float((now + 127) << 23);
+#pragma unroll
+                    for (int i = 0; i < NR; ++i) ws[i][c] *= f;
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int c = 0; c < C; ++c)
+                        for (int j = 0; j < 4; ++j)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) O[nt][c][j][i] *= f;
+                            for (int i = 0; i < 4; ++i) O[nt][c][j][i] *= f;
                 }
                 weights();
             }
@@ -853,7 +874,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         zv[u][c][k] = fmaf(7.5f, sv[u][c][k], zv[u][c][k]);
-                        sv[u][c][k] *= vs;
+                        // (finite beside a weight of zero)
+                        if constexpr (!S::kPacked) w[u][c][k] = fminf(sv[u][c][k] * vs[c], 0x1p127f);
                     }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -863,7 +885,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         za[i][c] = fmaf(p[u][i][0], zv[u][c][0], fmaf(p[u][i][1], zv[u][c][1], za[i][c]));
-                        ws[i][c] = fmaf(p[u][i][0], sv[u][c][0], fmaf(p[u][i][1], sv[u][c][1], ws[i][c]));
+                        if constexpr (S::kPacked) ws[i][c] += w[u][c][0] + w[u][c][1];
+                        else ws[i][c] = fmaf(p[u][i][0], w[u][c][0], fmaf(p[u][i][1], w[u][c][1], ws[i][c]));
                     }
                 }
 #pragma unroll
@@ -876,9 +899,8 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         uint32_t b[2];
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
-                            const float w = p[u][0][k] * sv[u][c][k];
-                            const float2 hi = Pack<__half>::up(Pack<__half>::down(w, w));
-                            b[k] = q4_transpose(Pack<__half>::down(w, w - hi.x));
+                            const float2 hi = Pack<__half>::up(Pack<__half>::down(w[u][c][k], w[u][c][k]));
+                            b[k] = q4_transpose(Pack<__half>::down(w[u][c][k], w[u][c][k] - hi.x));
                         }
 #pragma unroll
                         for (int j = 0; j < kPack; ++j) {
@@ -891,37 +913,23 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         }
                     }
                 } else {
-                    // the weights' parts, tokens g and g + 8, of two columns
-                    uint32_t ph[NT][2], pl[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float p0 = p[u][2 * nt % NR][k], p1 = p[u][(2 * nt + 1) % NR][k];
-                            ph[nt][k] = Pack<__half>::down(p0, p1);
-                            const float2 h = Pack<__half>::up(ph[nt][k]);
-                            pl[nt][k] = Pack<__half>::down(p0 - h.x, p1 - h.y);
-                        }
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
-                        uint32_t r[4], s2[2];
+                        uint32_t r[4];
                         ldsm_x4_trans(r[0], r[1], r[2], r[3], v_base + c * kQ4CellBytes);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            s2[k] = Pack<__half>::down(sv[u][c][k], sv[u][c][k]);
-                        }
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if (empty(nt)) break;
                             uint32_t b[2], bl[2];
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                // times the scale: rounded, and what that and the weight left
-                                const uint32_t hi = q4_mul2(ph[nt][k], s2[k]);
-                                const uint32_t lo = q4_fma2(
-                                    pl[nt][k], s2[k], q4_fma2(ph[nt][k], s2[k], hi ^ 0x80008000u));
+                                // tokens g and g + 8, of two columns: rounded, and what that left
+                                const float w0 = p[u][2 * nt % NR][k] * w[u][c][k];
+                                const float w1 = p[u][(2 * nt + 1) % NR][k] * w[u][c][k];
+                                const uint32_t hi = Pack<__half>::down(w0, w1);
+                                const float2 h = Pack<__half>::up(hi);
                                 b[k] = q4_transpose(hi);
-                                bl[k] = q4_transpose(lo);
+                                bl[k] = q4_transpose(Pack<__half>::down(w0 - h.x, w1 - h.y));
                             }
                             values(r, O[nt][c], b[0], b[1]);
                             values(r, O[nt][c], bl[0], bl[1]);
