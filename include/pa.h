@@ -838,6 +838,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads
  * scales, which are rounded in two parts: to 2^-22 of themselves, and no finer than
  * 2^-35 of the largest of them that up to 16 query rows of a KV head have met in that
  * group of 64 channels (scales alone, of tokens without weight, do not count).
+ * Values may be as large as the type has them; where a context has none above 2^-100
+ * (bf16), bits are lost.
  * A sequence without tokens (context_lens[s] = 0) gives
  * zero rows.  Longer chunks go through pa_unpack_blocks_q4 and
  * pa_prefill_attention.

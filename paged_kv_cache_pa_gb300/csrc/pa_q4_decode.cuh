@@ -79,9 +79,10 @@ constexpr int kQ4Threads = 32 * kQ4Warps;
 constexpr int kQ4Sms = 152;  // that the workers are sized for (right for any number)
 constexpr float kQ4NoMax = -3e38f;   // m before any token
 constexpr float kQ4NoRow = 3e38f;    // m of a tile's idle rows, whose weights are zero
-// A weight, 2^6 where the maximum was last taken, is taken anew beyond 2^10; weight times
-// scale, 2^10 where the power of two was last taken, beyond 2^15 (fp16 ends at 2^16).
-constexpr float kQ4TopP = 0x1p10f, kQ4TopW = 0x1p15f;
+// A weight, 2^-26 where the maximum was last taken, is taken anew beyond 2^-22 (so that
+// the sum of 2^22 tokens' values is in range wherever the values are); weight times scale,
+// 2^10 where the power of two was last taken, beyond 2^15 (fp16 ends at 2^16).
+constexpr float kQ4Lift = 26.f, kQ4TopP = 0x1p-22f, kQ4TopW = 0x1p15f;
 
 struct Q4DecodeParams {
     void *out;
@@ -572,10 +573,9 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             if (!all && first_chunk == 0)
                 tail = make_int4(cu.q.q0, cu.head, row0,
                                  (cu.q.chunks - stop + (int)per - 1) / (int)per << 5 | rows);
-            float unscale[C];  // 2^24 / vs
+            float unscale[C];  // 1 / vs (2^24, of the codes as fp16, apart: together they may overflow)
 #pragma unroll
-            for (int c = 0; c < C; ++c)
-                unscale[c] = 0x1p24f * __int_as_float((254 << 23) - __float_as_int(vs[c]));
+            for (int c = 0; c < C; ++c) unscale[c] = __int_as_float((254 << 23) - __float_as_int(vs[c]));
 #pragma unroll
             for (int i = 0; i < NR; ++i) {
                 const int nt = i / 2, e = i % 2;
@@ -602,8 +602,10 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                                 v[j] = O[nt][c][j][2 * h + e];
                             }
                         }
-                        v[1] = (v[1] - v[0]) * 0.0625f;  // n_0 + 16 n_1 -> n_1
-                        v[3] = (v[3] - v[2]) * 0.0625f;
+                        v[1] = (v[1] - v[0]) * 0x1p20f;  // n_0 + 16 n_1 -> n_1
+                        v[3] = (v[3] - v[2]) * 0x1p20f;
+                        v[0] *= 0x1p24f;
+                        v[2] *= 0x1p24f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) v[j] = fmaf(v[j], unscale[c], z) * inv;
                         const int d0 = c * 64 + h * 32 + 4 * g;
@@ -815,7 +817,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int o = S::kPacked ? R : 4; o < 32; o <<= 1)
                         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                    a = fmaxf(a - 6.f, m[i]);
+                    a = fmaxf(a + kQ4Lift, m[i]);
                     const float f = ex2(m[i] - a);
                     m[i] = a;
                     if (l[i] > 0.f) kept = fmaxf(kept, f);
@@ -853,7 +855,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     // up by no more than the sums have just come down, so that they stay in range
                     const int was = (__float_as_int(vs[c]) >> 23) - 127;
                     const int now = __float2int_rd(
-                        fmaxf(-126.f, fminf(116.f, fminf(10.f - e, (float)was - lg2(kept)))));
+                        fmaxf(-126.f, fminf(126.f, fminf(10.f - e, (float)was - lg2(kept)))));
                     const float f = __int_as_float((max(-126, min(127, now - was)) + 127) << 23);
                     vs[c] = __int_as_float((now + 127) << 23);
 #pragma unroll

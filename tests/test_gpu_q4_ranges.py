@@ -52,6 +52,26 @@ ROWS = [(1, 1, 64), (4, 2, 64), (8, 2, 64), (6, 1, 64), (16, 1, 64), (2, 2, 128)
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
 @pytest.mark.parametrize("H,Hkv,D", ROWS)
+def test_values_near_the_largest(H, Hkv, D, dtype):
+    """Groups whose range is just held, and others of ordinary size beside them: finite values
+    give finite outputs."""
+    top = torch.finfo(DT[dtype]).max
+    c = Q4Cache([300, 40, 2000, 16], Hkv, D, DT[dtype], seed=D)
+    g = torch.Generator(device=DEV).manual_seed(1)
+    live = ~torch.isnan(c.v[0])
+    c.v[0].copy_(torch.where(live, (torch.rand(c.v[0].shape, generator=g, device=DEV) * 0.98 - 0.49) * top, c.v[0]))
+    if D > 64:
+        c.v[0][..., 64:128] = torch.where(live[..., 64:128], c.v[0][..., 64:128] / top, c.v[0][..., 64:128])
+    _rewrite(c)
+    _check(c, _query(4, H, D, DT[dtype]), sharp=None)
+    # one sign: the sums of all tokens stay below the largest value only as they are weighted
+    c.v[0].copy_(torch.where(live, (c.v[0].abs() + 0.4 * top).to(DT[dtype]), c.v[0]))
+    _rewrite(c)
+    _check(c, _query(4, H, D, DT[dtype], seed=1), sharp=None)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("H,Hkv,D", ROWS)
 def test_a_token_without_weight_does_not_coarsen_the_others(H, Hkv, D, dtype):
     """A few tokens of huge values, far below every other token's logit: the others keep their
     bits, wherever in the context those tokens are."""
