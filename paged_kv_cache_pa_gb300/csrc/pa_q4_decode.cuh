@@ -82,6 +82,8 @@ constexpr float kQ4NoRow = 3e38f;    // m of a tile's idle rows, whose weights a
 // A weight, 2^-26 where the maximum was last taken, is taken anew beyond 2^-22 (so that
 // the sum of 2^22 tokens' values is in range wherever the values are); weight times scale,
 // 2^10 where the power of two was last taken, beyond 2^15 (fp16 ends at 2^16).
+constexpr int kQ4HalfLog = 12;  // (of the logits' unit: half of the codes' 2^24)
+constexpr float kQ4Half = 0x1p12f;
 constexpr float kQ4Lift = 26.f, kQ4TopP = 0x1p-22f, kQ4TopW = 0x1p15f;
 
 struct Q4DecodeParams {
@@ -472,21 +474,24 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 // zeros or with an infinity
                 const int nb = eb == 0 || eb == 255 ? 127 : max(1, min(250, 267 - eb));
                 const float norm = __int_as_float(nb << 23);
-                const float back = __int_as_float((254 - nb) << 23) * 0x1p24f * P.scale_log2;
+                // a product's factor (the codes' 2^24 in two halves, here and with the maxima:
+                // in one the factor may overflow where no logit does)
+                const float back = __int_as_float((254 + kQ4HalfLog - nb) << 23) * P.scale_log2;
                 float sum[C];
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     sum[c] = 0.f;
+                    float sum16 = 0.f;  // of the odd elements, a sixteenth
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) sum[c] += f[c][h][i];
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             // elements 2i (+ 4) and 2i + 1 (+ 4) of the word's eight
                             const float e0 = f[c][h][2 * i] * norm, e4 = f[c][h][2 * i + 4] * norm;
                             const float o0 = f[c][h][2 * i + 1] * (norm * 0.0625f);
                             const float o4 = f[c][h][2 * i + 5] * (norm * 0.0625f);
+                            sum[c] += e0 + e4;
+                            sum16 += o0 + o4;
                             uint32_t(&q)[2] = qf[nt][c][h][i];
                             if (!S::kPacked) {
                                 q[0] = Pack<__half>::down(e0, e4);
@@ -504,9 +509,10 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                             }
                         }
                     }
+                    sum[c] = fmaf(16.f, sum16, sum[c]);
                     sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 1);
                     sum[c] += __shfl_xor_sync(0xffffffffu, sum[c], 2);
-                    sum[c] *= P.scale_log2;
+                    sum[c] = sum[c] * 0x1p-24f * back;
                 }
 #pragma unroll
                 for (int e = 0; e < (S::kPacked ? 1 : 2); ++e) {
@@ -685,7 +691,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             const uint8_t *pk = ring + at_pack + jl * (S::kPacked ? S::kChunkBytes : 0) +
                                 kQ4CellParams + 4 * g;
             constexpr int kPackBytes = kPack * S::kChunkBytes;
-            // x = scale <q, k> in units of log2, tokens g and g + 8 of the lane's rows
+            // x = scale <q, k> in units of 2^12 log2, tokens g and g + 8 of the lane's rows
             float x[U][NR][2];
             float a[U][C][NR][2];
 #pragma unroll
@@ -787,7 +793,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                         pm[u][k] = 0.f;
 #pragma unroll
                         for (int i = 0; i < NR; ++i) {
-                            p[u][i][k] = ex2(x[u][i][k] - m[i]);
+                            p[u][i][k] = ex2(fmaf(x[u][i][k], kQ4Half, -m[i]));
                             pm[u][k] = fmaxf(pm[u][k], p[u][i][k]);
                         }
                         if constexpr (S::kPacked) {
@@ -817,7 +823,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int o = S::kPacked ? R : 4; o < 32; o <<= 1)
                         a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-                    a = fmaxf(a + kQ4Lift, m[i]);
+                    a = fmaxf(fmaf(a, kQ4Half, kQ4Lift), m[i]);
                     const float f = ex2(m[i] - a);
                     m[i] = a;
                     if (l[i] > 0.f) kept = fmaxf(kept, f);

@@ -1,4 +1,5 @@
-"""decode_attention_q4 against 64 bits with q4tight's bound: scales far apart."""
+"""decode_attention_q4 against 64 bits with q4tight's bound: values and queries next to the ends
+of their type, scales far apart."""
 import numpy as np
 import pytest
 
@@ -68,6 +69,31 @@ def test_values_near_the_largest(H, Hkv, D, dtype):
     c.v[0].copy_(torch.where(live, (c.v[0].abs() + 0.4 * top).to(DT[dtype]), c.v[0]))
     _rewrite(c)
     _check(c, _query(4, H, D, DT[dtype], seed=1), sharp=None)
+
+
+@pytest.mark.parametrize("H,Hkv,D", ROWS)
+def test_queries_and_keys_next_to_the_ends(H, Hkv, D):
+    """Powers of two on the query or the keys, taken back by the scale, change nothing."""
+    c = Q4Cache([300, 20, 1000], Hkv, D, torch.bfloat16, seed=8)
+    q = _query(3, H, D, torch.bfloat16)
+    scale = 2.0 ** -3
+    want = _decode(c, q, scale=scale)
+    _check(c, q, scale=scale, sharp=None)
+    for e in (-100, -60, 60, 110, 120):
+        assert torch.equal(_decode(c, q * 2.0 ** e, scale=scale * 2.0 ** -e), want), e
+    k = c.k[0].clone()
+    for e in (-60, 60, 100):
+        c.k[0].copy_(k * 2.0 ** e)
+        _rewrite(c)
+        assert torch.equal(_decode(c, q, scale=scale * 2.0 ** -e), want), e
+    # (the scale times the query's sums is subnormal here: off by 2^-149 of keys of 2^117, far
+    # less than a logit's bound)
+    c.k[0].copy_(k * 2.0 ** 115)
+    _rewrite(c)
+    _check(c, q, scale=scale * 2.0 ** -115, sharp=None)
+    c.k[0].copy_(k * 2.0 ** 60)
+    _rewrite(c)
+    assert torch.equal(_decode(c, q * 2.0 ** -60, scale=scale), want)
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
