@@ -77,8 +77,8 @@ namespace pa {
 constexpr int kQ4Warps = 4;  // of a CTA
 constexpr int kQ4Threads = 32 * kQ4Warps;
 constexpr int kQ4Sms = 152;  // that the workers are sized for (right for any number)
-constexpr float kQ4NoMax = -3e38f;   // m before any token
-constexpr float kQ4NoRow = 3e38f;    // m of a tile's idle rows, whose weights are zero
+constexpr float kQ4NoMax = -0x1.fffffep127f;  // m before any token: no finite logit is below it
+constexpr float kQ4NoRow = 0x1.fffffep127f;   // m of a tile's idle rows, whose weights are zero
 // A weight, 2^-26 where the maximum was last taken, is taken anew beyond 2^-22 (so that
 // the sum of 2^22 tokens' values is in range wherever the values are); weight times scale,
 // 2^10 where the power of two was last taken, beyond 2^15 (fp16 ends at 2^16).

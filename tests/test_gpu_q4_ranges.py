@@ -151,3 +151,18 @@ def test_values_that_grow_or_shrink_along_the_context(H, Hkv, D, up):
     q = _query(2, H, D, torch.bfloat16, factor=0.5)
     q[..., 0] = 1.0
     _check(c, q, scale=1.0 if D == 64 else 0.7, sharp=None)
+
+
+@pytest.mark.parametrize("H,Hkv,D", ROWS)
+@pytest.mark.parametrize("logit", [-2.3e38, -2.2e38, 2.3e38])
+def test_equal_logits_next_to_the_end_of_fp32(H, Hkv, D, logit):
+    """Keys that are all alike: every logit the same, next to the largest of either sign (in
+    units of log2 3.3e38), and every weight 1 / L."""
+    lens = [40, 600]
+    c = Q4Cache(lens, Hkv, D, torch.bfloat16, seed=21)
+    c.k[0][...] = torch.where(torch.isnan(c.k[0]), c.k[0], torch.ones_like(c.k[0]))
+    _rewrite(c)
+    q = torch.ones(2, H, D, dtype=torch.bfloat16, device=DEV)
+    out = _decode(c, q, scale=logit / D).double()
+    want, tol = q4tight.attention(c, torch.zeros_like(q), range(3), 1.0)
+    assert q4tight.off(out.float(), want, tol)[0] <= 1.0
