@@ -886,8 +886,9 @@ pa_status_t pa_decode_attention_q4(
  *
  * Defines: for every layer and pair i with (src, dst) = (block_pairs[2i],
  * block_pairs[2i+1]): every element of 16-bit block dst is s n + z of 4-bit block
- * src's (one fp32 rounding, then one to dtype), K and V.  Slots that were never
- * written give whatever their bytes stand for.
+ * src's (one fp32 rounding, then one to dtype; past the largest finite number of
+ * dtype, which a rounded scale may lead to, that number), K and V.  Slots that were
+ * never written give whatever their bytes stand for.
  *
  * dst_k_caches, dst_v_caches  HOST arrays of num_layers device pools
  *               [num_dst_blocks][num_kv_heads][block_size][head_dim], dtype

@@ -58,6 +58,12 @@ struct Pack<__half> {
         const __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+    // the same with the largest finite number past it (a NaN stays)
+    static __device__ __forceinline__ uint32_t down_finite(float a, float b) {
+        uint32_t d;
+        asm("cvt.rn.satfinite.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+        return d;
+    }
     // the lesser of each half; a NaN stays
     static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
         const __half2 h = __hmin2_nan(*reinterpret_cast<const __half2 *>(&a),
@@ -81,6 +87,12 @@ struct Pack<__nv_bfloat16> {
     static __device__ __forceinline__ uint32_t down(float a, float b) {
         const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<const uint32_t *>(&h);
+    }
+    // the same with the largest finite number past it (a NaN stays)
+    static __device__ __forceinline__ uint32_t down_finite(float a, float b) {
+        uint32_t d;
+        asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(b), "f"(a));
+        return d;
     }
     static __device__ __forceinline__ uint32_t min2(uint32_t a, uint32_t b) {
         const __nv_bfloat162 h = __hmin2_nan(*reinterpret_cast<const __nv_bfloat162 *>(&a),
@@ -183,7 +195,9 @@ __device__ __forceinline__ uint32_t q4_codes8(const uint4 &v, const Q4Scale &q) 
     return acc;
 }
 
-// Eight elements from their word, as T.
+// Eight elements from their word, as T.  A group's top may be past the type's largest number,
+// its scale having been rounded up (by 2^-12 and 15 s + z: 65520 for 0 .. 65504 in fp16): that
+// reads as the largest, where it would round to an infinity.  A NaN stays.
 template <typename T>
 __device__ __forceinline__ uint4 q4_values8(uint32_t w, float s, float z) {
     uint32_t o[4];
@@ -191,7 +205,7 @@ __device__ __forceinline__ uint4 q4_values8(uint32_t w, float s, float z) {
     for (int i = 0; i < 4; ++i) {
         const float a = __uint_as_float(0x4b000000u | ((w >> (8 * i)) & 15u)) - 8388608.0f;
         const float b = __uint_as_float(0x4b000000u | ((w >> (8 * i + 4)) & 15u)) - 8388608.0f;
-        o[i] = Pack<T>::down(fmaf(a, s, z), fmaf(b, s, z));
+        o[i] = Pack<T>::down_finite(fmaf(a, s, z), fmaf(b, s, z));
     }
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
