@@ -835,8 +835,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads
  *     x_j = scale * <query[t][h], k_j>,
  * with k_j and v_j what the cache's codes stand for, s n + z, unrounded.  fp32
  * sums; the products' operands are exact, but for the weights times the values'
- * scales, which are rounded in two parts: to 2^-22 of themselves, and no finer than
- * 2^-35 of the largest of them that up to 16 query rows of a KV head have met in that
+ * scales, which are rounded in two parts: to 2^-19 of themselves, and no finer than
+ * 2^-34 of the largest of them that up to 16 query rows of a KV head have met in that
  * group of 64 channels (scales alone, of tokens without weight, do not count).
  * Values may be as large as the type has them; where a context has none above 2^-100
  * (bf16), bits are lost.

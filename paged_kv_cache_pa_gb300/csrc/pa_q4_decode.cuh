@@ -22,20 +22,24 @@
 // the power of two that brings its largest element to 2^13; what fp16 then
 // cannot hold of an element is below 2^-34 of the largest.
 //
-// Sums around the middle.  The tensor cores cut what does not fit a sum off, always
-// towards zero: a sum of many terms of one sign, as n >= 0 makes it, loses half a
-// step a product, the same way every time (two documents of 131072 tokens: 1.6 10^-3
-// of the output, whose terms cancel to 1 / 200 of their size).  So the kernel adds up
-//     sum_j (p_j s_j) (n_j - 7.5) + sum_j p_j (z_j + 7.5 s_j),
-// the middle of a group in the second sum, which is fp32 with ordinary rounding,
-// and takes 7.5 sum p s off the products' sums every few chunks: they stay near zero
-// (1.2 10^-4 then, for 2 to 5% more time).
-//
-// The weights p s, in fp32, go to fp16 in two parts (their rounding, and its
-// remainder), so their error is 2^-22 of them.  A power of two for every group of
-// channels, moved now and then, keeps the largest of them between 2^10 and 2^15: what
-// is below 2^-35 of that is rounded off.  It follows the weights, not the scales: a
-// token of huge values without weight does not move it, and other groups' scales do not.
+// Sums.  The tensor cores cut what does not fit a sum off, always towards zero: a sum
+// of many terms of one sign, as n >= 0 makes it, loses half a step a product, the
+// same way every time.  Over two documents of 131072 tokens, whose terms cancel to 1 / 200
+// of their size, that was 1.6 10^-3 of the output.  So
+//   - the weights p s, in fp32, go to fp16 as their first 8 bits and the rest (2^-19 of
+//     them is rounded off that): products of 8 bits with l + 16 h below 256 fit the sum
+//     of a chunk, and of most pairs of chunks, without being cut.  (A first part of 11
+//     bits: 2^-22, but 8 10^-5 of the output.)
+//   - the parts are summed apart: in columns, or in products, of their own;
+//   - a sum is of one pack of chunks, or two; then it is added to the row's in fp32 with
+//     ordinary rounding.
+// 6 10^-6 of the output now.  (Sums that go on, and are brought back to their middle every
+// eight chunks: 1.2 10^-4, and 142 us where this takes 139 for 256 sequences of 40 heads;
+// whole numbers around 0, a subtraction for every operand: 1 10^-6, 156 us.)
+// A power of two for every group of channels, moved now and then, keeps the largest of
+// the weights p s between 2^10 and 2^15: what is below 2^-34 of that is rounded off.
+// It follows the weights, not the scales: a token of huge values without weight does
+// not move it, and other groups' scales do not.
 //
 // Few rows.  The products have eight columns.  With at most four rows a column is
 // (chunk of 16 tokens, row, part of the weight): a step of 4 / rows chunks fills
@@ -170,6 +174,11 @@ __device__ __forceinline__ uint32_t q4_transpose(uint32_t a) {
     return d;
 }
 
+// A weight's first part: its first 8 bits.
+__device__ __forceinline__ float q4_first(float w) {
+    return __int_as_float(__float_as_int(w) & 0xffff0000);
+}
+
 template <int D, int R>
 struct Q4Shape {
     static constexpr int kCells = D / kQ4Group;
@@ -188,8 +197,6 @@ struct Q4Shape {
     // What a unit costs beside its chunks, in chunks: its query, the first maxima, its
     // output, half a pack that is not full.  The warps' shares count it.
     static constexpr int kUnitCost = 3 + kPack;
-    // Steps between two corrections of the sums: about eight chunks.
-    static constexpr int kCentre = kStep >= 6 ? 1 : 8 / kStep;
     static constexpr int kStageBytes = kStep * kChunkBytes;
     // CTAs an SM: what the registers allow without spills, which cost more than warps bring
     // (drafts of five tokens, 32 heads on 8 of 128: 87 us with two, 105 with three; 12 heads
@@ -412,7 +419,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
         // every eight.
         float O[NT][C][4][4];     // [rows of 16 channels: cell, nibble][fragment]
         float m[NR], l[NR], za[NR][C];
-        float ws[NR][C];              // sum p s (scaled) that O has not been rid of 7.5 times of
         uint32_t qf[NT][C][2][2][2];  // the query's fragments: cell, half, nibble pair
         float c1[NR], qz[NR][C];
         int lim[NR], lim_min = 0;     // tokens a row sees; the fewest of any
@@ -523,7 +529,7 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         qz[i][c] = __shfl_sync(0xffffffffu, sum[c], src);
-                        za[i][c] = ws[i][c] = 0.f;
+                        za[i][c] = 0.f;
                     }
                     lim[i] = seen0 + q4_token_of(P, row0 + nt * 8 + mine);
                     m[i] = nt * 8 + mine < rows ? kQ4NoMax : kQ4NoRow;
@@ -535,30 +541,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int i = 0; i < 4; ++i) O[nt][c][j][i] = 0.f;
-            }
-        };
-
-        // Takes the middle of the values off the sums (see above): of a column's tokens, in
-        // the lanes of its t; packed, all from the first parts' column.
-        auto centre = [&]() {
-            constexpr float kMid0 = 7.5f * 0x1p-24f, kMid1 = 127.5f * 0x1p-24f;  // n_0, n_0 + 16 n_1
-#pragma unroll
-            for (int i = 0; i < NR; ++i) {
-                if (!S::kPacked && empty(i / 2)) break;
-#pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    float w = ws[i][c];
-                    ws[i][c] = 0.f;
-#pragma unroll
-                    for (int o = 4; o < 32; o <<= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float &o = O[i / 2][c][j][2 * h + i % 2];
-                            o = fmaf(w, j & 1 ? -kMid1 : -kMid0, o);
-                        }
-                }
             }
         };
 
@@ -667,17 +649,23 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     }
                 }
         };
-        // The products of a V tile's cell (its words in r) with weights.
-        auto values = [&](const uint32_t (&r)[4], float (&o)[4][4], uint32_t b0, uint32_t b1) {
+        // The products of a V tile's cell (its words in r) with weights; first: no sums yet.
+        auto values = [&](const uint32_t (&r)[4], float (&o)[4][4], uint32_t b0, uint32_t b1, bool first) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 uint32_t w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     w[i] = j ? __byte_perm(r[i], 0, 0x4341) : r[i] & 0x00ff00ffu;
-                q4_mma(o[2 * j], w[0] & 0x000f000fu, w[2] & 0x000f000fu, w[1] & 0x000f000fu,
-                       w[3] & 0x000f000fu, b0, b1);
-                q4_mma(o[2 * j + 1], w[0], w[2], w[1], w[3], b0, b1);
+                const uint32_t n[4] = {w[0] & 0x000f000fu, w[1] & 0x000f000fu, w[2] & 0x000f000fu,
+                                       w[3] & 0x000f000fu};
+                if (first) {
+                    q4_mma_first(o[2 * j], n[0], n[2], n[1], n[3], b0, b1);
+                    q4_mma_first(o[2 * j + 1], w[0], w[2], w[1], w[3], b0, b1);
+                } else {
+                    q4_mma(o[2 * j], n[0], n[2], n[1], n[3], b0, b1);
+                    q4_mma(o[2 * j + 1], w[0], w[2], w[1], w[3], b0, b1);
+                }
             }
         };
 
@@ -831,7 +819,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
 #pragma unroll
                     for (int c = 0; c < C; ++c) {
                         za[i][c] *= f;
-                        ws[i][c] *= f;
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             if (S::kPacked) {
@@ -865,8 +852,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                     const float f = __int_as_float((max(-126, min(127, now - was)) + 127) << 23);
                     vs[c] = __int_as_float((now + 127) << 23);
 #pragma unroll
-                    for (int i = 0; i < NR; ++i) ws[i][c] *= f;
-#pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -881,7 +866,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 for (int c = 0; c < C; ++c)
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
-                        zv[u][c][k] = fmaf(7.5f, sv[u][c][k], zv[u][c][k]);
                         // (finite beside a weight of zero)
                         if constexpr (!S::kPacked) w[u][c][k] = fminf(sv[u][c][k] * vs[c], 0x1p127f);
                     }
@@ -891,58 +875,54 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
                 for (int i = 0; i < NR; ++i) {
                     l[i] += p[u][i][0] + p[u][i][1];
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
+                    for (int c = 0; c < C; ++c)
                         za[i][c] = fmaf(p[u][i][0], zv[u][c][0], fmaf(p[u][i][1], zv[u][c][1], za[i][c]));
-                        if constexpr (S::kPacked) ws[i][c] += w[u][c][0] + w[u][c][1];
-                        else ws[i][c] = fmaf(p[u][i][0], w[u][c][0], fmaf(p[u][i][1], w[u][c][1], ws[i][c]));
-                    }
                 }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const uint32_t v_base = base + u * kPackBytes + S::kTileBytes + lm_off;
-                if constexpr (S::kPacked) {
+            for (int c = 0; c < C; ++c) {
 #pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        // both parts of a weight side by side: columns 2t and 2t + 1
-                        uint32_t b[2];
+                for (int nt = 0; nt < NT; ++nt) {
+                    if (empty(nt)) break;
+                    float o[4][4], ol[4][4];  // this step's sums; ol: not packed, of the second parts
 #pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float2 hi = Pack<__half>::up(Pack<__half>::down(w[u][c][k], w[u][c][k]));
-                            b[k] = q4_transpose(Pack<__half>::down(w[u][c][k], w[u][c][k] - hi.x));
-                        }
-#pragma unroll
-                        for (int j = 0; j < kPack; ++j) {
-                            uint32_t r[4];
-                            ldsm_x4_trans(r[0], r[1], r[2], r[3],
-                                          v_base + j * S::kChunkBytes + c * kQ4CellBytes);
-                            // a chunk's weights are in its own columns
-                            if (kPack == 1) values(r, O[0][c], b[0], b[1]);
-                            else values(r, O[0][c], b[0] * own_c[j], b[1] * own_c[j]);
-                        }
-                    }
-                } else {
-#pragma unroll
-                    for (int c = 0; c < C; ++c) {
-                        uint32_t r[4];
-                        ldsm_x4_trans(r[0], r[1], r[2], r[3], v_base + c * kQ4CellBytes);
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (empty(nt)) break;
-                            uint32_t b[2], bl[2];
+                    for (int u = 0; u < U; ++u) {
+                        const uint32_t v_at = base + u * kPackBytes + S::kTileBytes + lm_off + c * kQ4CellBytes;
+                        uint32_t b[2], bl[2];
+                        if constexpr (S::kPacked) {
+                            // both parts of a weight side by side: columns 2t and 2t + 1
 #pragma unroll
                             for (int k = 0; k < 2; ++k) {
-                                // tokens g and g + 8, of two columns: rounded, and what that left
+                                const float hi = q4_first(w[u][c][k]);
+                                b[k] = q4_transpose(Pack<__half>::down(hi, w[u][c][k] - hi));
+                            }
+#pragma unroll
+                            for (int j = 0; j < kPack; ++j) {
+                                uint32_t r[4];
+                                ldsm_x4_trans(r[0], r[1], r[2], r[3], v_at + j * S::kChunkBytes);
+                                // a chunk's weights are in its own columns
+                                if (kPack == 1) values(r, o, b[0], b[1], u == 0 && j == 0);
+                                else values(r, o, b[0] * own_c[j], b[1] * own_c[j], u == 0 && j == 0);
+                            }
+                        } else {
+                            uint32_t r[4];
+                            ldsm_x4_trans(r[0], r[1], r[2], r[3], v_at);
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {  // tokens g and g + 8, of two columns
                                 const float w0 = p[u][2 * nt % NR][k] * w[u][c][k];
                                 const float w1 = p[u][(2 * nt + 1) % NR][k] * w[u][c][k];
-                                const uint32_t hi = Pack<__half>::down(w0, w1);
-                                const float2 h = Pack<__half>::up(hi);
-                                b[k] = q4_transpose(hi);
-                                bl[k] = q4_transpose(Pack<__half>::down(w0 - h.x, w1 - h.y));
+                                const float h0 = q4_first(w0), h1 = q4_first(w1);
+                                b[k] = q4_transpose(Pack<__half>::down(h0, h1));
+                                bl[k] = q4_transpose(Pack<__half>::down(w0 - h0, w1 - h1));
                             }
-                            values(r, O[nt][c], b[0], b[1]);
-                            values(r, O[nt][c], bl[0], bl[1]);
+                            values(r, ol, bl[0], bl[1], u == 0);
+                            values(r, o, b[0], b[1], u == 0);
                         }
                     }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            O[nt][c][j][i] += S::kPacked ? o[j][i] : o[j][i] + ol[j][i];
                 }
             }
         };
@@ -964,8 +944,6 @@ __global__ void __launch_bounds__(kQ4Threads, (Q4Shape<D, R>::kCtas))
             upos += n;
             cu.chunk += n;
             fresh = used == asked || cu.chunk == cu.q.chunks;
-            // every kCentre steps of the sequence; a unit's rest at its end
-            if (fresh || (cu.chunk / S::kStep) % S::kCentre == 0) centre();
             if (fresh) {
                 end_unit(cu.chunk);
                 if (cu.chunk == cu.q.chunks) {

@@ -6,15 +6,16 @@ With p_j the weights, v = s n + z a group's values, b = s n + |z|, the error of 
 channels of a group, as a length, is below the sum of
 
 * 4 sqrt(sum_j p_j^2 d_j^2 |b_j|^2): errors of the weights, independent from token to token (a
-  row's weights do not know its values), four deviations.  d_j = 2^-20 + 2^-20 |scale| sum |q| b:
-  two parts of a weight 2^-22, exponential and maximum 2^-22 each; a logit's sums are cut off
+  row's weights do not know its values), four deviations.  d_j = 2^-18 + 2^-20 |scale| sum |q| b:
+  two parts of a weight 2^-19, exponential and maximum 2^-22 each; a logit's sums are cut off
   up to eight times a group of channels, by 2^-23 of what they reach.
-* 8 (the length of 64 channels) times 2^-16 sum_j p_j s_j: the values' products are cut off
-  towards zero twice a chunk, by 2^-23 of sums which are brought back to their middle every
-  eight chunks: in a window they reach 7.5 sum p s of it, 2 8 7.5 2^-23 < 2^-16.
-* 8 times 2^-19 sum_j p_j (|z_j| + 7.5 s_j): a warp adds up the groups' middles of at most 2^13
-  tokens, an eighth in each lane: 2^10 roundings by 2^-24 of the sum, 2^-19 as a random walk;
-  the lanes' parts are an eighth each and independent, so that this is five deviations.
+* 8 (the length of 64 channels) times 2^-18 sum_j p_j s_j: the values' products are cut off
+  towards zero up to twice in a sum, which reaches 7.5 sum p s in two equal steps:
+  2^-23 (3.75 + 7.5) < 2^-19, for each of the two parts of a weight.
+* 8 times 2^-18 sum_j p_j (|z_j| + 7.5 s_j): a warp adds up at most 2^13 tokens, an eighth in each
+  lane: 2^10 roundings by 2^-24 of the sum, 2^-19 as a random walk, of the least values and of
+  the products' sums; the lanes' parts are an eighth each and independent, so that this is five
+  deviations.
 
 and one rounding of the output.
 """
@@ -54,14 +55,14 @@ def rows_attention(k, v, q, scale):
     keys, key_terms = (kn * ks + kz).flatten(-2), (kn * ks + kz.abs()).flatten(-2)
     vals, val_terms = (vn * vs + vz).flatten(-2), vn * vs + vz.abs()          # [L][D], [L][C][64]
     x = q.double().reshape(n * G, D)
-    d = 2.0 ** -20 * (1 + abs(scale) * (x.abs() @ key_terms.T))
+    d = 2.0 ** -18 + 2.0 ** -20 * abs(scale) * (x.abs() @ key_terms.T)
     mask = torch.ones(n, L, dtype=torch.bool, device=q.device).triu(L - n + 1)
     mask = mask[:, None].expand(n, G, L).reshape(n * G, L)
     p = torch.softmax((x @ keys.T * scale).masked_fill(mask, float("-inf")), -1)
     squares = val_terms.square().sum(-1)                                     # [L][C]
     tol = 4 * ((p * d).square() @ squares).sqrt()
-    tol += 8 * 2.0 ** -16 * (p @ vs[..., 0])
-    tol += 8 * 2.0 ** -19 * (p @ (vz.abs() + 7.5 * vs)[..., 0])
+    tol += 8 * 2.0 ** -18 * (p @ vs[..., 0])
+    tol += 8 * 2.0 ** -18 * (p @ (vz.abs() + 7.5 * vs)[..., 0])
     return (p @ vals).view(n, G, D), tol.view(n, G, D // GROUP)
 
 

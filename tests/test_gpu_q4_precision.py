@@ -59,7 +59,7 @@ def test_long_drafts(H, Hkv, D, most):
 
 
 @pytest.mark.parametrize("H,Hkv,D", ROWS)
-def test_sums_stay_near_their_middle(H, Hkv, D):
+def test_sums_do_not_drift(H, Hkv, D):
     """Warps with hundreds of chunks of one context (32 sequences that share the blocks of a long
     one): sums of one sign that were cut off towards zero would be off by a percent of the output."""
     S, L = 32, 40000
