@@ -499,7 +499,7 @@ __device__ __forceinline__ void run_producer(const DecodeParams &P, T *sk, T *sv
     // The claim issued last is never used.  The fence waits until it (and
     // every claim before it) has been performed, so the counter is final
     // before the next call's plan kernel, which may start once this trigger
-    // has fired in every CTA, resets it.
+    // has fired in every CTA, resets it (behind its wait for this grid's end).
     __threadfence();
     pdl_trigger();
     if (P.after_sibling) pdl_wait();  // this grid ends after the tensor-core launch

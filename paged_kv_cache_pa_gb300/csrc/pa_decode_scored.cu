@@ -155,9 +155,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     decode_weights_kernel(const __grid_constant__ DecodeParams P, float *__restrict__ scores,
                           long long score_stride, int merges, int head_groups, int ranges,
                           unsigned tasks, bool vec) {
-    // (no dependent is let through early: the next call's plan writes its lists
-    // as soon as it starts, which for other sizes lie where this call's logits
-    // and states do)
+    // (no dependent is let through early)
     pdl_wait();  // the logits and the pieces' states
     if ((int)blockIdx.x < merges) {
         merge_heads<D, HPC>(P, (int)blockIdx.x / head_groups, (int)blockIdx.x % head_groups);

@@ -25,7 +25,7 @@
 // or past rotary_dim), so a rotation never leaves its thread.  A token's
 // sines and cosines are computed once a CTA, for all its heads, while its
 // first rows are in flight.  A CTA takes as many tokens as give each thread
-// four rows, unless that leaves fewer than two CTAs an SM: with few rows a
+// four rows (two with 4-bit pools), unless that leaves fewer than two CTAs an SM: with few rows a
 // token (grouped queries) one row a thread is one round trip to memory a CTA
 // and half the rate (4099 tokens of 12 + 2 + 2 heads of 128: 12.4 us with four
 // rows, 3.4 more with one).
@@ -159,8 +159,8 @@ __device__ __forceinline__ void store_q4(uint8_t *pool, size_t tile, int token, 
 // A CTA takes `rounds` times 256 / (threads a row * rows at once) tokens; thread
 // = (token, row, unit j of the row).  A token's rows are its query heads, its
 // key heads and its value heads; a thread goes through its rows of all its
-// tokens as one list, four at a time.  QD: 0 for 16-bit pools, else 4-bit pools of
-// that head_dim.
+// tokens as one list, four at a time (4-bit pools: two).  QD: 0 for 16-bit pools, else
+// 4-bit pools of that head_dim.
 template <typename T, bool IL, int QD>
 __global__ void __launch_bounds__(kRotThreads, kRotCtas<(QD > 0)>)
     rotary_cache_write_kernel(const __grid_constant__ RotaryParams P) {
@@ -372,7 +372,7 @@ inline pa_status_t rotary_write(void *query_out, int64_t query_out_stride, const
     P.err = dev_error_word;
     if (plain) std::memset(&P.rot, 0, sizeof(P.rot));
     else P.rot = *rotary;
-    // tokens a CTA: enough for four rows a thread, while two CTAs an SM are left
+    // tokens a CTA: enough for kRotBatch rows a thread, while two CTAs an SM are left
     const int lanes = kRotThreads >> (P.lg_lpr + P.lg_rows);
     const int groups = (rows + (1 << P.lg_rows) - 1) >> P.lg_rows;  // rows a thread and token
     const int sms = device_sms();
