@@ -867,6 +867,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads
  *               whose lengths break the rules (its rows are zeroed),
  *               PA_ERRBIT_BLOCK_OOB (the block's tokens are skipped),
  *               PA_ERRBIT_TIMEOUT (out is not to be used)
+ * Blocks that sequences share are read once a sequence (pa_decode_attention reads
+ * them once a run of neighbours).
  * Results do not depend on the block size or on the order in which work
  * finishes.  Enqueues one kernel, and a merge kernel where max_context_len is
  * above 256.

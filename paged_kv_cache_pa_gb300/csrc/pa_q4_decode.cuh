@@ -59,12 +59,11 @@
 // rows) that is cut leaves partial results, which the merge kernel puts together.
 //
 // Bound: HBM, 72 bytes a group and token of K and V.  256 sequences of 40 heads of
-// 128, one row each: 140 us, 5.9 TB/s, 0.87 of the measured copy; before the sums'
-// correction the same work without the copies took 123, without the products
-// 131, all of it 137.  With more rows the products and the softmax bound it (64 heads on 8, 125000
-// tokens: 48 us; 39 without the values' products, 27 without any and without
-// copies): the warps that the registers leave (8 an SM) do not hide each other's
-// latencies.
+// 128, one row each: 139 us, 5.95 TB/s, 0.88 of the measured copy (an early form, of 137 us:
+// 123 without the copies, 131 without the products).  With more rows the products and
+// the softmax bound it (64 heads on 8, 125000 tokens: 49 us; the early form 48, 39 without
+// the values' products, 27 without any and without copies): the warps that the
+// registers leave (8 an SM) do not hide each other's latencies.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -5,7 +5,7 @@
 //
 // Bound: instructions.  16384 tokens of 40 heads of 128, K and V turned and all in 4 bits:
 // 165 us where the bytes alone would take 113 and the 16-bit write, with a third more
-// bytes, takes 150.
+// bytes, takes 150.  K and V alone, not turned: 117 us, the bytes 64.
 #include <cuda_runtime.h>
 
 #include "pa.h"
