@@ -857,7 +857,8 @@ size_t pa_decode_q4_workspace_size(int num_seqs, int num_heads, int num_kv_heads
  *               max_context_len; lengths, tables and query_start_loc are read as
  *               soon as the kernel starts (as pa_decode_attention reads them)
  * max_query_len host-known bound on n_s, 1 .. PA_MAX_Q4_QUERY (PA_ERR_UNSUPPORTED
- *               beyond); max_context_len host-known bound on context_lens,
+ *               beyond), which chooses the kernel's form for the whole batch;
+ *               max_context_len host-known bound on context_lens,
  *               <= block_size * max_blocks_per_seq
  * num_heads % num_kv_heads == 0; head_dim 64, 128 or 256; dtype PA_F16 or PA_BF16
  * workspace     device, >= pa_decode_q4_workspace_size(...) bytes, 256-byte
